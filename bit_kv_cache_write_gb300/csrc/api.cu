@@ -73,6 +73,12 @@ oscar_status record_failure(oscar_status st, const char* fmt, ...) {
     return st;
 }
 
+oscar_status check_context(const oscar_ctx* ctx) {
+    return ctx ? check_device(ctx) : fail(OSCAR_ERR_INVALID_ARG, "ctx is NULL");
+}
+
+bool injected_fault(const char* what) { return fault(what); }
+
 LayerParams layer_params(const oscar_ctx* ctx, int layer) {
     const Shape& s = ctx->shape;
     const size_t hdd = (size_t)s.h_kv * s.d * s.d, hd = (size_t)s.h_kv * s.d;

@@ -115,6 +115,12 @@ LayerParams layer_params(const oscar_ctx* ctx, int layer);
 // Records `st` and a formatted message as the calling thread's last failure; returns st.
 oscar_status record_failure(oscar_status st, const char* fmt, ...);
 
+// For calls that need no layer: ctx is there and its device is the current one.
+oscar_status check_context(const oscar_ctx* ctx);
+
+// Whether OSCAR_FAULT asks this step to fail.
+bool injected_fault(const char* what);
+
 // ---- write path (write_kernels.cu)
 cudaError_t launch_write(const Shape& s, const LayerParams& p, int num_sms,
                          const void* k, const void* v, const int64_t* slots, int n,

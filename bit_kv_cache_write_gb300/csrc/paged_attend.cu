@@ -1,0 +1,259 @@
+// Attention of one new token over BF16 pages (oscar_decode_bf16, oscar_decode_bf16_sparse).
+//
+// o = sum_t p_t v_t / sum_t p_t with p_t = 2^(l_t - m), l_t = sm_scale log2(e) q.k_t and a running reference m:
+// one pass over the pages, split over the length, the splits' (m, l, acc) joined afterwards.
+//
+// One warp takes one 16-token page of a (sequence, KV head) at a time, for all g <= 8 query heads, with
+// mma.sync m16n8k16 on operands that go from HBM straight to registers:
+//   logits  S[heads, tokens] = Q[16 (8 used), d] K^T: lane (gid, t) loads 16 bytes, channels 32 j + 8 t ..
+//           + 7 of token gid, which hold its part of two k-steps (the contraction's order is free, Q is
+//           permuted alike);
+//   output  O^T[channels, heads] = V^T[channels, 16 tokens] P^T: lane (gid, t) loads 8 channels of the tokens
+//           2t, 2t+1, 2t+8, 2t+9, and byte permutations pair the tokens. S leaves the first product in the
+//           layout that P^T has to enter the second one in.
+// Weights enter as three bf16 pieces (24 bits), products of bf16 are exact, and each page's sums are added to
+// the fp32 accumulators with rounded additions, so nothing is lost to the bf16 operands.
+#include "paged_device.cuh"
+
+namespace oscar {
+namespace {
+
+constexpr int kAttendWarps = 4;
+constexpr float kNoLogit = -1e30f;       // running reference before any token
+constexpr float kHeadroom = 8.0f;        // the reference is raised when a logit passes it by this much (log2)
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two fp32 to packed bf16 (first argument in the low half).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+template <int D>
+struct Page {
+    uint4 k[2][D / 32];                  // tokens gid, gid + 8
+    uint4 v[4][D / 64];                  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+};
+
+template <int D>
+__device__ __forceinline__ void load_k(Page<D>& p, const uint16_t* page, int gid, int t) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) p.k[n][j] = ldg_stream(page + (gid + 8 * n) * D + 32 * j + 8 * t);
+}
+template <int D>
+__device__ __forceinline__ void load_v(Page<D>& p, const uint16_t* page, int gid, int t) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int f = 0; f < D / 64; ++f)
+            p.v[n][f] = ldg_stream(page + kPage * D + (2 * t + (n & 1) + 8 * (n >> 1)) * D + 64 * f + 8 * gid);
+}
+
+template <int D, bool SPARSE>
+__global__ void __launch_bounds__(kAttendWarps * 32, 3) attend_kernel(AttendArgs a) {
+    constexpr int kTiles = D / 16;       // m-tiles of the output product
+    __shared__ float warp_m[kAttendWarps][8], warp_l[kAttendWarps][8];
+    __shared__ float warp_acc[kAttendWarps][8][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, t = lane & 3;
+    const int split = blockIdx.x % a.splits;
+    const int unit = blockIdx.x / a.splits, h = unit % a.h_kv, b = unit / a.h_kv;
+    grid_wait();
+    grid_release();
+    const int len = checked_len(a.seq_len[b], a.max_len, a.debug && split == 0 && threadIdx.x == 0, a.dbg);
+    const int listed = SPARSE ? a.n_chosen[unit] : (len + kPage - 1) / kPage;
+    const int first = split * a.pages_per_split, last = min(listed, first + a.pages_per_split);
+    if (first >= last && !(a.splits == 1)) return;       // the merge skips empty splits by the same rule
+    const int32_t* table = a.tables + (int64_t)b * a.stride;
+    const int32_t* list = SPARSE ? a.chosen + (int64_t)unit * a.cap : nullptr;
+
+    // Q as the A operand: rows gid (heads), the upper eight rows are empty.
+    uint4 q[D / 32];
+    const uint16_t* qrow = a.q + b * a.q_stride + (int64_t)(h * a.g + gid) * D;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+        q[j] = gid < a.g ? *reinterpret_cast<const uint4*>(qrow + 32 * j + 8 * t) : make_uint4(0, 0, 0, 0);
+
+    float m = kNoLogit, l = 0.0f;        // head gid (l: this lane's tokens)
+    float acc[kTiles][4] = {};           // channels of gid, heads 2t and 2t + 1
+
+    for (int i = first + warp; i < last; i += kAttendWarps) {
+        const int logical = SPARSE ? list[i] : i;
+        const int id = table[logical];
+        int valid = min(kPage, len - logical * kPage);
+        const uint16_t* page = a.pool;
+        if (id < 0 || id >= a.pages) {
+            if (a.debug && lane == 0) record_error(&a.dbg->kind, &a.dbg->index, 2, id);
+            valid = 0;
+        } else {
+            page += ((int64_t)id * a.h_kv + h) * (2 * kPage * D);
+        }
+        Page<D> p;
+        load_k<D>(p, page, gid, t);
+        load_v<D>(p, page, gid, t);
+
+        float s[2][4] = {};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                mma_bf16(s[n], q[j].x, 0, q[j].y, 0, p.k[n][j].x, p.k[n][j].y);
+                mma_bf16(s[n], q[j].z, 0, q[j].w, 0, p.k[n][j].z, p.k[n][j].w);
+            }
+        float x[4];                      // tokens 2t, 2t + 1, 2t + 8, 2t + 9 of head gid
+#pragma unroll
+        for (int n = 0; n < 4; ++n) x[n] = s[n >> 1][n & 1] * a.scale_log2;
+        if (valid < kPage) {             // masked tokens: no weight, and their V cannot carry a NaN in
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                if (2 * t + (n & 1) + 8 * (n >> 1) >= valid) {
+                    x[n] = -INFINITY;
+#pragma unroll
+                    for (int f = 0; f < D / 64; ++f) p.v[n][f] = make_uint4(0, 0, 0, 0);
+                }
+        }
+        float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        if (__any_sync(~0u, top > m + kHeadroom)) {
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+            const float m_new = fmaxf(m, top), f = exp2f(m - m_new);
+            m = m_new;
+            l *= f;
+            const float f0 = __shfl_sync(~0u, f, 8 * t), f1 = __shfl_sync(~0u, f, 8 * t + 4);
+#pragma unroll
+            for (int i2 = 0; i2 < kTiles; ++i2) {
+                acc[i2][0] *= f0; acc[i2][1] *= f1; acc[i2][2] *= f0; acc[i2][3] *= f1;
+            }
+        }
+        uint32_t w[3][2];                // pieces of the weights as the B operand
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            float p0 = exp2f(x[2 * n] - m), p1 = exp2f(x[2 * n + 1] - m);
+            l += p0 + p1;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                w[k][n] = pack_bf16(p0, p1);
+                p0 -= bf16_lo(w[k][n]);
+                p1 -= bf16_hi(w[k][n]);
+            }
+        }
+#pragma unroll
+        for (int f = 0; f < D / 64; ++f)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t v0 = (&p.v[0][f].x)[u], v1 = (&p.v[1][f].x)[u], v2 = (&p.v[2][f].x)[u],
+                               v3 = (&p.v[3][f].x)[u];
+                const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632),
+                               a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+                float c[4] = {};
+#pragma unroll
+                for (int k = 2; k >= 0; --k) mma_bf16(c, a0, a1, a2, a3, w[k][0], w[k][1]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[4 * f + u][k] += c[k];
+            }
+    }
+
+    // Join the warps: reference and sum per head, accumulators through shared memory.
+    l += __shfl_xor_sync(~0u, l, 1);
+    l += __shfl_xor_sync(~0u, l, 2);
+    if (t == 0) { warp_m[warp][gid] = m; warp_l[warp][gid] = l; }
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)      // rows gid and gid + 8 of m-tile (f, u) are channels 64 f + 8 gid + 2 u and + 1
+            warp_acc[warp][2 * t + (k & 1)][64 * (i / 4) + 8 * gid + 2 * (i % 4) + (k >> 1)] = acc[i][k];
+    __syncthreads();
+    for (int x = threadIdx.x; x < a.g * D; x += kAttendWarps * 32) {
+        const int head = x / D, c = x % D;
+        float mm = warp_m[0][head];
+#pragma unroll
+        for (int w = 1; w < kAttendWarps; ++w) mm = fmaxf(mm, warp_m[w][head]);
+        float ll = 0.0f, o = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttendWarps; ++w) {
+            const float f = exp2f(warp_m[w][head] - mm);
+            ll += f * warp_l[w][head];
+            o += f * warp_acc[w][head][c];
+        }
+        const int64_t row = (int64_t)b * a.h_kv * a.g + h * a.g + head;
+        if (a.splits == 1) {
+            const float r = ll == 0.0f ? 0.0f : o / ll;      // no token: zeros
+            if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[row * D + c] = __float2bfloat16(r);
+            else static_cast<float*>(a.out)[row * D + c] = r;
+        } else {
+            float* part = a.partials + (row * a.splits + split) * (D + 2);
+            part[2 + c] = o;
+            if (c == 0) { part[0] = mm; part[1] = ll; }
+        }
+    }
+}
+
+// Joins the splits of one query head: thread c owns channel c.
+template <int D, bool SPARSE>
+__global__ void __launch_bounds__(D) join_kernel(AttendArgs a) {
+    const int c = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const int hq = a.h_kv * a.g, b = (int)(row / hq), unit = b * a.h_kv + (int)(row % hq) / a.g;
+    grid_wait();
+    grid_release();
+    const int len = checked_len(a.seq_len[b], a.max_len, 0, a.dbg);
+    const int listed = SPARSE ? a.n_chosen[unit] : (len + kPage - 1) / kPage;
+    const int n = (listed + a.pages_per_split - 1) / a.pages_per_split;
+    const float* part = a.partials + row * a.splits * (D + 2);
+    float m = kNoLogit;
+    for (int i = 0; i < n; ++i) m = fmaxf(m, part[(int64_t)i * (D + 2)]);
+    float l = 0.0f, o = 0.0f;
+    for (int i = 0; i < n; ++i) {
+        const float* p = part + (int64_t)i * (D + 2);
+        const float f = exp2f(p[0] - m);
+        l += f * p[1];
+        o += f * p[2 + c];
+    }
+    const float r = l == 0.0f ? 0.0f : o / l;
+    if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[row * D + c] = __float2bfloat16(r);
+    else static_cast<float*>(a.out)[row * D + c] = r;
+}
+
+template <int D, bool SPARSE>
+cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
+    const long long ctas = (long long)a.splits * a.h_kv * a.batch;
+    if (ctas > 0x7fffffffLL || (long long)a.batch * a.h_kv * a.g > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cudaError_t e = launch_dependent(attend_kernel<D, SPARSE>, dim3((unsigned)ctas), dim3(kAttendWarps * 32), 0, st, 1, a);
+    if (e != cudaSuccess || a.splits == 1) return e;
+    return launch_dependent(join_kernel<D, SPARSE>, dim3(a.batch * a.h_kv * a.g), dim3(D), 0, st, 1, a);
+}
+
+}  // namespace
+
+AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages) {
+    AttendPlan p{};
+    const long long units = (long long)batch * s.h_kv;
+    const int slots = 3 * num_sms;                       // resident CTAs
+    long long splits = units > 0 ? slots / units : 1;
+    const long long by_len = (max_pages + 255) / 256;    // at most 256 pages a split
+    if (splits < by_len) splits = by_len;
+    const long long most = (max_pages + kAttendWarps - 1) / kAttendWarps;
+    if (splits > most) splits = most;
+    if (splits < 1) splits = 1;
+    p.pages_per_split = max_pages > 0 ? (int)((max_pages + splits - 1) / splits) : 1;
+    p.splits = max_pages > 0 ? (max_pages + p.pages_per_split - 1) / p.pages_per_split : 1;
+    p.ws_partials = p.splits == 1 ? 0 : ((size_t)batch * s.h_q * p.splits * (s.d + 2) * sizeof(float) + 255) / 256 * 256;
+    return p;
+}
+
+cudaError_t launch_attend(const AttendArgs& a, int d, cudaStream_t st) {
+    if (d == 128) return a.chosen ? launch<128, true>(a, st) : launch<128, false>(a, st);
+    return a.chosen ? launch<64, true>(a, st) : launch<64, false>(a, st);
+}
+
+}  // namespace oscar

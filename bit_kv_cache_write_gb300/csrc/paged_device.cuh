@@ -1,0 +1,55 @@
+// Device helpers shared by the BF16 paged-cache kernels, and their launch with programmatic dependence.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "layout.cuh"
+#include "paged_internal.h"
+
+namespace oscar {
+namespace {
+
+// Waits for the grids before this one in the stream (everything they wrote is visible afterwards).
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next grid's CTAs start where there is room; they wait in grid_wait().
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+// Sequence length as the kernels use it: within [0, max_len]; anything else is recorded.
+__device__ __forceinline__ int checked_len(int len, int max_len, int debug, DebugWord* dbg) {
+    if (len < 0 || len > max_len) {
+        if (debug) record_error(&dbg->kind, &dbg->index, 3, len);
+        len = len < 0 ? 0 : max_len;
+    }
+    return len;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, int cluster,
+                             Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace
+}  // namespace oscar

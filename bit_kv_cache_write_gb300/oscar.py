@@ -60,11 +60,21 @@ _SIGS = {
     "oscar_calibration_workspace_size": (_sz, [_i, _i, _i, _i]),
     "oscar_calibration_targets": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, ctypes.c_double, _vp, _vp, _vp, _sz,
                                        _vp]),
+    "oscar_plan_append": (_i, [_vp, _vp, _vp, _i, _vp, _i, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp]),
+    "oscar_append_bf16": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i, _vp, _i64, _vp, _vp, _vp]),
+    "oscar_decode_bf16_workspace_size": (_sz, [_vp, _i, _i]),
+    "oscar_decode_bf16": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i, _vp, _i, _vp, _i, _vp, _sz, _i, _vp]),
+    "oscar_sparse_capacity": (_i, [_vp, _i]),
+    "oscar_decode_bf16_sparse_workspace_size": (_sz, [_vp, _i, _i, _i]),
+    "oscar_decode_bf16_sparse": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _i,
+                                      _vp, _sz, _i, _vp]),
     "oscar_profile_enable": (_i, [_vp, _i]),
     "oscar_profile_read": (_i, [_vp, _i, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_longlong)]),
 }
 
 OSCAR_KERNEL_WRITE, OSCAR_KERNEL_QROT, OSCAR_KERNEL_SPLIT, OSCAR_KERNEL_MERGE = 0, 1, 2, 3
+OSCAR_KERNEL_PLAN, OSCAR_KERNEL_APPEND, OSCAR_KERNEL_SELECT, OSCAR_KERNEL_ATTEND = 4, 5, 6, 7
+OSCAR_OUT_FP32, OSCAR_OUT_BF16 = 0, 1
 
 
 def lib():
@@ -125,10 +135,12 @@ def oscar_create(n_layers, n_q_heads, n_kv_heads, head_dim, group, page_size=16,
                          float(sm_scale), int(debug_bounds), int(codebook))
     ctx = _vp()
     _check(lib().oscar_create(ctypes.byref(cfg), ctypes.byref(ctx)), "oscar_create")
+    _configs[ctx.value] = (n_q_heads, n_kv_heads, head_dim)
     return ctx.value
 
 
 def oscar_destroy(ctx):
+    _configs.pop(ctx, None)
     lib().oscar_destroy(ctx)
 
 
@@ -258,6 +270,142 @@ def oscar_decode_static_workspace(ctx, layer, q, int2_pool, int2_tables, hist_le
         _dptr(out, torch.float32, "out"), batch, _stream(stream)), "oscar_decode_static_workspace")
 
 
+_configs = {}     # context handle -> (H_q, H_kv, d) of the contexts created here, for the shape checks below
+
+
+def _shape_of(ctx):
+    try:
+        return _configs[ctx]
+    except KeyError:
+        raise ValueError("the context was not created by oscar_create") from None
+
+
+def _out_type(out):
+    import torch
+    if out.dtype == torch.float32:
+        return OSCAR_OUT_FP32
+    if out.dtype == torch.bfloat16:
+        return OSCAR_OUT_BF16
+    raise ValueError("out must be torch.float32 or torch.bfloat16, got %s" % out.dtype)
+
+
+def _rows(t, heads, d, name):
+    """(pointer, row stride in elements) of bf16 rows [n][heads][d] whose heads lie together."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise ValueError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError("%s must be [n][%d][%d], got %s" % (name, heads, d, tuple(t.shape)))
+    s = t.stride()
+    if t.numel() and (s[2] != 1 or (heads > 1 and s[1] != d)):
+        raise ValueError("%s: a row's heads must be contiguous (strides %s)" % (name, s))
+    return t.data_ptr(), s[0] if t.shape[0] > 1 else heads * d
+
+
+def _sized(t, dtype, n, name):
+    """Pointer of a contiguous tensor of n elements."""
+    p = _dptr(t, dtype, name)
+    if p is None or t.numel() != n:
+        raise ValueError("%s must hold %d elements, holds %s" % (name, n, None if t is None else t.numel()))
+    return p
+
+
+def oscar_plan_append(ctx, seq_len, new_len, free_pages, free_head, tables, slots, row_start, total_len, state,
+                      stream=None):
+    """seq_len, new_len int32 [B]; free_pages int32; free_head int32 [1]; tables int32 [B][stride] (in and out);
+    out: slots int64, row_start int32 [B + 1], total_len int32 [B], state int32 [4]."""
+    import torch
+    i32, batch = torch.int32, seq_len.numel()
+    if tables.dim() != 2 or tables.shape[0] != batch:
+        raise ValueError("tables must be [%d][stride], got %s" % (batch, tuple(tables.shape)))
+    _check(lib().oscar_plan_append(
+        ctx, _dptr(seq_len, i32, "seq_len"), _sized(new_len, i32, batch, "new_len"), batch,
+        _dptr(free_pages, i32, "free_pages"), free_pages.numel(), _sized(free_head, i32, 1, "free_head"),
+        _dptr(tables, i32, "tables"), tables.shape[1], _dptr(slots, torch.int64, "slots"), slots.numel(),
+        _sized(row_start, i32, batch + 1, "row_start"), _sized(total_len, i32, batch, "total_len"),
+        _sized(state, i32, 4, "state"), _stream(stream)), "oscar_plan_append")
+
+
+def oscar_append_bf16(ctx, k, v, slots, bf16_pool, key_steps=None, key_bounds=None, stream=None):
+    """k, v: bf16 [n][H_kv][d], rows at any stride; slots int64 [n]; bf16_pool: whole pages; key_steps int8
+    [H_kv][d] and key_bounds int8 [pages][H_kv][2][d], or neither."""
+    import torch
+    _, h_kv, d = _shape_of(ctx)
+    pages = bf16_pool.numel() // (h_kv * 32 * d)
+    kp, ks = _rows(k, h_kv, d, "k")
+    vp, vs = _rows(v, h_kv, d, "v")
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise ValueError("k and v differ in length")
+    steps = bounds = None
+    if key_steps is not None or key_bounds is not None:
+        steps = _sized(key_steps, torch.int8, h_kv * d, "key_steps")
+        bounds = _sized(key_bounds, torch.int8, pages * h_kv * 2 * d, "key_bounds")
+    _check(lib().oscar_append_bf16(ctx, kp, ks, vp, vs, _sized(slots, torch.int64, n, "slots"), n,
+                                   _dptr(bf16_pool, torch.bfloat16, "bf16_pool"), pages, steps, bounds,
+                                   _stream(stream)), "oscar_append_bf16")
+
+
+def oscar_decode_bf16_workspace_size(ctx, batch, max_len):
+    return lib().oscar_decode_bf16_workspace_size(ctx, batch, max_len)
+
+
+def _decode_shapes(q, tables, out):
+    batch = q.shape[0]
+    if tables.dim() != 2 or tables.shape[0] != batch:
+        raise ValueError("tables must be [%d][stride], got %s" % (batch, tuple(tables.shape)))
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape %s, has %s" % (tuple(q.shape), tuple(out.shape)))
+    return batch
+
+
+def oscar_decode_bf16(ctx, q, bf16_pool, tables, seq_len, max_len, out, workspace, stream=None):
+    """q: bf16 [B][H_q][d], rows at any stride; tables int32 [B][stride]; seq_len int32 [B], at most max_len;
+    out fp32 or bf16 [B][H_q][d]; workspace uint8."""
+    import torch
+    h_q, h_kv, d = _shape_of(ctx)
+    qp, qs = _rows(q, h_q, d, "q")
+    batch = _decode_shapes(q, tables, out)
+    _check(lib().oscar_decode_bf16(
+        ctx, qp, qs, _dptr(bf16_pool, torch.bfloat16, "bf16_pool"), bf16_pool.numel() // (h_kv * 32 * d),
+        _dptr(tables, torch.int32, "tables"), tables.shape[1], _sized(seq_len, torch.int32, batch, "seq_len"),
+        int(max_len), _dptr(out, None, "out"), _out_type(out), _dptr(workspace, None, "workspace"),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), batch, _stream(stream)),
+        "oscar_decode_bf16")
+
+
+def oscar_sparse_capacity(ctx, top_pages):
+    return lib().oscar_sparse_capacity(ctx, top_pages)
+
+
+def oscar_decode_bf16_sparse_workspace_size(ctx, batch, max_len, top_pages):
+    return lib().oscar_decode_bf16_sparse_workspace_size(ctx, batch, max_len, top_pages)
+
+
+def oscar_decode_bf16_sparse(ctx, q, bf16_pool, key_steps, key_bounds, tables, seq_len, max_len, top_pages, chosen,
+                             n_chosen, out, workspace, stream=None):
+    """oscar_decode_bf16 over the sink, the recent window and the top_pages best pages by their key bounds; chosen
+    int32 [B][H_kv][oscar_sparse_capacity(ctx, top_pages)] and n_chosen int32 [B][H_kv] say which."""
+    import torch
+    h_q, h_kv, d = _shape_of(ctx)
+    qp, qs = _rows(q, h_q, d, "q")
+    batch = _decode_shapes(q, tables, out)
+    pages = bf16_pool.numel() // (h_kv * 32 * d)
+    handle = lib()
+    cap = handle.oscar_sparse_capacity(ctx, top_pages)
+    _check(handle.oscar_decode_bf16_sparse(
+        ctx, qp, qs, _dptr(bf16_pool, torch.bfloat16, "bf16_pool"), pages,
+        _sized(key_steps, torch.int8, h_kv * d, "key_steps"),
+        _sized(key_bounds, torch.int8, pages * h_kv * 2 * d, "key_bounds"),
+        _dptr(tables, torch.int32, "tables"), tables.shape[1], _sized(seq_len, torch.int32, batch, "seq_len"),
+        int(max_len), int(top_pages), _sized(chosen, torch.int32, batch * h_kv * cap, "chosen") if cap else None,
+        _sized(n_chosen, torch.int32, batch * h_kv, "n_chosen"), _dptr(out, None, "out"), _out_type(out),
+        _dptr(workspace, None, "workspace"), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        batch, _stream(stream)), "oscar_decode_bf16_sparse")
+
+
 def oscar_debug_error(ctx):
     """Returns (status, kind, index) and clears the device error word."""
     kind = _i(0)
@@ -325,6 +473,31 @@ class Oscar:
                              bf16_tables, bf16_len, out, workspace, stream=None):
         oscar_decode_shared_prefix(self.ctx, layer, q, int2_pool, prefix_table, int2_tables, hist_len, max_hist,
                                    bf16_pool, bf16_tables, bf16_len, out, workspace, stream)
+
+    def plan_append(self, seq_len, new_len, free_pages, free_head, tables, slots, row_start, total_len, state,
+                    stream=None):
+        oscar_plan_append(self.ctx, seq_len, new_len, free_pages, free_head, tables, slots, row_start, total_len,
+                          state, stream)
+
+    def append_bf16(self, k, v, slots, bf16_pool, key_steps=None, key_bounds=None, stream=None):
+        oscar_append_bf16(self.ctx, k, v, slots, bf16_pool, key_steps, key_bounds, stream)
+
+    def decode_bf16_workspace_size(self, batch, max_len):
+        return oscar_decode_bf16_workspace_size(self.ctx, batch, max_len)
+
+    def decode_bf16(self, q, bf16_pool, tables, seq_len, max_len, out, workspace, stream=None):
+        oscar_decode_bf16(self.ctx, q, bf16_pool, tables, seq_len, max_len, out, workspace, stream)
+
+    def sparse_capacity(self, top_pages):
+        return oscar_sparse_capacity(self.ctx, top_pages)
+
+    def decode_bf16_sparse_workspace_size(self, batch, max_len, top_pages):
+        return oscar_decode_bf16_sparse_workspace_size(self.ctx, batch, max_len, top_pages)
+
+    def decode_bf16_sparse(self, q, bf16_pool, key_steps, key_bounds, tables, seq_len, max_len, top_pages, chosen,
+                           n_chosen, out, workspace, stream=None):
+        oscar_decode_bf16_sparse(self.ctx, q, bf16_pool, key_steps, key_bounds, tables, seq_len, max_len, top_pages,
+                                 chosen, n_chosen, out, workspace, stream)
 
     def int2_page_bytes(self):
         return oscar_int2_page_bytes(self.ctx)

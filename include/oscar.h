@@ -292,7 +292,6 @@ OSCAR_API oscar_status oscar_decode_static_workspace(oscar_ctx_t* ctx, int layer
                                                      const int32_t* bf16_tables, int bf16_table_stride,
                                                      const int32_t* bf16_len, float* out, int batch, void* stream);
 
-/* Bytes of one INT2 page (all heads, K and V) and of one BF16 page. */
 /* Offline calibration targets on the GPU ([QBIT] section "OSCAR aligns the
  * rotation with attention": per layer and per head, the key target Q^T Q and
  * the score-weighted value target V^T S^T S V, estimated from a few
@@ -316,6 +315,126 @@ OSCAR_API oscar_status oscar_calibration_targets(const float* q_cal, const float
                                                  double sm_scale, double* target_k, double* target_v,
                                                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * BF16 paged cache: planning, appending, decode attention
+ * ---------------------------------------------------------------------------
+ * For layers whose cache stays BF16, and for the BF16 pool that oscar_decode and
+ * oscar_demote_recent read. These calls need no calibration and take no layer;
+ * heads, d, sm_scale, sink and recent are the context's. Pools, tables and slots
+ * are laid out as above. A page id outside the pool is never read: its tokens
+ * count as masked (and are recorded with debug_bounds, kind 2). */
+
+/* Block tables and slot maps of one step, from the requests' lengths (no
+ * counterpart on the pages: what a serving loop has to do before it can call
+ * oscar_write_tokens, oscar_append_bf16 or a decode).
+ *   seq_len:    DEVICE int32 [batch], tokens that request b has cached.
+ *   new_len:    DEVICE int32 [batch], tokens to append; 0 is allowed.
+ *   free_pages: DEVICE int32 [n_free], unused page ids; entries from *free_head
+ *               on are handed out, in request order.
+ *   free_head:  DEVICE int32 [1]. It may be state[0] of the previous step.
+ *   tables:     DEVICE int32 [batch][table_stride], in and out: the entries of
+ *               the pages that a request needs anew are written.
+ *   slots:      DEVICE int64 [slot_cap], written: the slots of the new tokens,
+ *               request after request; -1 behind them and for the tokens of a
+ *               rejected request. oscar_append_bf16 skips such tokens.
+ *               oscar_write_tokens and oscar_demote_recent do not: give those
+ *               exactly state[1] slots, and only where state[2] is 0.
+ *   row_start:  DEVICE int32 [batch + 1], written: first slot of each request.
+ *   total_len:  DEVICE int32 [batch], written: seq_len + new_len, or seq_len
+ *               where the request was rejected.
+ *   state:      DEVICE int32 [4], written: the new free head, all new tokens,
+ *               rejected requests, the first of them or -1.
+ * A request is rejected, and takes no page, when a length is negative, when
+ * seq_len + new_len passes 16 * table_stride, when its slots pass slot_cap, or
+ * when it needs pages and the pages needed up to and with it (by requests not
+ * rejected for another reason) are more than the free list holds. A free_head
+ * outside the list counts as an empty list.
+ * The buffers must not overlap, but for free_head. Asynchronous on `stream`. */
+OSCAR_API oscar_status oscar_plan_append(oscar_ctx_t* ctx, const int32_t* seq_len, const int32_t* new_len, int batch,
+                                         const int32_t* free_pages, int n_free, const int32_t* free_head,
+                                         int32_t* tables, int table_stride, int64_t* slots, int slot_cap,
+                                         int32_t* row_start, int32_t* total_len, int32_t* state, void* stream);
+
+/* New K/V rows into the BF16 pool, and the key bounds of their pages.
+ *   k, v:       DEVICE bf16, token i at k + i * k_stride elements, [H_kv][d]
+ *               each (a slice of a projection's rows will do). The strides are
+ *               multiples of 8; the pointers are 16-byte aligned.
+ *   slots:      DEVICE int64 [n], distinct BF16 slots. A negative slot skips its
+ *               token; one behind the pool does too (recorded with debug_bounds).
+ *   key_steps:  DEVICE int8 [H_kv][d], or NULL for no bounds: the bounds of a
+ *               channel are in units of 2^key_steps (within +-100).
+ *   key_bounds: DEVICE int8 [bf16_pool_pages][H_kv][2][d], or NULL.
+ * The code of a key is clamp(rint(k * 2^-step), -127, 127), 0 for a NaN.
+ * key_bounds[page][h] holds the least (0) and the largest (1) code of the rows
+ * appended to the page since its row 0: tokens that are adjacent in `slots` and
+ * go to one page are one run; a run that has row 0 starts the page's bounds
+ * anew, another one widens them. With bounds, a page's tokens of one call must
+ * be one run (oscar_plan_append's slots are).
+ * Asynchronous on `stream`. n == 0 is a no-op. */
+OSCAR_API oscar_status oscar_append_bf16(oscar_ctx_t* ctx, const void* k, int64_t k_stride, const void* v,
+                                         int64_t v_stride, const int64_t* slots, int n, void* bf16_pool,
+                                         int64_t bf16_pool_pages, const int8_t* key_steps, int8_t* key_bounds,
+                                         void* stream);
+
+/* Type of the output of the BF16 decodes. */
+typedef enum {
+    OSCAR_OUT_FP32 = 0,
+    OSCAR_OUT_BF16 = 1    /* the fp32 result rounded once, to nearest even */
+} oscar_out_type;
+
+/* Paged decode attention of one new token over a BF16 cache of any length:
+ *   out = softmax(sm_scale * q . K^T) V over the sequence's seq_len tokens.
+ *   q:          DEVICE bf16, sequence b at q + b * q_stride elements, [H_q][d].
+ *               q_stride is a multiple of 8, q 16-byte aligned.
+ *   tables:     DEVICE int32 [batch][table_stride].
+ *   seq_len:    DEVICE int32 [batch], each within [0, max_len]; a length outside
+ *               counts as the nearer end. 0 gives zeros.
+ *   max_len:    host bound of the lengths, <= 16 * table_stride and <= 2^30.
+ *   out:        DEVICE [batch][H_q][d] of out_type.
+ *   workspace:  DEVICE, >= oscar_decode_bf16_workspace_size(ctx, batch, max_len)
+ *               bytes, 256-byte aligned; scratch, nothing in it is kept. It may
+ *               be NULL where that size is 0. Calls that overlap on the GPU need
+ *               a workspace each.
+ * Tokens behind a sequence's length are not looked at: what they hold, NaN or
+ * infinity too, does not matter. The result does not change from run to run.
+ * Asynchronous on `stream`. batch == 0 is a no-op; batch > 65535 returns
+ * OSCAR_ERR_UNSUPPORTED. */
+OSCAR_API size_t oscar_decode_bf16_workspace_size(const oscar_ctx_t* ctx, int batch, int max_len);
+OSCAR_API oscar_status oscar_decode_bf16(oscar_ctx_t* ctx, const void* q, int64_t q_stride, const void* bf16_pool,
+                                         int64_t bf16_pool_pages, const int32_t* tables, int table_stride,
+                                         const int32_t* seq_len, int max_len, void* out, int out_type,
+                                         void* workspace, size_t workspace_bytes, int batch, void* stream);
+
+/* oscar_decode_bf16 that reads only some pages of each (sequence, KV head): the
+ * sink (the first `sink` tokens' pages), the pages of the last `recent` tokens,
+ * and of the pages between them the top_pages with the largest score (all of
+ * them where there are no more; 0 is allowed).
+ *   Score, from the key bounds alone, per KV head: with x = q * 2^key_step per
+ *   channel (0 where that is not finite) and 2^w the least power of two above
+ *   max |x|, a query head's codes are u = clamp(rint(x * 2^-e), -127, 127),
+ *   e = min(w - 7, 60) (all 0 where max |x| < 2^-60). The score of a page is the
+ *   largest of 2^e * sum_c max(u_c * lo_c, u_c * hi_c) over the g query heads:
+ *   up to rounding, a bound of the page's logits. It is exact in fp32, so the
+ *   choice is well-defined; of equal scores the lower page is taken. A page
+ *   id outside the pool scores below every other.
+ *   key_steps, key_bounds: as oscar_append_bf16 takes and writes them.
+ *   top_pages:  0 .. 65536.
+ *   chosen:     DEVICE int32 [batch][H_kv][oscar_sparse_capacity(ctx, top_pages)],
+ *               written: the logical pages read, ascending, then -1.
+ *   n_chosen:   DEVICE int32 [batch][H_kv], written: how many.
+ *   workspace:  >= oscar_decode_bf16_sparse_workspace_size(...) bytes.
+ * Everything else as for oscar_decode_bf16. */
+OSCAR_API int oscar_sparse_capacity(const oscar_ctx_t* ctx, int top_pages);
+OSCAR_API size_t oscar_decode_bf16_sparse_workspace_size(const oscar_ctx_t* ctx, int batch, int max_len, int top_pages);
+OSCAR_API oscar_status oscar_decode_bf16_sparse(oscar_ctx_t* ctx, const void* q, int64_t q_stride,
+                                                const void* bf16_pool, int64_t bf16_pool_pages,
+                                                const int8_t* key_steps, const int8_t* key_bounds,
+                                                const int32_t* tables, int table_stride, const int32_t* seq_len,
+                                                int max_len, int top_pages, int32_t* chosen, int32_t* n_chosen,
+                                                void* out, int out_type, void* workspace, size_t workspace_bytes,
+                                                int batch, void* stream);
+
+/* Bytes of one INT2 page (all heads, K and V) and of one BF16 page. */
 OSCAR_API size_t oscar_int2_page_bytes(const oscar_ctx_t* ctx);
 OSCAR_API size_t oscar_bf16_page_bytes(const oscar_ctx_t* ctx);
 
@@ -325,7 +444,11 @@ typedef enum {
     OSCAR_KERNEL_QROT = 1,    /* query rotation q @ R_k */
     OSCAR_KERNEL_SPLIT = 2,   /* split-K partials over INT2 history and BF16 segment */
     OSCAR_KERNEL_MERGE = 3,   /* online-softmax merge + un-rotation */
-    OSCAR_KERNEL_COUNT = 4
+    OSCAR_KERNEL_PLAN = 4,    /* oscar_plan_append */
+    OSCAR_KERNEL_APPEND = 5,  /* oscar_append_bf16 */
+    OSCAR_KERNEL_SELECT = 6,  /* page scores and selection of the sparse decode */
+    OSCAR_KERNEL_ATTEND = 7,  /* attention over BF16 pages and the join of its splits */
+    OSCAR_KERNEL_COUNT = 8
 } oscar_kernel_id;
 
 /* Measurement hook (no counterpart on the pages): while enabled, every launch
