@@ -193,13 +193,13 @@ oscar_status oscar_decode_bf16_sparse(oscar_ctx_t* ctx, const void* q, int64_t q
     s.tables = tables; s.stride = table_stride;
     s.seq_len = seq_len; s.max_len = max_len;
     s.chosen = chosen; s.n_chosen = n_chosen; s.cap = oscar::sparse_capacity(ctx->shape, top_pages);
-    s.scores = static_cast<float*>(workspace);
+    s.keys = static_cast<uint32_t*>(workspace);
     s.max_pages = max_pages; s.top = top_pages; s.sink = ctx->shape.sink; s.recent = ctx->shape.recent;
     s.h_kv = ctx->shape.h_kv; s.g = ctx->shape.h_q / ctx->shape.h_kv; s.batch = batch;
     s.debug = ctx->shape.debug; s.dbg = ctx->dbg;
     {
         oscar::ProfScope ps(&ctx->prof, OSCAR_KERNEL_SELECT, static_cast<cudaStream_t>(stream));
-        st = cuda_status(oscar::launch_select(s, ctx->shape.d, static_cast<cudaStream_t>(stream)), "page selection launch");
+        st = cuda_status(oscar::launch_select(s, ctx->shape.d, ctx->num_sms, static_cast<cudaStream_t>(stream)), "page selection launch");
         if (st != OSCAR_OK) return st;
     }
     oscar::AttendArgs a = attend_args(ctx, plan, q, q_stride, bf16_pool, bf16_pool_pages, tables, table_stride,

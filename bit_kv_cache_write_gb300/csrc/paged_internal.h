@@ -67,13 +67,13 @@ struct SelectArgs {
     const int32_t* tables; int stride;
     const int32_t* seq_len; int max_len;
     int32_t* chosen; int32_t* n_chosen; int cap;
-    float* scores;                           // [batch][H_kv][max_pages]
+    uint32_t* keys;                          // [batch][H_kv][max_pages], for sequences too long for shared memory
     int max_pages, top, sink, recent;
     int h_kv, g, batch;
     int debug; DebugWord* dbg;
 };
 size_t select_workspace_bytes(const Shape& s, int batch, int max_pages);
-cudaError_t launch_select(const SelectArgs& a, int d, cudaStream_t st);
+cudaError_t launch_select(const SelectArgs& a, int d, int num_sms, cudaStream_t st);
 
 // Entries of one (sequence, KV head)'s list of chosen pages: the sink's pages, the pages that a recent
 // window can touch (one more than it fills), the selected ones.

@@ -423,6 +423,15 @@ def test_sparse_matches_the_oracle(cuda, lens, top, h_kv, g, d):
         close(got, want, c.tolerance(want, out_type, d ** -0.5))
 
 
+def test_sparse_beyond_the_keys_that_shared_memory_holds(cuda):
+    c = Cache(15, [265001, 40000], 2, 1, 64)
+    ctx = context(2, 1, 64)
+    want, lists = paged.decode_sparse(c.q, c.pool, c.bounds, c.steps, c.tables, c.lens, 70, 64, 256, 0.125)
+    got, chosen = run_sparse(ctx, c, cuda, torch.float32, 70)
+    assert chosen == lists
+    close(got, want, c.tolerance(want, None, 0.125))
+
+
 @pytest.mark.parametrize("sink,recent", [(0, 0), (0, 1), (5, 0), (16, 17), (64, 448)])
 def test_sparse_windows(cuda, sink, recent):
     c = Cache(12, [1000, 1008, 3], 4, 2, 64)
