@@ -5,8 +5,10 @@
 // are taken over the bf16 keys of a run (adjacent tokens of one page), with packed bf16 instructions, and
 // only the two results are turned into codes.
 //
-// A unit of 2 d / 8 lanes takes the runs that begin in its tokens, one KV head each: half of its lanes move
-// K, the other half V, 16 bytes a lane. A run has one owner, so bounds need no atomics.
+// A warp takes a few adjacent tokens of one KV head (two at d = 64): half of a head's lanes move K, the other
+// half V, 16 bytes a lane, eight rows at once. With bounds it takes the runs that begin in its tokens, to
+// their end, so that a run has one owner and needs no atomics. The kernel does not let its successor start
+// early: a decode prefetches pages.
 #include "paged_device.cuh"
 
 namespace oscar {
@@ -41,72 +43,101 @@ __device__ __forceinline__ float inv_pow2(int step) {
 }
 
 template <int D, bool BOUNDS>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, int tokens_per_unit) {
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, int tokens) {
     constexpr int kHalf = D / 8;                     // lanes that move one row of K (or V)
-    constexpr int kUnit = 2 * kHalf;
+    constexpr int kHeads = 32 / (2 * kHalf);         // KV heads of a warp
+    constexpr int kRows = 8;                         // rows in flight per lane
     grid_wait();
-    const long long unit = ((long long)blockIdx.x * kAppendThreads + threadIdx.x) / kUnit;
-    const int lane = threadIdx.x % kUnit, part = lane / kHalf, c0 = lane % kHalf * 8;
-    const int h = (int)(unit % a.h_kv);
-    const long long i0 = unit / a.h_kv * tokens_per_unit;
+    const int lane = threadIdx.x & 31;
+    const int groups = (a.h_kv + kHeads - 1) / kHeads;
+    const long long unit = ((long long)blockIdx.x * kAppendThreads + threadIdx.x) / 32;
+    const int h = (int)(unit % groups) * kHeads + lane / (2 * kHalf);
+    const int part = lane / kHalf % 2, c0 = lane % kHalf * 8;
+    const long long i0 = unit / groups * tokens;
     if (i0 >= a.n) return;
-    const long long i1 = min(i0 + tokens_per_unit, (long long)a.n);
-    const uint16_t* src = (part ? a.v : a.k) + (long long)h * D + c0;
-    const int64_t src_stride = part ? a.v_stride : a.k_stride;
-    const long long limit = a.pages * kPage;
-    // The slot's page, or -1 for a token that is skipped.
-    auto page_of = [&](long long i, long long& slot) -> long long {
-        slot = a.slots[i];
-        if (slot >= 0 && slot < limit) return slot / kPage;
-        if (slot >= limit && a.debug) record_error(&a.dbg->kind, &a.dbg->index, 1, slot);
-        return -1;
-    };
-    auto row_at = [&](long long page, long long slot) {
-        return a.pool + (((page * a.h_kv + h) * 2 + part) * kPage + slot % kPage) * D + c0;
-    };
-    long long i = i0, slot;
+
+    // Lane l holds the page and the row of token i0 - 1 + l, page -1 where there is none to write.
+    const long long i = i0 - 1 + lane;
+    const int64_t slot = i >= 0 && i < a.n ? a.slots[i] : -1;
+    const bool real = slot >= 0 && slot < a.pages * kPage;
+    if (slot >= a.pages * kPage && a.debug) record_error(&a.dbg->kind, &a.dbg->index, 1, slot);
+    const int page = real ? (int)(slot / kPage) : -1, row = (int)(slot % kPage);
+    const int before = __shfl_up_sync(~0u, page, 1);
+    const uint32_t live = __ballot_sync(~0u, real) & ~1u;                     // tokens that are written
+    uint32_t starts = __ballot_sync(~0u, real && page != before) & ~1u;       // that begin a run
+    const uint32_t own = (1u << (tokens + 1)) - 2;                            // that are this warp's
+    if (!BOUNDS) starts = live;                                               // each token for itself
+    const bool active = h < a.h_kv;
+    const uint16_t* src = (part ? a.v : a.k) + (i0 - 1) * (part ? a.v_stride : a.k_stride) + (int64_t)(active ? h : 0) * D + c0;
+    const int64_t stride = part ? a.v_stride : a.k_stride;
+    uint16_t* dst = a.pool + ((int64_t)(active ? h : 0) * 2 + part) * kPage * D + c0;
+
     if (!BOUNDS) {
-        for (; i < i1; ++i) {
-            const long long page = page_of(i, slot);
-            if (page >= 0)
-                *reinterpret_cast<uint4*>(row_at(page, slot)) = ldg_stream(src + i * src_stride);
+        for (uint32_t todo = starts & own; todo;) {
+            uint4 x[kRows];
+            uint16_t* to[kRows];
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                const int l = todo ? __ffs(todo) - 1 : 0;
+                to[k] = nullptr;
+                const int p = __shfl_sync(~0u, page, l), r = __shfl_sync(~0u, row, l);
+                if (todo && active) {
+                    to[k] = dst + (int64_t)p * a.h_kv * 2 * kPage * D + r * D;
+                    x[k] = ldg_stream(src + l * stride);
+                }
+                todo &= todo - 1;
+            }
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+                if (to[k]) *reinterpret_cast<uint4*>(to[k]) = x[k];
         }
         return;
     }
-    if (i > 0) {                                     // the run that reaches into these tokens has its owner
-        const long long before = page_of(i - 1, slot);
-        while (i < i1 && before >= 0 && page_of(i, slot) == before) ++i;
-    }
-    while (i < i1) {
-        const long long page = page_of(i, slot);
-        if (page < 0) { ++i; continue; }
-        bool fresh = false;
+    for (uint32_t todo = starts & own; todo; todo &= todo - 1) {
+        const int first = __ffs(todo) - 1;
+        // the run's tokens: up to the next one that begins another run or is not written
+        const uint32_t stop = (starts | ~live) & ~((2u << first) - 1);
+        const int end = stop ? __ffs(stop) - 1 : 32;
+        const int p = __shfl_sync(~0u, page, first);
+        uint16_t* to = dst + (int64_t)p * a.h_kv * 2 * kPage * D;
+        const bool fresh = __any_sync(~0u, lane >= first && lane < end && row == 0);
         uint32_t lo[4], hi[4];
-        for (int first = 1; i < a.n; ++i, first = 0) {
-            if (!first && page_of(i, slot) != page) break;
-            fresh |= slot % kPage == 0;
-            const uint4 x = ldg_stream(src + i * src_stride);
-            *reinterpret_cast<uint4*>(row_at(page, slot)) = x;
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        for (int l0 = first; l0 < end; l0 += kRows) {
+            uint4 x[kRows];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t z = bf2_no_nan(w[j]);
-                lo[j] = first ? z : bf2_min(lo[j], z);
-                hi[j] = first ? z : bf2_max(hi[j], z);
+            for (int k = 0; k < kRows; ++k)
+                if (l0 + k < end && active) x[k] = ldg_stream(src + (l0 + k) * stride);
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                const int r = __shfl_sync(~0u, row, l0 + k);
+                if (l0 + k >= end || !active) continue;
+                *reinterpret_cast<uint4*>(to + r * D) = x[k];
+                const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t z = bf2_no_nan(w[j]);
+                    lo[j] = l0 + k == first ? z : bf2_min(lo[j], z);
+                    hi[j] = l0 + k == first ? z : bf2_max(hi[j], z);
+                }
             }
         }
-        if (part == 0) {
-            int8_t* b = a.bounds + ((page * a.h_kv + h) * 2) * D + c0;
-            const int8_t* steps = a.steps + h * D + c0;
+        if (part == 0 && active) {
+            int8_t* b = a.bounds + ((int64_t)p * a.h_kv + h) * 2 * D + c0;
+            const uint2 steps = *reinterpret_cast<const uint2*>(a.steps + h * D + c0);
+            const uint2 old_lo = fresh ? make_uint2(0, 0) : *reinterpret_cast<const uint2*>(b);
+            const uint2 old_hi = fresh ? make_uint2(0, 0) : *reinterpret_cast<const uint2*>(b + D);
             uint32_t word[2][2] = {};
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                const float inv = inv_pow2(steps[c]);
-                const int shift = 16 * (c & 1);
-                int l = code_of(lo[c / 2] >> shift & 0xffffu, inv), u = code_of(hi[c / 2] >> shift & 0xffffu, inv);
-                if (!fresh) { l = min(l, (int)b[c]); u = max(u, (int)b[D + c]); }
-                word[0][c / 4] |= (uint32_t)(l & 0xff) << (8 * (c & 3));
-                word[1][c / 4] |= (uint32_t)(u & 0xff) << (8 * (c & 3));
+                const int at = 8 * (c & 3), half = 16 * (c & 1);
+                const float inv = inv_pow2((int8_t)((c < 4 ? steps.x : steps.y) >> at));
+                int l = code_of(lo[c / 2] >> half & 0xffffu, inv), u = code_of(hi[c / 2] >> half & 0xffffu, inv);
+                if (!fresh) {
+                    l = min(l, (int)(int8_t)((c < 4 ? old_lo.x : old_lo.y) >> at));
+                    u = max(u, (int)(int8_t)((c < 4 ? old_hi.x : old_hi.y) >> at));
+                }
+                word[0][c / 4] |= (uint32_t)(l & 0xff) << at;
+                word[1][c / 4] |= (uint32_t)(u & 0xff) << at;
             }
             *reinterpret_cast<uint2*>(b) = make_uint2(word[0][0], word[0][1]);
             *reinterpret_cast<uint2*>(b + D) = make_uint2(word[1][0], word[1][1]);
@@ -116,9 +147,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, in
 
 template <int D>
 cudaError_t launch(const AppendArgs& a, int num_sms, cudaStream_t st) {
-    const int tokens = 1;
-    const long long units = ((long long)a.n + tokens - 1) / tokens * a.h_kv;
-    const long long ctas = (units * (2 * D / 8) + kAppendThreads - 1) / kAppendThreads;
+    constexpr int kHeads = 32 / (D / 4);
+    const int groups = (a.h_kv + kHeads - 1) / kHeads;
+    // one token a warp while those warps fit on the card about once, 16 (a page) beyond
+    const int tokens = (long long)a.n * groups <= 64LL * num_sms ? 1 : kPage;
+    const long long warps = ((long long)a.n + tokens - 1) / tokens * groups;
+    const long long ctas = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)ctas), block(kAppendThreads);
     return a.bounds ? launch_dependent(append_kernel<D, true>, grid, block, 0, st, 1, a, tokens)

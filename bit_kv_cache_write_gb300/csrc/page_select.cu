@@ -293,19 +293,9 @@ cudaError_t launch(const SelectArgs& a, int num_sms, cudaStream_t st) {
         cluster *= 2;
     if (cluster * units > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int smem_keys = a.max_pages < kSmemKeys ? a.max_pages : kSmemKeys;
-    static std::atomic<unsigned long long> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = smem_opt_in<select_kernel<D>>(kSmemKeys * sizeof(uint32_t));
+    if (e == cudaSuccess) e = allow_large_clusters<select_kernel<D>>();
     if (e != cudaSuccess) return e;
-    const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
-    if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kSmemKeys * (int)sizeof(uint32_t));
-        if (e != cudaSuccess) return e;
-        done.fetch_or(bit, std::memory_order_acq_rel);
-    }
     return launch_dependent(select_kernel<D>, dim3((unsigned)(units * cluster)), dim3(kSelectThreads),
                             smem_keys * sizeof(uint32_t), st, cluster, a, smem_keys);
 }

@@ -40,9 +40,9 @@ oscar_status check_decode(const oscar_ctx_t* ctx, const void* q, int64_t q_strid
         return record_failure(OSCAR_ERR_INVALID_ARG, "BF16 pool/tables missing");
     if (max_len > 0 && (long long)max_len > (long long)stride * oscar::kPage)
         return record_failure(OSCAR_ERR_INVALID_ARG, "max_len %d exceeds table stride %d pages", max_len, stride);
-    if (q_stride < 0 || q_stride % 8 || !aligned(q, 16) || !aligned(pool, 16))
+    if (q_stride < 0 || q_stride % 8 || !aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16))
         return record_failure(OSCAR_ERR_INVALID_ARG,
-                              "q and the pool must be 16-byte aligned, q_stride a multiple of 8 (is %lld)",
+                              "q, the pool and out must be 16-byte aligned, q_stride a multiple of 8 (is %lld)",
                               (long long)q_stride);
     return OSCAR_OK;
 }
@@ -67,7 +67,8 @@ oscar::AttendArgs attend_args(oscar_ctx_t* ctx, const oscar::AttendPlan& plan, c
     a.tables = tables; a.stride = stride;
     a.seq_len = seq_len; a.max_len = max_len;
     a.out = out; a.out_bf16 = out_type == OSCAR_OUT_BF16;
-    a.partials = static_cast<float*>(workspace);
+    a.split_acc = static_cast<float*>(workspace);
+    a.split_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.ws_acc);
     a.h_kv = ctx->shape.h_kv; a.g = ctx->shape.h_q / ctx->shape.h_kv;
     a.splits = plan.splits; a.pages_per_split = plan.pages_per_split; a.batch = batch;
     a.scale_log2 = (float)(ctx->shape.sm_scale * 1.4426950408889634073599);
@@ -132,7 +133,7 @@ oscar_status oscar_append_bf16(oscar_ctx_t* ctx, const void* k, int64_t k_stride
 
 size_t oscar_decode_bf16_workspace_size(const oscar_ctx_t* ctx, int batch, int max_len) {
     if (!sizes_ok(ctx, batch, max_len)) return 0;
-    return oscar::plan_attend(ctx->shape, ctx->num_sms, batch, pages_of(max_len)).ws_partials;
+    return oscar::plan_attend(ctx->shape, ctx->num_sms, batch, pages_of(max_len)).ws_total;
 }
 
 oscar_status oscar_decode_bf16(oscar_ctx_t* ctx, const void* q, int64_t q_stride, const void* bf16_pool,
@@ -144,7 +145,7 @@ oscar_status oscar_decode_bf16(oscar_ctx_t* ctx, const void* q, int64_t q_stride
                                    out, out_type, batch);
     if (st != OSCAR_OK || batch == 0) return st;
     const oscar::AttendPlan plan = oscar::plan_attend(ctx->shape, ctx->num_sms, batch, pages_of(max_len));
-    st = check_workspace(workspace, workspace_bytes, plan.ws_partials);
+    st = check_workspace(workspace, workspace_bytes, plan.ws_total);
     if (st != OSCAR_OK) return st;
     const oscar::AttendArgs a = attend_args(ctx, plan, q, q_stride, bf16_pool, bf16_pool_pages, tables, table_stride,
                                             seq_len, max_len, out, out_type, workspace, batch);
@@ -159,7 +160,7 @@ int oscar_sparse_capacity(const oscar_ctx_t* ctx, int top_pages) {
 
 size_t oscar_decode_bf16_sparse_workspace_size(const oscar_ctx_t* ctx, int batch, int max_len, int top_pages) {
     if (!sizes_ok(ctx, batch, max_len) || top_pages < 0 || top_pages > oscar::kMaxTopPages) return 0;
-    return oscar::plan_attend(ctx->shape, ctx->num_sms, batch, sparse_pages(ctx, max_len, top_pages)).ws_partials +
+    return oscar::plan_attend(ctx->shape, ctx->num_sms, batch, sparse_pages(ctx, max_len, top_pages)).ws_total +
            oscar::select_workspace_bytes(ctx->shape, batch, pages_of(max_len));
 }
 
@@ -184,7 +185,7 @@ oscar_status oscar_decode_bf16_sparse(oscar_ctx_t* ctx, const void* q, int64_t q
     const oscar::AttendPlan plan =
         oscar::plan_attend(ctx->shape, ctx->num_sms, batch, sparse_pages(ctx, max_len, top_pages));
     const size_t scores = oscar::select_workspace_bytes(ctx->shape, batch, max_pages);
-    st = check_workspace(workspace, workspace_bytes, scores + plan.ws_partials);
+    st = check_workspace(workspace, workspace_bytes, scores + plan.ws_total);
     if (st != OSCAR_OK) return st;
 
     oscar::SelectArgs s{};

@@ -19,6 +19,7 @@ namespace oscar {
 namespace {
 
 constexpr int kAttendWarps = 4;
+constexpr int kJoinThreads = 256;
 constexpr float kNoLogit = -1e30f;       // running reference before any token
 constexpr float kHeadroom = 8.0f;        // the reference is raised when a logit passes it by this much (log2)
 
@@ -191,37 +192,75 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 3) attend_kernel(AttendArgs
             if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[row * D + c] = __float2bfloat16(r);
             else static_cast<float*>(a.out)[row * D + c] = r;
         } else {
-            float* part = a.partials + (row * a.splits + split) * (D + 2);
-            part[2 + c] = o;
-            if (c == 0) { part[0] = mm; part[1] = ll; }
+            a.split_acc[(row * a.splits + split) * D + c] = o;
+            if (c == 0) a.split_ml[row * a.splits + split] = make_float2(mm, ll);
         }
     }
 }
 
-// Joins the splits of one query head: thread c owns channel c.
-template <int D, bool SPARSE>
-__global__ void __launch_bounds__(D) join_kernel(AttendArgs a) {
-    const int c = threadIdx.x;
-    const int64_t row = blockIdx.x;
-    const int hq = a.h_kv * a.g, b = (int)(row / hq), unit = b * a.h_kv + (int)(row % hq) / a.g;
+// Joins the splits of query heads, W warps to a head: a warp takes every W-th split, 16 bytes a lane.
+template <int D, bool SPARSE, int W>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
+    constexpr int kLanes = D / 4;                        // lanes that hold one split's channels
+    constexpr int kPer = 32 / kLanes;                    // splits that a warp reads at a time
+    constexpr int kRows = kJoinThreads / 32 / W;
+    __shared__ float4 warp_o[kJoinThreads / 32][kLanes];
+    __shared__ float warp_l[kJoinThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
+    const int64_t row = (int64_t)blockIdx.x * kRows + warp / W;
+    const int hq = a.h_kv * a.g;
     grid_wait();
     grid_release();
-    const int len = checked_len(a.seq_len[b], a.max_len, 0, a.dbg);
-    const int listed = SPARSE ? a.n_chosen[unit] : (len + kPage - 1) / kPage;
-    const int n = (listed + a.pages_per_split - 1) / a.pages_per_split;
-    const float* part = a.partials + row * a.splits * (D + 2);
-    float m = kNoLogit;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, part[(int64_t)i * (D + 2)]);
-    float l = 0.0f, o = 0.0f;
-    for (int i = 0; i < n; ++i) {
-        const float* p = part + (int64_t)i * (D + 2);
-        const float f = exp2f(p[0] - m);
-        l += f * p[1];
-        o += f * p[2 + c];
+    const bool inside = row < (int64_t)a.batch * hq;
+    float4 o = make_float4(0, 0, 0, 0);
+    float l = 0.0f;
+    if (inside) {
+        const int b = (int)(row / hq), unit = b * a.h_kv + (int)(row % hq) / a.g;
+        const int listed = SPARSE ? a.n_chosen[unit] : (checked_len(a.seq_len[b], a.max_len, 0, a.dbg) + kPage - 1) / kPage;
+        const int n = (listed + a.pages_per_split - 1) / a.pages_per_split;
+        const float2* ml = a.split_ml + row * a.splits;
+        const float4* acc = reinterpret_cast<const float4*>(a.split_acc + row * a.splits * D) + lane % kLanes;
+        float m = kNoLogit;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, ml[i].x);
+#pragma unroll
+        for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, s));
+#pragma unroll 4
+        for (int i = part * kPer + lane / kLanes; i < n; i += W * kPer) {
+            const float2 x = ml[i];
+            const float4 y = acc[(int64_t)i * kLanes];
+            const float f = exp2f(x.x - m);
+            l += f * x.y;
+            o.x += f * y.x; o.y += f * y.y; o.z += f * y.z; o.w += f * y.w;
+        }
+        if (kPer == 2) {
+            l += __shfl_xor_sync(~0u, l, 16);
+            o.x += __shfl_xor_sync(~0u, o.x, 16); o.y += __shfl_xor_sync(~0u, o.y, 16);
+            o.z += __shfl_xor_sync(~0u, o.z, 16); o.w += __shfl_xor_sync(~0u, o.w, 16);
+        }
     }
-    const float r = l == 0.0f ? 0.0f : o / l;
-    if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[row * D + c] = __float2bfloat16(r);
-    else static_cast<float*>(a.out)[row * D + c] = r;
+    if (W > 1) {
+        if (lane < kLanes) warp_o[warp][lane] = o;
+        if (lane == 0) warp_l[warp] = l;
+        __syncthreads();
+        if (part != 0) return;
+        o = make_float4(0, 0, 0, 0);
+        l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float4 y = warp_o[warp + w][lane % kLanes];
+            l += warp_l[warp + w];
+            o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
+        }
+    }
+    if (!inside || lane >= kLanes) return;
+    // no token: zeros
+    const float4 r = l == 0.0f ? make_float4(0, 0, 0, 0) : make_float4(o.x / l, o.y / l, o.z / l, o.w / l);
+    if (a.out_bf16) {
+        uint2 x = make_uint2(pack_bf16(r.x, r.y), pack_bf16(r.z, r.w));
+        reinterpret_cast<uint2*>(a.out)[row * kLanes + lane] = x;
+    } else {
+        reinterpret_cast<float4*>(a.out)[row * kLanes + lane] = r;
+    }
 }
 
 template <int D, bool SPARSE>
@@ -230,7 +269,13 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
     if (ctas > 0x7fffffffLL || (long long)a.batch * a.h_kv * a.g > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaError_t e = launch_dependent(attend_kernel<D, SPARSE>, dim3((unsigned)ctas), dim3(kAttendWarps * 32), 0, st, 1, a);
     if (e != cudaSuccess || a.splits == 1) return e;
-    return launch_dependent(join_kernel<D, SPARSE>, dim3(a.batch * a.h_kv * a.g), dim3(D), 0, st, 1, a);
+    // a CTA per head where there are many splits, a warp per head otherwise
+    const long long rows = (long long)a.batch * a.h_kv * a.g;
+    constexpr int kJoinWarps = kJoinThreads / 32;
+    if (a.splits > kJoinWarps)
+        return launch_dependent(join_kernel<D, SPARSE, kJoinWarps>, dim3((unsigned)rows), dim3(kJoinThreads), 0, st, 1, a);
+    return launch_dependent(join_kernel<D, SPARSE, 1>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)),
+                            dim3(kJoinThreads), 0, st, 1, a);
 }
 
 }  // namespace
@@ -247,7 +292,9 @@ AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages) {
     if (splits < 1) splits = 1;
     p.pages_per_split = max_pages > 0 ? (int)((max_pages + splits - 1) / splits) : 1;
     p.splits = max_pages > 0 ? (max_pages + p.pages_per_split - 1) / p.pages_per_split : 1;
-    p.ws_partials = p.splits == 1 ? 0 : ((size_t)batch * s.h_q * p.splits * (s.d + 2) * sizeof(float) + 255) / 256 * 256;
+    const size_t parts = p.splits == 1 ? 0 : (size_t)batch * s.h_q * p.splits;
+    p.ws_acc = (parts * s.d * sizeof(float) + 255) / 256 * 256;
+    p.ws_total = p.ws_acc + (parts * sizeof(float2) + 255) / 256 * 256;
     return p;
 }
 

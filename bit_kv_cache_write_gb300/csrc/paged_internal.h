@@ -41,7 +41,8 @@ cudaError_t launch_append(const AppendArgs& a, int d, int num_sms, cudaStream_t 
 struct AttendPlan {
     int pages_per_split;
     int splits;
-    size_t ws_partials;
+    size_t ws_acc;               // bytes of the splits' accumulators
+    size_t ws_total;             // and of their references and sums
 };
 struct AttendArgs {
     const uint16_t* q; int64_t q_stride;     // sequence stride in elements
@@ -50,7 +51,8 @@ struct AttendArgs {
     const int32_t* seq_len; int max_len;
     const int32_t* chosen; const int32_t* n_chosen; int cap;   // sparse: logical pages per (sequence, KV head)
     void* out; int out_bf16;
-    float* partials;                         // [batch][H_q][splits][d + 2]
+    float* split_acc;                        // [batch][H_q][splits][d]
+    float2* split_ml;                        // [batch][H_q][splits] reference and sum of weights
     int h_kv, g, splits, pages_per_split, batch;
     float scale_log2;                        // sm_scale * log2(e)
     int debug; DebugWord* dbg;

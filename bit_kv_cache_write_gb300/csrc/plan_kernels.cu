@@ -5,16 +5,24 @@
 // pages of the requests before it (an inclusive sum P_b decides whether they are there). Row r_b + i goes to
 // slot page * 16 + (s_b + i) % 16 of logical page (s_b + i) / 16.
 //
-// One cluster. Every CTA scans all requests (two 64-bit sums), 1,024 at a time, and writes its share of the
-// chunk's table entries and slots; a page id is read from the free list, so no CTA reads what another one
-// writes. The free head may be the word that the new head goes to, so the last barrier stands between every
-// CTA's read of it and the write.
+// One cluster. Every CTA scans all requests, kPlanThreads at a time (one pass of two sums; two more only
+// where a request does not fit), and writes its share of the chunk's table entries and slots; a page id is
+// read from the free list, so no CTA reads what another one writes. The free head may be the word that the
+// new head goes to, so the last barrier stands between every CTA's read of it and the write.
+//
+// Nothing here is large: the time is a chain of dependent loads (lengths, sums, page ids). The kernel does not
+// let its successor start early: page ids and slots may be read ahead by the one after that.
+#include <climits>
+
 #include "paged_device.cuh"
 
 namespace oscar {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanMaxCluster = 16;
+constexpr int kPlanTokens = 4;                       // slots that a thread looks up at once
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -27,26 +35,26 @@ __device__ __forceinline__ uint32_t cluster_size() {
     return r;
 }
 
-// Inclusive sums of two values over the CTA; returns the totals too.
-__device__ void scan2(long long& a, long long& b, long long& total_a, long long& total_b, long long (*warp_sum)[2]) {
+// Inclusive sums of two values over the CTA, and their totals. Consecutive calls alternate `sums`.
+__device__ void scan2(long long& a, long long& b, long long& total_a, long long& total_b, long long (*sums)[2]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(~0u, a, o), y = __shfl_up_sync(~0u, b, o);
         if (lane >= o) { a += x; b += y; }
     }
-    __syncthreads();                             // the sums of the last chunk have been read
-    if (lane == 31) { warp_sum[warp][0] = a; warp_sum[warp][1] = b; }
+    if (lane == 31) { sums[warp][0] = a; sums[warp][1] = b; }
     __syncthreads();
-    long long before_a = 0, before_b = 0;
-    total_a = total_b = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w == warp) { before_a = total_a; before_b = total_b; }
-        total_a += warp_sum[w][0];
-        total_b += warp_sum[w][1];
+    long long wa = lane < kPlanWarps ? sums[lane][0] : 0, wb = lane < kPlanWarps ? sums[lane][1] : 0;
+#pragma unroll
+    for (int o = 1; o < kPlanWarps; o <<= 1) {
+        const long long x = __shfl_up_sync(~0u, wa, o), y = __shfl_up_sync(~0u, wb, o);
+        if (lane >= o) { wa += x; wb += y; }
     }
-    a += before_a;
-    b += before_b;
+    total_a = __shfl_sync(~0u, wa, kPlanWarps - 1);
+    total_b = __shfl_sync(~0u, wb, kPlanWarps - 1);
+    const long long before_a = __shfl_sync(~0u, wa, warp ? warp - 1 : 0), before_b = __shfl_sync(~0u, wb, warp ? warp - 1 : 0);
+    if (warp) { a += before_a; b += before_b; }
 }
 
 // First i in [0, n) with key < v[i], for ascending v; n if none.
@@ -61,7 +69,7 @@ __device__ __forceinline__ int upper(const long long* v, int n, long long key) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
-    __shared__ long long warp_sum[kPlanThreads / 32][2];
+    __shared__ long long sums[2][kPlanWarps][2];
     __shared__ long long row_end[kPlanThreads];      // rows up to and with request i of the chunk
     __shared__ long long page_end[kPlanThreads];     // its pages likewise
     __shared__ int cached[kPlanThreads];             // tokens cached; -1: request rejected
@@ -73,27 +81,28 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     grid_wait();
     const long long head = *reinterpret_cast<const volatile int32_t*>(a.free_head);
     const long long avail = head >= 0 && head < a.n_free ? a.n_free - head : 0;
-    long long rows = 0, pages = 0, taken = 0;        // sums over the chunks so far; pages that were handed out
+    long long rows = 0, wanted = 0, taken = 0;       // over the chunks so far: rows, pages needed, handed out
     for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
         const int b = b0 + tid, count = min(kPlanThreads, a.batch - b0);
         const int s = b < a.batch ? a.seq_len[b] : 0, n = b < a.batch ? a.new_len[b] : 0;
-        long long r = n > 0 ? n : 0, p = 0, total_r, total_p;
         bool ok = s >= 0 && n >= 0 && (long long)s + n <= (long long)kPage * a.stride;
-        const int old = ok ? (s + kPage - 1) / kPage : 0;
-        const int need = ok ? (int)(((long long)s + n + kPage - 1) / kPage) - old : 0;
-        // A request whose rows pass the slot map takes no pages, but that is known only after the sum of rows.
-        long long unused = 0, total_unused;
-        scan2(r, unused, total_r, total_unused, warp_sum);
-        ok = ok && rows + r <= a.slot_cap;
-        p = ok ? need : 0;
-        long long mine = p;
-        unused = 0;
-        scan2(p, unused, total_p, total_unused, warp_sum);
-        ok = ok && (mine == 0 || pages + p <= avail);
-        const long long got = ok ? mine : 0;
-        long long g = got, total_g;
-        unused = 0;
-        scan2(g, unused, total_g, total_unused, warp_sum);
+        const long long need = ok ? ((long long)s + n + kPage - 1) / kPage - (s + kPage - 1) / kPage : 0;
+        const long long own_rows = n > 0 ? n : 0;
+        long long r = own_rows, p = need, total_r, total_p;
+        scan2(r, p, total_r, total_p, sums[0]);
+        long long g = p, total_g = total_p;
+        if (rows + total_r > a.slot_cap || wanted + total_p > avail) {
+            // Some request passes the slot map or the free list. One that passes the map needs no page.
+            long long unused = 0, t;
+            ok = ok && rows + r <= a.slot_cap;
+            const long long still = ok ? need : 0;
+            p = still;
+            scan2(p, unused, total_p, t, sums[1]);
+            ok = ok && (still == 0 || wanted + p <= avail);
+            g = ok ? still : 0;
+            unused = 0;
+            scan2(g, unused, total_g, t, sums[0]);
+        }
         row_end[tid] = rows + r;
         page_end[tid] = taken + g;
         cached[tid] = ok ? s : -1;
@@ -101,7 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
             if (!ok) { atomicAdd(&rejected, 1); atomicMin(&first_rejected, b); }
             if (b % ranks == rank) {
                 a.total_len[b] = ok ? s + n : s;
-                a.row_start[b] = (int32_t)min(rows + r - (n > 0 ? n : 0), (long long)INT_MAX);
+                a.row_start[b] = (int32_t)min(rows + r - own_rows, (long long)INT_MAX);
             }
         }
         __syncthreads();
@@ -112,22 +121,32 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
             a.tables[(long long)(b0 + i) * a.stride + (cached[i] + kPage - 1) / kPage + (j - before)] =
                 a.free_pages[head + j];
         }
-        // slots
+        // slots, several at once: each waits for a page id
         const long long end = min(rows + total_r, (long long)a.slot_cap);
-        for (long long t = rows + share; t < end; t += shares) {
-            const int i = upper(row_end, count, t);
-            int64_t slot = -1;
-            if (cached[i] >= 0) {
+        for (long long t0 = rows + share; t0 < end; t0 += (long long)kPlanTokens * shares) {
+            int id[kPlanTokens], in_page[kPlanTokens];
+#pragma unroll
+            for (int k = 0; k < kPlanTokens; ++k) {
+                const long long t = t0 + (long long)k * shares;
+                in_page[k] = -1;
+                id[k] = 0;
+                if (t >= end) continue;
+                const int i = upper(row_end, count, t);
+                if (cached[i] < 0) continue;
                 const int pos = cached[i] + (int)(t - (i ? row_end[i - 1] : rows));
                 const int page = pos / kPage, first_new = (cached[i] + kPage - 1) / kPage;
-                const int id = page < first_new ? a.tables[(long long)(b0 + i) * a.stride + page]
-                                                : a.free_pages[head + (i ? page_end[i - 1] : taken) + page - first_new];
-                slot = (int64_t)id * kPage + pos % kPage;
+                in_page[k] = pos % kPage;
+                id[k] = page < first_new ? a.tables[(long long)(b0 + i) * a.stride + page]
+                                         : a.free_pages[head + (i ? page_end[i - 1] : taken) + page - first_new];
             }
-            a.slots[t] = slot;
+#pragma unroll
+            for (int k = 0; k < kPlanTokens; ++k) {
+                const long long t = t0 + (long long)k * shares;
+                if (t < end) a.slots[t] = in_page[k] < 0 ? -1 : (int64_t)id[k] * kPage + in_page[k];
+            }
         }
         rows += total_r;
-        pages += total_p;
+        wanted += total_p;
         taken += total_g;
         __syncthreads();                             // the chunk's arrays have been read
     }
@@ -145,7 +164,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
 }  // namespace
 
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st) {
-    return launch_dependent(plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a);
+    // as many CTAs as have kPlanTokens slots a thread to write
+    int cluster = 1;
+    while (cluster < kPlanMaxCluster && (long long)cluster * kPlanThreads * kPlanTokens < a.slot_cap) cluster *= 2;
+    if (cluster > 8) {
+        const cudaError_t e = allow_large_clusters<plan_kernel>();
+        if (e != cudaSuccess) return e;
+    }
+    return launch_dependent(plan_kernel, dim3(cluster), dim3(kPlanThreads), 0, st, cluster, a);
 }
 
 }  // namespace oscar

@@ -135,7 +135,8 @@ def oscar_create(n_layers, n_q_heads, n_kv_heads, head_dim, group, page_size=16,
                          float(sm_scale), int(debug_bounds), int(codebook))
     ctx = _vp()
     _check(lib().oscar_create(ctypes.byref(cfg), ctypes.byref(ctx)), "oscar_create")
-    _configs[ctx.value] = (n_q_heads, n_kv_heads, head_dim)
+    import torch
+    _configs[ctx.value] = (n_q_heads, n_kv_heads, head_dim, torch.cuda.current_device())
     return ctx.value
 
 
@@ -270,46 +271,92 @@ def oscar_decode_static_workspace(ctx, layer, q, int2_pool, int2_tables, hist_le
         _dptr(out, torch.float32, "out"), batch, _stream(stream)), "oscar_decode_static_workspace")
 
 
-_configs = {}     # context handle -> (H_q, H_kv, d) of the contexts created here, for the shape checks below
+_configs = {}     # context handle -> (H_q, H_kv, d, device) of the contexts created here, for the checks below
 
 
-def _shape_of(ctx):
+def _config_of(ctx):
     try:
         return _configs[ctx]
     except KeyError:
         raise ValueError("the context was not created by oscar_create") from None
 
 
-def _out_type(out):
-    import torch
-    if out.dtype == torch.float32:
-        return OSCAR_OUT_FP32
-    if out.dtype == torch.bfloat16:
-        return OSCAR_OUT_BF16
-    raise ValueError("out must be torch.float32 or torch.bfloat16, got %s" % out.dtype)
+def _stream_on(stream, device):
+    """Raw handle of the stream, by default of the device's current one."""
+    if stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # a 30th of current_stream()'s cost
+        return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _rows(t, heads, d, name):
-    """(pointer, row stride in elements) of bf16 rows [n][heads][d] whose heads lie together."""
+def _refuse(t, dtype, n, device, name):
+    """Says why _ptr does not take a tensor."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dtype != torch.bfloat16:
-        raise ValueError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+    if t.get_device() != device:
+        raise ValueError("%s is on device %d, the context on %d" % (name, t.get_device(), device))
+    if t.dtype is not dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    raise ValueError("%s must hold %d elements, holds %d" % (name, n, t.numel()))
+
+
+def _ptr(t, dtype, n, device, name):
+    """Pointer of a contiguous tensor of n elements on the context's device."""
+    try:
+        if t.dtype is dtype and t.get_device() == device and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, n, device, name)
+
+
+def _rows(t, bf16, heads, d, device, name):
+    """(pointer, row stride in elements) of bf16 rows [n][heads][d] whose heads lie together."""
+    try:
+        n, h, c = t.shape
+        row, head, one = t.stride()
+        if h == heads and c == d and t.dtype is bf16 and t.get_device() == device and (
+                n == 0 or (one == 1 and (head == d or heads == 1))):
+            return t.data_ptr(), row if n > 1 else heads * d
+    except (AttributeError, ValueError):
+        pass
+    if getattr(t, "dim", lambda: 0)() == 3 and tuple(t.shape[1:]) == (heads, d) and t.dtype is bf16 and \
+            t.get_device() == device:
+        raise ValueError("%s: a row's heads must be contiguous (strides %s)" % (name, t.stride()))
+    if getattr(t, "is_cuda", False) and t.dtype is bf16 and t.get_device() == device:
         raise ValueError("%s must be [n][%d][%d], got %s" % (name, heads, d, tuple(t.shape)))
-    s = t.stride()
-    if t.numel() and (s[2] != 1 or (heads > 1 and s[1] != d)):
-        raise ValueError("%s: a row's heads must be contiguous (strides %s)" % (name, s))
-    return t.data_ptr(), s[0] if t.shape[0] > 1 else heads * d
+    _refuse(t, bf16, 0, device, name)
 
 
-def _sized(t, dtype, n, name):
-    """Pointer of a contiguous tensor of n elements."""
-    p = _dptr(t, dtype, name)
-    if p is None or t.numel() != n:
-        raise ValueError("%s must hold %d elements, holds %s" % (name, n, None if t is None else t.numel()))
-    return p
+def _table(t, batch, dtype, device, name="tables"):
+    """(pointer, row length) of contiguous block tables [batch][stride]."""
+    if t.dim() != 2 or t.shape[0] != batch:
+        raise ValueError("%s must be [%d][stride], got %s" % (name, batch, tuple(t.shape)))
+    return _ptr(t, dtype, t.numel(), device, name), t.shape[1]
+
+
+def _output(out, q, device, torch):
+    """(pointer, oscar_out_type) of an output of q's shape."""
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape %s, has %s" % (tuple(q.shape), tuple(out.shape)))
+    dtype = out.dtype
+    if dtype is torch.float32:
+        return _ptr(out, dtype, out.numel(), device, "out"), OSCAR_OUT_FP32
+    if dtype is torch.bfloat16:
+        return _ptr(out, dtype, out.numel(), device, "out"), OSCAR_OUT_BF16
+    raise ValueError("out must be torch.float32 or torch.bfloat16, got %s" % dtype)
+
+
+def _scratch(workspace, device):
+    """(pointer, bytes) of a workspace tensor or None."""
+    if workspace is None:
+        return None, 0
+    n = workspace.numel()
+    return _ptr(workspace, workspace.dtype, n, device, "workspace"), n * workspace.element_size()
 
 
 def oscar_plan_append(ctx, seq_len, new_len, free_pages, free_head, tables, slots, row_start, total_len, state,
@@ -317,63 +364,60 @@ def oscar_plan_append(ctx, seq_len, new_len, free_pages, free_head, tables, slot
     """seq_len, new_len int32 [B]; free_pages int32; free_head int32 [1]; tables int32 [B][stride] (in and out);
     out: slots int64, row_start int32 [B + 1], total_len int32 [B], state int32 [4]."""
     import torch
-    i32, batch = torch.int32, seq_len.numel()
-    if tables.dim() != 2 or tables.shape[0] != batch:
-        raise ValueError("tables must be [%d][stride], got %s" % (batch, tuple(tables.shape)))
-    _check(lib().oscar_plan_append(
-        ctx, _dptr(seq_len, i32, "seq_len"), _sized(new_len, i32, batch, "new_len"), batch,
-        _dptr(free_pages, i32, "free_pages"), free_pages.numel(), _sized(free_head, i32, 1, "free_head"),
-        _dptr(tables, i32, "tables"), tables.shape[1], _dptr(slots, torch.int64, "slots"), slots.numel(),
-        _sized(row_start, i32, batch + 1, "row_start"), _sized(total_len, i32, batch, "total_len"),
-        _sized(state, i32, 4, "state"), _stream(stream)), "oscar_plan_append")
+    dev = _config_of(ctx)[3]
+    i32, batch, n_free, n_slots = torch.int32, seq_len.numel(), free_pages.numel(), slots.numel()
+    tp, ts = _table(tables, batch, i32, dev)
+    st = lib().oscar_plan_append(
+        ctx, _ptr(seq_len, i32, batch, dev, "seq_len"), _ptr(new_len, i32, batch, dev, "new_len"), batch,
+        _ptr(free_pages, i32, n_free, dev, "free_pages"), n_free, _ptr(free_head, i32, 1, dev, "free_head"), tp, ts,
+        _ptr(slots, torch.int64, n_slots, dev, "slots"), n_slots, _ptr(row_start, i32, batch + 1, dev, "row_start"),
+        _ptr(total_len, i32, batch, dev, "total_len"), _ptr(state, i32, 4, dev, "state"), _stream_on(stream, dev))
+    if st:
+        _check(st, "oscar_plan_append")
 
 
 def oscar_append_bf16(ctx, k, v, slots, bf16_pool, key_steps=None, key_bounds=None, stream=None):
     """k, v: bf16 [n][H_kv][d], rows at any stride; slots int64 [n]; bf16_pool: whole pages; key_steps int8
     [H_kv][d] and key_bounds int8 [pages][H_kv][2][d], or neither."""
     import torch
-    _, h_kv, d = _shape_of(ctx)
-    pages = bf16_pool.numel() // (h_kv * 32 * d)
-    kp, ks = _rows(k, h_kv, d, "k")
-    vp, vs = _rows(v, h_kv, d, "v")
-    n = k.shape[0]
+    _, h_kv, d, dev = _config_of(ctx)
+    bf16 = torch.bfloat16
+    kp, ks = _rows(k, bf16, h_kv, d, dev, "k")
+    vp, vs = _rows(v, bf16, h_kv, d, dev, "v")
+    n, size = k.shape[0], bf16_pool.numel()
     if v.shape[0] != n:
         raise ValueError("k and v differ in length")
+    pages = size // (h_kv * 32 * d)
     steps = bounds = None
     if key_steps is not None or key_bounds is not None:
-        steps = _sized(key_steps, torch.int8, h_kv * d, "key_steps")
-        bounds = _sized(key_bounds, torch.int8, pages * h_kv * 2 * d, "key_bounds")
-    _check(lib().oscar_append_bf16(ctx, kp, ks, vp, vs, _sized(slots, torch.int64, n, "slots"), n,
-                                   _dptr(bf16_pool, torch.bfloat16, "bf16_pool"), pages, steps, bounds,
-                                   _stream(stream)), "oscar_append_bf16")
+        steps = _ptr(key_steps, torch.int8, h_kv * d, dev, "key_steps")
+        bounds = _ptr(key_bounds, torch.int8, pages * h_kv * 2 * d, dev, "key_bounds")
+    st = lib().oscar_append_bf16(ctx, kp, ks, vp, vs, _ptr(slots, torch.int64, n, dev, "slots"), n,
+                                 _ptr(bf16_pool, bf16, size, dev, "bf16_pool"), pages, steps, bounds,
+                                 _stream_on(stream, dev))
+    if st:
+        _check(st, "oscar_append_bf16")
 
 
 def oscar_decode_bf16_workspace_size(ctx, batch, max_len):
     return lib().oscar_decode_bf16_workspace_size(ctx, batch, max_len)
 
 
-def _decode_shapes(q, tables, out):
-    batch = q.shape[0]
-    if tables.dim() != 2 or tables.shape[0] != batch:
-        raise ValueError("tables must be [%d][stride], got %s" % (batch, tuple(tables.shape)))
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape %s, has %s" % (tuple(q.shape), tuple(out.shape)))
-    return batch
-
-
 def oscar_decode_bf16(ctx, q, bf16_pool, tables, seq_len, max_len, out, workspace, stream=None):
     """q: bf16 [B][H_q][d], rows at any stride; tables int32 [B][stride]; seq_len int32 [B], at most max_len;
     out fp32 or bf16 [B][H_q][d]; workspace uint8."""
     import torch
-    h_q, h_kv, d = _shape_of(ctx)
-    qp, qs = _rows(q, h_q, d, "q")
-    batch = _decode_shapes(q, tables, out)
-    _check(lib().oscar_decode_bf16(
-        ctx, qp, qs, _dptr(bf16_pool, torch.bfloat16, "bf16_pool"), bf16_pool.numel() // (h_kv * 32 * d),
-        _dptr(tables, torch.int32, "tables"), tables.shape[1], _sized(seq_len, torch.int32, batch, "seq_len"),
-        int(max_len), _dptr(out, None, "out"), _out_type(out), _dptr(workspace, None, "workspace"),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), batch, _stream(stream)),
-        "oscar_decode_bf16")
+    h_q, h_kv, d, dev = _config_of(ctx)
+    qp, qs = _rows(q, torch.bfloat16, h_q, d, dev, "q")
+    batch, size = q.shape[0], bf16_pool.numel()
+    tp, ts = _table(tables, batch, torch.int32, dev)
+    op, ot = _output(out, q, dev, torch)
+    wp, ws = _scratch(workspace, dev)
+    st = lib().oscar_decode_bf16(
+        ctx, qp, qs, _ptr(bf16_pool, torch.bfloat16, size, dev, "bf16_pool"), size // (h_kv * 32 * d), tp, ts,
+        _ptr(seq_len, torch.int32, batch, dev, "seq_len"), max_len, op, ot, wp, ws, batch, _stream_on(stream, dev))
+    if st:
+        _check(st, "oscar_decode_bf16")
 
 
 def oscar_sparse_capacity(ctx, top_pages):
@@ -389,21 +433,24 @@ def oscar_decode_bf16_sparse(ctx, q, bf16_pool, key_steps, key_bounds, tables, s
     """oscar_decode_bf16 over the sink, the recent window and the top_pages best pages by their key bounds; chosen
     int32 [B][H_kv][oscar_sparse_capacity(ctx, top_pages)] and n_chosen int32 [B][H_kv] say which."""
     import torch
-    h_q, h_kv, d = _shape_of(ctx)
-    qp, qs = _rows(q, h_q, d, "q")
-    batch = _decode_shapes(q, tables, out)
-    pages = bf16_pool.numel() // (h_kv * 32 * d)
+    h_q, h_kv, d, dev = _config_of(ctx)
+    i8, i32 = torch.int8, torch.int32
+    qp, qs = _rows(q, torch.bfloat16, h_q, d, dev, "q")
+    batch, size = q.shape[0], bf16_pool.numel()
+    pages = size // (h_kv * 32 * d)
+    tp, ts = _table(tables, batch, i32, dev)
+    op, ot = _output(out, q, dev, torch)
+    wp, ws = _scratch(workspace, dev)
     handle = lib()
-    cap = handle.oscar_sparse_capacity(ctx, top_pages)
-    _check(handle.oscar_decode_bf16_sparse(
-        ctx, qp, qs, _dptr(bf16_pool, torch.bfloat16, "bf16_pool"), pages,
-        _sized(key_steps, torch.int8, h_kv * d, "key_steps"),
-        _sized(key_bounds, torch.int8, pages * h_kv * 2 * d, "key_bounds"),
-        _dptr(tables, torch.int32, "tables"), tables.shape[1], _sized(seq_len, torch.int32, batch, "seq_len"),
-        int(max_len), int(top_pages), _sized(chosen, torch.int32, batch * h_kv * cap, "chosen") if cap else None,
-        _sized(n_chosen, torch.int32, batch * h_kv, "n_chosen"), _dptr(out, None, "out"), _out_type(out),
-        _dptr(workspace, None, "workspace"), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-        batch, _stream(stream)), "oscar_decode_bf16_sparse")
+    cap = handle.oscar_sparse_capacity(ctx, top_pages)       # 0 where top_pages is refused
+    st = handle.oscar_decode_bf16_sparse(
+        ctx, qp, qs, _ptr(bf16_pool, torch.bfloat16, size, dev, "bf16_pool"), pages,
+        _ptr(key_steps, i8, h_kv * d, dev, "key_steps"), _ptr(key_bounds, i8, pages * h_kv * 2 * d, dev, "key_bounds"),
+        tp, ts, _ptr(seq_len, i32, batch, dev, "seq_len"), max_len, top_pages,
+        _ptr(chosen, i32, batch * h_kv * cap, dev, "chosen") if cap else None,
+        _ptr(n_chosen, i32, batch * h_kv, dev, "n_chosen"), op, ot, wp, ws, batch, _stream_on(stream, dev))
+    if st:
+        _check(st, "oscar_decode_bf16_sparse")
 
 
 def oscar_debug_error(ctx):

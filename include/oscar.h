@@ -390,7 +390,7 @@ typedef enum {
  *   seq_len:    DEVICE int32 [batch], each within [0, max_len]; a length outside
  *               counts as the nearer end. 0 gives zeros.
  *   max_len:    host bound of the lengths, <= 16 * table_stride and <= 2^30.
- *   out:        DEVICE [batch][H_q][d] of out_type.
+ *   out:        DEVICE [batch][H_q][d] of out_type, 16-byte aligned.
  *   workspace:  DEVICE, >= oscar_decode_bf16_workspace_size(ctx, batch, max_len)
  *               bytes, 256-byte aligned; scratch, nothing in it is kept. It may
  *               be NULL where that size is 0. Calls that overlap on the GPU need
