@@ -18,10 +18,7 @@
 namespace oscar {
 namespace {
 
-constexpr int kSelectThreads = 256;
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kBinsPerThread = kBins / kSelectThreads;
 constexpr int kMaxCluster = 16;
 constexpr int kSmemKeys = 16384;                 // candidates whose keys fit in shared memory (64 KB); else the workspace
 
@@ -42,10 +39,10 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 
 // Integer codes of the g query heads of KV head h: min(u, 0) for the lower bounds in bytes [0, D), max(u, 0)
 // for the upper ones behind them, zeros for the heads that are not there. One warp a head.
-template <int D>
+template <int D, int T>
 __device__ void query_codes(const SelectArgs& a, int b, int h, int8_t (*codes)[2 * D + 16], int* exponent) {
     const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < 8; i += kSelectWarps) {
+    for (int i = threadIdx.x >> 5; i < 8; i += T / 32) {
         float x[D / 32] = {}, top = 0.0f;
         if (i < a.g) {
             const uint16_t* q = a.q + b * a.q_stride + (int64_t)(h * a.g + i) * D;
@@ -82,7 +79,7 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
 }
 
 // Scores of the candidates (logical pages w.sink + i) of one (sequence, KV head) as ordered keys.
-template <int D>
+template <int D, int T>
 __device__ void score_pages(const SelectArgs& a, int b, int h, const Window& w, uint32_t* keys, int warp, int warps,
                             int8_t (*codes)[2 * D + 16], int* exponent) {
     constexpr int kBlocks = 2 * D / 64;                  // 64-byte column blocks of a page's bounds
@@ -114,7 +111,7 @@ __device__ void score_pages(const SelectArgs& a, int b, int h, const Window& w, 
     load_ids(i0);
     load();                                              // on their way while the codes are made
     load_ids(i0 + step);
-    query_codes<D>(a, b, h, codes, exponent);
+    query_codes<D, T>(a, b, h, codes, exponent);
     __syncthreads();
     // the heads of this lane's two result columns; columns without a head repeat head 0
     const float s0 = __int_as_float((127 + exponent[2 * t]) << 23), s1 = __int_as_float((127 + exponent[2 * t + 1]) << 23);
@@ -146,18 +143,20 @@ __device__ void score_pages(const SelectArgs& a, int b, int h, const Window& w, 
 
 struct SelectShared {
     int hist[kBins];
-    int warp_sum[kSelectWarps], warp_ties[kSelectWarps];
-    uint32_t warp_lo[kSelectWarps], warp_hi[kSelectWarps];
+    int warp_sum[32], warp_ties[32];
+    uint32_t warp_lo[32], warp_hi[32];
     int bin, left, count;
 };
 
 // The take largest of n keys (0 < take < n), ties to the lowest index: keys above base + mask, and the first
 // `left` of those within [base, base + mask].
+template <int T>
 __device__ void find_threshold(const uint32_t* keys, int n, int take, SelectShared& s, uint32_t& base, uint32_t& mask,
                                int& left) {
+    constexpr int kWarps = T / 32, kBinsPerThread = kBins / T;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t lo = ~0u, hi = 0;
-    for (int i = tid; i < n; i += kSelectThreads) {
+    for (int i = tid; i < n; i += T) {
         const uint32_t k = keys[i];
         lo = min(lo, k);
         hi = max(hi, k);
@@ -166,20 +165,17 @@ __device__ void find_threshold(const uint32_t* keys, int n, int take, SelectShar
     hi = __reduce_max_sync(~0u, hi);
     if (lane == 0) { s.warp_lo[warp] = lo; s.warp_hi[warp] = hi; }
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSelectWarps; ++w) {
-        lo = min(lo, s.warp_lo[w]);
-        hi = max(hi, s.warp_hi[w]);
-    }
+    lo = __reduce_min_sync(~0u, s.warp_lo[lane % kWarps]);
+    hi = __reduce_max_sync(~0u, s.warp_hi[lane % kWarps]);
     base = lo;
     left = take;
     int bits = 32 - __clz(hi - lo);
     mask = bits == 32 ? ~0u : (1u << bits) - 1;
     while (bits > 0) {
         const int shift = max(bits - 11, 0);
-        for (int i = tid; i < kBins; i += kSelectThreads) s.hist[i] = 0;
+        for (int i = tid; i < kBins; i += T) s.hist[i] = 0;
         __syncthreads();
-        for (int i = tid; i < n; i += kSelectThreads) {
+        for (int i = tid; i < n; i += T) {
             const uint32_t d = keys[i] - base;
             if (d <= mask) atomicAdd(&s.hist[d >> shift], 1);
         }
@@ -196,8 +192,8 @@ __device__ void find_threshold(const uint32_t* keys, int n, int take, SelectShar
         }
         if (lane == 31) s.warp_sum[warp] = sum;
         __syncthreads();
-        int above = sum - own;
-        for (int w = 0; w < warp; ++w) above += s.warp_sum[w];
+        const int above_warp = __reduce_add_sync(~0u, lane < warp ? s.warp_sum[lane] : 0);
+        int above = sum - own + above_warp;
         if (above < left && left <= above + own) {       // one thread
             int bin = kBins - 1 - kBinsPerThread * tid;
             while (above + s.hist[bin] < left) above += s.hist[bin--];
@@ -214,8 +210,8 @@ __device__ void find_threshold(const uint32_t* keys, int n, int take, SelectShar
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(SelectArgs a, int smem_keys) {
+template <int D, int T>
+__global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int smem_keys) {
     __shared__ __align__(16) int8_t codes[8][2 * D + 16];     // padded: eight heads' words in eight bank groups
     __shared__ int exponent[8];
     __shared__ SelectShared s;
@@ -235,27 +231,27 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(SelectArgs a,
     uint32_t* keys = cand <= smem_keys ? cluster.map_shared_rank(key_store, 0)
                                        : a.keys + (int64_t)unit * a.max_pages;
     if (choose)
-        score_pages<D>(a, b, h, w, keys, rank + ranks * warp, ranks * kSelectWarps, codes, exponent);
+        score_pages<D, T>(a, b, h, w, keys, rank + ranks * warp, ranks * (T / 32), codes, exponent);
     cluster.sync();
     if (rank != 0) return;
     if (cand <= smem_keys) keys = key_store;
 
     int32_t* list = a.chosen + (int64_t)unit * a.cap;
     const int recent = w.pages - max(w.first, w.sink), total = w.sink + take + recent;
-    for (int i = tid; i < w.sink; i += kSelectThreads) list[i] = i;
-    for (int i = tid; i < recent; i += kSelectThreads) list[w.sink + take + i] = w.pages - recent + i;
-    for (int i = total + tid; i < a.cap; i += kSelectThreads) list[i] = -1;
+    for (int i = tid; i < w.sink; i += T) list[i] = i;
+    for (int i = tid; i < recent; i += T) list[w.sink + take + i] = w.pages - recent + i;
+    for (int i = total + tid; i < a.cap; i += T) list[i] = -1;
     if (tid == 0) a.n_chosen[unit] = total;
     list += w.sink;
     if (!choose) {
-        for (int i = tid; i < take; i += kSelectThreads) list[i] = w.sink + i;
+        for (int i = tid; i < take; i += T) list[i] = w.sink + i;
         return;
     }
     uint32_t base, mask;
     int left;
-    find_threshold(keys, cand, take, s, base, mask, left);
+    find_threshold<T>(keys, cand, take, s, base, mask, left);
     // Each warp lists its share of the candidates behind those of the warps before it.
-    const int share = (cand + kSelectThreads - 1) / kSelectThreads * 32;
+    const int share = (cand + T - 1) / T * 32;
     const int i0 = min(cand, warp * share), i1 = min(cand, i0 + share);
     int above = 0, ties = 0;
     for (int i = i0 + lane; i < i1; i += 32) {
@@ -267,8 +263,8 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(SelectArgs a,
     ties = __reduce_add_sync(~0u, ties);
     if (lane == 0) { s.warp_sum[warp] = above; s.warp_ties[warp] = ties; }
     __syncthreads();
-    int at = 0, tied = 0;
-    for (int v = 0; v < warp; ++v) { at += s.warp_sum[v]; tied += s.warp_ties[v]; }
+    int at = __reduce_add_sync(~0u, lane < warp ? s.warp_sum[lane] : 0);
+    int tied = __reduce_add_sync(~0u, lane < warp ? s.warp_ties[lane] : 0);
     at += min(tied, left);
     for (int i = i0; i < i1; i += 32) {
         const uint32_t k = i + lane < i1 ? keys[i + lane] : 0u;
@@ -283,21 +279,29 @@ __global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(SelectArgs a,
     }
 }
 
-template <int D>
+template <int D, int T>
 cudaError_t launch(const SelectArgs& a, int num_sms, cudaStream_t st) {
     const long long units = (long long)a.batch * a.h_kv;
-    // CTAs of a cluster: as many as find room next to those of the other units, each with a tile of 16 pages
-    // per warp at least.
+    // CTAs of a cluster: while all clusters fit on the card at once (1,024 threads an SM), with a tile of 16
+    // pages for every warp.
     int cluster = 1;
-    while (cluster < kMaxCluster && 2 * cluster * units <= 4 * num_sms && 2 * cluster * kSelectWarps * 16 <= a.max_pages)
+    while (cluster < kMaxCluster && 2 * cluster * units <= num_sms * (1024 / T) && 2 * cluster * (T / 2) <= a.max_pages)
         cluster *= 2;
     if (cluster * units > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int smem_keys = a.max_pages < kSmemKeys ? a.max_pages : kSmemKeys;
-    cudaError_t e = smem_opt_in<select_kernel<D>>(kSmemKeys * sizeof(uint32_t));
-    if (e == cudaSuccess) e = allow_large_clusters<select_kernel<D>>();
+    cudaError_t e = smem_opt_in<select_kernel<D, T>>(kSmemKeys * sizeof(uint32_t));
+    if (e == cudaSuccess) e = allow_large_clusters<select_kernel<D, T>>();
     if (e != cudaSuccess) return e;
-    return launch_dependent(select_kernel<D>, dim3((unsigned)(units * cluster)), dim3(kSelectThreads),
+    return launch_dependent(select_kernel<D, T>, dim3((unsigned)(units * cluster)), dim3(T),
                             smem_keys * sizeof(uint32_t), st, cluster, a, smem_keys);
+}
+
+template <int D>
+cudaError_t launch_threads(const SelectArgs& a, int num_sms, cudaStream_t st) {
+    const long long units = (long long)a.batch * a.h_kv;
+    if (units <= num_sms && a.max_pages > 512) return launch<D, 1024>(a, num_sms, st);
+    if (units <= 2 * num_sms && a.max_pages > 256) return launch<D, 512>(a, num_sms, st);
+    return launch<D, 256>(a, num_sms, st);
 }
 
 }  // namespace
@@ -308,7 +312,7 @@ size_t select_workspace_bytes(const Shape& s, int batch, int max_pages) {
 }
 
 cudaError_t launch_select(const SelectArgs& a, int d, int num_sms, cudaStream_t st) {
-    return d == 128 ? launch<128>(a, num_sms, st) : launch<64>(a, num_sms, st);
+    return d == 128 ? launch_threads<128>(a, num_sms, st) : launch_threads<64>(a, num_sms, st);
 }
 
 }  // namespace oscar

@@ -20,6 +20,10 @@ namespace {
 
 constexpr int kAttendWarps = 4;
 constexpr int kJoinThreads = 256;
+constexpr int kMaxSplitPages = 256;      // pages of a split at most
+constexpr int kSplitCost = 6;            // pages' time that a split costs apart from its pages
+// Resident CTAs an SM, by registers (168 and 128 a thread).
+constexpr int attend_ctas(int d) { return d == 128 ? 3 : 4; }
 constexpr float kNoLogit = -1e30f;       // running reference before any token
 constexpr float kHeadroom = 8.0f;        // the reference is raised when a logit passes it by this much (log2)
 
@@ -62,7 +66,7 @@ __device__ __forceinline__ void load_v(Page<D>& p, const uint16_t* page, int gid
 }
 
 template <int D, bool SPARSE>
-__global__ void __launch_bounds__(kAttendWarps * 32, 3) attend_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas(D)) attend_kernel(AttendArgs a) {
     constexpr int kTiles = D / 16;       // m-tiles of the output product
     __shared__ float warp_m[kAttendWarps][8], warp_l[kAttendWarps][8];
     __shared__ float warp_acc[kAttendWarps][8][D];
@@ -88,17 +92,26 @@ __global__ void __launch_bounds__(kAttendWarps * 32, 3) attend_kernel(AttendArgs
     float m = kNoLogit, l = 0.0f;        // head gid (l: this lane's tokens)
     float acc[kTiles][4] = {};           // channels of gid, heads 2t and 2t + 1
 
-    for (int i = first + warp; i < last; i += kAttendWarps) {
-        const int logical = SPARSE ? list[i] : i;
-        const int id = table[logical];
-        int valid = min(kPage, len - logical * kPage);
-        const uint16_t* page = a.pool;
-        if (id < 0 || id >= a.pages) {
-            if (a.debug && lane == 0) record_error(&a.dbg->kind, &a.dbg->index, 2, id);
-            valid = 0;
-        } else {
-            page += ((int64_t)id * a.h_kv + h) * (2 * kPage * D);
+    // This warp's pages are first + warp, + kAttendWarps, ...; lane l holds the id and the valid tokens of the
+    // l-th of every 32 of them, so that a page's address waits for no load.
+    const int mine = (last - first - warp + kAttendWarps - 1) / kAttendWarps;
+    int lane_id = 0, lane_valid = 0;
+    for (int n = 0; n < mine; ++n) {
+        if ((n & 31) == 0) {
+            lane_id = lane_valid = 0;
+            const int i = first + warp + kAttendWarps * (n + lane);
+            if (i < last) {
+                const int logical = SPARSE ? list[i] : i, id = table[logical];
+                if (id >= 0 && id < a.pages) {
+                    lane_id = id;
+                    lane_valid = min(kPage, len - logical * kPage);
+                } else if (a.debug) {
+                    record_error(&a.dbg->kind, &a.dbg->index, 2, id);
+                }
+            }
         }
+        const uint16_t* page = a.pool + ((int64_t)__shfl_sync(~0u, lane_id, n & 31) * a.h_kv + h) * (2 * kPage * D);
+        const int valid = __shfl_sync(~0u, lane_valid, n & 31);
         Page<D> p;
         load_k<D>(p, page, gid, t);
         load_v<D>(p, page, gid, t);
@@ -283,13 +296,22 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
 AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages) {
     AttendPlan p{};
     const long long units = (long long)batch * s.h_kv;
-    const int slots = 3 * num_sms;                       // resident CTAs
-    long long splits = units > 0 ? slots / units : 1;
-    const long long by_len = (max_pages + 255) / 256;    // at most 256 pages a split
-    if (splits < by_len) splits = by_len;
+    const long long slots = (long long)attend_ctas(s.d) * num_sms;     // resident CTAs
     const long long most = (max_pages + kAttendWarps - 1) / kAttendWarps;
-    if (splits > most) splits = most;
-    if (splits < 1) splits = 1;
+    // Splits that fill w waves of CTAs, for the w whose waves take least: a CTA's pages and about kSplitCost pages'
+    // time to start and join. No split is longer than kMaxSplitPages, so that sequences of several lengths share out.
+    long long best = 0, splits = 1;
+    for (int w = 1; w <= 16 && units > 0; ++w) {
+        long long n = w * slots / units;
+        n = n > most ? most : n;
+        if (n < 1) n = 1;
+        const long long pages = (max_pages + n - 1) / n, waves = (units * n + slots - 1) / slots;
+        const long long cost = waves * (pages + kSplitCost);
+        if (best == 0 || cost < best) { best = cost; splits = n; }
+        if (n == most) break;
+    }
+    const long long by_len = (max_pages + kMaxSplitPages - 1) / kMaxSplitPages;
+    if (splits < by_len) splits = by_len;
     p.pages_per_split = max_pages > 0 ? (int)((max_pages + splits - 1) / splits) : 1;
     p.splits = max_pages > 0 ? (max_pages + p.pages_per_split - 1) / p.pages_per_split : 1;
     const size_t parts = p.splits == 1 ? 0 : (size_t)batch * s.h_q * p.splits;
