@@ -3,15 +3,21 @@
 // Score of page p for KV head h: max over the head's g query heads of 2^e S with
 // S = sum_c max(u_c lo_c, u_c hi_c), u the query's integer codes in the steps of the key bounds [lo, hi]. It
 // bounds the logits of the page's keys (up to the rounding of u and to clipped codes). S is an integer below
-// 2^23 and the scale a power of two, so the score is exact in fp32 and the choice does not depend on the
-// order of any sum. sum max(u lo, u hi) = sum min(u, 0) lo + max(u, 0) hi, one integer product over 2 d bytes:
-// mma.sync m16n8k32 with 16 pages as rows and the heads as columns, operands straight from memory (the
-// order of the contraction is free, so a lane's 16 bytes serve two steps).
+// 2^22 and the scale a power of two, so the score is exact in fp32 and the choice does not depend on the
+// order of any sum. sum max(u lo, u hi) = sum min(u, 0) lo + max(u, 0) hi is one product over 2 d bytes.
+//
+// That product runs on mma.sync m16n8k16 in fp16, 16 pages as rows, the heads as columns: a byte b + 128 with a
+// zero above it is the fp16 subnormal (b + 128) 2^-24, so two byte permutations and one exclusive-or turn four
+// bounds into operands; products and sums are multiples of 2^-24 below 2^-2, exact in the fp32 accumulator, and
+// 128 sum u is taken off at the end. (The integer m16n8k32 takes 65 cycles a warp on sm_103a, this 8: the
+// scores of 64 sequences at 32k took 57k cycles with it, its rate.) Operands come straight from memory; the
+// contraction's order is free, so a lane's 16 bytes serve four steps.
 //
 // One cluster per (sequence, KV head). Its warps score the pages, 16 at a time, into the first CTA's shared
-// memory; that CTA finds the top-th largest key by counting (2,048 bins a pass, narrowed to the keys'
-// range first) and writes the list in ascending order.
+// memory; that CTA finds the top-th largest key by counting (2,048 bins a pass, from the keys' own range)
+// and writes the list in ascending order.
 #include <cooperative_groups.h>
+#include <cuda_fp16.h>
 
 #include "paged_device.cuh"
 
@@ -37,10 +43,16 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Integer codes of the g query heads of KV head h: min(u, 0) for the lower bounds in bytes [0, D), max(u, 0)
-// for the upper ones behind them, zeros for the heads that are not there. One warp a head.
+// The query heads of one KV head as the product takes them.
+template <int D>
+struct QueryCodes {
+    __half code[8][2 * D + 8];           // min(u, 0) in [0, D), max(u, 0) in [D, 2 D); zeros for absent heads; padded
+    float scale[8];                      // 2^e
+    float offset[8];                     // -128 sum u
+};
+
 template <int D, int T>
-__device__ void query_codes(const SelectArgs& a, int b, int h, int8_t (*codes)[2 * D + 16], int* exponent) {
+__device__ void query_codes(const SelectArgs& a, int b, int h, QueryCodes<D>& qc) {
     const int lane = threadIdx.x & 31;
     for (int i = threadIdx.x >> 5; i < 8; i += T / 32) {
         float x[D / 32] = {}, top = 0.0f;
@@ -60,28 +72,42 @@ __device__ void query_codes(const SelectArgs& a, int b, int h, int8_t (*codes)[2
         const int e = min((int)(__float_as_uint(top) >> 23) - 126 - 7, 60);
         const bool none = top < 0x1p-60f;
         const float inv = none ? 0.0f : __int_as_float((127 - e) << 23);
+        int sum = 0;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
             const int u = __float2int_rn(fminf(fmaxf(x[j] * inv, -127.0f), 127.0f));
-            codes[i][lane + 32 * j] = (int8_t)min(u, 0);
-            codes[i][D + lane + 32 * j] = (int8_t)max(u, 0);
+            qc.code[i][lane + 32 * j] = __int2half_rn(min(u, 0));
+            qc.code[i][D + lane + 32 * j] = __int2half_rn(max(u, 0));
+            sum += u;
         }
-        if (lane == 0) exponent[i] = none ? 0 : e;
+        sum = __reduce_add_sync(~0u, sum);
+        if (lane == 0) {
+            qc.scale[i] = none ? 1.0f : __int_as_float((127 + e) << 23);
+            qc.offset[i] = -128.0f * (float)sum;
+        }
     }
 }
 
-__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
-                 : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// One step: four bounds of page gid (x) and of page gid + 8 (y) against four codes of the lane's head.
+__device__ __forceinline__ void mma_bounds(float (&c)[4], uint32_t x, uint32_t y, uint32_t u0, uint32_t u1) {
+    x ^= 0x80808080u;
+    y ^= 0x80808080u;
+    mma_f16(c, __byte_perm(x, 0, 0x4140), __byte_perm(y, 0, 0x4140), __byte_perm(x, 0, 0x4342), __byte_perm(y, 0, 0x4342),
+            u0, u1);
+}
 
-// Scores of the candidates (logical pages w.sink + i) of one (sequence, KV head) as ordered keys.
-template <int D, int T>
-__device__ void score_pages(const SelectArgs& a, int b, int h, const Window& w, uint32_t* keys, int warp, int warps,
-                            int8_t (*codes)[2 * D + 16], int* exponent) {
+// Scores of the candidates (logical pages w.sink + i) of one (sequence, KV head) as ordered keys, and their
+// range. `meanwhile` runs while the first bounds are on their way.
+template <int D, int T, typename F>
+__device__ void score_pages(const SelectArgs& a, int b, int h, const Window& w, uint32_t* keys, uint32_t* range, int warp,
+                            int warps, QueryCodes<D>& qc, F meanwhile) {
     constexpr int kBlocks = 2 * D / 64;                  // 64-byte column blocks of a page's bounds
     const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
     const int32_t* table = a.tables + (int64_t)b * a.stride + w.sink;
@@ -111,18 +137,23 @@ __device__ void score_pages(const SelectArgs& a, int b, int h, const Window& w, 
     load_ids(i0);
     load();                                              // on their way while the codes are made
     load_ids(i0 + step);
-    query_codes<D, T>(a, b, h, codes, exponent);
+    query_codes<D, T>(a, b, h, qc);
+    meanwhile();
     __syncthreads();
-    // the heads of this lane's two result columns; columns without a head repeat head 0
-    const float s0 = __int_as_float((127 + exponent[2 * t]) << 23), s1 = __int_as_float((127 + exponent[2 * t + 1]) << 23);
+    // the heads of this lane's two result columns
+    const float s0 = qc.scale[2 * t], s1 = qc.scale[2 * t + 1], o0 = qc.offset[2 * t], o1 = qc.offset[2 * t + 1];
     const bool h0 = 2 * t < a.g, h1 = 2 * t + 1 < a.g;
+    uint32_t least = ~0u, most = 0;
     for (; i0 < cand; i0 += step) {
-        int c[4] = {};
+        float c[4] = {};
 #pragma unroll
         for (int j = 0; j < kBlocks; ++j) {
-            const uint4 u = *reinterpret_cast<const uint4*>(&codes[gid][64 * j + 16 * t]);
-            mma_s8(c, x[0][j].x, x[1][j].x, x[0][j].y, x[1][j].y, u.x, u.y);
-            mma_s8(c, x[0][j].z, x[1][j].z, x[0][j].w, x[1][j].w, u.z, u.w);
+            const uint4* u = reinterpret_cast<const uint4*>(&qc.code[gid][64 * j + 16 * t]);
+            const uint4 u0 = u[0], u1 = u[1];
+            mma_bounds(c, x[0][j].x, x[1][j].x, u0.x, u0.y);
+            mma_bounds(c, x[0][j].y, x[1][j].y, u0.z, u0.w);
+            mma_bounds(c, x[0][j].z, x[1][j].z, u1.x, u1.y);
+            mma_bounds(c, x[0][j].w, x[1][j].w, u1.z, u1.w);
         }
         const bool was[2] = {real[0], real[1]};
         if (i0 + step < cand) {
@@ -131,50 +162,55 @@ __device__ void score_pages(const SelectArgs& a, int b, int h, const Window& w, 
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            float best = h0 ? (float)c[2 * r] * s0 : -INFINITY;
-            if (h1) best = fmaxf(best, (float)c[2 * r + 1] * s1);
+            float best = h0 ? fmaf(c[2 * r], 0x1p24f, o0) * s0 : -INFINITY;
+            if (h1) best = fmaxf(best, fmaf(c[2 * r + 1], 0x1p24f, o1) * s1);
             best = fmaxf(best, __shfl_xor_sync(~0u, best, 1));
             best = fmaxf(best, __shfl_xor_sync(~0u, best, 2));
             const int i = i0 + gid + 8 * r;
-            if (t == 0 && i < cand) keys[i] = was[r] ? ordered(best) : 0u;
+            if (i < cand) {
+                const uint32_t key = was[r] ? ordered(best) : 0u;
+                if (t == 0) keys[i] = key;
+                least = min(least, key);
+                most = max(most, key);
+            }
         }
+    }
+    least = __reduce_min_sync(~0u, least);
+    most = __reduce_max_sync(~0u, most);
+    if (lane == 0) {
+        atomicMin(&range[0], least);
+        atomicMax(&range[1], most);
     }
 }
 
 struct SelectShared {
-    int hist[kBins];
+    int hist[kBins];                                     // zero before the first pass
+    uint32_t range[2];                                   // least and largest key
     int warp_sum[32], warp_ties[32];
-    uint32_t warp_lo[32], warp_hi[32];
-    int bin, left, count;
+    int bin, left, count, few;
+    uint32_t few_keys[32];
 };
 
 // The take largest of n keys (0 < take < n), ties to the lowest index: keys above base + mask, and the first
-// `left` of those within [base, base + mask].
+// `left` of those within [base, base + mask]. Counting passes narrow the range by 2^11 each, until all keys of
+// a bin are taken, or so few are left in it that a warp ranks them.
 template <int T>
 __device__ void find_threshold(const uint32_t* keys, int n, int take, SelectShared& s, uint32_t& base, uint32_t& mask,
                                int& left) {
-    constexpr int kWarps = T / 32, kBinsPerThread = kBins / T;
+    constexpr int kBinsPerThread = kBins / T;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t lo = ~0u, hi = 0;
-    for (int i = tid; i < n; i += T) {
-        const uint32_t k = keys[i];
-        lo = min(lo, k);
-        hi = max(hi, k);
-    }
-    lo = __reduce_min_sync(~0u, lo);
-    hi = __reduce_max_sync(~0u, hi);
-    if (lane == 0) { s.warp_lo[warp] = lo; s.warp_hi[warp] = hi; }
-    __syncthreads();
-    lo = __reduce_min_sync(~0u, s.warp_lo[lane % kWarps]);
-    hi = __reduce_max_sync(~0u, s.warp_hi[lane % kWarps]);
-    base = lo;
+    base = s.range[0];
     left = take;
-    int bits = 32 - __clz(hi - lo);
+    int bits = 32 - __clz(s.range[1] - base);
     mask = bits == 32 ? ~0u : (1u << bits) - 1;
-    while (bits > 0) {
+    for (bool again = false; bits > 0; again = true) {
         const int shift = max(bits - 11, 0);
-        for (int i = tid; i < kBins; i += T) s.hist[i] = 0;
-        __syncthreads();
+        if (again) {
+            for (int i = tid; i < kBins; i += T) s.hist[i] = 0;
+            __syncthreads();
+        }
+        if (tid == 0) s.few = 0;
+#pragma unroll 4
         for (int i = tid; i < n; i += T) {
             const uint32_t d = keys[i] - base;
             if (d <= mask) atomicAdd(&s.hist[d >> shift], 1);
@@ -192,8 +228,7 @@ __device__ void find_threshold(const uint32_t* keys, int n, int take, SelectShar
         }
         if (lane == 31) s.warp_sum[warp] = sum;
         __syncthreads();
-        const int above_warp = __reduce_add_sync(~0u, lane < warp ? s.warp_sum[lane] : 0);
-        int above = sum - own + above_warp;
+        int above = sum - own + __reduce_add_sync(~0u, lane < warp ? s.warp_sum[lane] : 0);
         if (above < left && left <= above + own) {       // one thread
             int bin = kBins - 1 - kBinsPerThread * tid;
             while (above + s.hist[bin] < left) above += s.hist[bin--];
@@ -205,15 +240,36 @@ __device__ void find_threshold(const uint32_t* keys, int n, int take, SelectShar
         base += (uint32_t)s.bin << shift;
         mask = (1u << shift) - 1;
         left = s.left;
-        bits = s.count == left ? 0 : shift;              // all keys of the bin are taken: no need to look closer
+        const int count = s.count;
+        if (count == left) return;
+        bits = shift;
+        if (bits > 0 && count <= 32) {
+            for (int i = tid; i < n; i += T) {
+                const uint32_t k = keys[i];
+                if (k - base <= mask) s.few_keys[atomicAdd(&s.few, 1)] = k;
+            }
+            __syncthreads();
+            // every warp alike: the key with fewer than `left` larger ones and at least that many not smaller
+            const uint32_t k = s.few_keys[lane];
+            int larger = 0, equal = 0;
+            for (int j = 0; j < count; ++j) {
+                const uint32_t other = s.few_keys[j];
+                larger += other > k;
+                equal += other == k;
+            }
+            const uint32_t hit = __ballot_sync(~0u, lane < count && larger < left && left <= larger + equal);
+            base = __shfl_sync(~0u, k, __ffs(hit) - 1);
+            left -= __shfl_sync(~0u, larger, __ffs(hit) - 1);
+            mask = 0;
+            return;
+        }
         __syncthreads();
     }
 }
 
 template <int D, int T>
 __global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int smem_keys) {
-    __shared__ __align__(16) int8_t codes[8][2 * D + 16];     // padded: eight heads' words in eight bank groups
-    __shared__ int exponent[8];
+    __shared__ __align__(16) QueryCodes<D> codes;
     __shared__ SelectShared s;
     extern __shared__ uint32_t key_store[];
     namespace cg = cooperative_groups;
@@ -221,6 +277,8 @@ __global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int s
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const int unit = blockIdx.x / ranks, b = unit / a.h_kv, h = unit % a.h_kv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < kBins; i += T) s.hist[i] = 0;
+    if (tid == 0) { s.range[0] = ~0u; s.range[1] = 0; }
     cluster.sync();                                      // the first CTA runs: its shared memory may be written
     grid_wait();
     grid_release();
@@ -230,18 +288,24 @@ __global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int s
     const bool choose = take > 0 && take < cand;
     uint32_t* keys = cand <= smem_keys ? cluster.map_shared_rank(key_store, 0)
                                        : a.keys + (int64_t)unit * a.max_pages;
+    const int recent = w.pages - max(w.first, w.sink), total = w.sink + take + recent;
+    int32_t* list = a.chosen + (int64_t)unit * a.cap;
+    auto write_frame = [&]() {                           // everything but the selected pages
+        if (rank != 0) return;
+        for (int i = tid; i < w.sink; i += T) list[i] = i;
+        for (int i = tid; i < recent; i += T) list[w.sink + take + i] = w.pages - recent + i;
+        for (int i = total + tid; i < a.cap; i += T) list[i] = -1;
+        if (tid == 0) a.n_chosen[unit] = total;
+    };
     if (choose)
-        score_pages<D, T>(a, b, h, w, keys, rank + ranks * warp, ranks * (T / 32), codes, exponent);
+        score_pages<D, T>(a, b, h, w, keys, cluster.map_shared_rank(s.range, 0), rank + ranks * warp, ranks * (T / 32),
+                          codes, write_frame);
+    else
+        write_frame();
     cluster.sync();
     if (rank != 0) return;
     if (cand <= smem_keys) keys = key_store;
 
-    int32_t* list = a.chosen + (int64_t)unit * a.cap;
-    const int recent = w.pages - max(w.first, w.sink), total = w.sink + take + recent;
-    for (int i = tid; i < w.sink; i += T) list[i] = i;
-    for (int i = tid; i < recent; i += T) list[w.sink + take + i] = w.pages - recent + i;
-    for (int i = total + tid; i < a.cap; i += T) list[i] = -1;
-    if (tid == 0) a.n_chosen[unit] = total;
     list += w.sink;
     if (!choose) {
         for (int i = tid; i < take; i += T) list[i] = w.sink + i;
@@ -254,6 +318,7 @@ __global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int s
     const int share = (cand + T - 1) / T * 32;
     const int i0 = min(cand, warp * share), i1 = min(cand, i0 + share);
     int above = 0, ties = 0;
+#pragma unroll 4
     for (int i = i0 + lane; i < i1; i += 32) {
         const uint32_t k = keys[i];
         above += k > base && k - base > mask;
@@ -266,6 +331,7 @@ __global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int s
     int at = __reduce_add_sync(~0u, lane < warp ? s.warp_sum[lane] : 0);
     int tied = __reduce_add_sync(~0u, lane < warp ? s.warp_ties[lane] : 0);
     at += min(tied, left);
+#pragma unroll 4
     for (int i = i0; i < i1; i += 32) {
         const uint32_t k = i + lane < i1 ? keys[i + lane] : 0u;
         const bool in_range = i + lane < i1;
@@ -282,10 +348,10 @@ __global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int s
 template <int D, int T>
 cudaError_t launch(const SelectArgs& a, int num_sms, cudaStream_t st) {
     const long long units = (long long)a.batch * a.h_kv;
-    // CTAs of a cluster: while all clusters fit on the card at once (1,024 threads an SM), with a tile of 16
-    // pages for every warp.
+    // CTAs of a cluster: up to about twice the card's threads (1,024 an SM) in all, so that long sequences among
+    // short ones spread out, and a tile of 16 pages for every warp.
     int cluster = 1;
-    while (cluster < kMaxCluster && 2 * cluster * units <= num_sms * (1024 / T) && 2 * cluster * (T / 2) <= a.max_pages)
+    while (cluster < kMaxCluster && 2 * cluster * units <= 4 * num_sms && 2 * cluster * (T / 2) <= a.max_pages)
         cluster *= 2;
     if (cluster * units > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int smem_keys = a.max_pages < kSmemKeys ? a.max_pages : kSmemKeys;
@@ -299,7 +365,8 @@ cudaError_t launch(const SelectArgs& a, int num_sms, cudaStream_t st) {
 template <int D>
 cudaError_t launch_threads(const SelectArgs& a, int num_sms, cudaStream_t st) {
     const long long units = (long long)a.batch * a.h_kv;
-    if (units <= num_sms && a.max_pages > 512) return launch<D, 1024>(a, num_sms, st);
+    // Few sequences: larger CTAs, so that one has the threads for the selection. Mixed batch of 16 (128 units):
+    // 89 us with 512 threads, 93 with 256, 97 with 1,024; batch 64 (512 units) 168, 164 and 182.
     if (units <= 2 * num_sms && a.max_pages > 256) return launch<D, 512>(a, num_sms, st);
     return launch<D, 256>(a, num_sms, st);
 }
