@@ -51,40 +51,55 @@ struct QueryCodes {
     float offset[8];                     // -128 sum u
 };
 
-template <int D, int T>
-__device__ void query_codes(const SelectArgs& a, int b, int h, QueryCodes<D>& qc) {
+// One warp a head: its query channels lane, lane + 32, ... and their steps, then their codes.
+template <int D>
+struct QueryRow {
+    uint16_t q[D / 32];
+    int8_t step[D / 32];
+};
+
+template <int D>
+__device__ __forceinline__ QueryRow<D> fetch_query(const SelectArgs& a, int b, int h, int i) {
     const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < 8; i += T / 32) {
-        float x[D / 32] = {}, top = 0.0f;
-        if (i < a.g) {
-            const uint16_t* q = a.q + b * a.q_stride + (int64_t)(h * a.g + i) * D;
+    const uint16_t* q = a.q + b * a.q_stride + (int64_t)(h * a.g + i) * D;
+    QueryRow<D> r;
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-                const int c = lane + 32 * j, step = max(-100, min(100, (int)a.steps[h * D + c]));
-                x[j] = __uint_as_float((uint32_t)q[c] << 16) * __int_as_float((127 + step) << 23);
-                if (!isfinite(x[j])) x[j] = 0.0f;
-                top = fmaxf(top, fabsf(x[j]));
-            }
-        }
+    for (int j = 0; j < D / 32; ++j) {
+        r.q[j] = i < a.g ? q[lane + 32 * j] : 0;
+        r.step[j] = a.steps[h * D + lane + 32 * j];
+    }
+    return r;
+}
+
+template <int D>
+__device__ __forceinline__ void query_codes(const QueryRow<D>& r, int i, QueryCodes<D>& qc) {
+    const int lane = threadIdx.x & 31;
+    float x[D / 32], top = 0.0f;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        // top = f 2^x with f in [1/2, 1): codes in units of 2^(x - 7)
-        const int e = min((int)(__float_as_uint(top) >> 23) - 126 - 7, 60);
-        const bool none = top < 0x1p-60f;
-        const float inv = none ? 0.0f : __int_as_float((127 - e) << 23);
-        int sum = 0;
+    for (int j = 0; j < D / 32; ++j) {
+        const int step = max(-100, min(100, (int)r.step[j]));
+        x[j] = __uint_as_float((uint32_t)r.q[j] << 16) * __int_as_float((127 + step) << 23);
+        if (!isfinite(x[j])) x[j] = 0.0f;
+        top = fmaxf(top, fabsf(x[j]));
+    }
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-            const int u = __float2int_rn(fminf(fmaxf(x[j] * inv, -127.0f), 127.0f));
-            qc.code[i][lane + 32 * j] = __int2half_rn(min(u, 0));
-            qc.code[i][D + lane + 32 * j] = __int2half_rn(max(u, 0));
-            sum += u;
-        }
-        sum = __reduce_add_sync(~0u, sum);
-        if (lane == 0) {
-            qc.scale[i] = none ? 1.0f : __int_as_float((127 + e) << 23);
-            qc.offset[i] = -128.0f * (float)sum;
-        }
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    // top = f 2^x with f in [1/2, 1): codes in units of 2^(x - 7)
+    const int e = min((int)(__float_as_uint(top) >> 23) - 126 - 7, 60);
+    const bool none = top < 0x1p-60f;
+    const float inv = none ? 0.0f : __int_as_float((127 - e) << 23);
+    int sum = 0;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+        const int u = __float2int_rn(fminf(fmaxf(x[j] * inv, -127.0f), 127.0f));
+        qc.code[i][lane + 32 * j] = __int2half_rn(min(u, 0));
+        qc.code[i][D + lane + 32 * j] = __int2half_rn(max(u, 0));
+        sum += u;
+    }
+    sum = __reduce_add_sync(~0u, sum);
+    if (lane == 0) {
+        qc.scale[i] = none ? 1.0f : __int_as_float((127 + e) << 23);
+        qc.offset[i] = -128.0f * (float)sum;
     }
 }
 
@@ -104,16 +119,14 @@ __device__ __forceinline__ void mma_bounds(float (&c)[4], uint32_t x, uint32_t y
 }
 
 // Scores of the candidates (logical pages w.sink + i) of one (sequence, KV head) as ordered keys, and their
-// range. `meanwhile` runs while the first bounds are on their way.
+// range. `id` holds the page ids of this warp's first tile; `meanwhile` runs while the first bounds are on
+// their way and ends with the query's codes in place.
 template <int D, int T, typename F>
-__device__ void score_pages(const SelectArgs& a, int b, int h, const Window& w, uint32_t* keys, uint32_t* range, int warp,
-                            int warps, QueryCodes<D>& qc, F meanwhile) {
+__device__ void score_pages(const SelectArgs& a, int h, const int32_t* table, int cand, uint32_t* keys, uint32_t* range,
+                            int warp, int warps, int (&id)[2], const QueryCodes<D>& qc, F meanwhile) {
     constexpr int kBlocks = 2 * D / 64;                  // 64-byte column blocks of a page's bounds
     const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
-    const int32_t* table = a.tables + (int64_t)b * a.stride + w.sink;
-    const int cand = w.first - w.sink;
     uint4 x[2][kBlocks];                                 // pages gid and gid + 8 of the tile
-    int id[2];                                           // their page ids, one tile ahead of the bounds
     bool real[2];
     auto load_ids = [&](int i0) {
 #pragma unroll
@@ -122,24 +135,22 @@ __device__ void score_pages(const SelectArgs& a, int b, int h, const Window& w, 
             id[r] = i < cand ? table[i] : 0;
         }
     };
-    auto load = [&]() {
+    auto load = [&](int i0) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
+            const bool inside = i0 + gid + 8 * r < cand;
             real[r] = id[r] >= 0 && id[r] < a.pages;
-            if (!real[r] && a.debug && t == 0) record_error(&a.dbg->kind, &a.dbg->index, 2, id[r]);
-            const int8_t* src = a.bounds + ((int64_t)(real[r] ? id[r] : 0) * a.h_kv + h) * (2 * D) + 16 * t;
+            if (inside && !real[r] && a.debug && t == 0) record_error(&a.dbg->kind, &a.dbg->index, 2, id[r]);
+            const int8_t* src = a.bounds + ((int64_t)(inside && real[r] ? id[r] : 0) * a.h_kv + h) * (2 * D) + 16 * t;
 #pragma unroll
             for (int j = 0; j < kBlocks; ++j) x[r][j] = ldg_stream(src + 64 * j);
         }
     };
     const int step = 16 * warps;
     int i0 = 16 * warp;
-    load_ids(i0);
-    load();                                              // on their way while the codes are made
+    load(i0);
     load_ids(i0 + step);
-    query_codes<D, T>(a, b, h, qc);
     meanwhile();
-    __syncthreads();
     // the heads of this lane's two result columns
     const float s0 = qc.scale[2 * t], s1 = qc.scale[2 * t + 1], o0 = qc.offset[2 * t], o1 = qc.offset[2 * t + 1];
     const bool h0 = 2 * t < a.g, h1 = 2 * t + 1 < a.g;
@@ -157,7 +168,7 @@ __device__ void score_pages(const SelectArgs& a, int b, int h, const Window& w, 
         }
         const bool was[2] = {real[0], real[1]};
         if (i0 + step < cand) {
-            load();
+            load(i0 + step);
             load_ids(i0 + 2 * step);
         }
 #pragma unroll
@@ -186,7 +197,7 @@ __device__ void score_pages(const SelectArgs& a, int b, int h, const Window& w, 
 struct SelectShared {
     int hist[kBins];                                     // zero before the first pass
     uint32_t range[2];                                   // least and largest key
-    int warp_sum[32], warp_ties[32];
+    int warp_sum[32];
     int bin, left, count, few;
     uint32_t few_keys[32];
 };
@@ -282,12 +293,23 @@ __global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int s
     cluster.sync();                                      // the first CTA runs: its shared memory may be written
     grid_wait();
     grid_release();
+    // What does not depend on the length is asked for with it: the query, and the page ids of the first tile
+    // (behind the sink, wherever the sequence ends).
+    const int tile = rank + ranks * warp, first_page = (a.sink + kPage - 1) / kPage;
+    const int32_t* table = a.tables + (int64_t)b * a.stride + first_page;
+    int id[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int i = 16 * tile + (lane >> 2) + 8 * r;
+        id[r] = first_page + i < a.stride ? table[i] : 0;
+    }
+    QueryRow<D> query = {};
+    if (warp < 8) query = fetch_query<D>(a, b, h, warp);
     const int len = checked_len(a.seq_len[b], a.max_len, a.debug && tid == 0 && rank == 0, a.dbg);
     const Window w = window_of(a, len);
     const int cand = max(w.first - w.sink, 0), take = min(a.top, cand);
     const bool choose = take > 0 && take < cand;
-    uint32_t* keys = cand <= smem_keys ? cluster.map_shared_rank(key_store, 0)
-                                       : a.keys + (int64_t)unit * a.max_pages;
+    uint32_t* keys = cand <= smem_keys ? cluster.map_shared_rank(key_store, 0) : a.keys + (int64_t)unit * a.max_pages;
     const int recent = w.pages - max(w.first, w.sink), total = w.sink + take + recent;
     int32_t* list = a.chosen + (int64_t)unit * a.cap;
     auto write_frame = [&]() {                           // everything but the selected pages
@@ -298,8 +320,12 @@ __global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int s
         if (tid == 0) a.n_chosen[unit] = total;
     };
     if (choose)
-        score_pages<D, T>(a, b, h, w, keys, cluster.map_shared_rank(s.range, 0), rank + ranks * warp, ranks * (T / 32),
-                          codes, write_frame);
+        score_pages<D, T>(a, h, table, cand, keys, cluster.map_shared_rank(s.range, 0), tile, ranks * (T / 32), id, codes,
+                          [&]() {
+                              if (warp < 8) query_codes<D>(query, warp, codes);
+                              write_frame();
+                              __syncthreads();
+                          });
     else
         write_frame();
     cluster.sync();
@@ -314,34 +340,45 @@ __global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int s
     uint32_t base, mask;
     int left;
     find_threshold<T>(keys, cand, take, s, base, mask, left);
-    // Each warp lists its share of the candidates behind those of the warps before it.
-    const int share = (cand + T - 1) / T * 32;
-    const int i0 = min(cand, warp * share), i1 = min(cand, i0 + share);
-    int above = 0, ties = 0;
+    // The list, 1,024 candidates a warp and round: lane j keeps the masks of the warp's j-th 32 of them, so the
+    // keys are read once; a lane lists its own bits behind those of the lanes and warps before it.
+    constexpr int kWarps = T / 32;
+    int at = 0, tied = 0;                                // listed, and ties seen, in the rounds so far
+    for (int i0 = 0; i0 < cand; i0 += kWarps * 1024) {
+        const int share = (min(cand - i0, kWarps * 1024) + T - 1) / T * 32;
+        const int from = i0 + warp * share, to = min(cand, from + share);
+        uint32_t above_mask = 0, tie_mask = 0;
 #pragma unroll 4
-    for (int i = i0 + lane; i < i1; i += 32) {
-        const uint32_t k = keys[i];
-        above += k > base && k - base > mask;
-        ties += k - base <= mask;
-    }
-    above = __reduce_add_sync(~0u, above);
-    ties = __reduce_add_sync(~0u, ties);
-    if (lane == 0) { s.warp_sum[warp] = above; s.warp_ties[warp] = ties; }
-    __syncthreads();
-    int at = __reduce_add_sync(~0u, lane < warp ? s.warp_sum[lane] : 0);
-    int tied = __reduce_add_sync(~0u, lane < warp ? s.warp_ties[lane] : 0);
-    at += min(tied, left);
-#pragma unroll 4
-    for (int i = i0; i < i1; i += 32) {
-        const uint32_t k = i + lane < i1 ? keys[i + lane] : 0u;
-        const bool in_range = i + lane < i1;
-        const bool tie = in_range && k - base <= mask;
-        const uint32_t before = (1u << lane) - 1, tie_mask = __ballot_sync(~0u, tie);
-        const bool in = in_range && (tie ? tied + __popc(tie_mask & before) < left : k > base);
-        const uint32_t in_mask = __ballot_sync(~0u, in);
-        if (in) list[at + __popc(in_mask & before)] = w.sink + i + lane;
-        at += __popc(in_mask);
-        tied += __popc(tie_mask);
+        for (int i = from; i < to; i += 32) {
+            const uint32_t k = keys[min(i + lane, cand - 1)];
+            const bool inside = i + lane < to, tie = k - base <= mask;
+            const uint32_t above = __ballot_sync(~0u, inside && !tie && k > base), ties = __ballot_sync(~0u, inside && tie);
+            if (lane == (i - from) / 32) { above_mask = above; tie_mask = ties; }
+        }
+        // sums over the lanes: ties and keys above, packed (each at most 1,024)
+        const int own = __popc(above_mask) | __popc(tie_mask) << 16;
+        int sum = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += y;
+        }
+        if (lane == 31) s.warp_sum[warp] = sum;
+        __syncthreads();
+        const int w_above = lane < kWarps ? s.warp_sum[lane] & 0xffff : 0, w_ties = lane < kWarps ? s.warp_sum[lane] >> 16 : 0;
+        const int above_before = __reduce_add_sync(~0u, lane < warp ? w_above : 0) + ((sum - own) & 0xffff);
+        int ties_before = tied + __reduce_add_sync(~0u, lane < warp ? w_ties : 0) + ((sum - own) >> 16);
+        int out = at + above_before + min(ties_before, left) - min(tied, left);
+        for (uint32_t bits = above_mask | tie_mask; bits; bits &= bits - 1) {
+            const int bit = __ffs(bits) - 1;
+            const bool tie = tie_mask >> bit & 1;
+            if (tie && ties_before++ >= left) continue;
+            list[out++] = w.sink + from + 32 * lane + bit;
+        }
+        const int all_ties = tied + __reduce_add_sync(~0u, w_ties);
+        at += __reduce_add_sync(~0u, w_above) + min(all_ties, left) - min(tied, left);
+        tied = all_ties;
+        __syncthreads();                                 // warp_sum has been read
     }
 }
 

@@ -75,12 +75,19 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas(D)) attend_kern
     const int unit = blockIdx.x / a.splits, h = unit % a.h_kv, b = unit / a.h_kv;
     grid_wait();
     grid_release();
-    const int len = checked_len(a.seq_len[b], a.max_len, a.debug && split == 0 && threadIdx.x == 0, a.dbg);
-    const int listed = SPARSE ? a.n_chosen[unit] : (len + kPage - 1) / kPage;
-    const int first = split * a.pages_per_split, last = min(listed, first + a.pages_per_split);
-    if (first >= last && !(a.splits == 1)) return;       // the merge skips empty splits by the same rule
     const int32_t* table = a.tables + (int64_t)b * a.stride;
     const int32_t* list = SPARSE ? a.chosen + (int64_t)unit * a.cap : nullptr;
+    // This warp's pages are first + warp, + kAttendWarps, ...; lane l holds the id and the valid tokens of the
+    // l-th of every 32 of them, so that a page's address waits for no load. The first 32 logical pages are asked
+    // for together with the length.
+    const int first = split * a.pages_per_split;
+    int lane_logical = first + warp + kAttendWarps * lane;
+    if (SPARSE) lane_logical = lane_logical < a.cap ? list[lane_logical] : -1;
+    int lane_id = lane_logical >= 0 && lane_logical < a.stride ? table[lane_logical] : -1;
+    const int len = checked_len(a.seq_len[b], a.max_len, a.debug && split == 0 && threadIdx.x == 0, a.dbg);
+    const int listed = SPARSE ? a.n_chosen[unit] : (len + kPage - 1) / kPage;
+    const int last = min(listed, first + a.pages_per_split);
+    if (first >= last && !(a.splits == 1)) return;       // the merge skips empty splits by the same rule
 
     // Q as the A operand: rows gid (heads), the upper eight rows are empty.
     uint4 q[D / 32];
@@ -92,23 +99,21 @@ __global__ void __launch_bounds__(kAttendWarps * 32, attend_ctas(D)) attend_kern
     float m = kNoLogit, l = 0.0f;        // head gid (l: this lane's tokens)
     float acc[kTiles][4] = {};           // channels of gid, heads 2t and 2t + 1
 
-    // This warp's pages are first + warp, + kAttendWarps, ...; lane l holds the id and the valid tokens of the
-    // l-th of every 32 of them, so that a page's address waits for no load.
     const int mine = (last - first - warp + kAttendWarps - 1) / kAttendWarps;
-    int lane_id = 0, lane_valid = 0;
+    int lane_valid = 0;
     for (int n = 0; n < mine; ++n) {
         if ((n & 31) == 0) {
-            lane_id = lane_valid = 0;
             const int i = first + warp + kAttendWarps * (n + lane);
-            if (i < last) {
-                const int logical = SPARSE ? list[i] : i, id = table[logical];
-                if (id >= 0 && id < a.pages) {
-                    lane_id = id;
-                    lane_valid = min(kPage, len - logical * kPage);
-                } else if (a.debug) {
-                    record_error(&a.dbg->kind, &a.dbg->index, 2, id);
-                }
+            if (n > 0 && i < last) {
+                lane_logical = SPARSE ? list[i] : i;
+                lane_id = table[lane_logical];
             }
+            lane_valid = 0;
+            if (i < last) {
+                if (lane_id >= 0 && lane_id < a.pages) lane_valid = min(kPage, len - lane_logical * kPage);
+                else if (a.debug) record_error(&a.dbg->kind, &a.dbg->index, 2, lane_id);
+            }
+            if (lane_valid <= 0) lane_id = lane_valid = 0;
         }
         const uint16_t* page = a.pool + ((int64_t)__shfl_sync(~0u, lane_id, n & 31) * a.h_kv + h) * (2 * kPage * D);
         const int valid = __shfl_sync(~0u, lane_valid, n & 31);
@@ -234,7 +239,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
         const float2* ml = a.split_ml + row * a.splits;
         const float4* acc = reinterpret_cast<const float4*>(a.split_acc + row * a.splits * D) + lane % kLanes;
         float m = kNoLogit;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, ml[i].x);
+        for (int i = lane; i < a.splits; i += 32) {      // a split that is not there holds anything
+            const float x = ml[i].x;
+            if (i < n) m = fmaxf(m, x);
+        }
 #pragma unroll
         for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, s));
 #pragma unroll 4
