@@ -70,7 +70,7 @@ oscar::AttendArgs attend_args(oscar_ctx_t* ctx, const oscar::AttendPlan& plan, c
     a.split_acc = static_cast<float*>(workspace);
     a.split_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.ws_acc);
     a.h_kv = ctx->shape.h_kv; a.g = ctx->shape.h_q / ctx->shape.h_kv;
-    a.splits = plan.splits; a.pages_per_split = plan.pages_per_split; a.batch = batch;
+    a.splits = plan.splits; a.pages_per_split = plan.pages_per_split; a.cluster = plan.cluster; a.batch = batch;
     a.scale_log2 = (float)(ctx->shape.sm_scale * 1.4426950408889634073599);
     a.debug = ctx->shape.debug; a.dbg = ctx->dbg;
     return a;

@@ -40,7 +40,8 @@ cudaError_t launch_append(const AppendArgs& a, int d, int num_sms, cudaStream_t 
 // ---- attention of one new token (paged_attend.cu)
 struct AttendPlan {
     int pages_per_split;
-    int splits;
+    int splits;                  // CTAs of one (sequence, KV head)
+    bool cluster;                // they are a cluster and join their parts without a second kernel
     size_t ws_acc;               // bytes of the splits' accumulators
     size_t ws_total;             // and of their references and sums
 };
@@ -53,7 +54,7 @@ struct AttendArgs {
     void* out; int out_bf16;
     float* split_acc;                        // [batch][H_q][splits][d]
     float2* split_ml;                        // [batch][H_q][splits] reference and sum of weights
-    int h_kv, g, splits, pages_per_split, batch;
+    int h_kv, g, splits, pages_per_split, cluster, batch;
     float scale_log2;                        // sm_scale * log2(e)
     int debug; DebugWord* dbg;
 };
