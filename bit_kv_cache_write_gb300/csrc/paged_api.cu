@@ -133,7 +133,7 @@ oscar_status oscar_append_bf16(oscar_ctx_t* ctx, const void* k, int64_t k_stride
 
 size_t oscar_decode_bf16_workspace_size(const oscar_ctx_t* ctx, int batch, int max_len) {
     if (!sizes_ok(ctx, batch, max_len)) return 0;
-    return oscar::plan_attend(ctx->shape, ctx->num_sms, batch, pages_of(max_len)).ws_total;
+    return oscar::plan_attend(ctx->shape, ctx->num_sms, batch, pages_of(max_len), false).ws_total;
 }
 
 oscar_status oscar_decode_bf16(oscar_ctx_t* ctx, const void* q, int64_t q_stride, const void* bf16_pool,
@@ -144,7 +144,7 @@ oscar_status oscar_decode_bf16(oscar_ctx_t* ctx, const void* q, int64_t q_stride
     oscar_status st = check_decode(ctx, q, q_stride, bf16_pool, bf16_pool_pages, tables, table_stride, seq_len, max_len,
                                    out, out_type, batch);
     if (st != OSCAR_OK || batch == 0) return st;
-    const oscar::AttendPlan plan = oscar::plan_attend(ctx->shape, ctx->num_sms, batch, pages_of(max_len));
+    const oscar::AttendPlan plan = oscar::plan_attend(ctx->shape, ctx->num_sms, batch, pages_of(max_len), false);
     st = check_workspace(workspace, workspace_bytes, plan.ws_total);
     if (st != OSCAR_OK) return st;
     const oscar::AttendArgs a = attend_args(ctx, plan, q, q_stride, bf16_pool, bf16_pool_pages, tables, table_stride,
@@ -160,7 +160,7 @@ int oscar_sparse_capacity(const oscar_ctx_t* ctx, int top_pages) {
 
 size_t oscar_decode_bf16_sparse_workspace_size(const oscar_ctx_t* ctx, int batch, int max_len, int top_pages) {
     if (!sizes_ok(ctx, batch, max_len) || top_pages < 0 || top_pages > oscar::kMaxTopPages) return 0;
-    return oscar::plan_attend(ctx->shape, ctx->num_sms, batch, sparse_pages(ctx, max_len, top_pages)).ws_total +
+    return oscar::plan_attend(ctx->shape, ctx->num_sms, batch, sparse_pages(ctx, max_len, top_pages), true).ws_total +
            oscar::select_workspace_bytes(ctx->shape, batch, pages_of(max_len));
 }
 
@@ -183,7 +183,7 @@ oscar_status oscar_decode_bf16_sparse(oscar_ctx_t* ctx, const void* q, int64_t q
         return record_failure(OSCAR_ERR_INVALID_ARG, "key_bounds must be 16-byte aligned");
     const int max_pages = pages_of(max_len);
     const oscar::AttendPlan plan =
-        oscar::plan_attend(ctx->shape, ctx->num_sms, batch, sparse_pages(ctx, max_len, top_pages));
+        oscar::plan_attend(ctx->shape, ctx->num_sms, batch, sparse_pages(ctx, max_len, top_pages), true);
     const size_t scores = oscar::select_workspace_bytes(ctx->shape, batch, max_pages);
     st = check_workspace(workspace, workspace_bytes, scores + plan.ws_total);
     if (st != OSCAR_OK) return st;

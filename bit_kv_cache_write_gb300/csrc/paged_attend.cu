@@ -22,14 +22,16 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kAttendWarps = 4;
+// Warps that share a split: four for the long splits of a dense decode, two for the short ones of a sparse one
+// (batch 64 at 32k, 148 pages a head: 154 us against 161 with four and 157 with one).
+constexpr int attend_warps(bool sparse) { return sparse ? 2 : 4; }
 constexpr int kClusterWarps = 8;         // of a split that a cluster joins
 constexpr int kMaxCluster = 16;
 constexpr int kJoinThreads = 256;
 constexpr int kMaxSplitPages = 256;      // pages of a split at most
 constexpr int kSplitCost = 6;            // pages' time that a split costs apart from its pages
 // Resident CTAs an SM, by registers (168 and 128 a thread).
-constexpr int attend_ctas(int d) { return d == 128 ? 3 : 4; }
+constexpr int attend_ctas(int d, int warps) { return (d == 128 ? 12 : 16) / warps; }
 constexpr float kNoLogit = -1e30f;       // running reference before any token
 constexpr float kHeadroom = 8.0f;        // the reference is raised when a logit passes it by this much (log2)
 
@@ -80,7 +82,7 @@ __device__ __forceinline__ void load_v(Page<D>& p, const uint16_t* page, int gid
 
 // W warps share a split. CLUSTER: the splits of a (sequence, KV head) are a cluster that joins them itself.
 template <int D, bool SPARSE, int W, bool CLUSTER>
-__global__ void __launch_bounds__(W * 32, CLUSTER ? 1 : attend_ctas(D)) attend_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(W * 32, CLUSTER ? 1 : attend_ctas(D, W)) attend_kernel(AttendArgs a) {
     constexpr int kTiles = D / 16;       // m-tiles of the output product
     __shared__ float warp_m[W][8], warp_l[W][8];
     __shared__ float warp_acc[W][8][D];
@@ -333,8 +335,9 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
         return launch_dependent(attend_kernel<D, SPARSE, kClusterWarps, true>, dim3((unsigned)ctas),
                                 dim3(kClusterWarps * 32), 0, st, a.splits, a);
     }
-    cudaError_t e = launch_dependent(attend_kernel<D, SPARSE, kAttendWarps, false>, dim3((unsigned)ctas),
-                                     dim3(kAttendWarps * 32), 0, st, 1, a);
+    constexpr int kWarps = attend_warps(SPARSE);
+    cudaError_t e = launch_dependent(attend_kernel<D, SPARSE, kWarps, false>, dim3((unsigned)ctas), dim3(kWarps * 32), 0,
+                                     st, 1, a);
     if (e != cudaSuccess || a.splits == 1) return e;
     // a CTA per head where there are many splits, a warp per head otherwise
     const long long rows = (long long)a.batch * a.h_kv * a.g;
@@ -347,7 +350,7 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages) {
+AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages, bool sparse) {
     AttendPlan p{};
     const long long units = (long long)batch * s.h_kv;
     // Small work, a page a warp: one cluster for each (sequence, KV head) and one launch. 84 pages, two KV heads:
@@ -361,8 +364,9 @@ AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages) {
         p.pages_per_split = (max_pages + ranks - 1) / ranks;
         return p;
     }
-    const long long slots = (long long)attend_ctas(s.d) * num_sms;     // resident CTAs
-    const long long most = (max_pages + kAttendWarps - 1) / kAttendWarps;
+    const int warps = attend_warps(sparse);
+    const long long slots = (long long)attend_ctas(s.d, warps) * num_sms;     // resident CTAs
+    const long long most = (max_pages + warps - 1) / warps;
     // Splits that fill w waves of CTAs, for the w whose waves take least: a CTA's pages and about kSplitCost pages'
     // time to start and join. No split is longer than kMaxSplitPages, so that sequences of several lengths share out.
     long long best = 0, splits = 1;

@@ -59,7 +59,7 @@ struct AttendArgs {
     int debug; DebugWord* dbg;
 };
 // max_pages: pages that one (sequence, KV head) reads at most.
-AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages);
+AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages, bool sparse);
 cudaError_t launch_attend(const AttendArgs& a, int d, cudaStream_t st);
 
 // ---- page selection of the sparse decode (page_select.cu)
