@@ -115,3 +115,14 @@ def calibrate_layer_gpu(q_cal, k_cal, v_cal, sm_scale, clip_ratio=0.9, device="c
         t_k[h] = clip_ratio * np.abs(kh_all[:, h] @ rk).max(axis=0)
         t_v[h] = clip_ratio * np.abs(vh_all[:, h] @ rv).max(axis=0)
     return r_k, r_v, t_k, t_v
+
+
+def key_steps(k_cal, margin=1.25):
+    """Steps of the BF16 cache's key bounds (``oscar_append_bf16``) from calibration keys [m, H_kv, d].
+
+    Per KV head and channel the least power of two 2^step at which ``margin`` times the largest calibration
+    magnitude is within the codes' +-127; int8 [H_kv, d], -100 where a channel is always zero."""
+    top = np.abs(np.asarray(k_cal, np.float64)).max(axis=0) * margin / 127.0
+    with np.errstate(divide="ignore"):
+        steps = np.ceil(np.log2(top))
+    return np.clip(steps, -100, 100).astype(np.int8)

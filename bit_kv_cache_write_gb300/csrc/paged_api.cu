@@ -64,7 +64,7 @@ oscar::AttendArgs attend_args(oscar_ctx_t* ctx, const oscar::AttendPlan& plan, c
     oscar::AttendArgs a{};
     a.q = static_cast<const uint16_t*>(q); a.q_stride = q_stride;
     a.pool = static_cast<const uint16_t*>(pool); a.pages = pages;
-    a.tables = tables; a.stride = stride;
+    a.tables = tables; a.stride = max_len > 0 ? stride : 0;      // page ids are looked up ahead of the lengths
     a.seq_len = seq_len; a.max_len = max_len;
     a.out = out; a.out_bf16 = out_type == OSCAR_OUT_BF16;
     a.split_acc = static_cast<float*>(workspace);
@@ -188,12 +188,15 @@ oscar_status oscar_decode_bf16_sparse(oscar_ctx_t* ctx, const void* q, int64_t q
     st = check_workspace(workspace, workspace_bytes, scores + plan.ws_total);
     if (st != OSCAR_OK) return st;
 
+    oscar::AttendArgs a = attend_args(ctx, plan, q, q_stride, bf16_pool, bf16_pool_pages, tables, table_stride,
+                                      seq_len, max_len, out, out_type, static_cast<char*>(workspace) + scores, batch);
+    a.chosen = chosen; a.n_chosen = n_chosen; a.cap = oscar::sparse_capacity(ctx->shape, top_pages);
     oscar::SelectArgs s{};
     s.q = static_cast<const uint16_t*>(q); s.q_stride = q_stride;
     s.steps = key_steps; s.bounds = key_bounds; s.pages = bf16_pool_pages;
-    s.tables = tables; s.stride = table_stride;
+    s.tables = tables; s.stride = a.stride;
     s.seq_len = seq_len; s.max_len = max_len;
-    s.chosen = chosen; s.n_chosen = n_chosen; s.cap = oscar::sparse_capacity(ctx->shape, top_pages);
+    s.chosen = chosen; s.n_chosen = n_chosen; s.cap = a.cap;
     s.keys = static_cast<uint32_t*>(workspace);
     s.max_pages = max_pages; s.top = top_pages; s.sink = ctx->shape.sink; s.recent = ctx->shape.recent;
     s.h_kv = ctx->shape.h_kv; s.g = ctx->shape.h_q / ctx->shape.h_kv; s.batch = batch;
@@ -203,9 +206,6 @@ oscar_status oscar_decode_bf16_sparse(oscar_ctx_t* ctx, const void* q, int64_t q
         st = cuda_status(oscar::launch_select(s, ctx->shape.d, ctx->num_sms, static_cast<cudaStream_t>(stream)), "page selection launch");
         if (st != OSCAR_OK) return st;
     }
-    oscar::AttendArgs a = attend_args(ctx, plan, q, q_stride, bf16_pool, bf16_pool_pages, tables, table_stride,
-                                      seq_len, max_len, out, out_type, static_cast<char*>(workspace) + scores, batch);
-    a.chosen = chosen; a.n_chosen = n_chosen; a.cap = s.cap;
     oscar::ProfScope ps(&ctx->prof, OSCAR_KERNEL_ATTEND, static_cast<cudaStream_t>(stream));
     return cuda_status(oscar::launch_attend(a, ctx->shape.d, static_cast<cudaStream_t>(stream)),
                        "sparse BF16 decode launch");

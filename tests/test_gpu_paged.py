@@ -232,6 +232,29 @@ def test_append_of_a_long_prefill(cuda):
     assert np.array_equal(gp.cpu().double().numpy(), pool) and np.array_equal(gb.cpu().numpy(), bounds)
 
 
+@pytest.mark.parametrize("h_kv,d", [(8, 128), (3, 64)])
+@pytest.mark.parametrize("with_bounds", [False, True])
+def test_append_of_many_ragged_runs(cuda, h_kv, d, with_bounds):
+    """Enough tokens that a warp takes sixteen: runs of every length, in and across the warps' shares, with padding."""
+    r = np.random.default_rng(d)
+    pages, runs = 2600, []
+    for p in r.permutation(pages)[:2500]:
+        lo = int(r.integers(0, 16)) if r.random() < 0.5 else 0
+        runs.append((int(p), lo, int(r.integers(lo + 1, 17))))
+        if r.random() < 0.2:
+            runs.append((-1, 0, int(r.integers(1, 4))))
+    slots = slots_of(runs)
+    assert len(slots) > 64 * 152
+    k, v, steps, _, bounds = append_case(3, h_kv, d, slots, pages)
+    pool = np.zeros((pages, h_kv, 2, P, d))
+    gp, gb = dev(pool, cuda, BF), dev(bounds.astype(np.int8), cuda)
+    context(h_kv, h_kv, d).append_bf16(dev(k, cuda, BF), dev(v, cuda, BF), dev(slots, cuda), gp,
+                                       *((dev(steps, cuda), gb) if with_bounds else ()))
+    torch.cuda.synchronize()
+    paged.append(pool, bounds if with_bounds else None, k, v, slots, steps)
+    assert np.array_equal(gp.cpu().double().numpy(), pool) and np.array_equal(gb.cpu().numpy(), bounds)
+
+
 # ---------------------------------------------------------------------------------------------- decoding
 
 class Cache:
@@ -473,6 +496,46 @@ def test_sparse_ties_and_odd_values(cuda, kind):
             close(got, want, c.tolerance(want, None, 0.125))
 
 
+@pytest.mark.parametrize("h_kv,d", [(3, 64), (4, 128)])
+def test_many_short_sequences(cuda, h_kv, d):
+    """More (sequence, KV head) units than the card has room for at once."""
+    r = np.random.default_rng(9)
+    lens = r.integers(0, 900, 160)
+    lens[[0, 5]] = 0, 1500
+    c = Cache(17, lens, h_kv * 2, h_kv, d)
+    ctx = context(h_kv * 2, h_kv, d)
+    want = paged.decode(c.q, c.pool, c.tables, c.lens, d ** -0.5)
+    close(run_dense(ctx, c, cuda, torch.float32), want, c.tolerance(want, None, d ** -0.5))
+    want, lists = paged.decode_sparse(c.q, c.pool, c.bounds, c.steps, c.tables, c.lens, 11, 64, 256, d ** -0.5)
+    got, chosen = run_sparse(ctx, c, cuda, torch.float32, 11)
+    assert chosen == lists
+    close(got, want, c.tolerance(want, None, d ** -0.5))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_one_apart_are_told_apart(cuda, d, sign):
+    """Scores near the largest magnitude that differ by one unit: the product over the bounds is exact."""
+    c = Cache(18, [16 * 220], 2, 1, d)
+    r = np.random.default_rng(d)
+    codes = sign * np.where(np.arange(d) < d - 2, 127, 1)                    # the query's codes, e = 0
+    c.q[0, :] = bf16(codes[None] * 2.0 ** -5)                                # steps of 2^-5 below undo the scale
+    c.steps[:] = 5
+    c.bounds[:] = 127 if sign > 0 else -128
+    rank = r.permutation(220)                                                # two channels of weight one: 0 .. 219
+    low = np.minimum(rank, 120)
+    for p in range(220):
+        c.bounds[c.tables[0, p], 0, :, d - 2] = low[p] - (0 if sign > 0 else 120)
+        c.bounds[c.tables[0, p], 0, :, d - 1] = rank[p] - low[p] - (0 if sign > 0 else 120)
+    for top in (1, 17, 100):
+        want = paged.select(c.q[0], c.steps[0], c.bounds[:, 0], c.tables[0], 16 * 220, top, 64, 256)
+        _, chosen = run_sparse(context(2, 1, d), c, cuda, torch.float32, top)
+        assert chosen[0][0] == want
+        middle = [p for p in range(4, 204)]
+        best = sorted(middle, key=lambda p: -sign * rank[p])[:top]
+        assert want == sorted(set(range(4)) | set(range(204, 220)) | set(best))
+
+
 def test_results_do_not_change_from_run_to_run(cuda):
     c = Cache(14, [3000, 1, 700, 2222], 8, 2, 128)
     ctx = context(8, 2, 128)
@@ -576,6 +639,21 @@ def test_injected_launch_failure(cuda, monkeypatch):
     with pytest.raises(O.OscarError) as e:
         ctx.append_bf16(k, k, slots, pool)
     assert e.value.status == -4 and float(pool.float().min()) == 1.0
+
+
+def test_no_room_for_tokens(cuda):
+    """max_len 0, no tables: zeros, and lists of nothing."""
+    ctx = context(4, 2, 64)
+    q, pool = torch.ones(3, 4, 64, dtype=BF, device=cuda), torch.ones(1, 2, 2, P, 64, dtype=BF, device=cuda)
+    t, n = torch.zeros(3, 0, dtype=I32, device=cuda), torch.zeros(3, dtype=I32, device=cuda)
+    out = torch.ones(3, 4, 64, device=cuda)
+    ctx.decode_bf16(q, pool, t, n, 0, out, None)
+    assert float(out.abs().max()) == 0
+    out.fill_(1)
+    chosen, count = torch.zeros(3, 2, ctx.sparse_capacity(2), dtype=I32, device=cuda), torch.ones(3, 2, dtype=I32, device=cuda)
+    ctx.decode_bf16_sparse(q, pool, torch.zeros(2, 64, dtype=I8, device=cuda), torch.zeros(1, 2, 2, 64, dtype=I8, device=cuda),
+                           t, n, 0, 2, chosen, count, out, None)
+    assert float(out.abs().max()) == 0 and int(chosen.max()) == -1 and int(count.max()) == 0
 
 
 def test_empty_calls_do_nothing(cuda):

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+from bit_kv_cache_write_gb300 import calibration
 from bit_kv_cache_write_gb300 import oscar as O
 from oracle import paged
 
@@ -40,6 +41,18 @@ def test_query_codes_cover_the_range():
     codes, e = paged.query_codes([0.999999, 0.0], [0, 0])
     assert e == -7 and codes.tolist() == [127, 0]
     assert paged.query_codes([0.0, 2.0 ** -70], [0, 0])[0].tolist() == [0, 0]
+
+
+def test_key_steps_are_the_least_that_cover_the_calibration():
+    k = np.random.default_rng(3).standard_normal((50, 2, 64)) * np.exp2(np.arange(64) - 40.0)
+    k[:, 1, 5] = 0
+    steps = calibration.key_steps(k)
+    assert steps.dtype == np.int8 and steps[1, 5] == -100
+    top = 1.25 * np.abs(k).max(0)
+    live = top > 0
+    assert (top[live] <= 127 * np.exp2(steps[live].astype(float))).all()
+    assert (top[live] > 127 * np.exp2(steps[live] - 1.0)).all()
+    assert np.abs(paged.key_codes(k, steps)).max() < 127                     # the margin: nothing saturates
 
 
 def test_score_bounds_the_logits():
