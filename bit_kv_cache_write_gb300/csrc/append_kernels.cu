@@ -42,8 +42,27 @@ __device__ __forceinline__ float inv_pow2(int step) {
     return __int_as_float((127 - max(-100, min(100, step))) << 23);
 }
 
+// Widens a page's bounds of eight channels (old_lo and old_hi; none where the run begins the page) by a run's
+// least and largest keys and writes them.
+template <int D>
+__device__ __forceinline__ void write_bounds(int8_t* b, uint2 steps, const uint32_t (&lo)[4], const uint32_t (&hi)[4],
+                                             uint2 old_lo, uint2 old_hi) {
+    uint32_t word[2][2] = {};
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const int at = 8 * (c & 3), half = 16 * (c & 1);
+        const float inv = inv_pow2((int8_t)((c < 4 ? steps.x : steps.y) >> at));
+        const int l = min(code_of(lo[c / 2] >> half & 0xffffu, inv), (int)(int8_t)((c < 4 ? old_lo.x : old_lo.y) >> at));
+        const int u = max(code_of(hi[c / 2] >> half & 0xffffu, inv), (int)(int8_t)((c < 4 ? old_hi.x : old_hi.y) >> at));
+        word[0][c / 4] |= (uint32_t)(l & 0xff) << at;
+        word[1][c / 4] |= (uint32_t)(u & 0xff) << at;
+    }
+    *reinterpret_cast<uint2*>(b) = make_uint2(word[0][0], word[0][1]);
+    *reinterpret_cast<uint2*>(b + D) = make_uint2(word[1][0], word[1][1]);
+}
+
 template <int D, bool BOUNDS>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, int tokens) {
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(AppendArgs a, int tokens) {
     constexpr int kHalf = D / 8;                     // lanes that move one row of K (or V)
     constexpr int kHeads = 32 / (2 * kHalf);         // KV heads of a warp
     constexpr int kRows = 4;                         // rows in flight per lane (131,072 tokens: 165 us; with 8 189, with 16 253)
@@ -93,7 +112,44 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, in
         }
         return;
     }
-    for (uint32_t todo = starts & own; todo; todo &= todo - 1) {
+    const bool keeps = part == 0 && active;
+    const uint2 steps = keeps ? *reinterpret_cast<const uint2*>(a.steps + h * D + c0) : make_uint2(0, 0);
+    const uint2 none_lo = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu), none_hi = make_uint2(0x81818181u, 0x81818181u);
+    const uint32_t ends = live & ~((live & ~starts) >> 1);                    // tokens that end a run
+    uint32_t todo = starts & own;
+    if ((todo & ends) == (live & own)) {             // each token a run (a decode step): two at a time
+        while (todo) {
+            int8_t* b[2];
+            uint4 x[2];
+            uint2 old_lo[2], old_hi[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int l = todo ? __ffs(todo) - 1 : 0;
+                const int p = __shfl_sync(~0u, page, l), r = __shfl_sync(~0u, row, l);
+                b[k] = nullptr;
+                if (todo && active) {
+                    x[k] = ldg_stream(src + l * stride);
+                    b[k] = a.bounds + ((int64_t)p * a.h_kv + h) * 2 * D + c0;
+                    old_lo[k] = none_lo;
+                    old_hi[k] = none_hi;
+                    if (keeps && r) {
+                        old_lo[k] = *reinterpret_cast<const uint2*>(b[k]);
+                        old_hi[k] = *reinterpret_cast<const uint2*>(b[k] + D);
+                    }
+                    *reinterpret_cast<uint4*>(dst + (int64_t)p * a.h_kv * 2 * kPage * D + r * D) = x[k];
+                }
+                todo &= todo - 1;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (b[k] && keeps) {
+                    const uint32_t z[4] = {bf2_no_nan(x[k].x), bf2_no_nan(x[k].y), bf2_no_nan(x[k].z), bf2_no_nan(x[k].w)};
+                    write_bounds<D>(b[k], steps, z, z, old_lo[k], old_hi[k]);
+                }
+        }
+        return;
+    }
+    for (; todo; todo &= todo - 1) {
         const int first = __ffs(todo) - 1;
         // the run's tokens: up to the next one that begins another run or is not written
         const uint32_t stop = (starts | ~live) & ~((2u << first) - 1);
@@ -101,6 +157,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, in
         const int p = __shfl_sync(~0u, page, first);
         uint16_t* to = dst + (int64_t)p * a.h_kv * 2 * kPage * D;
         const bool fresh = __any_sync(~0u, lane >= first && lane < end && row == 0);
+        int8_t* b = a.bounds + ((int64_t)p * a.h_kv + (active ? h : 0)) * 2 * D + c0;
         uint32_t lo[4], hi[4];
         for (int l0 = first; l0 < end; l0 += kRows) {
             uint4 x[kRows];
@@ -121,26 +178,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, in
                 }
             }
         }
-        if (part == 0 && active) {
-            int8_t* b = a.bounds + ((int64_t)p * a.h_kv + h) * 2 * D + c0;
-            const uint2 steps = *reinterpret_cast<const uint2*>(a.steps + h * D + c0);
-            const uint2 old_lo = fresh ? make_uint2(0, 0) : *reinterpret_cast<const uint2*>(b);
-            const uint2 old_hi = fresh ? make_uint2(0, 0) : *reinterpret_cast<const uint2*>(b + D);
-            uint32_t word[2][2] = {};
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const int at = 8 * (c & 3), half = 16 * (c & 1);
-                const float inv = inv_pow2((int8_t)((c < 4 ? steps.x : steps.y) >> at));
-                int l = code_of(lo[c / 2] >> half & 0xffffu, inv), u = code_of(hi[c / 2] >> half & 0xffffu, inv);
-                if (!fresh) {
-                    l = min(l, (int)(int8_t)((c < 4 ? old_lo.x : old_lo.y) >> at));
-                    u = max(u, (int)(int8_t)((c < 4 ? old_hi.x : old_hi.y) >> at));
-                }
-                word[0][c / 4] |= (uint32_t)(l & 0xff) << at;
-                word[1][c / 4] |= (uint32_t)(u & 0xff) << at;
-            }
-            *reinterpret_cast<uint2*>(b) = make_uint2(word[0][0], word[0][1]);
-            *reinterpret_cast<uint2*>(b + D) = make_uint2(word[1][0], word[1][1]);
+        if (keeps) {
+            const uint2 old_lo = fresh ? none_lo : *reinterpret_cast<const uint2*>(b);
+            const uint2 old_hi = fresh ? none_hi : *reinterpret_cast<const uint2*>(b + D);
+            write_bounds<D>(b, steps, lo, hi, old_lo, old_hi);
         }
     }
 }

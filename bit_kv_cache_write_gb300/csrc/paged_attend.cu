@@ -26,8 +26,7 @@ namespace cg = cooperative_groups;
 // (batch 64 at 32k, 148 pages a head: 154 us against 161 with four and 157 with one).
 constexpr int attend_warps(bool sparse) { return sparse ? 2 : 4; }
 constexpr int kClusterWarps = 8;         // of a split that a cluster joins
-constexpr int kMaxCluster = 16;
-constexpr int kJoinThreads = 256;
+constexpr int kMaxCluster = 8;
 constexpr int kMaxSplitPages = 256;      // pages of a split at most
 constexpr int kSplitCost = 6;            // pages' time that a split costs apart from its pages
 // Resident CTAs an SM, by registers (168 and 128 a thread).
@@ -258,13 +257,13 @@ __global__ void __launch_bounds__(W * 32, CLUSTER ? 1 : attend_ctas(D, W)) atten
 }
 
 // Joins the splits of query heads, W warps to a head: a warp takes every W-th split, 16 bytes a lane.
-template <int D, bool SPARSE, int W>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
+template <int D, bool SPARSE, int W, int THREADS>
+__global__ void __launch_bounds__(THREADS) join_kernel(AttendArgs a) {
     constexpr int kLanes = D / 4;                        // lanes that hold one split's channels
     constexpr int kPer = 32 / kLanes;                    // splits that a warp reads at a time
-    constexpr int kRows = kJoinThreads / 32 / W;
-    __shared__ float4 warp_o[kJoinThreads / 32][kLanes];
-    __shared__ float warp_l[kJoinThreads / 32];
+    constexpr int kRows = THREADS / 32 / W;
+    __shared__ float4 warp_o[THREADS / 32][kLanes];
+    __shared__ float warp_l[THREADS / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
     const int64_t row = (int64_t)blockIdx.x * kRows + warp / W;
     const int hq = a.h_kv * a.g;
@@ -307,7 +306,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
         if (part != 0) return;
         o = make_float4(0, 0, 0, 0);
         l = 0.0f;
-#pragma unroll
+#pragma unroll 8
         for (int w = 0; w < W; ++w) {
             const float4 y = warp_o[warp + w][lane % kLanes];
             l += warp_l[warp + w];
@@ -330,8 +329,6 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
     const long long ctas = (long long)a.splits * a.h_kv * a.batch;
     if (ctas > 0x7fffffffLL || (long long)a.batch * a.h_kv * a.g > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (a.cluster) {
-        const cudaError_t e = allow_large_clusters<attend_kernel<D, SPARSE, kClusterWarps, true>>();
-        if (e != cudaSuccess) return e;
         return launch_dependent(attend_kernel<D, SPARSE, kClusterWarps, true>, dim3((unsigned)ctas),
                                 dim3(kClusterWarps * 32), 0, st, a.splits, a);
     }
@@ -339,13 +336,13 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
     cudaError_t e = launch_dependent(attend_kernel<D, SPARSE, kWarps, false>, dim3((unsigned)ctas), dim3(kWarps * 32), 0,
                                      st, 1, a);
     if (e != cudaSuccess || a.splits == 1) return e;
-    // a CTA per head where there are many splits, a warp per head otherwise
+    // few splits: a warp per head; more: a CTA of 8 warps; hundreds (one long sequence, few heads): of 32
     const long long rows = (long long)a.batch * a.h_kv * a.g;
-    constexpr int kJoinWarps = kJoinThreads / 32;
-    if (a.splits > kJoinWarps)
-        return launch_dependent(join_kernel<D, SPARSE, kJoinWarps>, dim3((unsigned)rows), dim3(kJoinThreads), 0, st, 1, a);
-    return launch_dependent(join_kernel<D, SPARSE, 1>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)),
-                            dim3(kJoinThreads), 0, st, 1, a);
+    if (a.splits > 96)
+        return launch_dependent(join_kernel<D, SPARSE, 32, 1024>, dim3((unsigned)rows), dim3(1024), 0, st, 1, a);
+    if (a.splits > 8)
+        return launch_dependent(join_kernel<D, SPARSE, 8, 256>, dim3((unsigned)rows), dim3(256), 0, st, 1, a);
+    return launch_dependent(join_kernel<D, SPARSE, 1, 256>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, 1, a);
 }
 
 }  // namespace
@@ -353,12 +350,12 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
 AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages, bool sparse) {
     AttendPlan p{};
     const long long units = (long long)batch * s.h_kv;
-    // Small work, a page a warp: one cluster for each (sequence, KV head) and one launch. 84 pages, two KV heads:
-    // 5.0 us on the GPU against 4.7 with the join as a kernel, but 7.0 us of host time against 8.5; 277 pages of a
-    // sparse decode with eight KV heads: 26.6 us against 22.0, its CTAs find no room next to the selection's.
+    // Small work, at most two pages a warp: one cluster for each (sequence, KV head) and one launch. 84 pages, two KV
+    // heads: 5.3 us on the GPU as with the join as a kernel, and 7.0 us of host time against 8.5. Clusters of 16 do
+    // not all find their place at once (128 pages, eight heads: 13 us against 7.4).
     int ranks = 1;
     while (ranks < kMaxCluster && ranks * kClusterWarps < max_pages) ranks *= 2;
-    if (max_pages > 0 && units * ranks <= num_sms && max_pages <= ranks * kClusterWarps) {
+    if (max_pages > attend_warps(sparse) && units * ranks <= num_sms && max_pages <= 2 * ranks * kClusterWarps) {
         p.cluster = true;
         p.splits = ranks;
         p.pages_per_split = (max_pages + ranks - 1) / ranks;

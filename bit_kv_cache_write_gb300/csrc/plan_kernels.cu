@@ -5,7 +5,7 @@
 // pages of the requests before it (an inclusive sum P_b decides whether they are there). Row r_b + i goes to
 // slot page * 16 + (s_b + i) % 16 of logical page (s_b + i) / 16.
 //
-// One cluster. Every CTA scans all requests, kPlanThreads at a time (one pass of two sums; two more only
+// One cluster. Every CTA scans all requests, 2,048 at a time (one pass of two sums; two more only
 // where a request does not fit), and writes its share of the chunk's table entries and slots; a page id is
 // read from the free list, so no CTA reads what another one writes. The free head may be the word that the
 // new head goes to, so the last barrier stands between every CTA's read of it and the write.
@@ -22,7 +22,9 @@ namespace {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanMaxCluster = 16;
-constexpr int kPlanTokens = 4;                       // slots that a thread looks up at once
+constexpr int kPlanPer = 4;                          // requests that a thread adds up
+constexpr int kPlanChunk = kPlanThreads * kPlanPer;
+constexpr int kPlanTokens = 4;                       // slots that a thread writes in a row
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -70,9 +72,9 @@ __device__ __forceinline__ int upper(const long long* v, int n, long long key) {
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     __shared__ long long sums[2][kPlanWarps][2];
-    __shared__ long long row_end[kPlanThreads];      // rows up to and with request i of the chunk
-    __shared__ long long page_end[kPlanThreads];     // its pages likewise
-    __shared__ int cached[kPlanThreads];             // tokens cached; -1: request rejected
+    __shared__ long long row_end[kPlanChunk];        // rows up to and with request i of the chunk
+    __shared__ long long page_end[kPlanChunk];       // its pages likewise
+    __shared__ int cached[kPlanChunk];               // tokens cached; -1: request rejected
     __shared__ int rejected, first_rejected;
     const int tid = threadIdx.x;
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
@@ -82,36 +84,67 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     const long long head = *reinterpret_cast<const volatile int32_t*>(a.free_head);
     const long long avail = head >= 0 && head < a.n_free ? a.n_free - head : 0;
     long long rows = 0, wanted = 0, taken = 0;       // over the chunks so far: rows, pages needed, handed out
-    for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
-        const int b = b0 + tid, count = min(kPlanThreads, a.batch - b0);
-        const int s = b < a.batch ? a.seq_len[b] : 0, n = b < a.batch ? a.new_len[b] : 0;
-        bool ok = s >= 0 && n >= 0 && (long long)s + n <= (long long)kPage * a.stride;
-        const long long need = ok ? ((long long)s + n + kPage - 1) / kPage - (s + kPage - 1) / kPage : 0;
-        const long long own_rows = n > 0 ? n : 0;
-        long long r = own_rows, p = need, total_r, total_p;
+    for (int b0 = 0; b0 < a.batch; b0 += kPlanChunk) {
+        const int count = min(kPlanChunk, a.batch - b0), i0 = tid * kPlanPer;
+        int s[kPlanPer], n[kPlanPer];
+#pragma unroll
+        for (int k = 0; k < kPlanPer; ++k) {
+            const bool inside = i0 + k < count;
+            s[k] = inside ? a.seq_len[b0 + i0 + k] : 0;
+            n[k] = inside ? a.new_len[b0 + i0 + k] : 0;
+        }
+        bool ok[kPlanPer];
+        long long need[kPlanPer], r = 0, p = 0, total_r, total_p;
+#pragma unroll
+        for (int k = 0; k < kPlanPer; ++k) {
+            ok[k] = s[k] >= 0 && n[k] >= 0 && (long long)s[k] + n[k] <= (long long)kPage * a.stride;
+            need[k] = ok[k] ? ((long long)s[k] + n[k] + kPage - 1) / kPage - (s[k] + kPage - 1) / kPage : 0;
+            r += max(n[k], 0);
+            p += need[k];
+        }
+        const long long own_r = r, own_p = p;
         scan2(r, p, total_r, total_p, sums[0]);
-        long long g = p, total_g = total_p;
+        long long before_r = rows + r - own_r, before_g = taken + p - own_p, total_g = total_p;
         if (rows + total_r > a.slot_cap || wanted + total_p > avail) {
             // Some request passes the slot map or the free list. One that passes the map needs no page.
-            long long unused = 0, t;
-            ok = ok && rows + r <= a.slot_cap;
-            const long long still = ok ? need : 0;
-            p = still;
-            scan2(p, unused, total_p, t, sums[1]);
-            ok = ok && (still == 0 || wanted + p <= avail);
-            g = ok ? still : 0;
+            long long end = before_r, unused = 0, t, q = 0;
+#pragma unroll
+            for (int k = 0; k < kPlanPer; ++k) {
+                end += max(n[k], 0);
+                ok[k] = ok[k] && end <= a.slot_cap;
+                if (!ok[k]) need[k] = 0;
+                q += need[k];
+            }
+            const long long own_q = q;
+            scan2(q, unused, total_p, t, sums[1]);
+            long long upto = wanted + q - own_q, g = 0;
+#pragma unroll
+            for (int k = 0; k < kPlanPer; ++k) {
+                upto += need[k];
+                ok[k] = ok[k] && (need[k] == 0 || upto <= avail);
+                if (!ok[k]) need[k] = 0;
+                g += need[k];
+            }
+            const long long own_g = g;
             unused = 0;
             scan2(g, unused, total_g, t, sums[0]);
+            before_g = taken + g - own_g;
         }
-        row_end[tid] = rows + r;
-        page_end[tid] = taken + g;
-        cached[tid] = ok ? s : -1;
-        if (b < a.batch) {
-            if (!ok) { atomicAdd(&rejected, 1); atomicMin(&first_rejected, b); }
-            if (b % ranks == rank) {
-                a.total_len[b] = ok ? s + n : s;
-                a.row_start[b] = (int32_t)min(rows + r - own_rows, (long long)INT_MAX);
+#pragma unroll
+        for (int k = 0; k < kPlanPer; ++k) {
+            const int b = b0 + i0 + k;
+            if (b < a.batch) {
+                if (!ok[k]) { atomicAdd(&rejected, 1); atomicMin(&first_rejected, b); }
+                if (b % ranks == rank) {
+                    a.total_len[b] = ok[k] ? s[k] + n[k] : s[k];
+                    a.row_start[b] = (int32_t)min(before_r, (long long)INT_MAX);
+                }
             }
+            before_r += max(n[k], 0);
+            before_g += need[k];
+            row_end[i0 + k] = before_r;
+            page_end[i0 + k] = before_g;
+            cached[i0 + k] = ok[k] ? s[k] : -1;
         }
         __syncthreads();
         // new table entries
@@ -121,29 +154,33 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
             a.tables[(long long)(b0 + i) * a.stride + (cached[i] + kPage - 1) / kPage + (j - before)] =
                 a.free_pages[head + j];
         }
-        // slots, several at once: each waits for a page id
+        // slots, kPlanTokens in a row a thread: one search, and the page ids asked for together
         const long long end = min(rows + total_r, (long long)a.slot_cap);
-        for (long long t0 = rows + share; t0 < end; t0 += (long long)kPlanTokens * shares) {
-            int id[kPlanTokens], in_page[kPlanTokens];
+        for (long long t0 = rows + (long long)kPlanTokens * share; t0 < end; t0 += (long long)kPlanTokens * shares) {
+            int i = upper(row_end, count, t0);
+            int pos = cached[i] + (int)(t0 - (i ? row_end[i - 1] : rows));
+            const int32_t* from[kPlanTokens];
+            int in_page[kPlanTokens];
 #pragma unroll
-            for (int k = 0; k < kPlanTokens; ++k) {
-                const long long t = t0 + (long long)k * shares;
-                in_page[k] = -1;
-                id[k] = 0;
-                if (t >= end) continue;
-                const int i = upper(row_end, count, t);
+            for (int k = 0; k < kPlanTokens; ++k, ++pos) {
+                from[k] = nullptr;
+                if (t0 + k >= end) continue;
+                if (t0 + k >= row_end[i]) {          // on to the next request that has rows
+                    while (t0 + k >= row_end[i]) ++i;
+                    pos = cached[i];
+                }
                 if (cached[i] < 0) continue;
-                const int pos = cached[i] + (int)(t - (i ? row_end[i - 1] : rows));
                 const int page = pos / kPage, first_new = (cached[i] + kPage - 1) / kPage;
                 in_page[k] = pos % kPage;
-                id[k] = page < first_new ? a.tables[(long long)(b0 + i) * a.stride + page]
-                                         : a.free_pages[head + (i ? page_end[i - 1] : taken) + page - first_new];
+                from[k] = page < first_new ? a.tables + (long long)(b0 + i) * a.stride + page
+                                           : a.free_pages + head + (i ? page_end[i - 1] : taken) + page - first_new;
             }
+            int id[kPlanTokens];
 #pragma unroll
-            for (int k = 0; k < kPlanTokens; ++k) {
-                const long long t = t0 + (long long)k * shares;
-                if (t < end) a.slots[t] = in_page[k] < 0 ? -1 : (int64_t)id[k] * kPage + in_page[k];
-            }
+            for (int k = 0; k < kPlanTokens; ++k) id[k] = from[k] ? *from[k] : 0;
+#pragma unroll
+            for (int k = 0; k < kPlanTokens; ++k)
+                if (t0 + k < end) a.slots[t0 + k] = from[k] ? (int64_t)id[k] * kPage + in_page[k] : -1;
         }
         rows += total_r;
         wanted += total_p;
