@@ -5,7 +5,7 @@
 // pages of the requests before it (an inclusive sum P_b decides whether they are there). Row r_b + i goes to
 // slot page * 16 + (s_b + i) % 16 of logical page (s_b + i) / 16.
 //
-// One cluster. Every CTA scans all requests, 2,048 at a time (one pass of two sums; two more only
+// One cluster. Every CTA scans all requests, 512 or 2,048 at a time (one pass of two sums; two more only
 // where a request does not fit), and writes its share of the chunk's table entries and slots; a page id is
 // read from the free list, so no CTA reads what another one writes. The free head may be the word that the
 // new head goes to, so the last barrier stands between every CTA's read of it and the write.
@@ -22,9 +22,7 @@ namespace {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanMaxCluster = 16;
-constexpr int kPlanPer = 4;                          // requests that a thread adds up
-constexpr int kPlanChunk = kPlanThreads * kPlanPer;
-constexpr int kPlanTokens = 4;                       // slots that a thread writes in a row
+constexpr int kPlanTokens = 4;                       // slots that a thread looks up at once
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -70,7 +68,11 @@ __device__ __forceinline__ int upper(const long long* v, int n, long long key) {
     return lo;
 }
 
+// PER: requests that a thread adds up. BULK: a thread writes several slots in a row (one search), else one of each
+// stride's (a shorter program: 64 single tokens take 3.5 us against 5.3).
+template <int PER, bool BULK>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
+    constexpr int kPlanPer = PER, kPlanChunk = kPlanThreads * PER;
     __shared__ long long sums[2][kPlanWarps][2];
     __shared__ long long row_end[kPlanChunk];        // rows up to and with request i of the chunk
     __shared__ long long page_end[kPlanChunk];       // its pages likewise
@@ -154,22 +156,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
             a.tables[(long long)(b0 + i) * a.stride + (cached[i] + kPage - 1) / kPage + (j - before)] =
                 a.free_pages[head + j];
         }
-        // slots, kPlanTokens in a row a thread: one search, and the page ids asked for together
+        // slots, kPlanTokens a thread at once, whose page ids are asked for together
         const long long end = min(rows + total_r, (long long)a.slot_cap);
-        for (long long t0 = rows + (long long)kPlanTokens * share; t0 < end; t0 += (long long)kPlanTokens * shares) {
-            int i = upper(row_end, count, t0);
-            int pos = cached[i] + (int)(t0 - (i ? row_end[i - 1] : rows));
+        const long long next = BULK ? 1 : shares;    // from one of a thread's slots to the next
+        for (long long t0 = rows + (BULK ? (long long)kPlanTokens * share : share); t0 < end;
+             t0 += (long long)kPlanTokens * shares) {
             const int32_t* from[kPlanTokens];
-            int in_page[kPlanTokens];
+            int in_page[kPlanTokens], i = 0;
 #pragma unroll
-            for (int k = 0; k < kPlanTokens; ++k, ++pos) {
+            for (int k = 0; k < kPlanTokens; ++k) {
+                const long long t = t0 + k * next;
                 from[k] = nullptr;
-                if (t0 + k >= end) continue;
-                if (t0 + k >= row_end[i]) {          // on to the next request that has rows
-                    while (t0 + k >= row_end[i]) ++i;
-                    pos = cached[i];
-                }
+                if (t >= end) continue;
+                if (!BULK || k == 0) i = upper(row_end, count, t);
+                else while (t >= row_end[i]) ++i;
                 if (cached[i] < 0) continue;
+                const int pos = cached[i] + (int)(t - (i ? row_end[i - 1] : rows));
                 const int page = pos / kPage, first_new = (cached[i] + kPage - 1) / kPage;
                 in_page[k] = pos % kPage;
                 from[k] = page < first_new ? a.tables + (long long)(b0 + i) * a.stride + page
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
             for (int k = 0; k < kPlanTokens; ++k) id[k] = from[k] ? *from[k] : 0;
 #pragma unroll
             for (int k = 0; k < kPlanTokens; ++k)
-                if (t0 + k < end) a.slots[t0 + k] = from[k] ? (int64_t)id[k] * kPage + in_page[k] : -1;
+                if (t0 + k * next < end) a.slots[t0 + k * next] = from[k] ? (int64_t)id[k] * kPage + in_page[k] : -1;
         }
         rows += total_r;
         wanted += total_p;
@@ -204,11 +206,16 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st) {
     // as many CTAs as have kPlanTokens slots a thread to write
     int cluster = 1;
     while (cluster < kPlanMaxCluster && (long long)cluster * kPlanThreads * kPlanTokens < a.slot_cap) cluster *= 2;
+    const auto kernel = a.batch > 2 * kPlanThreads ? plan_kernel<4, true>
+                        : a.slot_cap > 65536       ? plan_kernel<1, true>
+                                                   : plan_kernel<1, false>;
     if (cluster > 8) {
-        const cudaError_t e = allow_large_clusters<plan_kernel>();
+        cudaError_t e = allow_large_clusters<plan_kernel<4, true>>();
+        if (e == cudaSuccess) e = allow_large_clusters<plan_kernel<1, true>>();
+        if (e == cudaSuccess) e = allow_large_clusters<plan_kernel<1, false>>();
         if (e != cudaSuccess) return e;
     }
-    return launch_dependent(plan_kernel, dim3(cluster), dim3(kPlanThreads), 0, st, cluster, a);
+    return launch_dependent(kernel, dim3(cluster), dim3(kPlanThreads), 0, st, cluster, a);
 }
 
 }  // namespace oscar
