@@ -160,6 +160,7 @@ int oscar_sparse_capacity(const oscar_ctx_t* ctx, int top_pages) {
 
 size_t oscar_decode_bf16_sparse_workspace_size(const oscar_ctx_t* ctx, int batch, int max_len, int top_pages) {
     if (!sizes_ok(ctx, batch, max_len) || top_pages < 0 || top_pages > oscar::kMaxTopPages) return 0;
+    if (oscar::sparse_small_ranks(ctx->shape, ctx->num_sms, batch, pages_of(max_len), top_pages)) return 0;
     return oscar::plan_attend(ctx->shape, ctx->num_sms, batch, sparse_pages(ctx, max_len, top_pages), true).ws_total +
            oscar::select_workspace_bytes(ctx->shape, batch, pages_of(max_len));
 }
@@ -182,9 +183,10 @@ oscar_status oscar_decode_bf16_sparse(oscar_ctx_t* ctx, const void* q, int64_t q
     if (!aligned(key_bounds, 16))
         return record_failure(OSCAR_ERR_INVALID_ARG, "key_bounds must be 16-byte aligned");
     const int max_pages = pages_of(max_len);
+    const int ranks = oscar::sparse_small_ranks(ctx->shape, ctx->num_sms, batch, max_pages, top_pages);
     const oscar::AttendPlan plan =
-        oscar::plan_attend(ctx->shape, ctx->num_sms, batch, sparse_pages(ctx, max_len, top_pages), true);
-    const size_t scores = oscar::select_workspace_bytes(ctx->shape, batch, max_pages);
+        ranks ? oscar::AttendPlan{} : oscar::plan_attend(ctx->shape, ctx->num_sms, batch, sparse_pages(ctx, max_len, top_pages), true);
+    const size_t scores = ranks ? 0 : oscar::select_workspace_bytes(ctx->shape, batch, max_pages);
     st = check_workspace(workspace, workspace_bytes, scores + plan.ws_total);
     if (st != OSCAR_OK) return st;
 
@@ -201,6 +203,11 @@ oscar_status oscar_decode_bf16_sparse(oscar_ctx_t* ctx, const void* q, int64_t q
     s.max_pages = max_pages; s.top = top_pages; s.sink = ctx->shape.sink; s.recent = ctx->shape.recent;
     s.h_kv = ctx->shape.h_kv; s.g = ctx->shape.h_q / ctx->shape.h_kv; s.batch = batch;
     s.debug = ctx->shape.debug; s.dbg = ctx->dbg;
+    if (ranks) {
+        oscar::ProfScope ps(&ctx->prof, OSCAR_KERNEL_ATTEND, static_cast<cudaStream_t>(stream));
+        return cuda_status(oscar::launch_sparse_small(s, a, ctx->shape.d, ranks, static_cast<cudaStream_t>(stream)),
+                           "sparse BF16 decode launch");
+    }
     {
         oscar::ProfScope ps(&ctx->prof, OSCAR_KERNEL_SELECT, static_cast<cudaStream_t>(stream));
         st = cuda_status(oscar::launch_select(s, ctx->shape.d, ctx->num_sms, static_cast<cudaStream_t>(stream)), "page selection launch");

@@ -78,6 +78,11 @@ struct SelectArgs {
 size_t select_workspace_bytes(const Shape& s, int batch, int max_pages);
 cudaError_t launch_select(const SelectArgs& a, int d, int num_sms, cudaStream_t st);
 
+// ---- both in one kernel, for few (sequence, KV head) pairs (sparse_small.cu)
+// CTAs of a pair's cluster, or 0 where the separate kernels serve better.
+int sparse_small_ranks(const Shape& s, int num_sms, int batch, int max_pages, int top);
+cudaError_t launch_sparse_small(const SelectArgs& a, const AttendArgs& t, int d, int ranks, cudaStream_t st);
+
 // Entries of one (sequence, KV head)'s list of chosen pages: the sink's pages, the pages that a recent
 // window can touch (one more than it fills), the selected ones.
 inline int sparse_capacity(const Shape& s, int top) {

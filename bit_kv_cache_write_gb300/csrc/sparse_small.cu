@@ -1,0 +1,143 @@
+// The sparse decode of few (sequence, KV head) pairs in one kernel: selection (page_select.cuh) and attention
+// (paged_attend.cuh) by one cluster each.
+//
+// With few pairs everything is latency: three kernels' starts, the loads of lengths, lists and tables in each, and
+// a join. Here the cluster that has scored the pages stays. While its first CTA selects, the warps of the others
+// attend to the sink and the recent window; the selected pages come as page ids through the first CTA's shared
+// memory, a page or two a warp, and the cluster joins its warps' parts.
+#include "page_select.cuh"
+#include "paged_attend.cuh"
+
+namespace oscar {
+namespace {
+
+constexpr int kSmallThreads = 512;
+constexpr int kSmallWarps = kSmallThreads / 32;
+constexpr int kSmallCluster = 8;                     // larger ones do not all find their place at once
+constexpr int kSmallPages = 3;                       // selected pages a warp at most
+constexpr int kSmallTop = kSmallCluster * kSmallWarps * kSmallPages;
+
+template <int D>
+__global__ void __launch_bounds__(kSmallThreads, 1) sparse_small_kernel(SelectArgs a, AttendArgs t, int smem_keys) {
+    __shared__ __align__(16) QueryCodes<D> codes;
+    __shared__ SelectShared s;
+    __shared__ int2 selected[kSmallTop];             // page id and logical page, in the first CTA
+    extern __shared__ __align__(16) unsigned char dynamic[];     // keys (first CTA), then the warps' parts
+    uint32_t* key_store = reinterpret_cast<uint32_t*>(dynamic);
+    auto& parts = *reinterpret_cast<WarpParts<D, kSmallWarps>*>(dynamic);
+    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const int unit = blockIdx.x / ranks, b = unit / a.h_kv, h = unit % a.h_kv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, quad = lane & 3;
+    const int32_t* table = a.tables + (int64_t)b * a.stride;
+    int32_t* list = a.chosen + (int64_t)unit * a.cap;
+
+    const Scored u = score_unit<D, kSmallThreads>(a, smem_keys, codes, s, key_store, [&](const Scored& u) {
+        if (rank != 0) return;                       // everything but the selected pages
+        const int recent = u.recent(), total = u.total();
+        for (int i = threadIdx.x; i < u.w.sink; i += kSmallThreads) list[i] = i;
+        for (int i = threadIdx.x; i < recent; i += kSmallThreads) list[u.w.sink + u.take + i] = u.w.pages - recent + i;
+        for (int i = total + threadIdx.x; i < a.cap; i += kSmallThreads) list[i] = -1;
+        if (threadIdx.x == 0) a.n_chosen[unit] = total;
+    });
+    uint4 q[D / 32];
+    load_query<D>(q, t, b, h, gid, quad);
+    Gathered<D> g;
+    auto attend = [&](int id, int logical) {
+        int valid = 0;
+        if (id >= 0 && id < t.pages) valid = min(kPage, u.len - logical * kPage);
+        else if (t.debug && lane == 0) record_error(&t.dbg->kind, &t.dbg->index, 2, id);
+        const uint16_t* page = t.pool + ((int64_t)(valid > 0 ? id : 0) * t.h_kv + h) * (2 * kPage * D);
+        attend_page<D>(g, q, page, max(valid, 0), t.scale_log2, gid, quad);
+    };
+    cluster.sync();                                  // the keys are there
+    if (rank == 0)
+        list_selected<kSmallThreads>(u, s, [&](int i, int p) {
+            const int logical = u.w.sink + p;
+            list[logical - p + i] = logical;
+            selected[i] = make_int2(table[logical], logical);
+        });
+    if (rank != 0 || ranks == 1) {                   // the windows, whose pages need no selection
+        const int kept = u.w.sink + u.recent(), warps = (ranks > 1 ? ranks - 1 : 1) * kSmallWarps;
+        for (int i = (ranks > 1 ? rank - 1 : 0) + warp * (ranks > 1 ? ranks - 1 : 1); i < kept; i += warps) {
+            const int logical = i < u.w.sink ? i : u.w.pages - u.recent() + i - u.w.sink;
+            attend(table[logical], logical);
+        }
+    }
+    cluster.sync();                                  // the selected pages are listed
+    const int2* from = cluster.map_shared_rank(selected, 0);
+    for (int i = rank + ranks * warp; i < u.take; i += ranks * kSmallWarps) {
+        const int2 e = from[i];
+        attend(e.x, e.y);
+    }
+    put_warp<D, kSmallWarps>(parts, g, warp, gid, quad);     // the keys have been read
+    __syncthreads();
+    join_cluster<D, kSmallWarps, kSmallCluster>(t, parts, (int64_t)b * t.h_kv * t.g + h * t.g, rank, ranks);
+}
+
+template <int D>
+constexpr size_t kSmallSmem = kSmemKeys * sizeof(uint32_t) > sizeof(WarpParts<D, kSmallWarps>)
+                                  ? kSmemKeys * sizeof(uint32_t) : sizeof(WarpParts<D, kSmallWarps>);
+
+// Clusters of `ranks` CTAs that the current device holds at once (asked once per device and size); 0 if unknown.
+template <int D>
+int resident_clusters(int ranks) {
+    static std::atomic<int> known[64][kSmallCluster + 1];    // 1 + the number
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev][ranks].load(std::memory_order_acquire);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(ranks);
+        cfg.blockDim = dim3(kSmallThreads);
+        cfg.dynamicSmemBytes = kSmallSmem<D>;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = ranks;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (smem_opt_in<sparse_small_kernel<D>>(kSmallSmem<D>) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&clusters, sparse_small_kernel<D>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        n = 1 + clusters;
+        known[dev][ranks].store(n, std::memory_order_release);
+    }
+    return n - 1;
+}
+
+template <int D>
+cudaError_t launch(const SelectArgs& a, const AttendArgs& t, int ranks, cudaStream_t st) {
+    const size_t keys = (size_t)a.max_pages * sizeof(uint32_t), parts = sizeof(WarpParts<D, kSmallWarps>);
+    const size_t smem = keys > parts ? keys : parts;
+    const cudaError_t e = smem_opt_in<sparse_small_kernel<D>>(kSmallSmem<D>);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(sparse_small_kernel<D>, dim3((unsigned)(a.batch * a.h_kv * ranks)), dim3(kSmallThreads), smem,
+                            st, ranks, a, t, a.max_pages);
+}
+
+}  // namespace
+
+int sparse_small_ranks(const Shape& s, int num_sms, int batch, int max_pages, int top) {
+    const long long units = (long long)batch * s.h_kv;
+    const int take = top < max_pages ? top : max_pages, all = sparse_capacity(s, top);
+    int ranks = 1;                                   // a page a warp in all, and a tile of 16 scores
+    while (ranks < kSmallCluster && (ranks * kSmallWarps < (all < max_pages ? all : max_pages) ||
+                                     ranks * kSmallThreads / 2 < max_pages) && 2 * ranks * units <= num_sms)
+        ranks *= 2;
+    // few selected pages and few tiles a warp, and every cluster on the card at once
+    if (max_pages == 0 || units * ranks > num_sms || take > ranks * kSmallWarps * kSmallPages ||
+        max_pages > ranks * kSmallThreads * 4 || max_pages > kSmemKeys)
+        return 0;
+    const int fit = s.d == 128 ? resident_clusters<128>(ranks) : resident_clusters<64>(ranks);
+    return units <= fit ? ranks : 0;
+}
+
+cudaError_t launch_sparse_small(const SelectArgs& a, const AttendArgs& t, int d, int ranks, cudaStream_t st) {
+    return d == 128 ? launch<128>(a, t, ranks, st) : launch<64>(a, t, ranks, st);
+}
+
+}  // namespace oscar
