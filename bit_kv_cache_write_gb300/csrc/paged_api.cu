@@ -11,6 +11,12 @@ oscar_status cuda_status(cudaError_t e, const char* where) {
 
 bool aligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
+// Whether n ints at a and m ints at b share memory.
+bool overlap(const int32_t* a, long long n, const int32_t* b, long long m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return n > 0 && m > 0 && x < y + 4 * (uintptr_t)m && y < x + 4 * (uintptr_t)n;
+}
+
 int pages_of(int tokens) { return (tokens + oscar::kPage - 1) / oscar::kPage; }
 
 bool sizes_ok(const oscar_ctx_t* ctx, int batch, int max_len) {
@@ -94,6 +100,15 @@ oscar_status oscar_plan_append(oscar_ctx_t* ctx, const int32_t* seq_len, const i
     if (!free_head || !row_start || !state || (batch > 0 && (!seq_len || !new_len || !total_len)) ||
         (n_free > 0 && !free_pages) || (slot_cap > 0 && !slots) || (batch > 0 && table_stride > 0 && !tables))
         return record_failure(OSCAR_ERR_INVALID_ARG, "device pointer is NULL");
+    // every CTA reads the lengths while others write: what is written has to lie apart
+    if (overlap(total_len, batch, seq_len, batch) || overlap(total_len, batch, new_len, batch) ||
+        overlap(row_start, batch + 1LL, seq_len, batch) || overlap(row_start, batch + 1LL, new_len, batch) ||
+        overlap(row_start, batch + 1LL, total_len, batch) || overlap(state, 4, seq_len, batch) ||
+        overlap(state, 4, new_len, batch) || overlap(state, 4, total_len, batch) ||
+        overlap(state, 4, row_start, batch + 1LL) || overlap(total_len, batch, free_head, 1) ||
+        overlap(row_start, batch + 1LL, free_head, 1))
+        return record_failure(OSCAR_ERR_INVALID_ARG,
+                              "seq_len, new_len, row_start, total_len and state must not overlap (free_head may lie in state)");
     if (oscar::injected_fault("launch"))
         return record_failure(OSCAR_ERR_CUDA, "injected launch failure (OSCAR_FAULT=launch)");
     oscar::PlanArgs a{seq_len, new_len, free_pages, n_free, free_head, tables, table_stride, slots, slot_cap,

@@ -10,8 +10,9 @@
 // read from the free list, so no CTA reads what another one writes. The free head may be the word that the
 // new head goes to, so the last barrier stands between every CTA's read of it and the write.
 //
-// Nothing here is large: the time is a chain of dependent loads (lengths, sums, page ids). The kernel does not
-// let its successor start early: page ids and slots may be read ahead by the one after that.
+// Nothing here is large: the time is a chain of dependent loads (lengths, sums, page ids), 3.6 us for 64 single
+// tokens; 94,000 tokens of 96 requests take 8.4 us, their searches and writes on 16 SMs. The kernel does not let
+// its successor start early: page ids and slots may be read ahead by the one after that.
 #include <climits>
 
 #include "paged_device.cuh"

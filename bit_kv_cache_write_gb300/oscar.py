@@ -351,6 +351,13 @@ def _output(out, q, device, torch):
     raise ValueError("out must be torch.float32 or torch.bfloat16, got %s" % dtype)
 
 
+def _bound(value, name):
+    """An int that the C ABI takes whole (ctypes would cut it to 32 bits)."""
+    if not -0x80000000 <= value <= 0x7fffffff:
+        raise ValueError("%s %s does not fit in 32 bits" % (name, value))
+    return value
+
+
 def _scratch(workspace, device):
     """(pointer, bytes) of a workspace tensor or None."""
     if workspace is None:
@@ -415,7 +422,8 @@ def oscar_decode_bf16(ctx, q, bf16_pool, tables, seq_len, max_len, out, workspac
     wp, ws = _scratch(workspace, dev)
     st = lib().oscar_decode_bf16(
         ctx, qp, qs, _ptr(bf16_pool, torch.bfloat16, size, dev, "bf16_pool"), size // (h_kv * 32 * d), tp, ts,
-        _ptr(seq_len, torch.int32, batch, dev, "seq_len"), max_len, op, ot, wp, ws, batch, _stream_on(stream, dev))
+        _ptr(seq_len, torch.int32, batch, dev, "seq_len"), _bound(max_len, "max_len"), op, ot, wp, ws, batch,
+        _stream_on(stream, dev))
     if st:
         _check(st, "oscar_decode_bf16")
 
@@ -442,11 +450,11 @@ def oscar_decode_bf16_sparse(ctx, q, bf16_pool, key_steps, key_bounds, tables, s
     op, ot = _output(out, q, dev, torch)
     wp, ws = _scratch(workspace, dev)
     handle = lib()
-    cap = handle.oscar_sparse_capacity(ctx, top_pages)       # 0 where top_pages is refused
+    cap = handle.oscar_sparse_capacity(ctx, _bound(top_pages, "top_pages"))      # 0 where top_pages is refused
     st = handle.oscar_decode_bf16_sparse(
         ctx, qp, qs, _ptr(bf16_pool, torch.bfloat16, size, dev, "bf16_pool"), pages,
         _ptr(key_steps, i8, h_kv * d, dev, "key_steps"), _ptr(key_bounds, i8, pages * h_kv * 2 * d, dev, "key_bounds"),
-        tp, ts, _ptr(seq_len, i32, batch, dev, "seq_len"), max_len, top_pages,
+        tp, ts, _ptr(seq_len, i32, batch, dev, "seq_len"), _bound(max_len, "max_len"), top_pages,
         _ptr(chosen, i32, batch * h_kv * cap, dev, "chosen") if cap else None,
         _ptr(n_chosen, i32, batch * h_kv, dev, "n_chosen"), op, ot, wp, ws, batch, _stream_on(stream, dev))
     if st:

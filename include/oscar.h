@@ -349,7 +349,8 @@ OSCAR_API oscar_status oscar_calibration_targets(const float* q_cal, const float
  * when it needs pages and the pages needed up to and with it (by requests not
  * rejected for another reason) are more than the free list holds. A free_head
  * outside the list counts as an empty list.
- * The buffers must not overlap, but for free_head. Asynchronous on `stream`. */
+ * The buffers must not overlap, but for free_head in state (lengths, starts and
+ * state that do are refused). Asynchronous on `stream`. */
 OSCAR_API oscar_status oscar_plan_append(oscar_ctx_t* ctx, const int32_t* seq_len, const int32_t* new_len, int batch,
                                          const int32_t* free_pages, int n_free, const int32_t* free_head,
                                          int32_t* tables, int table_stride, int64_t* slots, int slot_cap,
@@ -369,7 +370,8 @@ OSCAR_API oscar_status oscar_plan_append(oscar_ctx_t* ctx, const int32_t* seq_le
  * appended to the page since its row 0: tokens that are adjacent in `slots` and
  * go to one page are one run; a run that has row 0 starts the page's bounds
  * anew, another one widens them. With bounds, a page's tokens of one call must
- * be one run (oscar_plan_append's slots are).
+ * be one run (oscar_plan_append's slots are). A row written again only widens
+ * the bounds; a page that the caller copies takes its bounds along.
  * Asynchronous on `stream`. n == 0 is a no-op. */
 OSCAR_API oscar_status oscar_append_bf16(oscar_ctx_t* ctx, const void* k, int64_t k_stride, const void* v,
                                          int64_t v_stride, const int64_t* slots, int n, void* bf16_pool,
@@ -423,7 +425,8 @@ OSCAR_API oscar_status oscar_decode_bf16(oscar_ctx_t* ctx, const void* q, int64_
  *               written: the logical pages read, ascending, then -1.
  *   n_chosen:   DEVICE int32 [batch][H_kv], written: how many.
  *   workspace:  >= oscar_decode_bf16_sparse_workspace_size(...) bytes.
- * Everything else as for oscar_decode_bf16. */
+ * Everything else as for oscar_decode_bf16. oscar_sparse_capacity gives 0 on bad
+ * arguments. */
 OSCAR_API int oscar_sparse_capacity(const oscar_ctx_t* ctx, int top_pages);
 OSCAR_API size_t oscar_decode_bf16_sparse_workspace_size(const oscar_ctx_t* ctx, int batch, int max_len, int top_pages);
 OSCAR_API oscar_status oscar_decode_bf16_sparse(oscar_ctx_t* ctx, const void* q, int64_t q_stride,

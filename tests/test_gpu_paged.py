@@ -627,6 +627,17 @@ def test_refusals(cuda):
     z = lambda m, dt=I32: torch.zeros(m, dtype=dt, device=cuda)
     with pytest.raises(ValueError, match="row_start"):
         ctx.plan_append(n, n, z(1), z(1), t, z(4, I64), z(1), z(1), z(4))
+    lens, starts = z(3), z(4)
+    plan = lambda seq, total, rows, state: ctx.plan_append(seq, z(3), z(1), z(1), z(12).view(3, 4), z(4, I64), rows, total, state)
+    assert status(plan, lens, lens, starts, z(4)) == -1                               # in place
+    both = z(8)
+    assert status(plan, both[:3], both[2:5], starts, z(4)) == -1
+    assert status(plan, lens, z(3), both[:4], both[3:7]) == -1
+    for bad in (1 << 31, -(1 << 31) - 1):
+        with pytest.raises(ValueError, match="32 bits"):
+            ctx.decode_bf16(q, pool, t, n, bad, out, ws)
+        with pytest.raises(ValueError, match="32 bits"):
+            sparse(bad, chosen, count)
     big = 65536
     assert status(ctx.plan_append, z(big), z(big), z(1), z(1), z(big).view(big, 1), z(4, I64), z(big + 1), z(big), z(4)) == -2
 
