@@ -136,7 +136,8 @@ def oscar_create(n_layers, n_q_heads, n_kv_heads, head_dim, group, page_size=16,
     ctx = _vp()
     _check(lib().oscar_create(ctypes.byref(cfg), ctypes.byref(ctx)), "oscar_create")
     import torch
-    _configs[ctx.value] = (n_q_heads, n_kv_heads, head_dim, torch.cuda.current_device())
+    _configs[ctx.value] = (n_q_heads, n_kv_heads, head_dim, torch.cuda.current_device(),
+                           lib().oscar_sparse_capacity(ctx, 0))
     return ctx.value
 
 
@@ -271,7 +272,9 @@ def oscar_decode_static_workspace(ctx, layer, q, int2_pool, int2_tables, hist_le
         _dptr(out, torch.float32, "out"), batch, _stream(stream)), "oscar_decode_static_workspace")
 
 
-_configs = {}     # context handle -> (H_q, H_kv, d, device) of the contexts created here, for the checks below
+# context handle -> (H_q, H_kv, d, device, pages that a sparse decode always keeps at most) of the contexts created
+# here, for the checks below
+_configs = {}
 
 
 def _config_of(ctx):
@@ -332,22 +335,24 @@ def _rows(t, bf16, heads, d, device, name):
     _refuse(t, bf16, 0, device, name)
 
 
-def _table(t, batch, dtype, device, name="tables"):
+def _table(t, batch, dtype, device):
     """(pointer, row length) of contiguous block tables [batch][stride]."""
-    if t.dim() != 2 or t.shape[0] != batch:
-        raise ValueError("%s must be [%d][stride], got %s" % (name, batch, tuple(t.shape)))
-    return _ptr(t, dtype, t.numel(), device, name), t.shape[1]
+    try:
+        rows, stride = t.shape
+    except ValueError:
+        rows = -1
+    if rows != batch:
+        raise ValueError("tables must be [%d][stride], got %s" % (batch, tuple(t.shape)))
+    return _ptr(t, dtype, rows * stride, device, "tables"), stride
 
 
-def _output(out, q, device, torch):
-    """(pointer, oscar_out_type) of an output of q's shape."""
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape %s, has %s" % (tuple(q.shape), tuple(out.shape)))
+def _output(out, n, device, torch):
+    """(pointer, oscar_out_type) of an output of n elements."""
     dtype = out.dtype
     if dtype is torch.float32:
-        return _ptr(out, dtype, out.numel(), device, "out"), OSCAR_OUT_FP32
+        return _ptr(out, dtype, n, device, "out"), OSCAR_OUT_FP32
     if dtype is torch.bfloat16:
-        return _ptr(out, dtype, out.numel(), device, "out"), OSCAR_OUT_BF16
+        return _ptr(out, dtype, n, device, "out"), OSCAR_OUT_BF16
     raise ValueError("out must be torch.float32 or torch.bfloat16, got %s" % dtype)
 
 
@@ -362,8 +367,9 @@ def _scratch(workspace, device):
     """(pointer, bytes) of a workspace tensor or None."""
     if workspace is None:
         return None, 0
-    n = workspace.numel()
-    return _ptr(workspace, workspace.dtype, n, device, "workspace"), n * workspace.element_size()
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        _refuse(workspace, workspace.dtype, 0, device, "workspace")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def oscar_plan_append(ctx, seq_len, new_len, free_pages, free_head, tables, slots, row_start, total_len, state,
@@ -387,7 +393,7 @@ def oscar_append_bf16(ctx, k, v, slots, bf16_pool, key_steps=None, key_bounds=No
     """k, v: bf16 [n][H_kv][d], rows at any stride; slots int64 [n]; bf16_pool: whole pages; key_steps int8
     [H_kv][d] and key_bounds int8 [pages][H_kv][2][d], or neither."""
     import torch
-    _, h_kv, d, dev = _config_of(ctx)
+    _, h_kv, d, dev, _ = _config_of(ctx)
     bf16 = torch.bfloat16
     kp, ks = _rows(k, bf16, h_kv, d, dev, "k")
     vp, vs = _rows(v, bf16, h_kv, d, dev, "v")
@@ -414,11 +420,11 @@ def oscar_decode_bf16(ctx, q, bf16_pool, tables, seq_len, max_len, out, workspac
     """q: bf16 [B][H_q][d], rows at any stride; tables int32 [B][stride]; seq_len int32 [B], at most max_len;
     out fp32 or bf16 [B][H_q][d]; workspace uint8."""
     import torch
-    h_q, h_kv, d, dev = _config_of(ctx)
+    h_q, h_kv, d, dev, _ = _config_of(ctx)
     qp, qs = _rows(q, torch.bfloat16, h_q, d, dev, "q")
     batch, size = q.shape[0], bf16_pool.numel()
     tp, ts = _table(tables, batch, torch.int32, dev)
-    op, ot = _output(out, q, dev, torch)
+    op, ot = _output(out, batch * h_q * d, dev, torch)
     wp, ws = _scratch(workspace, dev)
     st = lib().oscar_decode_bf16(
         ctx, qp, qs, _ptr(bf16_pool, torch.bfloat16, size, dev, "bf16_pool"), size // (h_kv * 32 * d), tp, ts,
@@ -441,21 +447,20 @@ def oscar_decode_bf16_sparse(ctx, q, bf16_pool, key_steps, key_bounds, tables, s
     """oscar_decode_bf16 over the sink, the recent window and the top_pages best pages by their key bounds; chosen
     int32 [B][H_kv][oscar_sparse_capacity(ctx, top_pages)] and n_chosen int32 [B][H_kv] say which."""
     import torch
-    h_q, h_kv, d, dev = _config_of(ctx)
+    h_q, h_kv, d, dev, kept = _config_of(ctx)
     i8, i32 = torch.int8, torch.int32
     qp, qs = _rows(q, torch.bfloat16, h_q, d, dev, "q")
     batch, size = q.shape[0], bf16_pool.numel()
     pages = size // (h_kv * 32 * d)
     tp, ts = _table(tables, batch, i32, dev)
-    op, ot = _output(out, q, dev, torch)
+    op, ot = _output(out, batch * h_q * d, dev, torch)
     wp, ws = _scratch(workspace, dev)
-    handle = lib()
-    cap = handle.oscar_sparse_capacity(ctx, _bound(top_pages, "top_pages"))      # 0 where top_pages is refused
-    st = handle.oscar_decode_bf16_sparse(
+    listed = 0 <= _bound(top_pages, "top_pages") <= 65536        # else the library refuses it
+    st = lib().oscar_decode_bf16_sparse(
         ctx, qp, qs, _ptr(bf16_pool, torch.bfloat16, size, dev, "bf16_pool"), pages,
         _ptr(key_steps, i8, h_kv * d, dev, "key_steps"), _ptr(key_bounds, i8, pages * h_kv * 2 * d, dev, "key_bounds"),
         tp, ts, _ptr(seq_len, i32, batch, dev, "seq_len"), _bound(max_len, "max_len"), top_pages,
-        _ptr(chosen, i32, batch * h_kv * cap, dev, "chosen") if cap else None,
+        _ptr(chosen, i32, batch * h_kv * (kept + top_pages), dev, "chosen") if listed else None,
         _ptr(n_chosen, i32, batch * h_kv, dev, "n_chosen"), op, ot, wp, ws, batch, _stream_on(stream, dev))
     if st:
         _check(st, "oscar_decode_bf16_sparse")

@@ -612,6 +612,16 @@ def test_refusals(cuda):
         ctx.decode_bf16(q, pool, t, n, 64, out.half(), ws)
     with pytest.raises(ValueError, match="tables"):
         ctx.decode_bf16(q, pool, t[0], n, 64, out, ws)
+    with pytest.raises(ValueError, match="tables"):
+        ctx.decode_bf16(q, pool, t.expand(2, 4), n, 64, out, ws)
+    with pytest.raises(ValueError, match="out must hold"):
+        ctx.decode_bf16(q, pool, t, n, 64, out[:, :3].contiguous(), ws)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        ctx.decode_bf16(q, pool, t, n, 64, out, ws[::2])
+    with pytest.raises(ValueError, match="seq_len must be torch.int32"):
+        ctx.decode_bf16(q, pool, t, n.long(), 64, out, ws)
+    with pytest.raises(ValueError, match="bf16_pool must be a CUDA tensor"):
+        ctx.decode_bf16(q, pool.cpu(), t, n, 64, out, ws)
     k = torch.zeros(2, 2, 64, dtype=BF, device=cuda)
     slots = torch.zeros(2, dtype=I64, device=cuda)
     with pytest.raises(ValueError, match="key_bounds"):

@@ -113,7 +113,7 @@ def test_null_context_is_refused(liboscar):
 
 
 def test_binding_refuses_host_tensors(liboscar, monkeypatch):
-    monkeypatch.setitem(O._configs, 12345, (4, 2, 64, 0))
+    monkeypatch.setitem(O._configs, 12345, (4, 2, 64, 0, 21))
     bf = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="k must be a CUDA tensor"):
         O.oscar_append_bf16(12345, bf, bf, torch.zeros(2, dtype=torch.int64), torch.zeros(4096, dtype=torch.bfloat16))
