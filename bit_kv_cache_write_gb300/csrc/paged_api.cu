@@ -46,9 +46,9 @@ oscar_status check_decode(const oscar_ctx_t* ctx, const void* q, int64_t q_strid
         return record_failure(OSCAR_ERR_INVALID_ARG, "BF16 pool/tables missing");
     if (max_len > 0 && (long long)max_len > (long long)stride * oscar::kPage)
         return record_failure(OSCAR_ERR_INVALID_ARG, "max_len %d exceeds table stride %d pages", max_len, stride);
-    if (q_stride < 0 || q_stride % 8 || !aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16))
+    if (q_stride < 0 || q_stride % 8 || !aligned(q, 16) || !aligned(pool, 32) || !aligned(out, 16))
         return record_failure(OSCAR_ERR_INVALID_ARG,
-                              "q, the pool and out must be 16-byte aligned, q_stride a multiple of 8 (is %lld)",
+                              "q and out must be 16-byte aligned, the pool 32-byte, q_stride a multiple of 8 (is %lld)",
                               (long long)q_stride);
     return OSCAR_OK;
 }
@@ -195,8 +195,8 @@ oscar_status oscar_decode_bf16_sparse(oscar_ctx_t* ctx, const void* q, int64_t q
     if (batch == 0) return OSCAR_OK;
     if (!key_steps || !key_bounds || !chosen || !n_chosen)
         return record_failure(OSCAR_ERR_INVALID_ARG, "device pointer is NULL");
-    if (!aligned(key_bounds, 16))
-        return record_failure(OSCAR_ERR_INVALID_ARG, "key_bounds must be 16-byte aligned");
+    if (!aligned(key_bounds, 32))
+        return record_failure(OSCAR_ERR_INVALID_ARG, "key_bounds must be 32-byte aligned");
     const int max_pages = pages_of(max_len);
     const int ranks = oscar::sparse_small_ranks(ctx->shape, ctx->num_sms, batch, max_pages, top_pages);
     const oscar::AttendPlan plan =

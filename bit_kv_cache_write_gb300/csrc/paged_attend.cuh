@@ -5,12 +5,12 @@
 //
 // One warp takes one 16-token page of a (sequence, KV head) at a time, for all g <= 8 query heads, with
 // mma.sync m16n8k16 on operands that go from HBM straight to registers:
-//   logits  S[heads, tokens] = Q[16 (8 used), d] K^T: lane (gid, t) loads 16 bytes, channels 32 j + 8 t ..
-//           + 7 of token gid, which hold its part of two k-steps (the contraction's order is free, Q is
+//   logits  S[heads, tokens] = Q[16 (8 used), d] K^T: lane (gid, t) loads 32 bytes, channels 64 j + 16 t ..
+//           + 15 of token gid, which hold its part of four k-steps (the contraction's order is free, Q is
 //           permuted alike);
-//   output  O^T[channels, heads] = V^T[channels, 16 tokens] P^T: lane (gid, t) loads 8 channels of the tokens
-//           2t, 2t+1, 2t+8, 2t+9, and byte permutations pair the tokens. S leaves the first product in the
-//           layout that P^T has to enter the second one in.
+//   output  O^T[channels, heads] = V^T[channels, 16 tokens] P^T: lane (gid, t) loads d / 8 channels of the
+//           tokens 2t, 2t+1, 2t+8, 2t+9, and byte permutations pair the tokens. S leaves the first product in
+//           the layout that P^T has to enter the second one in.
 // Weights enter as three bf16 pieces (24 bits), products of bf16 are exact, and each page's sums are added to
 // the fp32 accumulators with rounded additions, so nothing is lost to the bf16 operands.
 //
@@ -55,8 +55,8 @@ __device__ __forceinline__ void store_out(const AttendArgs& a, int64_t i, float 
 
 template <int D>
 struct Page {
-    uint4 k[2][D / 32];                  // tokens gid, gid + 8
-    uint4 v[4][D / 64];                  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+    uint4 k[2][D / 32];                  // tokens gid, gid + 8: channels 64 (j / 2) + 16 t + 8 (j % 2) ..
+    uint4 v[4][D / 64];                  // tokens 2t, 2t + 1, 2t + 8, 2t + 9: channels d / 8 gid + 8 f ..
 };
 
 template <int D>
@@ -64,15 +64,17 @@ __device__ __forceinline__ void load_k(Page<D>& p, const uint16_t* page, int gid
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) p.k[n][j] = ldg_stream(page + (gid + 8 * n) * D + 32 * j + 8 * t);
+        for (int j = 0; j < D / 64; ++j)
+            ldg_stream32(p.k[n][2 * j], p.k[n][2 * j + 1], page + (gid + 8 * n) * D + 64 * j + 16 * t);
 }
 template <int D>
 __device__ __forceinline__ void load_v(Page<D>& p, const uint16_t* page, int gid, int t) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int f = 0; f < D / 64; ++f)
-            p.v[n][f] = ldg_stream(page + kPage * D + (2 * t + (n & 1) + 8 * (n >> 1)) * D + 64 * f + 8 * gid);
+    for (int n = 0; n < 4; ++n) {
+        const uint16_t* row = page + kPage * D + (2 * t + (n & 1) + 8 * (n >> 1)) * D + D / 8 * gid;
+        if constexpr (D == 128) ldg_stream32(p.v[n][0], p.v[n][1], row);
+        else p.v[n][0] = ldg_stream(row);
+    }
 }
 
 // What a warp has gathered of a (sequence, KV head): reference and sum of weights of head gid (the sum over this
@@ -89,7 +91,7 @@ __device__ __forceinline__ void load_query(uint4 (&q)[D / 32], const AttendArgs&
     const uint16_t* row = a.q + b * a.q_stride + (int64_t)(h * a.g + gid) * D;
 #pragma unroll
     for (int j = 0; j < D / 32; ++j)
-        q[j] = gid < a.g ? *reinterpret_cast<const uint4*>(row + 32 * j + 8 * t) : make_uint4(0, 0, 0, 0);
+        q[j] = gid < a.g ? *reinterpret_cast<const uint4*>(row + 64 * (j / 2) + 16 * t + 8 * (j % 2)) : make_uint4(0, 0, 0, 0);
 }
 
 // One page of which the first `valid` tokens count.
@@ -161,9 +163,10 @@ __device__ __forceinline__ void attend_page(Gathered<D>& s, const uint4 (&q)[D /
         }
 }
 
-// A CTA's W warps side by side in shared memory. Channel 64 f + 8 i + j of a head lies at 64 f + 8 j + i, rows are
-// D + 4 apart: a warp's lanes (gid, t) write 32 banks, a row is read two lanes to a bank.
-__device__ __forceinline__ int place(int c) { return (c & ~63) | (c & 7) << 3 | (c >> 3 & 7); }
+// A CTA's W warps side by side in shared memory. Channel D / 8 i + j of a head lies at 8 j + i, rows are D + 4
+// apart: a warp's lanes (gid, t) write 32 banks.
+template <int D>
+__device__ __forceinline__ int place(int c) { return c % (D / 8) * 8 + c / (D / 8); }
 template <int D, int W>
 struct WarpParts {
     float acc[W][8][D + 4];
@@ -180,8 +183,8 @@ __device__ __forceinline__ void put_warp(WarpParts<D, W>& w, const Gathered<D>& 
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)      // rows gid and gid + 8 of m-tile (f, u) are channels 64 f + 8 gid + 2 u and + 1
-            w.acc[warp][2 * t + (k & 1)][64 * (i / 4) + 8 * (2 * (i % 4) + (k >> 1)) + gid] = s.acc[i][k];
+        for (int k = 0; k < 4; ++k)      // rows gid and gid + 8 of m-tile i are channels D / 8 gid + 2 i and + 1
+            w.acc[warp][2 * t + (k & 1)][8 * (2 * i + (k >> 1)) + gid] = s.acc[i][k];
 }
 
 // The warps' parts of one output value joined: its reference, sum of weights and accumulator.
@@ -195,7 +198,7 @@ __device__ __forceinline__ void join_warps(const WarpParts<D, W>& w, int head, i
     for (int i = 0; i < W; ++i) {
         const float f = exp2f(w.m[i][head] - m);
         l += f * w.l[i][head];
-        o += f * w.acc[i][head][place(c)];
+        o += f * w.acc[i][head][place<D>(c)];
     }
 }
 
@@ -207,7 +210,7 @@ __device__ __forceinline__ void join_cluster(const AttendArgs& a, WarpParts<D, W
         const int head = x / D, c = x % D;
         float m, l, o;
         join_warps<D, W>(w, head, c, m, l, o);
-        w.acc[0][head][place(c)] = o;                    // read by this thread alone so far
+        w.acc[0][head][place<D>(c)] = o;                    // read by this thread alone so far
         if (c == 0) { w.cta_m[head] = m; w.cta_l[head] = l; }
     }
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
@@ -226,7 +229,7 @@ __device__ __forceinline__ void join_cluster(const AttendArgs& a, WarpParts<D, W
             if (r >= ranks) continue;
             const float f = exp2f(rm[r] - m);
             l += f * *cluster.map_shared_rank(&w.cta_l[head], r);
-            o += f * *cluster.map_shared_rank(&w.acc[0][head][place(c)], r);
+            o += f * *cluster.map_shared_rank(&w.acc[0][head][place<D>(c)], r);
         }
         store_out(a, (row0 + head) * D + c, o, l);
     }

@@ -22,6 +22,12 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
     return r;
 }
 
+// 32 bytes of a 32-byte aligned address: four lanes cover a cache line, half the requests of 16-byte loads.
+__device__ __forceinline__ void ldg_stream32(uint4& a, uint4& b, const void* p) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "l"(p));
+}
+
 // Sequence length as the kernels use it: within [0, max_len]; anything else is recorded.
 __device__ __forceinline__ int checked_len(int len, int max_len, int debug, DebugWord* dbg) {
     if (len < 0 || len > max_len) {

@@ -321,7 +321,8 @@ OSCAR_API oscar_status oscar_calibration_targets(const float* q_cal, const float
  * For layers whose cache stays BF16, and for the BF16 pool that oscar_decode and
  * oscar_demote_recent read. These calls need no calibration and take no layer;
  * heads, d, sm_scale, sink and recent are the context's. Pools, tables and slots
- * are laid out as above. A page id outside the pool is never read: its tokens
+ * are laid out as above; pools and key bounds of the decodes are 32-byte aligned
+ * (16 bytes do for appending). A page id outside the pool is never read: its tokens
  * count as masked (and are recorded with debug_bounds, kind 2). */
 
 /* Block tables and slot maps of one step, from the requests' lengths (no
