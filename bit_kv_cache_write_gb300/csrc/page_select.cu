@@ -13,7 +13,7 @@ __global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int s
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const int64_t unit = blockIdx.x / ranks;
     int32_t* list = a.chosen + unit * a.cap;
-    const Scored u = score_unit<D, T, 1>(a, smem_keys, codes, s, key_store, [&](const Scored& u) {
+    const Scored u = score_unit<D, T>(a, smem_keys, codes, s, key_store, [&](const Scored& u) {
         if (rank != 0) return;                           // everything but the selected pages
         const int recent = u.recent(), total = u.total();
         for (int i = threadIdx.x; i < u.w.sink; i += T) list[i] = i;

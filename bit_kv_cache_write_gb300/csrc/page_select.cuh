@@ -116,7 +116,7 @@ __device__ __forceinline__ void query_codes(const QueryRow<D>& r, int i, QueryCo
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -130,77 +130,71 @@ __device__ __forceinline__ void mma_bounds(float (&c)[4], uint32_t x, uint32_t y
 }
 
 // Scores of the candidates (logical pages w.sink + i) of one (sequence, KV head) as ordered keys, and their
-// range, DEPTH tiles of 16 pages on their way to a warp. `id` holds the page ids of its first tiles; `meanwhile`
-// runs while their bounds are on their way and ends with the query's codes in place.
-template <int D, int DEPTH, typename F>
+// range. `id` holds the page ids of this warp's first tile; `meanwhile` runs while its bounds are on their way and
+// ends with the query's codes in place.
+template <int D, typename F>
 __device__ void score_pages(const SelectArgs& a, int h, const int32_t* table, int cand, uint32_t* keys, uint32_t* range,
-                            int warp, int warps, int (&id)[DEPTH][2], const QueryCodes<D>& qc, F meanwhile) {
+                            int warp, int warps, int (&id)[2], const QueryCodes<D>& qc, F meanwhile) {
     constexpr int kBlocks = 2 * D / 64;                  // a lane's 16-byte pieces of a page's bounds
     const int lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
-    uint4 x[DEPTH][2][kBlocks];                          // pages gid and gid + 8 of the tile
-    bool real[DEPTH][2];
-    auto load_ids = [&](int d, int i0) {
+    uint4 x[2][kBlocks];                                 // pages gid and gid + 8 of the tile
+    bool real[2];
+    auto load_ids = [&](int i0) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int i = i0 + gid + 8 * r;
-            id[d][r] = i < cand ? table[i] : 0;
+            id[r] = i < cand ? table[i] : 0;
         }
     };
-    auto load = [&](int d, int i0) {
+    auto load = [&](int i0) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int page = id[d][r];
+            const int page = id[r];
             const bool inside = i0 + gid + 8 * r < cand;
-            real[d][r] = page >= 0 && page < a.pages;
-            if (inside && !real[d][r] && a.debug && t == 0) record_error(&a.dbg->kind, &a.dbg->index, 2, page);
-            const int8_t* src = a.bounds + ((int64_t)(inside && real[d][r] ? page : 0) * a.h_kv + h) * (2 * D) + 32 * t;
+            real[r] = page >= 0 && page < a.pages;
+            if (inside && !real[r] && a.debug && t == 0) record_error(&a.dbg->kind, &a.dbg->index, 2, page);
+            const int8_t* src = a.bounds + ((int64_t)(inside && real[r] ? page : 0) * a.h_kv + h) * (2 * D) + 32 * t;
 #pragma unroll
-            for (int j = 0; j < kBlocks; j += 2) ldg_stream32(x[d][r][j], x[d][r][j + 1], src + 64 * j);
+            for (int j = 0; j < kBlocks; j += 2) ldg_stream32(x[r][j], x[r][j + 1], src + 64 * j);
         }
     };
     const int step = 16 * warps;
     int i0 = 16 * warp;
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) load(d, i0 + d * step);
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) load_ids(d, i0 + (DEPTH + d) * step);
+    load(i0);
+    load_ids(i0 + step);
     meanwhile();
     // the heads of this lane's two result columns
     const float s0 = qc.scale[2 * t], s1 = qc.scale[2 * t + 1], o0 = qc.offset[2 * t], o1 = qc.offset[2 * t + 1];
     const bool h0 = 2 * t < a.g, h1 = 2 * t + 1 < a.g;
     uint32_t least = ~0u, most = 0;
-    while (i0 < cand) {
+    for (; i0 < cand; i0 += step) {
+        float c[4] = {};
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d, i0 += step) {
-            if (i0 >= cand) break;
-            float c[4] = {};
+        for (int j = 0; j < kBlocks; ++j) {
+            const uint4* u = reinterpret_cast<const uint4*>(&qc.code[gid][qc.at(128 * (j / 2) + 32 * t) + 16 * (j % 2)]);
+            const uint4 u0 = u[0], u1 = u[1];
+            mma_bounds(c, x[0][j].x, x[1][j].x, u0.x, u0.y);
+            mma_bounds(c, x[0][j].y, x[1][j].y, u0.z, u0.w);
+            mma_bounds(c, x[0][j].z, x[1][j].z, u1.x, u1.y);
+            mma_bounds(c, x[0][j].w, x[1][j].w, u1.z, u1.w);
+        }
+        const bool was[2] = {real[0], real[1]};
+        if (i0 + step < cand) {
+            load(i0 + step);
+            load_ids(i0 + 2 * step);
+        }
 #pragma unroll
-            for (int j = 0; j < kBlocks; ++j) {
-                const uint4* u = reinterpret_cast<const uint4*>(&qc.code[gid][qc.at(128 * (j / 2) + 32 * t) + 16 * (j % 2)]);
-                const uint4 u0 = u[0], u1 = u[1];
-                mma_bounds(c, x[d][0][j].x, x[d][1][j].x, u0.x, u0.y);
-                mma_bounds(c, x[d][0][j].y, x[d][1][j].y, u0.z, u0.w);
-                mma_bounds(c, x[d][0][j].z, x[d][1][j].z, u1.x, u1.y);
-                mma_bounds(c, x[d][0][j].w, x[d][1][j].w, u1.z, u1.w);
-            }
-            const bool was[2] = {real[d][0], real[d][1]};
-            if (i0 + DEPTH * step < cand) {
-                load(d, i0 + DEPTH * step);
-                load_ids(d, i0 + 2 * DEPTH * step);
-            }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float best = h0 ? fmaf(c[2 * r], 0x1p24f, o0) * s0 : -INFINITY;
-                if (h1) best = fmaxf(best, fmaf(c[2 * r + 1], 0x1p24f, o1) * s1);
-                best = fmaxf(best, __shfl_xor_sync(~0u, best, 1));
-                best = fmaxf(best, __shfl_xor_sync(~0u, best, 2));
-                const int i = i0 + gid + 8 * r;
-                if (i < cand) {
-                    const uint32_t key = was[r] ? ordered(best) : 0u;
-                    if (t == 0) keys[i] = key;
-                    least = min(least, key);
-                    most = max(most, key);
-                }
+        for (int r = 0; r < 2; ++r) {
+            float best = h0 ? fmaf(c[2 * r], 0x1p24f, o0) * s0 : -INFINITY;
+            if (h1) best = fmaxf(best, fmaf(c[2 * r + 1], 0x1p24f, o1) * s1);
+            best = fmaxf(best, __shfl_xor_sync(~0u, best, 1));
+            best = fmaxf(best, __shfl_xor_sync(~0u, best, 2));
+            const int i = i0 + gid + 8 * r;
+            if (i < cand) {
+                const uint32_t key = was[r] ? ordered(best) : 0u;
+                if (t == 0) keys[i] = key;
+                least = min(least, key);
+                most = max(most, key);
             }
         }
     }
@@ -307,7 +301,7 @@ struct Scored {
 };
 
 // The cluster's CTAs score the candidates of unit blockIdx.x / ranks; `frame` is called once in each, on the way.
-template <int D, int T, int DEPTH, typename F>
+template <int D, int T, typename F>
 __device__ Scored score_unit(const SelectArgs& a, int smem_keys, QueryCodes<D>& codes, SelectShared& s, uint32_t* key_store,
                              F frame) {
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
@@ -323,14 +317,12 @@ __device__ Scored score_unit(const SelectArgs& a, int smem_keys, QueryCodes<D>& 
     // (behind the sink, wherever the sequence ends).
     const int tile = rank + ranks * warp, first_page = (a.sink + kPage - 1) / kPage;
     const int32_t* table = a.tables + (int64_t)b * a.stride + first_page;
-    int id[DEPTH][2];
+    int id[2];
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int i = 16 * (tile + d * ranks * (T / 32)) + (lane >> 2) + 8 * r;
-            id[d][r] = first_page + i < a.stride ? table[i] : 0;
-        }
+    for (int r = 0; r < 2; ++r) {
+        const int i = 16 * tile + (lane >> 2) + 8 * r;
+        id[r] = first_page + i < a.stride ? table[i] : 0;
+    }
     QueryRow<D> query = {};
     if (warp < 8) query = fetch_query<D>(a, b, h, warp);
     Scored u;
@@ -341,7 +333,7 @@ __device__ Scored score_unit(const SelectArgs& a, int smem_keys, QueryCodes<D>& 
     uint32_t* keys = u.cand <= smem_keys ? cluster.map_shared_rank(key_store, 0) : a.keys + (int64_t)unit * a.max_pages;
     u.keys = u.cand <= smem_keys ? key_store : keys;
     if (u.take > 0 && u.take < u.cand)
-        score_pages<D, DEPTH>(a, h, table, u.cand, keys, cluster.map_shared_rank(s.range, 0), tile, ranks * (T / 32), id, codes,
+        score_pages<D>(a, h, table, u.cand, keys, cluster.map_shared_rank(s.range, 0), tile, ranks * (T / 32), id, codes,
                           [&]() {
                               if (warp < 8) query_codes<D>(query, warp, codes);
                               frame(u);

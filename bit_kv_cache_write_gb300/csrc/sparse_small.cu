@@ -17,7 +17,6 @@ namespace {
 
 constexpr int kSmallThreads = 512;
 constexpr int kSmallWarps = kSmallThreads / 32;
-constexpr int kSmallDepth = 2;                       // tiles of scores on their way to a warp
 constexpr int kSmallCluster = 8;                     // larger ones do not all find their place at once
 constexpr int kSmallPages = 3;                       // selected pages a warp at most
 constexpr int kSmallTop = kSmallCluster * kSmallWarps * kSmallPages;
@@ -37,7 +36,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) sparse_small_kernel(SelectAr
     const int32_t* table = a.tables + (int64_t)b * a.stride;
     int32_t* list = a.chosen + (int64_t)unit * a.cap;
 
-    const Scored u = score_unit<D, kSmallThreads, kSmallDepth>(a, smem_keys, codes, s, key_store, [&](const Scored& u) {
+    const Scored u = score_unit<D, kSmallThreads>(a, smem_keys, codes, s, key_store, [&](const Scored& u) {
         if (rank != 0) return;                       // everything but the selected pages
         const int recent = u.recent(), total = u.total();
         for (int i = threadIdx.x; i < u.w.sink; i += kSmallThreads) list[i] = i;
