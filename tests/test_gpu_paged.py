@@ -14,6 +14,7 @@ import numpy as np
 import pytest
 import torch
 
+import cases
 from bit_kv_cache_write_gb300 import oscar as O
 from oracle import paged
 
@@ -348,7 +349,6 @@ def test_dense_with_more_room_than_tokens(cuda):
 def test_dense_with_sharp_logits(cuda):
     """Logits far apart, and rising along the sequence: the running reference is raised again and again."""
     c = Cache(5, [900], 8, 2, 64, gain=4.0)
-    c.pool[:, :, 0] *= 1.0
     ids = c.tables[0, :paged.pages_for(900)]
     for i, p in enumerate(ids):
         c.pool[p, :, 0] = bf16(c.pool[p, :, 0] * (0.05 + i / len(ids)))
@@ -488,12 +488,11 @@ def test_sparse_ties_and_odd_values(cuda, kind):
         c.steps[:] = r.integers(-100, 101, c.steps.shape)
     ctx = context(8, 2, 64)
     _, lists = paged.decode_sparse(np.nan_to_num(c.q, posinf=0.0), c.pool, c.bounds, c.steps, c.tables, c.lens, 50, 64, 256, 0.125)
-    for top in (50,):
-        got, chosen = run_sparse(ctx, c, cuda, torch.float32, top)
-        assert chosen == lists
-        if kind not in ("odd_query",):
-            want, _ = paged.decode_sparse(c.q, c.pool, c.bounds, c.steps, c.tables, c.lens, top, 64, 256, 0.125)
-            close(got, want, c.tolerance(want, None, 0.125))
+    got, chosen = run_sparse(ctx, c, cuda, torch.float32, 50)
+    assert chosen == lists
+    if kind != "odd_query":
+        want, _ = paged.decode_sparse(c.q, c.pool, c.bounds, c.steps, c.tables, c.lens, 50, 64, 256, 0.125)
+        close(got, want, c.tolerance(want, None, 0.125))
 
 
 @pytest.mark.parametrize("h_kv,d", [(3, 64), (4, 128)])
@@ -755,3 +754,35 @@ def test_serving_loop(cuda):
         assert [[chosen[b, h, :count[b, h]].tolist() for h in range(h_kv)] for b in range(batch)] == lists
         assert np.abs(sparse.cpu().numpy() - want).max() <= 2.2e-3
     assert np.array_equal(pool.cpu().double().numpy(), o_pool) and np.array_equal(bounds.cpu().numpy(), o_bounds)
+
+
+def test_plan_and_append_feed_the_three_segment_decode(cuda):
+    """The slots of two plans, for the INT2 history and the BF16 segment, into oscar_write_tokens, oscar_append_bf16
+    and oscar_decode, one after the other on the stream: the cache and the output of the oracle's own case."""
+    cfg = cases.workload("tiny")
+    case = cases.DecodeCase(cfg, [300, 1000], [320, 37])
+    h_kv, d, batch = cfg["h_kv"], cfg["d"], 2
+    ctx = O.Oscar(n_layers=1, n_q_heads=cfg["h_q"], n_kv_heads=h_kv, head_dim=d, group=cfg["group"])
+    ctx.calibrate_upload(0, case.rk, case.rv, case.tk, case.tv)
+    i = lambda *s: torch.zeros(*s, dtype=I32, device=cuda)
+
+    def plan(lens, tables, stride):
+        ids = np.concatenate([tables[b, :paged.pages_for(int(n))] for b, n in enumerate(lens)])
+        t, slots, total = i(batch, stride), torch.zeros(int(lens.sum()), dtype=I64, device=cuda), i(batch)
+        ctx.plan_append(i(batch), dev(lens, cuda), dev(ids, cuda), i(1), t, slots, i(batch + 1), total, i(4))
+        return t, slots, total
+
+    rows = lambda kind, lens: [dev(np.concatenate(x), cuda, BF) for x in
+                               zip(*(case.li.kv("%s/%d" % (kind, b), int(n)) for b, n in enumerate(lens)))]
+    int2, bf = torch.zeros(case.int2_pool.size, dtype=torch.uint8, device=cuda), torch.zeros(case.bf16_pool.size, dtype=BF, device=cuda)
+    t2, s2, n2 = plan(case.hist_lens, case.int2_tables, case.int2_stride)
+    tb, sb, nb = plan(case.bf16_lens, case.bf16_tables, case.bf16_stride)
+    ctx.write_tokens(0, *rows("hist", case.hist_lens), s2, int2)
+    ctx.append_bf16(*rows("bf16", case.bf16_lens), sb, bf)
+    ws = torch.empty(ctx.decode_workspace_size(batch, 1000), dtype=torch.uint8, device=cuda)
+    out = torch.empty(batch, cfg["h_q"], d, device=cuda)
+    ctx.decode(0, dev(case.q, cuda, BF), int2, t2, n2, 1000, bf, tb, nb, out, ws)
+    torch.cuda.synchronize()
+    assert np.array_equal(bf.float().cpu().numpy(), case.bf16_pool)
+    case.int2_pool = int2.cpu().numpy()
+    cases.check_decode(out.cpu().numpy(), case.oracle_out())
