@@ -15,7 +15,7 @@
 // the fp32 accumulators with rounded additions, so nothing is lost to the bf16 operands.
 //
 // HBM bounds it (g flops a byte): 12 warps an SM with up to 8 KB of a page on its way each. 100,000 tokens of 8 KV
-// heads at batch 1 in 65 us, 92 % of the measured copy rate; 64 x 32,768 in 1.2 ms, 106 % (a copy is slower than
+// heads at batch 1 in 66 us, 92 % of the measured copy rate; 64 x 32,768 in 1.19 ms, 106 % (a copy is slower than
 // reads alone). The tensor cores are a tenth busy; tcgen05 would want its operands in shared memory and 128 rows.
 #pragma once
 

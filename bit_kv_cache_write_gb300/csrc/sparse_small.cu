@@ -6,7 +6,7 @@
 // attend to the sink and the recent window; the selected pages come as page ids through the first CTA's shared
 // memory, a page or two a warp, and the cluster joins its warps' parts.
 //
-// 100,000 tokens, 8 KV heads, 256 + 20 pages: 20.5 us on the GPU against 22.3 with separate kernels, and one launch
+// 100,000 tokens, 8 KV heads, 256 + 21 pages: 19.9 us on the GPU against 22.3 with separate kernels, and one launch
 // instead of three (3.4 us of host time against 6.8). About 7 us go to the scores, 4.5 to the selection, 9 to the
 // pages and the join: 64 of the 152 SMs fetch them.
 #include "page_select.cuh"
