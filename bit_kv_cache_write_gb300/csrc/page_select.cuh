@@ -29,10 +29,9 @@
 namespace oscar {
 namespace {
 
-
 constexpr int kBins = 2048;
 constexpr int kSelectMaxCluster = 16;
-constexpr int kLongShare = 1536;
+constexpr int kLongShare = 1536;                 // candidates that make a CTA's share a long one
 constexpr int kSmemKeys = 16384;                 // candidates whose keys fit in shared memory (64 KB); else the workspace
 
 struct Window { int pages, sink, first; };       // pages of the sequence; kept: p < sink or p >= first

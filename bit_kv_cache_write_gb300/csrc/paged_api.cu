@@ -148,7 +148,7 @@ oscar_status oscar_append_bf16(oscar_ctx_t* ctx, const void* k, int64_t k_stride
 
 size_t oscar_decode_bf16_workspace_size(const oscar_ctx_t* ctx, int batch, int max_len) {
     if (!sizes_ok(ctx, batch, max_len)) return 0;
-    return oscar::plan_attend(ctx->shape, ctx->num_sms, batch, pages_of(max_len), false).ws_total;
+    return oscar::attend_workspace_bytes(ctx->shape, ctx->num_sms, batch, pages_of(max_len), false);
 }
 
 oscar_status oscar_decode_bf16(oscar_ctx_t* ctx, const void* q, int64_t q_stride, const void* bf16_pool,
@@ -175,8 +175,7 @@ int oscar_sparse_capacity(const oscar_ctx_t* ctx, int top_pages) {
 
 size_t oscar_decode_bf16_sparse_workspace_size(const oscar_ctx_t* ctx, int batch, int max_len, int top_pages) {
     if (!sizes_ok(ctx, batch, max_len) || top_pages < 0 || top_pages > oscar::kMaxTopPages) return 0;
-    if (oscar::sparse_small_ranks(ctx->shape, ctx->num_sms, batch, pages_of(max_len), top_pages)) return 0;
-    return oscar::plan_attend(ctx->shape, ctx->num_sms, batch, sparse_pages(ctx, max_len, top_pages), true).ws_total +
+    return oscar::attend_workspace_bytes(ctx->shape, ctx->num_sms, batch, sparse_pages(ctx, max_len, top_pages), true) +
            oscar::select_workspace_bytes(ctx->shape, batch, pages_of(max_len));
 }
 

@@ -12,8 +12,11 @@ constexpr int kClusterWarps = 8;         // of a split that a cluster joins
 constexpr int kMaxSplitPages = 256;      // pages of a split at most
 constexpr int kSplitCost = 6;            // pages' time that a split costs apart from its pages
 constexpr int kJoinCost = 16;            // and the join of several
+constexpr int kMaxWaves = 8;             // waves of CTAs, unless kMaxSplitPages asks for more
 // Resident CTAs an SM, by registers (168 and 128 a thread).
 constexpr int attend_ctas(int d, int warps) { return (d == 128 ? 12 : 16) / warps; }
+
+size_t part_bytes(size_t parts, size_t each) { return (parts * each + 255) / 256 * 256; }
 
 // W warps share a split. CLUSTER: the splits of a (sequence, KV head) are a cluster that joins them itself.
 template <int D, bool SPARSE, int W, bool CLUSTER>
@@ -193,7 +196,7 @@ AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages, bo
     // kSplitCost pages' time to start, and the join's kJoinCost. No split is longer than kMaxSplitPages, so that
     // sequences of several lengths share out. 32 sequences of 1,024 tokens, 8 heads: 26.7 us in one split, 30 in three.
     long long best = 0, splits = 1;
-    for (int w = 0; w <= 16 && units > 0; ++w) {
+    for (int w = 0; w <= kMaxWaves && units > 0; ++w) {
         long long n = w * slots / units;
         n = n > most ? most : n;
         if (n < 1) n = 1;
@@ -207,9 +210,19 @@ AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages, bo
     p.pages_per_split = max_pages > 0 ? (int)((max_pages + splits - 1) / splits) : 1;
     p.splits = max_pages > 0 ? (max_pages + p.pages_per_split - 1) / p.pages_per_split : 1;
     const size_t parts = p.splits == 1 ? 0 : (size_t)batch * s.h_q * p.splits;
-    p.ws_acc = (parts * s.d * sizeof(float) + 255) / 256 * 256;
-    p.ws_total = p.ws_acc + (parts * sizeof(float2) + 255) / 256 * 256;
+    p.ws_acc = part_bytes(parts, s.d * sizeof(float));
+    p.ws_total = p.ws_acc + part_bytes(parts, sizeof(float2));
     return p;
+}
+
+size_t attend_workspace_bytes(const Shape& s, int num_sms, int batch, int max_pages, bool sparse) {
+    const int warps = attend_warps(sparse);
+    const long long units = (long long)batch * s.h_kv, most = (max_pages + warps - 1) / warps;
+    const long long waves = (long long)kMaxWaves * attend_ctas(s.d, warps) * num_sms;
+    const long long by_len = units * ((max_pages + kMaxSplitPages - 1) / kMaxSplitPages);
+    const long long bound = waves > by_len ? waves : by_len;
+    const size_t parts = most < 2 ? 0 : (size_t)(units * most < bound ? units * most : bound) * (s.h_q / s.h_kv);
+    return part_bytes(parts, s.d * sizeof(float)) + part_bytes(parts, sizeof(float2));
 }
 
 cudaError_t launch_attend(const AttendArgs& a, int d, cudaStream_t st) {

@@ -60,6 +60,8 @@ struct AttendArgs {
 };
 // max_pages: pages that one (sequence, KV head) reads at most.
 AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages, bool sparse);
+// What plan_attend's workspaces need at most for this many sequences and pages, or fewer of either.
+size_t attend_workspace_bytes(const Shape& s, int num_sms, int batch, int max_pages, bool sparse);
 cudaError_t launch_attend(const AttendArgs& a, int d, cudaStream_t st);
 
 // ---- page selection of the sparse decode (page_select.cu)

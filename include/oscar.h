@@ -395,9 +395,10 @@ typedef enum {
  *   max_len:    host bound of the lengths, <= 16 * table_stride and <= 2^30.
  *   out:        DEVICE [batch][H_q][d] of out_type, 16-byte aligned.
  *   workspace:  DEVICE, >= oscar_decode_bf16_workspace_size(ctx, batch, max_len)
- *               bytes, 256-byte aligned; scratch, nothing in it is kept. It may
- *               be NULL where that size is 0. Calls that overlap on the GPU need
- *               a workspace each.
+ *               bytes, 256-byte aligned; scratch, nothing in it is kept. The
+ *               size serves every smaller batch and max_len too. It may be NULL
+ *               where the size is 0. Calls that overlap on the GPU need a
+ *               workspace each.
  * Tokens behind a sequence's length are not looked at: what they hold, NaN or
  * infinity too, does not matter. The result does not change from run to run.
  * Asynchronous on `stream`. batch == 0 is a no-op; batch > 65535 returns
@@ -425,7 +426,8 @@ OSCAR_API oscar_status oscar_decode_bf16(oscar_ctx_t* ctx, const void* q, int64_
  *   chosen:     DEVICE int32 [batch][H_kv][oscar_sparse_capacity(ctx, top_pages)],
  *               written: the logical pages read, ascending, then -1.
  *   n_chosen:   DEVICE int32 [batch][H_kv], written: how many.
- *   workspace:  >= oscar_decode_bf16_sparse_workspace_size(...) bytes.
+ *   workspace:  >= oscar_decode_bf16_sparse_workspace_size(...) bytes, which
+ *               serve every smaller batch, max_len and top_pages too.
  * Everything else as for oscar_decode_bf16. oscar_sparse_capacity gives 0 on bad
  * arguments. */
 OSCAR_API int oscar_sparse_capacity(const oscar_ctx_t* ctx, int top_pages);

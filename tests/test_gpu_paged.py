@@ -592,9 +592,10 @@ def test_refusals(cuda):
     assert status(ctx.decode_bf16, q, pool, t, n, 65, out, ws) == -1                  # past the table
     assert status(ctx.decode_bf16, q, pool, t, n, -1, out, ws) == -1
     assert status(ctx.decode_bf16, q, pool, t, n, (1 << 30) + 1, out, ws) == -2
-    if ctx.decode_bf16_workspace_size(1, 64):
-        assert status(ctx.decode_bf16, q, pool, t, n, 64, out, ws[:16]) == -7
-        assert status(ctx.decode_bf16, q, pool, t, n, 64, out, ws[8:]) == -1
+    wide = torch.zeros(1, 1024, dtype=I32, device=cuda)
+    assert status(ctx.decode_bf16, q, pool, wide, n, 16384, out, ws[:16]) == -7
+    assert status(ctx.decode_bf16, q, pool, wide, n, 16384, out, None) == -7
+    assert status(ctx.decode_bf16, q, pool, wide, n, 16384, out, torch.zeros(1 << 23, dtype=torch.uint8, device=cuda)[8:]) == -1
     assert status(ctx.decode_bf16, q, pool[:0], t, n, 64, out, ws) == -1
     odd = torch.zeros(1 + 4 * 64, dtype=BF, device=cuda)[1:].view(1, 4, 64)
     assert status(ctx.decode_bf16, odd, pool, t, n, 64, out, ws) == -1
@@ -659,6 +660,30 @@ def test_injected_launch_failure(cuda, monkeypatch):
     with pytest.raises(O.OscarError) as e:
         ctx.append_bf16(k, k, slots, pool)
     assert e.value.status == -4 and float(pool.float().min()) == 1.0
+
+
+def test_a_workspace_serves_smaller_calls(cuda):
+    """Sized once for the largest batch and lengths; the sizes never fall as either grows."""
+    ctx = context(8, 2, 128)
+    sizes = [[ctx.decode_bf16_workspace_size(b, n) for n in (0, 16, 60, 500, 3000, 20000, 131072)] for b in (0, 1, 2, 7, 40, 500, 65535)]
+    assert (np.diff(np.array(sizes, np.float64), axis=0) >= 0).all() and (np.diff(np.array(sizes, np.float64), axis=1) >= 0).all()
+    sizes = [[ctx.decode_bf16_sparse_workspace_size(b, n, t) for n in (16, 500, 20000, 131072, 400000) for t in (0, 9, 300)] for b in (1, 7, 500)]
+    assert (np.diff(np.array(sizes, np.float64), axis=0) >= 0).all()
+    ws = torch.full((ctx.decode_bf16_workspace_size(200, 4000),), 255, dtype=torch.uint8, device=cuda)
+    big = torch.full((ctx.decode_bf16_sparse_workspace_size(200, 4000, 100),), 255, dtype=torch.uint8, device=cuda)
+    for lens in ([4000], [3999, 10], [100] * 30, [2000, 1500] * 8, [600] * 160, [60] * 200):
+        c = Cache(len(lens), lens, 8, 2, 128)
+        want = paged.decode(c.q, c.pool, c.tables, c.lens, 128 ** -0.5)
+        q, pool, t, n = dev(c.q, cuda, BF), dev(c.pool, cuda, BF), dev(c.tables, cuda), dev(c.lens, cuda)
+        out = torch.empty(len(lens), 8, 128, device=cuda)
+        ctx.decode_bf16(q, pool, t, n, int(c.lens.max()), out, ws)
+        close(out.cpu().double().numpy(), want, c.tolerance(want, None, 128 ** -0.5))
+        for top in (3, 100):
+            cap = ctx.sparse_capacity(top)
+            chosen, count = torch.empty(len(lens), 2, cap, dtype=I32, device=cuda), torch.empty(len(lens), 2, dtype=I32, device=cuda)
+            ctx.decode_bf16_sparse(q, pool, dev(c.steps, cuda), dev(c.bounds, cuda), t, n, int(c.lens.max()), top, chosen, count, out, big)
+            want, _ = paged.decode_sparse(c.q, c.pool, c.bounds, c.steps, c.tables, c.lens, top, 64, 256, 128 ** -0.5)
+            close(out.cpu().double().numpy(), want, c.tolerance(want, None, 128 ** -0.5))
 
 
 def test_no_room_for_tokens(cuda):
