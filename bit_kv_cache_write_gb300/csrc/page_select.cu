@@ -11,23 +11,23 @@ __global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int s
     extern __shared__ uint32_t key_store[];
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
-    const int64_t unit = blockIdx.x / ranks;
-    int32_t* list = a.chosen + unit * a.cap;
     const Scored u = score_unit<D, T>(a, smem_keys, codes, s, key_store, [&](const Scored& u) {
         if (rank != 0) return;                           // everything but the selected pages
+        int32_t* list = a.chosen + (int64_t)u.unit * a.cap;
         const int recent = u.recent(), total = u.total();
         for (int i = threadIdx.x; i < u.w.sink; i += T) list[i] = i;
         for (int i = threadIdx.x; i < recent; i += T) list[u.w.sink + u.take + i] = u.w.pages - recent + i;
         for (int i = total + threadIdx.x; i < a.cap; i += T) list[i] = -1;
-        if (threadIdx.x == 0) a.n_chosen[unit] = total;
+        if (threadIdx.x == 0) a.n_chosen[u.unit] = total;
     });
     cluster.sync();
     if (rank != 0) return;
+    int32_t* list = a.chosen + (int64_t)u.unit * a.cap;
     list_selected<T>(u, s, [&](int i, int p) { list[u.w.sink + i] = u.w.sink + p; });
 }
 
 template <int D, int T>
-cudaError_t launch(const SelectArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch(SelectArgs a, int num_sms, cudaStream_t st) {
     const long long units = (long long)a.batch * a.h_kv;
     // CTAs of a cluster: as many as the card holds at once (1,024 threads an SM) with a tile of 16 pages for every
     // warp, and twice as many where each still has kLongShare pages, so that long sequences among short ones spread
@@ -38,6 +38,8 @@ cudaError_t launch(const SelectArgs& a, int num_sms, cudaStream_t st) {
         if (threads > 1024LL * num_sms && (threads > 2048LL * num_sms || a.max_pages < 2 * cluster * kLongShare)) break;
         cluster *= 2;
     }
+    // Where not all clusters run at once the longest sequences go first: that mixed batch 77 us against 83.
+    a.sorted = cluster > 1 && a.batch <= kSortedBatch && cluster * units * T > 1024LL * num_sms;
     if (cluster * units > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int smem_keys = a.max_pages < kSmemKeys ? a.max_pages : kSmemKeys;
     cudaError_t e = smem_opt_in<select_kernel<D, T>>(kSmemKeys * sizeof(uint32_t));

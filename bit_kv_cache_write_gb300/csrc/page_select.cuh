@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kBins = 2048;
 constexpr int kSelectMaxCluster = 16;
+constexpr int kSortedBatch = 64;                 // sequences whose clusters may start with the longest
 constexpr int kLongShare = 1536;                 // candidates that make a CTA's share a long one
 constexpr int kSmemKeys = 16384;                 // candidates whose keys fit in shared memory (64 KB); else the workspace
 
@@ -291,6 +292,7 @@ __device__ void find_threshold(const uint32_t* keys, int n, int take, SelectShar
 
 // What a cluster knows of its (sequence, KV head) once the candidates' keys are there.
 struct Scored {
+    int unit, b, h;                                      // the pair, its sequence and KV head
     int len;                                             // tokens
     Window w;
     int cand, take;                                      // candidates, and how many of them are selected
@@ -299,19 +301,44 @@ struct Scored {
     __device__ int total() const { return w.sink + take + recent(); }
 };
 
-// The cluster's CTAs score the candidates of unit blockIdx.x / ranks; `frame` is called once in each, on the way.
+// The sequence at place `at` in the order of falling length (equal ones in their own order), for the whole CTA;
+// batch <= kSortedBatch.
+__device__ __forceinline__ int longest_first(const int32_t* seq_len, int batch, int at) {
+    __shared__ int lens[kSortedBatch], found;
+    const int i = threadIdx.x, mine = i < batch ? seq_len[i] : 0;
+    if (i < batch) lens[i] = mine;
+    __syncthreads();
+    if (i < batch) {
+        int before = 0;
+        for (int j = 0; j < batch; ++j) before += lens[j] > mine || (lens[j] == mine && j < i);
+        if (before == at) found = i;
+    }
+    __syncthreads();
+    return found;
+}
+
+// The cluster's CTAs score the candidates of pair blockIdx.x / ranks, or of the one at that place among the longest
+// sequences; `frame` is called once in each, on the way.
 template <int D, int T, typename F>
 __device__ Scored score_unit(const SelectArgs& a, int smem_keys, QueryCodes<D>& codes, SelectShared& s, uint32_t* key_store,
                              F frame) {
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
-    const int unit = blockIdx.x / ranks, b = unit / a.h_kv, h = unit % a.h_kv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int i = tid; i < kBins; i += T) s.hist[i] = 0;
     if (tid == 0) { s.range[0] = ~0u; s.range[1] = 0; }
     cluster.sync();                                      // the first CTA runs: its shared memory may be written
     grid_wait();
     grid_release();
+    Scored u;
+    u.unit = blockIdx.x / ranks;
+    u.b = u.unit / a.h_kv;
+    u.h = u.unit % a.h_kv;
+    if (a.sorted) {
+        u.b = longest_first(a.seq_len, a.batch, u.b);
+        u.unit = u.b * a.h_kv + u.h;
+    }
+    const int b = u.b, h = u.h;
     // What does not depend on the length is asked for with it: the query, and the page ids of the first tile
     // (behind the sink, wherever the sequence ends).
     const int tile = rank + ranks * warp, first_page = (a.sink + kPage - 1) / kPage;
@@ -324,12 +351,11 @@ __device__ Scored score_unit(const SelectArgs& a, int smem_keys, QueryCodes<D>& 
     }
     QueryRow<D> query = {};
     if (warp < 8) query = fetch_query<D>(a, b, h, warp);
-    Scored u;
     u.len = checked_len(a.seq_len[b], a.max_len, a.debug && tid == 0 && rank == 0, a.dbg);
     u.w = window_of(a, u.len);
     u.cand = max(u.w.first - u.w.sink, 0);
     u.take = min(a.top, u.cand);
-    uint32_t* keys = u.cand <= smem_keys ? cluster.map_shared_rank(key_store, 0) : a.keys + (int64_t)unit * a.max_pages;
+    uint32_t* keys = u.cand <= smem_keys ? cluster.map_shared_rank(key_store, 0) : a.keys + (int64_t)u.unit * a.max_pages;
     u.keys = u.cand <= smem_keys ? key_store : keys;
     if (u.take > 0 && u.take < u.cand)
         score_pages<D>(a, h, table, u.cand, keys, cluster.map_shared_rank(s.range, 0), tile, ranks * (T / 32), id, codes,

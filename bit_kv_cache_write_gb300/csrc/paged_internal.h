@@ -74,6 +74,7 @@ struct SelectArgs {
     int32_t* chosen; int32_t* n_chosen; int cap;
     uint32_t* keys;                          // [batch][H_kv][max_pages], for sequences too long for shared memory
     int max_pages, top, sink, recent;
+    int sorted;                              // clusters start with the longest sequences
     int h_kv, g, batch;
     int debug; DebugWord* dbg;
 };

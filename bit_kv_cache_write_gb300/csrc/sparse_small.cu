@@ -31,19 +31,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1) sparse_small_kernel(SelectAr
     auto& parts = *reinterpret_cast<WarpParts<D, kSmallWarps>*>(dynamic);
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
-    const int unit = blockIdx.x / ranks, b = unit / a.h_kv, h = unit % a.h_kv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, quad = lane & 3;
-    const int32_t* table = a.tables + (int64_t)b * a.stride;
-    int32_t* list = a.chosen + (int64_t)unit * a.cap;
-
     const Scored u = score_unit<D, kSmallThreads>(a, smem_keys, codes, s, key_store, [&](const Scored& u) {
         if (rank != 0) return;                       // everything but the selected pages
+        int32_t* list = a.chosen + (int64_t)u.unit * a.cap;
         const int recent = u.recent(), total = u.total();
         for (int i = threadIdx.x; i < u.w.sink; i += kSmallThreads) list[i] = i;
         for (int i = threadIdx.x; i < recent; i += kSmallThreads) list[u.w.sink + u.take + i] = u.w.pages - recent + i;
         for (int i = total + threadIdx.x; i < a.cap; i += kSmallThreads) list[i] = -1;
-        if (threadIdx.x == 0) a.n_chosen[unit] = total;
+        if (threadIdx.x == 0) a.n_chosen[u.unit] = total;
     });
+    const int b = u.b, h = u.h;
+    const int32_t* table = a.tables + (int64_t)b * a.stride;
+    int32_t* list = a.chosen + (int64_t)u.unit * a.cap;
     uint4 q[D / 32];
     load_query<D>(q, t, b, h, gid, quad);
     Gathered<D> g;

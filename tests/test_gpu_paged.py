@@ -446,6 +446,22 @@ def test_sparse_matches_the_oracle(cuda, lens, top, h_kv, g, d):
         close(got, want, c.tolerance(want, out_type, d ** -0.5))
 
 
+def test_sparse_with_the_longest_sequences_first(cuda):
+    """Lengths far apart and enough heads that not all clusters run at once (they start with the longest): lists and
+    outputs in the sequences' own order, for equal and empty ones too."""
+    lens = [100, 50000, 0, 16, 50000, 7000, 1, 49000, 300, 300, 20000, 64, 900, 0, 31000, 12]
+    c = Cache(16, lens, 8, 8, 64)
+    want, lists = paged.decode_sparse(c.q, c.pool, c.bounds, c.steps, c.tables, c.lens, 60, 64, 256, 0.125)
+    got, chosen = run_sparse(context(8, 8, 64), c, cuda, torch.float32, 60)
+    assert chosen == lists
+    close(got, want, c.tolerance(want, None, 0.125))
+    wide = Cache(16, lens, 8, 8, 64, pad=6000)                       # a bound of 131k, as a server passes it
+    got, chosen = run_sparse(context(8, 8, 64), wide, cuda, torch.float32, 60, max_len=131072)
+    want, lists = paged.decode_sparse(wide.q, wide.pool, wide.bounds, wide.steps, wide.tables, wide.lens, 60, 64, 256, 0.125)
+    assert chosen == lists
+    close(got, want, wide.tolerance(want, None, 0.125))
+
+
 def test_sparse_beyond_the_keys_that_shared_memory_holds(cuda):
     c = Cache(15, [265001, 40000], 2, 1, 64)
     ctx = context(2, 1, 64)
