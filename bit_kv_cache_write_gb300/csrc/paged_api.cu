@@ -128,10 +128,10 @@ oscar_status oscar_append_bf16(oscar_ctx_t* ctx, const void* k, int64_t k_stride
         return record_failure(OSCAR_ERR_INVALID_ARG, "key_steps and key_bounds go together");
     if (bf16_pool_pages <= 0) return record_failure(OSCAR_ERR_INVALID_ARG, "bf16_pool_pages must be positive");
     if (k_stride < 0 || v_stride < 0 || k_stride % 8 || v_stride % 8 || !aligned(k, 16) || !aligned(v, 16) ||
-        !aligned(bf16_pool, 16) || !aligned(key_bounds, 16))
+        !aligned(bf16_pool, 16) || !aligned(key_bounds, 16) || !aligned(key_steps, 8))
         return record_failure(OSCAR_ERR_INVALID_ARG,
-                              "k, v, the pool and the bounds must be 16-byte aligned, the strides multiples of 8 "
-                              "(are %lld and %lld)", (long long)k_stride, (long long)v_stride);
+                              "k, v, the pool and the bounds must be 16-byte aligned, the steps 8-byte, the strides "
+                              "multiples of 8 (are %lld and %lld)", (long long)k_stride, (long long)v_stride);
     if (oscar::injected_fault("launch"))
         return record_failure(OSCAR_ERR_CUDA, "injected launch failure (OSCAR_FAULT=launch)");
     oscar::AppendArgs a{};

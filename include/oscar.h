@@ -363,8 +363,8 @@ OSCAR_API oscar_status oscar_plan_append(oscar_ctx_t* ctx, const int32_t* seq_le
  *               multiples of 8; the pointers are 16-byte aligned.
  *   slots:      DEVICE int64 [n], distinct BF16 slots. A negative slot skips its
  *               token; one behind the pool does too (recorded with debug_bounds).
- *   key_steps:  DEVICE int8 [H_kv][d], or NULL for no bounds: the bounds of a
- *               channel are in units of 2^key_steps (within +-100).
+ *   key_steps:  DEVICE int8 [H_kv][d], 8-byte aligned, or NULL for no bounds: the
+ *               bounds of a channel are in units of 2^key_steps (within +-100).
  *   key_bounds: DEVICE int8 [bf16_pool_pages][H_kv][2][d], or NULL.
  * The code of a key is clamp(rint(k * 2^-step), -127, 127), 0 for a NaN.
  * key_bounds[page][h] holds the least (0) and the largest (1) code of the rows
