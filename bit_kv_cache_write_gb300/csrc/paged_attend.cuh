@@ -27,7 +27,7 @@ namespace oscar {
 namespace {
 
 constexpr int kAttendMaxCluster = 8;
-constexpr float kNoLogit = -1e30f;       // running reference before any token
+constexpr float kNoLogit = -3.402823466e38f; // running reference before any token: no finite logit is below it
 constexpr float kHeadroom = 8.0f;        // the reference is raised when a logit passes it by this much (log2)
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,

@@ -400,7 +400,10 @@ typedef enum {
  *               where the size is 0. Calls that overlap on the GPU need a
  *               workspace each.
  * Tokens behind a sequence's length are not looked at: what they hold, NaN or
- * infinity too, does not matter. The result does not change from run to run.
+ * infinity too, does not matter. Logits are held in fp32: one that passes its
+ * range counts as infinite. A token whose logit is -infinity has no weight, and a
+ * head that has no other token gives zeros, as for an empty sequence.
+ * The result does not change from run to run.
  * Asynchronous on `stream`. batch == 0 is a no-op; batch > 65535 returns
  * OSCAR_ERR_UNSUPPORTED. */
 OSCAR_API size_t oscar_decode_bf16_workspace_size(const oscar_ctx_t* ctx, int batch, int max_len);
