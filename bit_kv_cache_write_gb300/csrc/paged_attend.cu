@@ -18,6 +18,54 @@ constexpr int attend_ctas(int d, int warps) { return (d == 128 ? 12 : 16) / warp
 
 size_t part_bytes(size_t parts, size_t each) { return (parts * each + 255) / 256 * 256; }
 
+// Block and thread once more, as values that the compiler cannot trace to the first ones: what follows a NaN works out
+// anew what it needs, and the main loop keeps nothing for it in registers (40 bytes of spills and 1 % otherwise).
+struct Place { int block, thread; };
+__device__ __forceinline__ Place place_anew() {
+    Place p;
+    asm volatile("mov.u32 %0, %%ctaid.x;\nmov.u32 %1, %%tid.x;" : "=r"(p.block), "=r"(p.thread));
+    return p;
+}
+
+// A warp's second way over its pages.
+template <int D, bool SPARSE, int W>
+__device__ __forceinline__ void odd_pages(const AttendArgs& a, WarpParts<D, W>& parts) {
+    const Place p = place_anew();
+    const int lane = p.thread & 31, warp = p.thread >> 5, gid = lane >> 2, t = lane & 3;
+    const int unit = p.block / a.splits, h = unit % a.h_kv, b = unit / a.h_kv;
+    const int32_t* table = a.tables + (int64_t)b * a.stride;
+    const int32_t* list = SPARSE ? a.chosen + (int64_t)unit * a.cap : nullptr;
+    const int len = max(0, min(a.seq_len[b], a.max_len)), first = p.block % a.splits * a.pages_per_split;
+    const int last = min(SPARSE ? a.n_chosen[unit] : (len + kPage - 1) / kPage, first + a.pages_per_split);
+    uint4 q[D / 32];
+    load_query<D>(q, a, b, h, gid, t);
+    float sum[D / 16][4] = {};
+    for (int i = first + warp; i < last; i += W) {
+        const int logical = SPARSE ? list[i] : i, id = table[logical];
+        const int valid = id >= 0 && id < a.pages ? min(kPage, len - logical * kPage) : 0;
+        if (valid > 0)
+            odd_page<D>(sum, q, a.pool + ((int64_t)id * a.h_kv + h) * (2 * kPage * D), valid, a.scale_log2, gid, t);
+    }
+    put_sums<D, W>(parts, sum, warp, gid, t);
+}
+
+// The outputs that such a way decides; `odd` has a bit for each of this thread's NaN.
+template <int D, int W>
+__device__ __forceinline__ void rewrite_odd(const AttendArgs& a, const WarpParts<D, W>& parts, uint32_t odd) {
+    const Place p = place_anew();
+    const int unit = p.block / a.splits, split = p.block % a.splits;
+    const int64_t row0 = (int64_t)unit * a.g;
+    for (int x = p.thread; odd; x += W * 32, odd >>= 1) {
+        const int head = x / D, c = x % D;
+        const float o = odd & 1 ? odd_sum<D, W>(parts, head, c) : 0.0f;
+        if (o == 0.0f) continue;
+        float l = 0.0f;                                      // 0, NaN: a head without weight, without result
+        for (int i = 0; i < W; ++i) l += parts.l[i][head];
+        if (a.splits == 1) store_out(a, (row0 + head) * D + c, o, l);
+        else a.split_acc[((row0 + head) * a.splits + split) * D + c] = o;
+    }
+}
+
 // W warps share a split. CLUSTER: the splits of a (sequence, KV head) are a cluster that joins them itself.
 template <int D, bool SPARSE, int W, bool CLUSTER>
 __global__ void __launch_bounds__(W * 32, CLUSTER ? 1 : attend_ctas(D, W)) attend_kernel(AttendArgs a) {
@@ -65,16 +113,19 @@ __global__ void __launch_bounds__(W * 32, CLUSTER ? 1 : attend_ctas(D, W)) atten
     }
 
     put_warp<D, W>(parts, s, warp, gid, t);
-    __syncthreads();
     const int64_t row0 = (int64_t)b * a.h_kv * a.g + h * a.g;
     if (CLUSTER) {
-        join_cluster<D, W, kAttendMaxCluster>(a, parts, row0, split, a.splits);
+        join_cluster<D, W, kAttendMaxCluster>(a, parts, row0, split, a.splits, [&]() { odd_pages<D, SPARSE, W>(a, parts); });
         return;
     }
-    for (int x = threadIdx.x; x < a.g * D; x += W * 32) {
+    __syncthreads();
+    static_assert(8 * D <= 32 * W * 32, "a bit for each output of a thread");
+    uint32_t odd = 0;
+    for (int x = threadIdx.x, n = 0; x < a.g * D; x += W * 32, ++n) {
         const int head = x / D, c = x % D;
         float m, l, o;
         join_warps<D, W>(parts, head, c, m, l, o);
+        odd |= (o != o) << n;
         if (a.splits == 1) {
             store_out(a, (row0 + head) * D + c, o, l);
         } else {
@@ -82,6 +133,10 @@ __global__ void __launch_bounds__(W * 32, CLUSTER ? 1 : attend_ctas(D, W)) atten
             if (c == 0) a.split_ml[(row0 + head) * a.splits + split] = make_float2(m, l);
         }
     }
+    if (!__syncthreads_or(odd)) return;
+    odd_pages<D, SPARSE, W>(a, parts);
+    __syncthreads();
+    rewrite_odd<D, W>(a, parts, odd);
 }
 
 // Joins the splits of query heads, W warps to a head: a warp takes every W-th split, 16 bytes a lane.
@@ -120,6 +175,20 @@ __global__ void __launch_bounds__(THREADS) join_kernel(AttendArgs a) {
             const float f = exp2f(x.x - m);
             l += f * x.y;
             o.x += f * y.x; o.y += f * y.y; o.z += f * y.z; o.w += f * y.w;
+        }
+        if (o.x != o.x || o.y != o.y || o.z != o.z || o.w != o.w) {      // a NaN: infinities may be among its parts
+            float4 r = make_float4(0, 0, 0, 0);
+            for (int i = part * kPer + lane / kLanes; i < n; i += W * kPer) {
+                const float4 y = acc[(int64_t)i * kLanes];
+                const float f = exp2f(ml[i].x - m);
+                // f x, where an infinite x stays one however small f has become
+                const auto add = [f](float& sum, float x) { sum += fabsf(x) == INFINITY ? x : f * x; };
+                add(r.x, y.x); add(r.y, y.y); add(r.z, y.z); add(r.w, y.w);
+            }
+            if (o.x != o.x) o.x = r.x;
+            if (o.y != o.y) o.y = r.y;
+            if (o.z != o.z) o.z = r.z;
+            if (o.w != o.w) o.w = r.w;
         }
         if (kPer == 2) {
             l += __shfl_xor_sync(~0u, l, 16);

@@ -111,14 +111,9 @@ __device__ __forceinline__ void load_query(uint4 (&q)[D / 32], const AttendArgs&
         q[j] = gid < a.g ? *reinterpret_cast<const uint4*>(row + channel_of<D>(j, t)) : make_uint4(0, 0, 0, 0);
 }
 
-// One page of which the first `valid` tokens count.
+// Logits of a page's tokens 2t, 2t + 1, 2t + 8, 2t + 9 for head gid.
 template <int D>
-__device__ __forceinline__ void attend_page(Gathered<D>& s, const uint4 (&q)[D / 32], const uint16_t* page, int valid,
-                                            float scale_log2, int gid, int t) {
-    Page<D> p;
-    load_k<D>(p, page, gid, t);
-    load_v<D>(p, page, gid, t);
-
+__device__ __forceinline__ void page_logits(float (&x)[4], const uint4 (&q)[D / 32], const Page<D>& p, float scale_log2) {
     float c2[2][4] = {};
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -127,9 +122,28 @@ __device__ __forceinline__ void attend_page(Gathered<D>& s, const uint4 (&q)[D /
             mma_bf16(c2[n], q[j].x, 0, q[j].y, 0, p.k[n][j].x, p.k[n][j].y);
             mma_bf16(c2[n], q[j].z, 0, q[j].w, 0, p.k[n][j].z, p.k[n][j].w);
         }
-    float x[4];                      // tokens 2t, 2t + 1, 2t + 8, 2t + 9 of head gid
 #pragma unroll
     for (int n = 0; n < 4; ++n) x[n] = c2[n >> 1][n & 1] * scale_log2;
+}
+
+// V^T as the A operand: channels of m-tile 4 f + u, tokens 2t, 2t + 1 and 2t + 8, 2t + 9.
+__device__ __forceinline__ void pair_tokens(uint32_t (&a)[4], uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+    a[0] = __byte_perm(v0, v1, 0x5410);
+    a[1] = __byte_perm(v0, v1, 0x7632);
+    a[2] = __byte_perm(v2, v3, 0x5410);
+    a[3] = __byte_perm(v2, v3, 0x7632);
+}
+
+// One page of which the first `valid` tokens count.
+template <int D>
+__device__ __forceinline__ void attend_page(Gathered<D>& s, const uint4 (&q)[D / 32], const uint16_t* page, int valid,
+                                            float scale_log2, int gid, int t) {
+    Page<D> p;
+    load_k<D>(p, page, gid, t);
+    load_v<D>(p, page, gid, t);
+
+    float x[4];
+    page_logits<D>(x, q, p, scale_log2);
     if (valid < kPage) {             // masked tokens: no weight, and their V cannot carry a NaN in
 #pragma unroll
         for (int n = 0; n < 4; ++n)
@@ -168,15 +182,52 @@ __device__ __forceinline__ void attend_page(Gathered<D>& s, const uint4 (&q)[D /
     for (int f = 0; f < D / 64; ++f)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const uint32_t v0 = (&p.v[0][f].x)[u], v1 = (&p.v[1][f].x)[u], v2 = (&p.v[2][f].x)[u],
-                           v3 = (&p.v[3][f].x)[u];
-            const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632),
-                           a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+            uint32_t a[4];
+            pair_tokens(a, (&p.v[0][f].x)[u], (&p.v[1][f].x)[u], (&p.v[2][f].x)[u], (&p.v[3][f].x)[u]);
             float c[4] = {};
 #pragma unroll
-            for (int k = 2; k >= 0; --k) mma_bf16(c, a0, a1, a2, a3, w[k][0], w[k][1]);
+            for (int k = 2; k >= 0; --k) mma_bf16(c, a[0], a[1], a[2], a[3], w[k][0], w[k][1]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) s.acc[4 * f + u][k] += c[k];
+        }
+}
+
+// Infinite values. The three pieces of a weight cannot carry them: a zero piece makes NaN of an infinity, a negative
+// one the opposite infinity, and so does a weight or a factor that has shrunk to zero. But an infinity always ends as
+// itself or as NaN, and a NaN stays: where an output is one, the warps go over their pages again. This time only V's
+// infinities and NaN enter, with weight one for every token that has a weight, and a sum other than zero is the output,
+// whatever the finite values add. Without a NaN this costs a comparison an output and a vote: 1,344 tokens of 2 KV heads
+// take 4.5 us against 4.3 without it, longer sequences the same as without.
+
+// Two bf16, zeros in place of finite ones.
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+    return ((x & 0x7f80u) == 0x7f80u ? x & 0xffffu : 0u) | ((x & 0x7f800000u) == 0x7f800000u ? x & 0xffff0000u : 0u);
+}
+
+// What one page of which the first `valid` tokens count adds to those sums, laid out as Gathered::acc.
+template <int D>
+__device__ __forceinline__ void odd_page(float (&sum)[D / 16][4], const uint4 (&q)[D / 32], const uint16_t* page, int valid,
+                                         float scale_log2, int gid, int t) {
+    Page<D> p;
+    load_k<D>(p, page, gid, t);
+    float x[4];
+    page_logits<D>(x, q, p, scale_log2);
+    const auto counts = [&](int n) { return 2 * t + (n & 1) + 8 * (n >> 1) < valid; };
+    uint32_t w[2];                   // 1 where the token has a weight; 0 makes NaN of an infinity, as it should
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+        w[n] = (counts(2 * n) && x[2 * n] > -INFINITY ? 0x3f80u : 0u) |
+               (counts(2 * n + 1) && x[2 * n + 1] > -INFINITY ? 0x3f800000u : 0u);
+    load_v<D>(p, page, gid, t);
+#pragma unroll
+    for (int f = 0; f < D / 64; ++f)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            uint32_t v[4], a[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) v[n] = counts(n) ? not_finite((&p.v[n][f].x)[u]) : 0u;
+            pair_tokens(a, v[0], v[1], v[2], v[3]);
+            mma_bf16(sum[4 * f + u], a[0], a[1], a[2], a[3], w[0], w[1]);
         }
 }
 
@@ -189,7 +240,17 @@ struct WarpParts {
     float acc[W][8][D + 4];
     float m[W][8], l[W][8];
     float cta_m[8], cta_l[8];            // of the CTA, for its cluster; its accumulators replace acc[0]
+    int odd;                             // an accumulator of the CTA, its warps joined, is not finite
 };
+
+template <int D, int W>
+__device__ __forceinline__ void put_sums(WarpParts<D, W>& w, const float (&sum)[D / 16][4], int warp, int gid, int t) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)      // rows gid and gid + 8 of m-tile i are channels D / 8 gid + 2 i and + 1
+            w.acc[warp][2 * t + (k & 1)][8 * (2 * i + (k >> 1)) + gid] = sum[i][k];
+}
 
 template <int D, int W>
 __device__ __forceinline__ void put_warp(WarpParts<D, W>& w, const Gathered<D>& s, int warp, int gid, int t) {
@@ -197,11 +258,7 @@ __device__ __forceinline__ void put_warp(WarpParts<D, W>& w, const Gathered<D>& 
     l += __shfl_xor_sync(~0u, l, 1);
     l += __shfl_xor_sync(~0u, l, 2);
     if (t == 0) { w.m[warp][gid] = s.m; w.l[warp][gid] = l; }
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)      // rows gid and gid + 8 of m-tile i are channels D / 8 gid + 2 i and + 1
-            w.acc[warp][2 * t + (k & 1)][8 * (2 * i + (k >> 1)) + gid] = s.acc[i][k];
+    put_sums<D, W>(w, s.acc, warp, gid, t);
 }
 
 // The warps' parts of one output value joined: its reference, sum of weights and accumulator.
@@ -219,16 +276,29 @@ __device__ __forceinline__ void join_warps(const WarpParts<D, W>& w, int head, i
     }
 }
 
+// The warps' sums of a second way over the pages: 0, an infinity or NaN.
+template <int D, int W>
+__device__ __forceinline__ float odd_sum(const WarpParts<D, W>& w, int head, int c) {
+    float o = 0.0f;
+    for (int i = 0; i < W; ++i) o += w.acc[i][head][place<D>(c)];
+    return o;
+}
+
 // The cluster's CTAs join their parts, each its share of the unit's g x D outputs, and write them. RANKS: CTAs of a
-// cluster at most. All threads of the cluster call it, behind a __syncthreads after put_warp.
-template <int D, int W, int RANKS>
-__device__ __forceinline__ void join_cluster(const AttendArgs& a, WarpParts<D, W>& w, int64_t row0, int rank, int ranks) {
+// cluster at most. All threads of the cluster call it after put_warp; `again` takes a warp over its pages a second
+// time, up to put_sums.
+template <int D, int W, int RANKS, typename G>
+__device__ __forceinline__ void join_cluster(const AttendArgs& a, WarpParts<D, W>& w, int64_t row0, int rank, int ranks,
+                                             G again) {
+    if (threadIdx.x == 0) w.odd = 0;
+    __syncthreads();
     for (int x = threadIdx.x; x < a.g * D; x += W * 32) {
         const int head = x / D, c = x % D;
         float m, l, o;
         join_warps<D, W>(w, head, c, m, l, o);
         w.acc[0][head][place<D>(c)] = o;                    // read by this thread alone so far
         if (c == 0) { w.cta_m[head] = m; w.cta_l[head] = l; }
+        if (!(fabsf(o) < INFINITY)) w.odd = 1;
     }
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     cluster.sync();
@@ -250,7 +320,22 @@ __device__ __forceinline__ void join_cluster(const AttendArgs& a, WarpParts<D, W
         }
         store_out(a, (row0 + head) * D + c, o, l);
     }
+    const int lane = threadIdx.x & 31;
+    const bool odd = __any_sync(~0u, lane < ranks && *cluster.map_shared_rank(&w.odd, lane < ranks ? lane : 0));
     cluster.sync();                                      // the other CTAs have read this one's memory
+    if (!odd) return;
+    again();
+    cluster.sync();
+    for (int x = rank * share + threadIdx.x; x < end; x += W * 32) {
+        const int head = x / D, c = x % D;
+        float o = 0.0f, l = 0.0f;
+        for (int r = 0; r < ranks; ++r) {
+            o += odd_sum(*cluster.map_shared_rank(&w, r), head, c);
+            l += *cluster.map_shared_rank(&w.cta_l[head], r);      // 0, NaN: a head without weight, without result
+        }
+        if (o != 0.0f) store_out(a, (row0 + head) * D + c, o, l);
+    }
+    cluster.sync();
 }
 
 }  // namespace

@@ -75,8 +75,30 @@ __global__ void __launch_bounds__(kSmallThreads, 1) sparse_small_kernel(SelectAr
         attend(e.x, e.y);
     }
     put_warp<D, kSmallWarps>(parts, g, warp, gid, quad);     // the keys have been read
-    __syncthreads();
-    join_cluster<D, kSmallWarps, kSmallCluster>(t, parts, (int64_t)b * t.h_kv * t.g + h * t.g, rank, ranks);
+    const auto again = [&]() {                       // the selected pages, then the windows'
+        const bool windows = rank != 0 || ranks == 1;
+        const int others = ranks > 1 ? ranks - 1 : 1, kept = windows ? u.w.sink + u.recent() : 0;
+        int i = rank + ranks * warp, j = windows ? (ranks > 1 ? rank - 1 : 0) + warp * others : kept;
+        float sum[D / 16][4] = {};
+        while (i < u.take || j < kept) {
+            int id, logical;
+            if (i < u.take) {
+                const int2 e = from[i];
+                id = e.x;
+                logical = e.y;
+                i += ranks * kSmallWarps;
+            } else {
+                logical = j < u.w.sink ? j : u.w.pages - u.recent() + j - u.w.sink;
+                id = table[logical];
+                j += others * kSmallWarps;
+            }
+            const int valid = id >= 0 && id < t.pages ? min(kPage, u.len - logical * kPage) : 0;
+            if (valid > 0)
+                odd_page<D>(sum, q, t.pool + ((int64_t)id * t.h_kv + h) * (2 * kPage * D), valid, t.scale_log2, gid, quad);
+        }
+        put_sums<D, kSmallWarps>(parts, sum, warp, gid, quad);
+    };
+    join_cluster<D, kSmallWarps, kSmallCluster>(t, parts, (int64_t)b * t.h_kv * t.g + h * t.g, rank, ranks, again);
 }
 
 template <int D>

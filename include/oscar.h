@@ -402,7 +402,10 @@ typedef enum {
  * Tokens behind a sequence's length are not looked at: what they hold, NaN or
  * infinity too, does not matter. Logits are held in fp32: one that passes its
  * range counts as infinite. A token whose logit is -infinity has no weight, and a
- * head that has no other token gives zeros, as for an empty sequence.
+ * head that has no other token gives zeros, as for an empty sequence. An infinite
+ * value of a token with weight makes its channel infinite, NaN where another sign
+ * or a NaN meets it. Finite values are summed in fp32 with weights up to 2^8: up
+ * to 2^88 they cannot pass its range.
  * The result does not change from run to run.
  * Asynchronous on `stream`. batch == 0 is a no-op; batch > 65535 returns
  * OSCAR_ERR_UNSUPPORTED. */

@@ -81,3 +81,84 @@ def test_logits_of_any_finite_size_count(cuda, lens, h_q, h_kv, d):
         assert torch.allclose(want[b].view(h_kv, -1, d), v.mean(1)[:, None].expand(-1, h_q // h_kv, -1), rtol=1e-12, atol=1e-12)
         size = v.abs().mean(1)[:, None].expand(-1, h_q // h_kv, -1).reshape(h_q, d)
         assert bool(((out[b] - want[b]).abs() <= size * 64 * 2.0 ** -23).all())       # 17 truncations and the joins' roundings
+
+
+def same_values(out, want, bound):
+    """Infinities and NaN at the same places, the rest within the bound; zeros' bounds are zeros."""
+    got, want, bound = out.double().cpu(), want.cpu(), bound.cpu()
+    assert torch.equal(got.isnan(), want.isnan())
+    odd = ~want.isfinite()
+    assert torch.equal(got[odd & ~want.isnan()], want[odd & ~want.isnan()])
+    within(got[~odd], want[~odd], bound[~odd])
+    return odd
+
+
+def spread_infinities(c, seed):
+    """Infinities of both signs and a few NaN among the values, at places that leave most outputs finite."""
+    r = np.random.default_rng(seed)
+    inf = float("inf")
+    for x in (inf, -inf, inf, -inf, float("nan")):
+        page, h, row, ch = r.integers(300), r.integers(c.h_kv), r.integers(P), r.integers(4, c.d)
+        c.pool[page, h, 1, row, ch] = x
+    for b, n in enumerate(map(int, c.lens)):
+        if n == 0:
+            continue
+        last, h = 300 + b, int(r.integers(c.h_kv))
+        c.pool[last, h, 1, (n - 1) % P, 0] = -inf                          # the last token
+        first = int(c.tables[b, 0])
+        c.pool[first, h, 1, 0, 1] = inf                                    # the first one
+        c.pool[first, h, 1, 0, 2], c.pool[last, h, 1, (n - 1) % P, 2] = inf, -inf      # both: NaN
+        c.pool[first, -1 - h, 1, 0, 3] = c.pool[last, -1 - h, 1, (n - 1) % P, 3] = inf
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -5, 4.0])
+@pytest.mark.parametrize("lens,h_q,h_kv,d", SHAPES + [([0, 1, 33, 500], 4, 2, 64)], ids=str)
+def test_infinite_values(cuda, lens, h_q, h_kv, d, scale):
+    """softmax(..) V with infinities in V: the output's channel is infinite, of either sign, however small the token's
+    weight (scale 4: far below what fp32 holds), NaN where both signs or a NaN meet; other channels and heads as ever."""
+    c = IntCache(41, lens, h_q, h_kv, d)
+    ctx = context(c, scale)
+    clean = dense(ctx, c, cuda), sparse(ctx, c, cuda, 40)
+    spread_infinities(c, 5)
+    for out_type in (torch.float32, BF):
+        out = dense(ctx, c, cuda, out_type)
+        want, bound = c.reference(scale)
+        if out_type == torch.float32:
+            odd = same_values(out, want, bound)
+            assert bool(odd.any()) and torch.equal(out.cpu()[~odd], clean[0].cpu()[~odd])
+            full = out
+        else:
+            assert torch.equal(out.isnan(), full.isnan()) and torch.equal(out[~out.isnan()], full.to(BF)[~full.isnan()])
+    out, lists = sparse(ctx, c, cuda, 40)
+    assert lists == clean[1][1]
+    odd = same_values(out, *c.reference(scale, lists))
+    assert torch.equal(out.cpu()[~odd], clean[1][0].cpu()[~odd])
+
+
+@pytest.mark.parametrize("lens", [[20], [3000, 77]], ids=str)
+def test_infinite_values_of_tokens_without_weight(cuda, lens):
+    """A logit of -infinity weighs zero: with a finite value it adds nothing, zero times infinity is NaN. Behind the
+    length and on pages outside the pool nothing counts."""
+    c = IntCache(42, lens, 4, 2, 64)
+    c.q[:, :, 0] = 1
+    c.pool[:, :, 0, :, 0] = 0
+    c.tables[:, 0] = torch.arange(len(lens), dtype=torch.int32)            # first pages of their own
+    if len(lens) > 1:
+        c.tables[0, 5] = -1
+        for b in range(len(lens)):                                         # and nowhere else
+            rest = c.tables[b, 1:paged.pages_for(lens[b]) - 1]
+            rest[(rest >= 0) & (rest < len(lens))] += 2
+    ctx = context(c, 0.0625)
+    pool = c.pool.clone()
+    c.pool[:len(lens), 0, 0, 4, 0] = -float("inf")
+    without = dense(ctx, c, cuda)
+    assert bool(without.isfinite().all())
+    c.pool[:len(lens), 0, 1, 4, 9] = float("inf")
+    out = dense(ctx, c, cuda)
+    nan = torch.zeros(len(lens), 4, 64, dtype=torch.bool, device=cuda)
+    nan[:, :2, 9] = True
+    assert bool(out[nan].isnan().all()) and torch.equal(out[~nan], without[~nan])
+    c.pool = pool
+    c.pool[:len(lens), :, 1, 4, 9] = float("inf")                          # now it has its weight
+    out = dense(ctx, c, cuda)
+    assert bool((out[:, :, 9] == float("inf")).all()) and bool(out[:, :, :9].isfinite().all())
