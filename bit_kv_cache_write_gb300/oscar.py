@@ -135,10 +135,19 @@ def oscar_create(n_layers, n_q_heads, n_kv_heads, head_dim, group, page_size=16,
                          float(sm_scale), int(debug_bounds), int(codebook))
     ctx = _vp()
     _check(lib().oscar_create(ctypes.byref(cfg), ctypes.byref(ctx)), "oscar_create")
-    import torch
-    _configs[ctx.value] = (n_q_heads, n_kv_heads, head_dim, torch.cuda.current_device(),
-                           lib().oscar_sparse_capacity(ctx, 0))
+    device = _torch_device()
+    if device is not None:
+        _configs[ctx.value] = (n_q_heads, n_kv_heads, head_dim, device, lib().oscar_sparse_capacity(ctx, 0))
     return ctx.value
+
+
+def _torch_device():
+    """The current device as torch counts it, or None: the calls that check their tensors' device need it, no other."""
+    try:
+        import torch
+        return torch.cuda.current_device()
+    except (ImportError, AssertionError, RuntimeError):
+        return None
 
 
 def oscar_destroy(ctx):
@@ -281,7 +290,7 @@ def _config_of(ctx):
     try:
         return _configs[ctx]
     except KeyError:
-        raise ValueError("the context was not created by oscar_create") from None
+        raise ValueError("the context was not created by oscar_create, or torch saw no device then") from None
 
 
 def _stream_on(stream, device):
