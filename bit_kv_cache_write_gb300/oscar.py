@@ -344,6 +344,13 @@ def _rows(t, bf16, heads, d, device, name):
     _refuse(t, bf16, 0, device, name)
 
 
+def _bound(value, name):
+    """An int that the C ABI takes whole (ctypes would cut it to 32 bits)."""
+    if not -0x80000000 <= value <= 0x7fffffff:
+        raise ValueError("%s %s does not fit in 32 bits" % (name, value))
+    return value
+
+
 def _table(t, batch, dtype, device):
     """(pointer, row length) of contiguous block tables [batch][stride]."""
     try:
@@ -352,6 +359,8 @@ def _table(t, batch, dtype, device):
         rows = -1
     if rows != batch:
         raise ValueError("tables must be [%d][stride], got %s" % (batch, tuple(t.shape)))
+    _bound(batch, "batch")
+    _bound(stride, "table stride")
     return _ptr(t, dtype, rows * stride, device, "tables"), stride
 
 
@@ -363,13 +372,6 @@ def _output(out, n, device, torch):
     if dtype is torch.bfloat16:
         return _ptr(out, dtype, n, device, "out"), OSCAR_OUT_BF16
     raise ValueError("out must be torch.float32 or torch.bfloat16, got %s" % dtype)
-
-
-def _bound(value, name):
-    """An int that the C ABI takes whole (ctypes would cut it to 32 bits)."""
-    if not -0x80000000 <= value <= 0x7fffffff:
-        raise ValueError("%s %s does not fit in 32 bits" % (name, value))
-    return value
 
 
 def _scratch(workspace, device):
@@ -391,8 +393,9 @@ def oscar_plan_append(ctx, seq_len, new_len, free_pages, free_head, tables, slot
     tp, ts = _table(tables, batch, i32, dev)
     st = lib().oscar_plan_append(
         ctx, _ptr(seq_len, i32, batch, dev, "seq_len"), _ptr(new_len, i32, batch, dev, "new_len"), batch,
-        _ptr(free_pages, i32, n_free, dev, "free_pages"), n_free, _ptr(free_head, i32, 1, dev, "free_head"), tp, ts,
-        _ptr(slots, torch.int64, n_slots, dev, "slots"), n_slots, _ptr(row_start, i32, batch + 1, dev, "row_start"),
+        _ptr(free_pages, i32, n_free, dev, "free_pages"), _bound(n_free, "free_pages"),
+        _ptr(free_head, i32, 1, dev, "free_head"), tp, ts, _ptr(slots, torch.int64, n_slots, dev, "slots"),
+        _bound(n_slots, "slots"), _ptr(row_start, i32, batch + 1, dev, "row_start"),
         _ptr(total_len, i32, batch, dev, "total_len"), _ptr(state, i32, 4, dev, "state"), _stream_on(stream, dev))
     if st:
         _check(st, "oscar_plan_append")
@@ -414,7 +417,7 @@ def oscar_append_bf16(ctx, k, v, slots, bf16_pool, key_steps=None, key_bounds=No
     if key_steps is not None or key_bounds is not None:
         steps = _ptr(key_steps, torch.int8, h_kv * d, dev, "key_steps")
         bounds = _ptr(key_bounds, torch.int8, pages * h_kv * 2 * d, dev, "key_bounds")
-    st = lib().oscar_append_bf16(ctx, kp, ks, vp, vs, _ptr(slots, torch.int64, n, dev, "slots"), n,
+    st = lib().oscar_append_bf16(ctx, kp, ks, vp, vs, _ptr(slots, torch.int64, n, dev, "slots"), _bound(n, "tokens"),
                                  _ptr(bf16_pool, bf16, size, dev, "bf16_pool"), pages, steps, bounds,
                                  _stream_on(stream, dev))
     if st:
@@ -422,7 +425,7 @@ def oscar_append_bf16(ctx, k, v, slots, bf16_pool, key_steps=None, key_bounds=No
 
 
 def oscar_decode_bf16_workspace_size(ctx, batch, max_len):
-    return lib().oscar_decode_bf16_workspace_size(ctx, batch, max_len)
+    return lib().oscar_decode_bf16_workspace_size(ctx, _bound(batch, "batch"), _bound(max_len, "max_len"))
 
 
 def oscar_decode_bf16(ctx, q, bf16_pool, tables, seq_len, max_len, out, workspace, stream=None):
@@ -444,11 +447,12 @@ def oscar_decode_bf16(ctx, q, bf16_pool, tables, seq_len, max_len, out, workspac
 
 
 def oscar_sparse_capacity(ctx, top_pages):
-    return lib().oscar_sparse_capacity(ctx, top_pages)
+    return lib().oscar_sparse_capacity(ctx, _bound(top_pages, "top_pages"))
 
 
 def oscar_decode_bf16_sparse_workspace_size(ctx, batch, max_len, top_pages):
-    return lib().oscar_decode_bf16_sparse_workspace_size(ctx, batch, max_len, top_pages)
+    return lib().oscar_decode_bf16_sparse_workspace_size(ctx, _bound(batch, "batch"), _bound(max_len, "max_len"),
+                                                         _bound(top_pages, "top_pages"))
 
 
 def oscar_decode_bf16_sparse(ctx, q, bf16_pool, key_steps, key_bounds, tables, seq_len, max_len, top_pages, chosen,
