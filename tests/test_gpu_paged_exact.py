@@ -52,6 +52,26 @@ def within(out, want, bound):
     assert float(off) <= 1, "%.3g of the bound (errors up to %.3g)" % (off, (got - want).abs().max())
 
 
+def check_dense(ctx, c, cuda, scale, max_len=None):
+    """fp32 within the bound; the same again; bf16 the same rounded."""
+    out = dense(ctx, c, cuda, max_len=max_len)
+    within(out, *c.reference(scale, device=cuda))
+    assert torch.equal(dense(ctx, c, cuda, max_len=max_len), out)
+    assert torch.equal(dense(ctx, c, cuda, BF, max_len), out.to(BF))
+
+
+def check_sparse(ctx, c, cuda, top, scale, max_len=None):
+    """The pages that choose() gives, outputs over them within the bound; the same again; bf16 the same rounded."""
+    out, lists = sparse(ctx, c, cuda, top, max_len=max_len)
+    q, steps, bounds, tables = c.q.double().numpy(), c.steps.numpy(), c.bounds.numpy(), c.tables.numpy()
+    for b, n in enumerate(map(int, c.lens)):
+        assert lists[b] == choose(q[b], steps, bounds, tables[b], n, top, SINK, RECENT), b
+    within(out, *c.reference(scale, lists, cuda))
+    again, other = sparse(ctx, c, cuda, top, max_len=max_len)
+    assert other == lists and torch.equal(again, out)
+    assert torch.equal(sparse(ctx, c, cuda, top, BF, max_len)[0], out.to(BF))
+
+
 # each takes another way to join: a cluster, one split, splits joined by one, eight and 32 warps, one-kernel sparse
 SHAPES = [([5], 2, 2, 64), ([700], 8, 2, 128), ([300] * 9, 64, 64, 64), ([4000, 4000], 8, 2, 128), ([40000], 16, 8, 128),
           ([9000], 2, 1, 64)]
@@ -162,3 +182,89 @@ def test_infinite_values_of_tokens_without_weight(cuda, lens):
     c.pool[:len(lens), :, 1, 4, 9] = float("inf")                          # now it has its weight
     out = dense(ctx, c, cuda)
     assert bool((out[:, :, 9] == float("inf")).all()) and bool(out[:, :, :9].isfinite().all())
+
+
+# Dense plans on 152 SMs: 57 splits of 144 pages (36 a warp: ids are looked up a second time); over 400 splits of few
+# pages, joined by 32 warps; splits of 256 pages; one split for each of many sequences; three of some 60 pages
+LONG = [([131072], 16, 8, 128), ([131072], 2, 1, 128), ([131071], 2, 1, 64), ([131000, 2049, 2111, 4097, 0, 8209], 16, 8, 128),
+        ([900] * 100, 8, 8, 128), ([3000] * 12, 8, 8, 128), ([2900] * 60, 16, 8, 64), ([33000, 100, 17], 8, 1, 64), ([70000, 65537], 64, 8, 64)]
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -5, 0.25])
+@pytest.mark.parametrize("lens,h_q,h_kv,d", SHAPES + LONG, ids=lambda x: str(x) if len(str(x)) < 40 else "many")
+def test_dense_is_within_its_rounding(cuda, lens, h_q, h_kv, d, scale):
+    """The last token, every page and every bit of the weights: the bound is below what each of them changes."""
+    c = IntCache(51, lens, h_q, h_kv, d)
+    check_dense(context(c, scale), c, cuda, scale)
+
+
+def test_pages_outside_the_pool_late_in_a_split(cuda):
+    """Ids that are looked up with the second and the third 32 of a warp's pages."""
+    c = IntCache(52, [131000, 30000], 8, 4, 128)
+    for i in (3, 127, 128, 131, 133, 200, 256 + 129, 256 + 130, 1000):
+        c.tables[:, i] = -1 if i % 2 else 10 ** 6
+    check_dense(context(c, 2.0 ** -5), c, cuda, 2.0 ** -5)
+    ctx = context(c, 2.0 ** -5, debug_bounds=1)
+    dense(ctx, c, cuda)
+    assert ctx.debug_error()[:2] == (-5, 2)
+
+
+# Sparse plans: splits of 73 pages (37 a warp) behind clusters of four CTAs of 512 threads; clusters of two of 256 threads
+# where all run at once and where they do not; keys in the workspace; 861 splits joined by 32 warps; the one-kernel form
+# with one, two, four and eight CTAs
+SELECT = [([30000, 20001, 29999, 5000, 30000, 0, 25000, 17], 16, 8, 128, 1000), ([4096] * 10 + [4000, 17, 900] * 4, 8, 8, 128, 30),
+          ([50000] * 30 + [49000, 300, 0, 9000, 50000, 33333, 2, 16, 400, 50000], 8, 8, 128, 20), ([270001, 300], 2, 1, 128, 90),
+          ([131072], 2, 1, 128, 6000), ([400], 4, 2, 128, 3), ([400] * 100, 1, 1, 64, 3), ([900] * 60, 2, 1, 64, 9),
+          ([1500] * 30, 8, 1, 128, 9), ([3000] * 25, 2, 1, 128, 20), ([8000] * 18, 4, 1, 64, 300), ([100000], 32, 8, 128, 256)]
+
+
+@pytest.mark.parametrize("lens,h_q,h_kv,d,top", SELECT, ids=lambda x: str(x) if len(str(x)) < 40 else "many")
+def test_sparse_is_within_its_rounding(cuda, lens, h_q, h_kv, d, top):
+    c = IntCache(53, lens, h_q, h_kv, d)
+    c.bounds[5:9] = 100                                                   # ties
+    check_sparse(context(c, 2.0 ** -5), c, cuda, top, 2.0 ** -5)
+
+
+@pytest.mark.parametrize("lens,h_q,h_kv,d,top", SELECT[:3], ids=lambda x: str(x) if len(str(x)) < 40 else "many")
+def test_sparse_with_room_for_more(cuda, lens, h_q, h_kv, d, top):
+    """A bound of the lengths as a server passes it, twice the longest."""
+    c = IntCache(54, lens, h_q, h_kv, d, pad=paged.pages_for(max(lens)))
+    c.tables[1, 40:43] = torch.tensor([-1, 10 ** 6, -9], dtype=I32)
+    check_sparse(context(c, 0.25), c, cuda, top, 0.25, 2 * max(lens))
+
+
+# ---------------------------------------------------------------------------------------------- plans of many CTAs
+
+def plan(ctx, cuda, seq, new, free, head, tables, cap):
+    dev = lambda x, dt=I32: torch.as_tensor(np.ascontiguousarray(x)).to(dt).to(cuda)
+    batch = len(seq)
+    t, slots = dev(tables), torch.full((cap,), 77, dtype=I64, device=cuda)
+    rows, total, state = (torch.full((n,), 77, dtype=I32, device=cuda) for n in (batch + 1, batch, 4))
+    ctx.plan_append(dev(seq), dev(new), dev(free), dev([head]), t, slots, rows, total, state)
+    return [x.cpu().numpy() for x in (t, slots, rows, total, state)]
+
+
+@pytest.mark.parametrize("batch,new_hi,spare", [(40, 4000, 9), (96, 1500, 5000), (600, 200, 3), (700, 20, 60000), (2100, 60, 11),
+                                                (5000, 3, 9), (5000, 9, 70000)])
+@pytest.mark.parametrize("kind", ["fits", "few_pages", "short_map", "bad_lengths", "all_of_it"])
+def test_plans_of_many_ctas_match_the_oracle(cuda, batch, new_hi, spare, kind):
+    """Slot maps of up to 80,000, clusters of up to 16 CTAs, several chunks of requests, in each some rejected."""
+    r = np.random.default_rng(batch + new_hi)
+    seq, new = r.integers(0, 90, batch), r.integers(0, new_hi + 1, batch)
+    stride = paged.pages_for(90 + new_hi)
+    tables = r.integers(0, 1 << 20, (batch, stride))
+    need = int(sum(paged.pages_for(int(s + n)) - paged.pages_for(int(s)) for s, n in zip(seq, new)))
+    free, head, cap = r.permutation(1 << 17)[:need + 7], 5, int(new.sum()) + spare
+    if kind in ("few_pages", "all_of_it"):
+        free = free[:need // 2]
+    if kind in ("short_map", "all_of_it"):
+        cap = int(new[:-batch // 3].sum())
+    if kind in ("bad_lengths", "all_of_it"):
+        seq[::7], new[3::11] = -1 - seq[::7], -3
+        seq[5::13] = 16 * stride + 1
+    c = IntCache(1, [1], 4, 2, 64)
+    got = plan(context(c), cuda, seq, new, free, head, tables, cap)
+    want = paged.plan_append(seq, new, free, head, tables, cap)
+    for g, w, name in zip(got, want, ("tables", "slots", "row_start", "total_len", "state")):
+        assert np.array_equal(g, w), name
+    assert (kind == "fits") == (want[4][2] == 0)
