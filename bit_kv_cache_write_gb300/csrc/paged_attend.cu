@@ -27,9 +27,9 @@ __device__ __forceinline__ Place place_anew() {
     return p;
 }
 
-// A warp's second way over its pages.
+// A warp's second way over its pages. The queries are still there: `out` may lie over them.
 template <int D, bool SPARSE, int W>
-__device__ __forceinline__ void odd_pages(const AttendArgs& a, WarpParts<D, W>& parts) {
+__device__ __forceinline__ void odd_pages(const AttendArgs& a, WarpParts<D, W>& parts, const uint4 (&q)[D / 32]) {
     const Place p = place_anew();
     const int lane = p.thread & 31, warp = p.thread >> 5, gid = lane >> 2, t = lane & 3;
     const int unit = p.block / a.splits, h = unit % a.h_kv, b = unit / a.h_kv;
@@ -37,8 +37,6 @@ __device__ __forceinline__ void odd_pages(const AttendArgs& a, WarpParts<D, W>& 
     const int32_t* list = SPARSE ? a.chosen + (int64_t)unit * a.cap : nullptr;
     const int len = max(0, min(a.seq_len[b], a.max_len)), first = p.block % a.splits * a.pages_per_split;
     const int last = min(SPARSE ? a.n_chosen[unit] : (len + kPage - 1) / kPage, first + a.pages_per_split);
-    uint4 q[D / 32];
-    load_query<D>(q, a, b, h, gid, t);
     float sum[D / 16][4] = {};
     for (int i = first + warp; i < last; i += W) {
         const int logical = SPARSE ? list[i] : i, id = table[logical];
@@ -115,7 +113,7 @@ __global__ void __launch_bounds__(W * 32, CLUSTER ? 1 : attend_ctas(D, W)) atten
     put_warp<D, W>(parts, s, warp, gid, t);
     const int64_t row0 = (int64_t)b * a.h_kv * a.g + h * a.g;
     if (CLUSTER) {
-        join_cluster<D, W, kAttendMaxCluster>(a, parts, row0, split, a.splits, [&]() { odd_pages<D, SPARSE, W>(a, parts); });
+        join_cluster<D, W, kAttendMaxCluster>(a, parts, row0, split, a.splits, [&]() { odd_pages<D, SPARSE, W>(a, parts, q); });
         return;
     }
     __syncthreads();
@@ -134,7 +132,7 @@ __global__ void __launch_bounds__(W * 32, CLUSTER ? 1 : attend_ctas(D, W)) atten
         }
     }
     if (!__syncthreads_or(odd)) return;
-    odd_pages<D, SPARSE, W>(a, parts);
+    odd_pages<D, SPARSE, W>(a, parts, q);
     __syncthreads();
     rewrite_odd<D, W>(a, parts, odd);
 }

@@ -361,6 +361,7 @@ OSCAR_API oscar_status oscar_plan_append(oscar_ctx_t* ctx, const int32_t* seq_le
  *   k, v:       DEVICE bf16, token i at k + i * k_stride elements, [H_kv][d]
  *               each (a slice of a projection's rows will do). The strides are
  *               multiples of 8; the pointers are 16-byte aligned.
+ *               The rows do not lie in slots that the call writes.
  *   slots:      DEVICE int64 [n], distinct BF16 slots. A negative slot skips its
  *               token; one behind the pool does too (recorded with debug_bounds).
  *   key_steps:  DEVICE int8 [H_kv][d], 8-byte aligned, or NULL for no bounds: the
@@ -393,7 +394,8 @@ typedef enum {
  *   seq_len:    DEVICE int32 [batch], each within [0, max_len]; a length outside
  *               counts as the nearer end. 0 gives zeros.
  *   max_len:    host bound of the lengths, <= 16 * table_stride and <= 2^30.
- *   out:        DEVICE [batch][H_q][d] of out_type, 16-byte aligned.
+ *   out:        DEVICE [batch][H_q][d] of out_type, 16-byte aligned. A bf16 out may
+ *               be q itself where q_stride is H_q * d; no other buffer overlaps it.
  *   workspace:  DEVICE, >= oscar_decode_bf16_workspace_size(ctx, batch, max_len)
  *               bytes, 256-byte aligned; scratch, nothing in it is kept. The
  *               size serves every smaller batch and max_len too. It may be NULL

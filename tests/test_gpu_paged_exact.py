@@ -268,3 +268,25 @@ def test_plans_of_many_ctas_match_the_oracle(cuda, batch, new_hi, spare, kind):
     for g, w, name in zip(got, want, ("tables", "slots", "row_start", "total_len", "state")):
         assert np.array_equal(g, w), name
     assert (kind == "fits") == (want[4][2] == 0)
+
+
+@pytest.mark.parametrize("lens,h_q,h_kv,d", SHAPES, ids=str)
+@pytest.mark.parametrize("odd", [False, True])
+def test_output_in_the_place_of_the_queries(cuda, lens, h_q, h_kv, d, odd):
+    """A bf16 output may be the queries' own tensor, also where an infinite value takes a second look at the pages."""
+    c = IntCache(61, lens, h_q, h_kv, d)
+    ctx = context(c, 0.25)
+    if odd:
+        spread_infinities(c, 3)
+    want, lists = dense(ctx, c, cuda, BF), sparse(ctx, c, cuda, 40, BF)
+    pool, tables, n, batch, top = c.pool.to(cuda), c.tables.to(cuda), torch.from_numpy(c.lens).to(cuda), len(lens), 40
+    ws = torch.empty(max(1, ctx.decode_bf16_workspace_size(batch, max(lens)),
+                         ctx.decode_bf16_sparse_workspace_size(batch, max(lens), top)), dtype=torch.uint8, device=cuda)
+    same = lambda a, b: torch.equal(a.isnan(), b.isnan()) and torch.equal(a[~a.isnan()], b[~b.isnan()])
+    q = c.q.to(cuda)
+    ctx.decode_bf16(q, pool, tables, n, max(lens), q, ws)
+    assert same(q, want)
+    q = c.q.to(cuda)
+    chosen, count = torch.empty(batch, h_kv, ctx.sparse_capacity(top), dtype=I32, device=cuda), torch.empty(batch, h_kv, dtype=I32, device=cuda)
+    ctx.decode_bf16_sparse(q, pool, c.steps.to(cuda), c.bounds.to(cuda), tables, n, max(lens), top, chosen, count, q, ws)
+    assert same(q, lists[0])
