@@ -11,7 +11,7 @@ __global__ void __launch_bounds__(T, 1024 / T) select_kernel(SelectArgs a, int s
     extern __shared__ uint32_t key_store[];
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
-    const Scored u = score_unit<D, T>(a, smem_keys, codes, s, key_store, [&](const Scored& u) {
+    const Scored u = score_unit<D, T, true>(a, smem_keys, codes, s, key_store, [&](const Scored& u) {
         if (rank != 0) return;                           // everything but the selected pages
         int32_t* list = a.chosen + (int64_t)u.unit * a.cap;
         const int recent = u.recent(), total = u.total();

@@ -318,8 +318,8 @@ __device__ __forceinline__ int longest_first(const int32_t* seq_len, int batch, 
 }
 
 // The cluster's CTAs score the candidates of pair blockIdx.x / ranks, or of the one at that place among the longest
-// sequences; `frame` is called once in each, on the way.
-template <int D, int T, typename F>
+// sequences (SORTED, where a.sorted says so); `frame` is called once in each, on the way.
+template <int D, int T, bool SORTED, typename F>
 __device__ Scored score_unit(const SelectArgs& a, int smem_keys, QueryCodes<D>& codes, SelectShared& s, uint32_t* key_store,
                              F frame) {
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
@@ -334,7 +334,7 @@ __device__ Scored score_unit(const SelectArgs& a, int smem_keys, QueryCodes<D>& 
     u.unit = blockIdx.x / ranks;
     u.b = u.unit / a.h_kv;
     u.h = u.unit % a.h_kv;
-    if (a.sorted) {
+    if (SORTED && a.sorted) {
         u.b = longest_first(a.seq_len, a.batch, u.b);
         u.unit = u.b * a.h_kv + u.h;
     }

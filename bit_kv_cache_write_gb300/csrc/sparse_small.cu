@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) sparse_small_kernel(SelectAr
     cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, quad = lane & 3;
-    const Scored u = score_unit<D, kSmallThreads>(a, smem_keys, codes, s, key_store, [&](const Scored& u) {
+    const Scored u = score_unit<D, kSmallThreads, false>(a, smem_keys, codes, s, key_store, [&](const Scored& u) {
         if (rank != 0) return;                       // everything but the selected pages
         int32_t* list = a.chosen + (int64_t)u.unit * a.cap;
         const int recent = u.recent(), total = u.total();
