@@ -123,6 +123,8 @@ def key_steps(k_cal, margin=1.25):
     Per KV head and channel the least power of two 2^step at which ``margin`` times the largest calibration
     magnitude is within the codes' +-127; int8 [H_kv, d], -100 where a channel is always zero."""
     top = np.abs(np.asarray(k_cal, np.float64)).max(axis=0) * margin / 127.0
+    if np.isnan(top).any():
+        raise ValueError("calibration keys contain NaN")
     with np.errstate(divide="ignore"):
         steps = np.ceil(np.log2(top))
     return np.clip(steps, -100, 100).astype(np.int8)
