@@ -31,14 +31,16 @@ cudaError_t launch(SelectArgs a, int num_sms, cudaStream_t st) {
     const long long units = (long long)a.batch * a.h_kv;
     // CTAs of a cluster: as many as the card holds at once (1,024 threads an SM) with a tile of 16 pages for every
     // warp, and twice as many where each still has kLongShare pages, so that long sequences among short ones spread
-    // out. 16 sequences of 4k to 131k (128 units): 84 us with four CTAs, 95 with two; 16 of 32k: 56 and 50.
+    // out. 16 sequences of 4k to 131k (128 units): 76 us with four CTAs, 85 with two, 84 with eight; 16 of 32k: 56 with
+    // four, 50 with two, 55 with one; 64 of 32k 159 with two, 150 with one.
     int cluster = 1;
     while (cluster < kSelectMaxCluster && 2 * cluster * (T / 2) <= a.max_pages) {
         const long long threads = 2 * cluster * units * T;
         if (threads > 1024LL * num_sms && (threads > 2048LL * num_sms || a.max_pages < 2 * cluster * kLongShare)) break;
         cluster *= 2;
     }
-    // Where not all clusters run at once the longest sequences go first: that mixed batch 77 us against 83.
+    // Where not all clusters run at once the longest sequences go first: that mixed batch 76 us against 82. More than
+    // kSortedBatch sequences keep their order: each CTA counts the longer ones, which has not been measured for more.
     a.sorted = cluster > 1 && a.batch <= kSortedBatch && cluster * units * T > 1024LL * num_sms;
     if (cluster * units > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int smem_keys = a.max_pages < kSmemKeys ? a.max_pages : kSmemKeys;
@@ -52,8 +54,8 @@ cudaError_t launch(SelectArgs a, int num_sms, cudaStream_t st) {
 template <int D>
 cudaError_t launch_threads(const SelectArgs& a, int num_sms, cudaStream_t st) {
     const long long units = (long long)a.batch * a.h_kv;
-    // Few sequences: larger CTAs, so that one has the threads for the selection. Mixed batch of 16 (128 units):
-    // 89 us with 512 threads, 93 with 256, 97 with 1,024; batch 64 (512 units) 168, 164 and 182.
+    // Few sequences: larger CTAs, so that one has the threads for the selection. Mixed batch of 16 (128 units): 76 us
+    // with 512 threads, 88 with 256; 64 of 32k (512 units) 154 and 150.
     if (units <= 2 * num_sms && a.max_pages > 256) return launch<D, 512>(a, num_sms, st);
     return launch<D, 256>(a, num_sms, st);
 }

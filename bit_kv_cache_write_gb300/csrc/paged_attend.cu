@@ -6,7 +6,7 @@ namespace oscar {
 namespace {
 
 // Warps that share a split: four for the long splits of a dense decode, two for the short ones of a sparse one
-// (batch 64 at 32k, 148 pages a head: 154 us against 161 with four and 157 with one).
+// (batch 64 at 32k, 148 pages a head: 151 us, 154 with four and 147 with one; 16 of 4k to 131k: 77, 79 and 79).
 constexpr int attend_warps(bool sparse) { return sparse ? 2 : 4; }
 constexpr int kClusterWarps = 8;         // of a split that a cluster joins
 constexpr int kMaxSplitPages = 256;      // pages of a split at most
@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(W * 32, CLUSTER ? 1 : attend_ctas(D, W)) atten
     put_warp<D, W>(parts, s, warp, gid, t);
     const int64_t row0 = (int64_t)b * a.h_kv * a.g + h * a.g;
     if (CLUSTER) {
-        join_cluster<D, W, kAttendMaxCluster>(a, parts, row0, split, a.splits, [&]() { odd_pages<D, SPARSE, W>(a, parts, q); });
+        join_cluster<D, W, kAttendMaxCluster>(a, parts, row0, split, a.splits,
+                                              [&]() { odd_pages<D, SPARSE, W>(a, parts, q); });
         return;
     }
     __syncthreads();
@@ -231,7 +232,9 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
     cudaError_t e = launch_dependent(attend_kernel<D, SPARSE, kWarps, false>, dim3((unsigned)ctas), dim3(kWarps * 32), 0,
                                      st, 1, a);
     if (e != cudaSuccess || a.splits == 1) return e;
-    // few splits: a warp per head; more: a CTA of 8 warps; hundreds (one long sequence, few heads): of 32
+    // Few splits: a warp per head; more: a CTA of 8 warps; hundreds (one long sequence, few heads): of 32. 32 x 4,000
+    // tokens (5 splits) take 86.0 us with a warp, 86.6 with 8; 16 x 4,000 (7) 48.8 and 46.7; 100,000 of eight heads (57)
+    // 72.4 and 65.7, with 32 66.0; of four heads (114) 37.7 with 8 and 37.2 with 32; of one (447) 17.4 and 15.0.
     const long long rows = (long long)a.batch * a.h_kv * a.g;
     if (a.splits > 96)
         return launch_dependent(join_kernel<D, SPARSE, 32, 1024>, dim3((unsigned)rows), dim3(1024), 0, st, 1, a);
@@ -246,8 +249,8 @@ AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages, bo
     AttendPlan p{};
     const long long units = (long long)batch * s.h_kv;
     // Small work, at most two pages a warp: one cluster for each (sequence, KV head) and one launch. 84 pages, two KV
-    // heads: 5.3 us on the GPU as with the join as a kernel, and 7.0 us of host time against 8.5. Clusters of 16 do
-    // not all find their place at once (128 pages, eight heads: 13 us against 7.4).
+    // heads: 4.4 us on the GPU against 4.7 with the join as a kernel, and 7.0 us of host time against 9.2; 125 pages,
+    // eight heads: 6.2 us both. Clusters of 16 do not all find their place at once (13 us there).
     int ranks = 1;
     while (ranks < kAttendMaxCluster && ranks * kClusterWarps < max_pages) ranks *= 2;
     if (max_pages > attend_warps(sparse) && units * ranks <= num_sms && max_pages <= 2 * ranks * kClusterWarps) {
@@ -261,7 +264,7 @@ AttendPlan plan_attend(const Shape& s, int num_sms, int batch, int max_pages, bo
     const long long most = (max_pages + warps - 1) / warps;
     // One split, or splits that fill w waves of CTAs, for the w whose waves take least: a CTA's pages, about
     // kSplitCost pages' time to start, and the join's kJoinCost. No split is longer than kMaxSplitPages, so that
-    // sequences of several lengths share out. 32 sequences of 1,024 tokens, 8 heads: 26.7 us in one split, 30 in three.
+    // sequences of several lengths share out. 32 sequences of 1,024 tokens, 8 heads: 26.6 us in one split, 29.1 in three.
     long long best = 0, splits = 1;
     for (int w = 0; w <= kMaxWaves && units > 0; ++w) {
         long long n = w * slots / units;

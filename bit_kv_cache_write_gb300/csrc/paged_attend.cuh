@@ -15,7 +15,7 @@
 // the fp32 accumulators with rounded additions, so nothing is lost to the bf16 operands.
 //
 // HBM bounds it (g flops a byte): 12 warps an SM with up to 8 KB of a page on its way each. 100,000 tokens of 8 KV
-// heads at batch 1 in 66 us, 92 % of the measured copy rate; 64 x 32,768 in 1.19 ms, 106 % (a copy is slower than
+// heads at batch 1 in 65 us, 93 % of the measured copy rate; 64 x 32,768 in 1.17 ms, 108 % (a copy is slower than
 // reads alone). The tensor cores are a tenth busy; tcgen05 would want its operands in shared memory and 128 rows.
 #pragma once
 
@@ -197,7 +197,7 @@ __device__ __forceinline__ void attend_page(Gathered<D>& s, const uint4 (&q)[D /
 // itself or as NaN, and a NaN stays: where an output is one, the warps go over their pages again. This time only V's
 // infinities and NaN enter, with weight one for every token that has a weight, and a sum other than zero is the output,
 // whatever the finite values add. Without a NaN this costs a comparison an output and a vote: 1,344 tokens of 2 KV heads
-// take 4.5 us against 4.3 without it, longer sequences the same as without.
+// take 4.5 us with and without it on one card, 4.3 and 4.1 on another; longer sequences the same.
 
 // Two bf16, zeros in place of finite ones.
 __device__ __forceinline__ uint32_t not_finite(uint32_t x) {

@@ -10,8 +10,8 @@
 // read from the free list, so no CTA reads what another one writes. The free head may be the word that the
 // new head goes to, so the last barrier stands between every CTA's read of it and the write.
 //
-// Nothing here is large: the time is a chain of dependent loads (lengths, sums, page ids), 3.6 us for 64 single
-// tokens; 94,000 tokens of 96 requests take 8.4 us, their searches and writes on 16 SMs. The kernel does not let
+// Nothing here is large: the time is a chain of dependent loads (lengths, sums, page ids), 3.7 us for 64 single
+// tokens; 94,000 tokens of 96 requests take 8.5 us, their searches and writes on 16 SMs. The kernel does not let
 // its successor start early: page ids and slots may be read ahead by the one after that.
 #include <climits>
 
@@ -70,7 +70,7 @@ __device__ __forceinline__ int upper(const long long* v, int n, long long key) {
 }
 
 // PER: requests that a thread adds up. BULK: a thread writes several slots in a row (one search), else one of each
-// stride's (a shorter program: 64 single tokens take 3.5 us against 5.3).
+// stride's (a shorter program).
 template <int PER, bool BULK>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     constexpr int kPlanPer = PER, kPlanChunk = kPlanThreads * PER;
@@ -207,6 +207,8 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t st) {
     // as many CTAs as have kPlanTokens slots a thread to write
     int cluster = 1;
     while (cluster < kPlanMaxCluster && (long long)cluster * kPlanThreads * kPlanTokens < a.slot_cap) cluster *= 2;
+    // 64 single tokens 3.7 us, in bulk 4.7; 64 x 512 slots 6.0 and 5.3; 64 x 2,000 12.1 and 9.7. Four requests a thread:
+    // 512 single tokens 6.0 us against 4.3 with one, 1,024 6.2 and 7.2, 2,048 8.0 and 13.3.
     const auto kernel = a.batch > 2 * kPlanThreads ? plan_kernel<4, true>
                         : a.slot_cap > 65536       ? plan_kernel<1, true>
                                                    : plan_kernel<1, false>;

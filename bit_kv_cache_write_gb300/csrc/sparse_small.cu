@@ -6,9 +6,9 @@
 // attend to the sink and the recent window; the selected pages come as page ids through the first CTA's shared
 // memory, a page or two a warp, and the cluster joins its warps' parts.
 //
-// 100,000 tokens, 8 KV heads, 256 + 21 pages: 19.9 us on the GPU against 22.3 with separate kernels, and one launch
-// instead of three (3.4 us of host time against 6.8). About 7 us go to the scores, 4.5 to the selection, 9 to the
-// pages and the join: 64 of the 152 SMs fetch them.
+// 100,000 tokens, 8 KV heads, 256 + 21 pages: 20.1 us on the GPU against 20.7 with separate kernels, and one launch
+// instead of three (9.6 us of host time a call against 14.0). About 7 us go to the scores, 4.5 to the selection, 9 to
+// the pages and the join: 64 of the 152 SMs fetch them.
 #include "page_select.cuh"
 #include "paged_attend.cuh"
 
@@ -154,7 +154,10 @@ int sparse_small_ranks(const Shape& s, int num_sms, int batch, int max_pages, in
     while (ranks < kSmallCluster && (ranks * kSmallWarps < (all < max_pages ? all : max_pages) ||
                                      ranks * kSmallThreads / 2 < max_pages) && 2 * ranks * units <= num_sms)
         ranks *= 2;
-    // few selected pages and few tiles a warp, and every cluster on the card at once
+    // Few selected pages and few tiles a warp, and every cluster on the card at once. 100,000 tokens, eight heads: 384
+    // pages 22.2 us against 22.6 with separate kernels, 512 24.1 and 22.7, 1,000 33.2 and 26.1; 4 x 100,000 with 128
+    // pages 24.9 and 29.5, 8 x 60,000 with 64 27.8 and 28.9; 250,000 tokens 26.6 and 29.0. d = 64, two heads, 256 pages:
+    // 14.8 and 13.9, for the one launch.
     if (max_pages == 0 || units * ranks > num_sms || take > ranks * kSmallWarps * kSmallPages ||
         max_pages > ranks * kSmallThreads * 4 || max_pages > kSmemKeys)
         return 0;

@@ -393,7 +393,8 @@ typedef enum {
  *   tables:     DEVICE int32 [batch][table_stride].
  *   seq_len:    DEVICE int32 [batch], each within [0, max_len]; a length outside
  *               counts as the nearer end. 0 gives zeros.
- *   max_len:    host bound of the lengths, <= 16 * table_stride and <= 2^30.
+ *   max_len:    host bound of the lengths, <= 16 * table_stride and <= 2^30. The
+ *               work is split by it: the nearer to the lengths, the faster.
  *   out:        DEVICE [batch][H_q][d] of out_type, 16-byte aligned. A bf16 out may
  *               be q itself where q_stride is H_q * d; no other buffer overlaps it.
  *   workspace:  DEVICE, >= oscar_decode_bf16_workspace_size(ctx, batch, max_len)
