@@ -1,0 +1,102 @@
+// Host side of the calls on chunks of new tokens in include/oscar.h: argument checks, launches.
+#include <cmath>
+
+#include "chunk_internal.h"
+
+namespace {
+
+using oscar::record_failure;
+
+oscar_status cuda_status(cudaError_t e, const char* where) {
+    return e == cudaSuccess ? OSCAR_OK : record_failure(OSCAR_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
+}
+
+bool aligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// n rows of `width` elements, `stride` apart.
+struct Rows {
+    const void* p;
+    int64_t stride, width;
+};
+
+// Whether two sets of n bf16 rows share an element. Sets of one stride that lie in each other's gaps (slices of one
+// row) do not; sets of different strides whose spans meet count as sharing.
+bool share(const Rows& a, const Rows& b, int n) {
+    if (n <= 0 || a.width == 0 || b.width == 0) return false;
+    const intptr_t x = reinterpret_cast<intptr_t>(a.p) / 2, y = reinterpret_cast<intptr_t>(b.p) / 2;
+    const int64_t sa = n > 1 ? a.stride : a.width, sb = n > 1 ? b.stride : b.width;
+    const intptr_t x_end = x + (n - 1) * sa + a.width, y_end = y + (n - 1) * sb + b.width;
+    if (x_end <= y || y_end <= x) return false;
+    if (n == 1 || sa != sb || sa == 0) return true;
+    const int64_t off = ((y - x) % sa + sa) % sa;
+    return off < a.width || sa - off < b.width;
+}
+
+oscar_status check_rows(const char* name, const void* in, int64_t in_stride, const void* out, int64_t out_stride,
+                        const float* weight, int width) {
+    if (!in != !out) return record_failure(OSCAR_ERR_INVALID_ARG, "%s and %s_out go together", name, name);
+    if (!in) return OSCAR_OK;
+    constexpr int64_t kMaxStride = (int64_t)1 << 31;
+    if (in_stride < 0 || in_stride % 8 || in_stride > kMaxStride || out_stride < 0 || out_stride % 8 ||
+        out_stride > kMaxStride || !aligned(in, 16) || !aligned(out, 16) || !aligned(weight, 16))
+        return record_failure(OSCAR_ERR_INVALID_ARG,
+                              "%s, %s_out and the weights must be 16-byte aligned, the strides multiples of 8 up to 2^31 "
+                              "(are %lld and %lld)", name, name, (long long)in_stride, (long long)out_stride);
+    if (out_stride < width)
+        return record_failure(OSCAR_ERR_INVALID_ARG, "%s_out's rows of %d elements overlap (stride %lld)", name, width,
+                              (long long)out_stride);
+    return OSCAR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+oscar_status oscar_norm_rope(oscar_ctx_t* ctx, const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                             const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride, const float* q_weight,
+                             const float* k_weight, float eps, const uint64_t* turns, int rot_dim, int layout,
+                             float scale, const int32_t* positions, const int32_t* row_start, const int32_t* total_len,
+                             int batch, int n, void* stream) {
+    if (oscar_status st = oscar::check_context(ctx); st != OSCAR_OK) return st;
+    const oscar::Shape& s = ctx->shape;
+    if (n < 0 || batch < 0) return record_failure(OSCAR_ERR_INVALID_ARG, "n %d or batch %d negative", n, batch);
+    if (batch > oscar::kMaxBatch)
+        return record_failure(OSCAR_ERR_UNSUPPORTED, "batch %d above %d", batch, oscar::kMaxBatch);
+    if (layout != OSCAR_ROPE_HALF && layout != OSCAR_ROPE_INTERLEAVED)
+        return record_failure(OSCAR_ERR_UNSUPPORTED, "layout %d not in {0 (half), 1 (interleaved)}", layout);
+    if (rot_dim < 0 || rot_dim > s.d || rot_dim % 8)
+        return record_failure(OSCAR_ERR_UNSUPPORTED, "rot_dim %d is not a multiple of 8 in [0, %d]", rot_dim, s.d);
+    if (!(eps >= 0.0f) || !std::isfinite(eps) || !std::isfinite(scale))
+        return record_failure(OSCAR_ERR_INVALID_ARG, "eps %g is not finite and >= 0, or scale %g not finite", eps, scale);
+    if (n == 0 || (!q && !k && !q_out && !k_out)) return OSCAR_OK;
+    if (rot_dim > 0 && !turns) return record_failure(OSCAR_ERR_INVALID_ARG, "turns is NULL");
+    if (!positions && (!row_start || (batch > 0 && !total_len)))
+        return record_failure(OSCAR_ERR_INVALID_ARG, "positions, or row_start and total_len, must be given");
+    const int q_width = s.h_q * s.d, k_width = s.h_kv * s.d;
+    oscar_status st = check_rows("q", q, q_stride, q_out, q_out_stride, q_weight, q_width);
+    if (st == OSCAR_OK) st = check_rows("k", k, k_stride, k_out, k_out_stride, k_weight, k_width);
+    if (st != OSCAR_OK) return st;
+    if (!aligned(turns, 8)) return record_failure(OSCAR_ERR_INVALID_ARG, "turns is not 8-byte aligned");
+    // in place means the very rows: another head's warp may still have to read any other element
+    const Rows qi{q, q_stride, q ? q_width : 0}, qo{q_out, q_out_stride, q ? q_width : 0};
+    const Rows ki{k, k_stride, k ? k_width : 0}, ko{k_out, k_out_stride, k ? k_width : 0};
+    const bool q_same = q == q_out && (n == 1 || q_stride == q_out_stride);
+    const bool k_same = k == k_out && (n == 1 || k_stride == k_out_stride);
+    if ((!q_same && share(qo, qi, n)) || (!k_same && share(ko, ki, n)) || share(qo, ki, n) || share(ko, qi, n) ||
+        share(qo, ko, n))
+        return record_failure(OSCAR_ERR_INVALID_ARG, "outputs overlap each other or other rows than their own input's");
+    if (oscar::injected_fault("launch"))
+        return record_failure(OSCAR_ERR_CUDA, "injected launch failure (OSCAR_FAULT=launch)");
+    oscar::RopeArgs a{};
+    a.q = {static_cast<const uint16_t*>(q), q_stride, static_cast<uint16_t*>(q_out), q_out_stride, q_weight, q ? s.h_q : 0};
+    a.k = {static_cast<const uint16_t*>(k), k_stride, static_cast<uint16_t*>(k_out), k_out_stride, k_weight, k ? s.h_kv : 0};
+    a.eps = eps;
+    a.turns = turns; a.rot = rot_dim; a.interleaved = layout == OSCAR_ROPE_INTERLEAVED; a.scale = scale;
+    a.positions = positions; a.row_start = row_start; a.total_len = total_len;
+    a.batch = batch; a.n = n;
+    oscar::ProfScope ps(&ctx->prof, OSCAR_KERNEL_ROPE, static_cast<cudaStream_t>(stream));
+    return cuda_status(oscar::launch_norm_rope(a, s.d, ctx->num_sms, static_cast<cudaStream_t>(stream)),
+                       "norm and rotation launch");
+}
+
+}  // extern "C"

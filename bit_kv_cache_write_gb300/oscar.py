@@ -68,13 +68,17 @@ _SIGS = {
     "oscar_decode_bf16_sparse_workspace_size": (_sz, [_vp, _i, _i, _i]),
     "oscar_decode_bf16_sparse": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _i,
                                       _vp, _sz, _i, _vp]),
+    "oscar_norm_rope": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, ctypes.c_float, _vp, _i, _i,
+                             ctypes.c_float, _vp, _vp, _vp, _i, _i, _vp]),
     "oscar_profile_enable": (_i, [_vp, _i]),
     "oscar_profile_read": (_i, [_vp, _i, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_longlong)]),
 }
 
 OSCAR_KERNEL_WRITE, OSCAR_KERNEL_QROT, OSCAR_KERNEL_SPLIT, OSCAR_KERNEL_MERGE = 0, 1, 2, 3
 OSCAR_KERNEL_PLAN, OSCAR_KERNEL_APPEND, OSCAR_KERNEL_SELECT, OSCAR_KERNEL_ATTEND = 4, 5, 6, 7
+OSCAR_KERNEL_ROPE = 8
 OSCAR_OUT_FP32, OSCAR_OUT_BF16 = 0, 1
+OSCAR_ROPE_HALF, OSCAR_ROPE_INTERLEAVED = 0, 1
 
 
 def lib():
@@ -479,6 +483,46 @@ def oscar_decode_bf16_sparse(ctx, q, bf16_pool, key_steps, key_bounds, tables, s
         _check(st, "oscar_decode_bf16_sparse")
 
 
+def _pair(x, out, weight, bf16, heads, d, n, device, torch, name):
+    """Pointers and strides of rows, their output's rows and their weights; nothing of either for None."""
+    if x is None and out is None:
+        return None, 0, None, 0, None
+    xp, xs = _rows(x, bf16, heads, d, device, name)
+    op, os_ = _rows(out, bf16, heads, d, device, name + "_out")
+    if x.shape[0] != n or out.shape[0] != n:
+        raise ValueError("%s and %s_out must have %d rows, have %d and %d" % (name, name, n, x.shape[0], out.shape[0]))
+    wp = _ptr(weight, torch.float32, d, device, name + "_weight") if weight is not None else None
+    return xp, xs, op, os_, wp
+
+
+def oscar_norm_rope(ctx, q, k, q_out, k_out, turns, positions=None, row_start=None, total_len=None, q_weight=None,
+                    k_weight=None, eps=1e-6, layout=OSCAR_ROPE_HALF, scale=1.0, stream=None):
+    """q bf16 [n][H_q][d] -> q_out, k bf16 [n][H_kv][d] -> k_out, rows at any stride, either pair None; turns int64
+    [rot_dim / 2] (rope.rope_turns) or None; positions int32 [n], or row_start int32 [B + 1] and total_len int32 [B]
+    of the plan; weights fp32 [d] or None."""
+    import torch
+    h_q, h_kv, d, dev, _ = _config_of(ctx)
+    bf16, i32 = torch.bfloat16, torch.int32
+    n = q.shape[0] if q is not None else k.shape[0] if k is not None else 0
+    qp, qs, qop, qos, qw = _pair(q, q_out, q_weight, bf16, h_q, d, n, dev, torch, "q")
+    kp, ks, kop, kos, kw = _pair(k, k_out, k_weight, bf16, h_kv, d, n, dev, torch, "k")
+    half = turns.numel() if turns is not None else 0
+    pp = _ptr(positions, i32, n, dev, "positions") if positions is not None else None
+    batch, rp, tp = 0, None, None
+    if pp is None:
+        if row_start is None or total_len is None:
+            raise ValueError("positions, or row_start and total_len, must be given")
+        batch = total_len.numel()
+        rp, tp = _ptr(row_start, i32, batch + 1, dev, "row_start"), _ptr(total_len, i32, batch, dev, "total_len")
+    st = lib().oscar_norm_rope(
+        ctx, qp, qs, qop, qos, kp, ks, kop, kos, qw, kw, eps,
+        _ptr(turns, torch.int64, half, dev, "turns") if half else None, _bound(2 * half, "rot_dim"),
+        _bound(layout, "layout"), scale, pp, rp, tp, _bound(batch, "batch"), _bound(n, "tokens"),
+        _stream_on(stream, dev))
+    if st:
+        _check(st, "oscar_norm_rope")
+
+
 def oscar_debug_error(ctx):
     """Returns (status, kind, index) and clears the device error word."""
     kind = _i(0)
@@ -571,6 +615,11 @@ class Oscar:
                            n_chosen, out, workspace, stream=None):
         oscar_decode_bf16_sparse(self.ctx, q, bf16_pool, key_steps, key_bounds, tables, seq_len, max_len, top_pages,
                                  chosen, n_chosen, out, workspace, stream)
+
+    def norm_rope(self, q, k, q_out, k_out, turns, positions=None, row_start=None, total_len=None, q_weight=None,
+                  k_weight=None, eps=1e-6, layout=OSCAR_ROPE_HALF, scale=1.0, stream=None):
+        oscar_norm_rope(self.ctx, q, k, q_out, k_out, turns, positions, row_start, total_len, q_weight, k_weight, eps,
+                        layout, scale, stream)
 
     def int2_page_bytes(self):
         return oscar_int2_page_bytes(self.ctx)

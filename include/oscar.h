@@ -449,6 +449,55 @@ OSCAR_API oscar_status oscar_decode_bf16_sparse(oscar_ctx_t* ctx, const void* q,
                                                 void* out, int out_type, void* workspace, size_t workspace_bytes,
                                                 int batch, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Chunks of new tokens: norm and rotation
+ * ---------------------------------------------------------------------------
+ * What stands between a layer's projections and the caches (no counterpart on
+ * the pages, whose caches hold keys as attention reads them). */
+
+/* Which channels of a head turn together, pair i of rot_dim / 2. */
+typedef enum {
+    OSCAR_ROPE_HALF = 0,          /* i and rot_dim / 2 + i */
+    OSCAR_ROPE_INTERLEAVED = 1    /* 2 i and 2 i + 1 */
+} oscar_rope_layout;
+
+/* RMS norm of every head of the new queries and keys, and the rotation of its
+ * first rot_dim channels by the token's position, in one pass:
+ *   y = w * x / sqrt(mean(x^2) + eps)     (y = x where the weight is NULL)
+ *   (a', b') = scale * (a cos t - b sin t, b cos t + a sin t) per pair i (a, b),
+ *   t = 2 pi * frac(position * turns[i] * 2^-64); channels from rot_dim on are y.
+ * All in fp32 (the angle's remainder in exact integers), rounded once to bf16.
+ *   q:          DEVICE bf16, token i at q + i * q_stride elements, [H_q][d] (a
+ *               slice of a projection's rows will do), or NULL with q_out.
+ *   q_out:      DEVICE bf16, likewise; q itself (at the same stride), or rows that
+ *               share no element with another argument's. An output whose span meets
+ *               that of rows of another stride is refused.
+ *   k, k_out:   the same for [H_kv][d].
+ *               Pointers are 16-byte aligned; strides are multiples of 8, up to
+ *               2^31, the outputs' at least a row.
+ *   q_weight, k_weight: DEVICE fp32 [d], 16-byte aligned, or NULL: no norm.
+ *   eps:        finite, >= 0. A head of zeros with eps 0 gives NaN.
+ *   turns:      DEVICE uint64 [rot_dim / 2]: pair i turns turns[i] * 2^-64 of a
+ *               full turn a position (rope.rope_turns makes it, for contexts
+ *               longer than the trained one too). May be NULL where rot_dim is 0.
+ *   rot_dim:    multiple of 8, 0 .. d. layout: an oscar_rope_layout.
+ *   scale:      of the rotated channels alone (1 without context scaling).
+ *   positions:  DEVICE int32 [n], the tokens' positions (any, negative ones too),
+ *               or NULL: row i belongs to the request b with row_start[b] <= i <
+ *               row_start[b + 1], its position is total_len[b] - row_start[b + 1]
+ *               + i, as oscar_plan_append's outputs have it.
+ *   row_start:  DEVICE int32 [batch + 1], ascending; total_len: DEVICE int32
+ *               [batch]. Neither is read where positions is given.
+ *   n:          rows. Without positions, those behind the last request are left as
+ *               they were.
+ * Asynchronous on `stream`. n == 0, or neither q nor k, is a no-op. */
+OSCAR_API oscar_status oscar_norm_rope(oscar_ctx_t* ctx, const void* q, int64_t q_stride, void* q_out,
+                                       int64_t q_out_stride, const void* k, int64_t k_stride, void* k_out,
+                                       int64_t k_out_stride, const float* q_weight, const float* k_weight, float eps,
+                                       const uint64_t* turns, int rot_dim, int layout, float scale,
+                                       const int32_t* positions, const int32_t* row_start, const int32_t* total_len,
+                                       int batch, int n, void* stream);
+
 /* Bytes of one INT2 page (all heads, K and V) and of one BF16 page. */
 OSCAR_API size_t oscar_int2_page_bytes(const oscar_ctx_t* ctx);
 OSCAR_API size_t oscar_bf16_page_bytes(const oscar_ctx_t* ctx);
@@ -463,7 +512,8 @@ typedef enum {
     OSCAR_KERNEL_APPEND = 5,  /* oscar_append_bf16 */
     OSCAR_KERNEL_SELECT = 6,  /* page scores and selection of the sparse decode */
     OSCAR_KERNEL_ATTEND = 7,  /* attention over BF16 pages and the join of its splits */
-    OSCAR_KERNEL_COUNT = 8
+    OSCAR_KERNEL_ROPE = 8,    /* oscar_norm_rope */
+    OSCAR_KERNEL_COUNT = 9
 } oscar_kernel_id;
 
 /* Measurement hook (no counterpart on the pages): while enabled, every launch
