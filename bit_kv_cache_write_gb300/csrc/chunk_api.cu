@@ -48,6 +48,12 @@ oscar_status check_rows(const char* name, const void* in, int64_t in_stride, con
     return OSCAR_OK;
 }
 
+// Largest batch and row count of an attention call: row and part indices stay in 32 bits.
+constexpr int kMaxChunkTokens = 1 << 24;
+bool sizes_ok(const oscar_ctx_t* ctx, int batch, int n) {
+    return ctx && batch >= 0 && batch <= oscar::kMaxBatch && n >= 0 && n <= kMaxChunkTokens;
+}
+
 }  // namespace
 
 extern "C" {
@@ -97,6 +103,57 @@ oscar_status oscar_norm_rope(oscar_ctx_t* ctx, const void* q, int64_t q_stride, 
     oscar::ProfScope ps(&ctx->prof, OSCAR_KERNEL_ROPE, static_cast<cudaStream_t>(stream));
     return cuda_status(oscar::launch_norm_rope(a, s.d, ctx->num_sms, static_cast<cudaStream_t>(stream)),
                        "norm and rotation launch");
+}
+
+size_t oscar_extend_bf16_workspace_size(const oscar_ctx_t* ctx, int batch, int n) {
+    if (!sizes_ok(ctx, batch, n) || batch == 0 || n == 0) return 0;
+    return oscar::plan_chunk(ctx->shape, ctx->num_sms, batch, n).total;
+}
+
+oscar_status oscar_extend_bf16(oscar_ctx_t* ctx, const void* q, int64_t q_stride, const void* bf16_pool,
+                               int64_t bf16_pool_pages, const int32_t* tables, int table_stride,
+                               const int32_t* row_start, const int32_t* total_len, int batch, int n, void* out,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+    if (oscar_status st = oscar::check_context(ctx); st != OSCAR_OK) return st;
+    const oscar::Shape& s = ctx->shape;
+    if (n < 0 || batch < 0 || table_stride < 0)
+        return record_failure(OSCAR_ERR_INVALID_ARG, "n %d, batch %d or table_stride %d negative", n, batch, table_stride);
+    if (!sizes_ok(ctx, batch, n) || table_stride > oscar::kMaxPagedLen / oscar::kPage)
+        return record_failure(OSCAR_ERR_UNSUPPORTED, "batch %d above %d, n %d above %d or table_stride %d above %d", batch,
+                              oscar::kMaxBatch, n, kMaxChunkTokens, table_stride, oscar::kMaxPagedLen / oscar::kPage);
+    if (n == 0 || batch == 0) return OSCAR_OK;
+    if (!q || !out || !row_start || !total_len) return record_failure(OSCAR_ERR_INVALID_ARG, "device pointer is NULL");
+    if (!bf16_pool || bf16_pool_pages <= 0 || (table_stride > 0 && !tables))
+        return record_failure(OSCAR_ERR_INVALID_ARG, "BF16 pool/tables missing");
+    if (bf16_pool_pages > 0x7ffffff0LL / (2 * s.h_kv))
+        return record_failure(OSCAR_ERR_UNSUPPORTED, "bf16_pool_pages %lld above %lld", (long long)bf16_pool_pages,
+                              0x7ffffff0LL / (2 * s.h_kv));
+    const int width = s.h_q * s.d;
+    if (q_stride < 0 || q_stride % 8 || q_stride > (int64_t)1 << 31 || !aligned(q, 16) || !aligned(bf16_pool, 32) ||
+        !aligned(out, 16))
+        return record_failure(OSCAR_ERR_INVALID_ARG,
+                              "q and out must be 16-byte aligned, the pool 32-byte, q_stride a multiple of 8 up to 2^31 (is %lld)",
+                              (long long)q_stride);
+    if (!(q == out && (n == 1 || q_stride == width)) && share({q, q_stride, width}, {out, width, width}, n))
+        return record_failure(OSCAR_ERR_INVALID_ARG, "out overlaps q without being it");
+    const oscar::ChunkPlan plan = oscar::plan_chunk(s, ctx->num_sms, batch, n);
+    if (!workspace || workspace_bytes < plan.total)
+        return record_failure(OSCAR_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace_bytes, plan.total);
+    if (!aligned(workspace, 256)) return record_failure(OSCAR_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+    if (oscar::injected_fault("launch"))
+        return record_failure(OSCAR_ERR_CUDA, "injected launch failure (OSCAR_FAULT=launch)");
+    oscar::ChunkArgs a{};
+    a.q = static_cast<const uint16_t*>(q); a.q_stride = q_stride;
+    a.pool = static_cast<const uint16_t*>(bf16_pool); a.pages = bf16_pool_pages;
+    a.tables = tables; a.stride = table_stride;
+    a.row_start = row_start; a.total_len = total_len;
+    a.out = static_cast<uint16_t*>(out);
+    a.batch = batch; a.n = n; a.h_kv = s.h_kv; a.g = s.h_q / s.h_kv;
+    a.scale_log2 = (float)(s.sm_scale * 1.4426950408889634073599);
+    a.debug = s.debug; a.dbg = ctx->dbg;
+    oscar::ProfScope ps(&ctx->prof, OSCAR_KERNEL_EXTEND, static_cast<cudaStream_t>(stream));
+    return cuda_status(oscar::launch_chunk(a, plan, workspace, s.d, ctx->num_sms, static_cast<cudaStream_t>(stream)),
+                       "chunk attention launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,958 @@
+// Attention of chunks of new tokens over a paged BF16 cache (oscar_extend_bf16).
+//
+//   out_i = sum_t w_t v_t / sum_t w_t,  w_t = 2^(c q_i.k_t - m),  t <= pos_i,  c = sm_scale log2(e)
+// with a running reference m that is raised only when a logit passes it by 2^8 (the lazy online softmax of the
+// decodes). The query rows of a (request, KV head) are its tokens times the g heads of the group, token by token, so
+// that the group's heads share every K and V tile.
+//
+// One CTA an SM takes work items: 256 query rows (two blocks of 128) against a range of 128-token tiles of the cache.
+//   warp 8      loads: K and V pages through TMA (page ids looked up four tiles at a time), 128-byte swizzle;
+//   warp 9      issues tcgen05.mma: S = Q K^T (128 x 128 x d) into tensor memory, O += P V with P read from tensor
+//               memory; a block's next S is issued behind its P V, so the softmax of one block runs under the
+//               matrix products of the other;
+//   warps 0..7  one warp group a block, a thread a row: the row's 128 logits in registers, weights rounded to bf16
+//               over the logits' own columns, O scaled only where the reference rises.
+// The weights' rounding to bf16 is the operand type of the product (a second piece would cost half again of the
+// tensor time that bounds long prompts). Their sum takes the rounded weights, in fp32, so each output is an exactly
+// normalised mean with weights off by 2^-8 at most; it is then rounded once to bf16.
+//
+// Items of requests with long caches and few rows are cut along the cache: chunk_plan_kernel chooses the cut from the
+// lengths on the device, so that the items fill the SMs evenly; chunk_join_kernel adds the parts of cut items.
+//
+// A weight of 0 does not undo an infinity or NaN in the value of a token that a row must not see (0 x inf): rows whose
+// accumulator is not finite are formed again token by token, with the tokens that they see alone.
+//
+// Every wait is bounded: a role that gives up records kind 4 and sets a flag, the others stop, copies and matrix
+// products in flight are waited for (bounded too), tensor memory is freed.
+#include <cudaTypedefs.h>
+
+#include "chunk_internal.h"
+#include "paged_device.cuh"
+#include "tc_device.cuh"
+
+namespace oscar {
+namespace {
+
+constexpr int kBlock = 128;                      // query rows of a block
+constexpr int kTilePages = kChunkTile / kPage;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = 384;                    // two softmax warp groups, one of loader and issuer
+constexpr int kMaskRing = 16;                    // tiles whose page masks are kept: more than the loader is ahead
+constexpr int kPlanThreads = 1024;
+constexpr int kJoinThreads = 256;
+constexpr float kNoReference = -3.402823466e38f; // reference before any token: no finite logit is below it
+constexpr float kHeadroom = 8.0f;                // the reference rises when a logit passes it by this much (log2)
+constexpr long long kWaitCycles = 2000000000LL;
+
+// A work item: rows r0 .. r0 + rows of request b's row space against cache tiles [kv0, kv1).
+struct alignas(16) Item {
+    int b, head, tok0, r0;        // tok0: the request's first row of q
+    int rows, pos0, kv0, kv1;     // pos0: position of the request's first new token (below 0 where it has no room)
+    int total, part, piece, pieces;   // part: first row of its partial results, or -1
+};
+static_assert(sizeof(Item) == 48, "copied as twelve words");
+
+struct Header {
+    int items, next;              // next: item after the CTAs' first ones
+};
+
+struct Work {
+    Header* head;
+    int* tiles;                   // [batch + 1] first row block of each request
+    int2* units;                  // per row block: request, cache tiles
+    Item* items;
+    float2* part_ml;              // per row of a cut item: reference and sum
+    float* part_acc;              // [rows][d]
+};
+
+__device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
+
+// The request's rows of q and the position of its first new token.
+struct Request {
+    int tok0, count, total, pos0;
+};
+__device__ __forceinline__ Request request(const ChunkArgs& a, int b) {
+    Request r;
+    r.tok0 = clamp_int(a.row_start[b], 0, a.n);
+    r.count = clamp_int(a.row_start[b + 1], r.tok0, a.n) - r.tok0;
+    r.total = checked_len(a.total_len[b], a.stride * kPage, a.debug, a.dbg);
+    r.pos0 = r.total - r.count;
+    return r;
+}
+
+// Cached tokens that row r of a request's row space sees.
+__device__ __forceinline__ int limit_of(int r, int pos0, int g_log2) { return max(pos0 + (r >> g_log2) + 1, 0); }
+
+// ---- plan ---------------------------------------------------------------------------------------------------
+
+// Exclusive sum over the block; every thread gets the total too.
+__device__ int block_scan(int x, int* shared, int& total) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    __syncthreads();
+    if (lane == 31) shared[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        int w = shared[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        shared[lane] = w;
+    }
+    __syncthreads();
+    total = shared[31];
+    return s - x + (warp ? shared[warp - 1] : 0);
+}
+
+// The last i in [0, n) with at[i] <= x; at[0] <= x.
+__device__ __forceinline__ int last_at_most(const int* at, int n, int x) {
+    int lo = 0;
+    while (n > 1) {
+        const int half = n / 2;
+        if (at[lo + half] <= x) {
+            lo += half;
+            n -= half;
+        } else {
+            n = half;
+        }
+    }
+    return lo;
+}
+
+// Work items from the lengths, by one CTA. Cutting every row block's tiles into pieces of at most L gives items whose
+// time on `sms` SMs is at most min(waves * (L + s), all / sms + L + s), s the cost of starting an item; each warp
+// tries one L. A cut item costs its share of the join, hence no L below half an SM's share.
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArgs a, const Work w, int unit_cap,
+                                                                  int item_cap, int part_cap, int sms) {
+    __shared__ int shared[32];
+    __shared__ long long sum;
+    __shared__ int longest;
+    __shared__ float cost[32];
+    __shared__ int first_item[kPlanThreads], unit_pieces[kPlanThreads], first_part[kPlanThreads];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int g_log2 = 31 - __clz(a.g);
+    constexpr int kStart = 3;                    // tiles' worth of starting an item
+    grid_release();
+    if (tid == 0) { sum = 0; longest = 0; }
+    grid_wait();
+
+    // row blocks of each request, numbered through; a request's last block, which sees the most, comes first
+    int base = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int blocks = 0;
+        if (b < a.batch) {
+            const Request r = request(a, b);
+            blocks = (int)(((long long)r.count * a.g + kChunkRows - 1) / kChunkRows);
+        }
+        int total;
+        const int at = block_scan(blocks, shared, total);
+        if (b < a.batch) w.tiles[b] = base + at;
+        base += total;
+    }
+    if (tid == 0) w.tiles[a.batch] = base;
+    const int units = min(base, unit_cap);       // more only where the starts do not ascend
+    __syncthreads();
+    int my_longest = 0;
+    long long my_sum = 0;
+    for (int u = tid; u < units; u += kPlanThreads) {
+        const int b = last_at_most(w.tiles, a.batch, u);
+        const Request r = request(a, b);
+        const int last = min((w.tiles[b + 1] - u) * kChunkRows, r.count * a.g) - 1;
+        const int tiles = (limit_of(last, r.pos0, g_log2) + kChunkTile - 1) / kChunkTile;
+        w.units[u] = make_int2(b, tiles);
+        my_longest = max(my_longest, tiles);
+        my_sum += tiles;
+    }
+    atomicMax(&longest, my_longest);
+    atomicAdd(reinterpret_cast<unsigned long long*>(&sum), (unsigned long long)my_sum);
+    __syncthreads();
+    const long long all = sum * a.h_kv;
+    // L of this warp: an SM's share times 2^(1 - warp / 15), the last warp without a cut
+    const int share = (int)((all + sms - 1) / sms);
+    auto length_of = [&](int i) {
+        return i == 31 ? max(longest, 1) : max(1, (int)ceilf((float)share * exp2f(1.0f - (float)i / 15.0f)));
+    };
+    {
+        const int len = min(length_of(warp), max(longest, 1));
+        long long pieces = 0;
+        for (int u = lane; u < units; u += 32) pieces += max(1, (w.units[u].y + len - 1) / len);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
+        pieces *= a.h_kv;
+        const float one = (float)(len + kStart);
+        const float waves = (float)((pieces + sms - 1) / sms) * one;
+        const float packed = ((float)all + (float)(kStart * pieces)) / (float)sms + one;
+        if (lane == 0) cost[warp] = fminf(waves, packed);
+    }
+    __syncthreads();
+    int best = 31;
+    for (int i = 30; i >= 0; --i)
+        if (cost[i] < cost[best]) best = i;
+    const int len = length_of(best);
+
+    int item_base = 0, part_base = 0;
+    for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
+        const int u = u0 + tid;
+        int pieces = 0, rows = 0;
+        if (u < units) {
+            const int2 unit = w.units[u];
+            pieces = max(1, (unit.y + len - 1) / len);
+            rows = pieces > 1 ? pieces * a.h_kv * min(kChunkRows, request(a, unit.x).count * a.g - (w.tiles[unit.x + 1] - 1 - u) * kChunkRows) : 0;
+        }
+        int items, parts;
+        first_item[tid] = block_scan(pieces * a.h_kv, shared, items);
+        first_part[tid] = block_scan(rows, shared, parts);
+        unit_pieces[tid] = pieces;
+        __syncthreads();
+        items = min(items, item_cap - item_base);
+        for (int i = tid; i < items; i += kPlanThreads) {
+            const int at = last_at_most(first_item, min(kPlanThreads, units - u0), i);
+            const int2 unit = w.units[u0 + at];
+            const Request r = request(a, unit.x);
+            const int p = unit_pieces[at], rest = i - first_item[at];
+            Item it;
+            it.b = unit.x;
+            it.head = rest % a.h_kv;
+            it.tok0 = r.tok0;
+            it.r0 = (w.tiles[unit.x + 1] - 1 - (u0 + at)) * kChunkRows;
+            it.rows = min(kChunkRows, r.count * a.g - it.r0);
+            it.pos0 = r.pos0;
+            it.piece = rest / a.h_kv;
+            it.pieces = p;
+            it.kv0 = (int)((long long)unit.y * it.piece / p);
+            it.kv1 = (int)((long long)unit.y * (it.piece + 1) / p);
+            it.total = r.total;
+            const int part = part_base + first_part[at] + (it.head * p + it.piece) * it.rows;
+            it.part = p > 1 ? min(part, part_cap - it.rows) : -1;
+            w.items[item_base + i] = it;
+        }
+        item_base += items;
+        part_base += parts;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        w.head->items = item_base;
+        w.head->next = 0;
+    }
+}
+
+// ---- attention ----------------------------------------------------------------------------------------------
+
+template <int D>
+struct Layout {
+    static constexpr int kHalves = D / 64;                     // blocks of 64 channels, 128 bytes a row
+    static constexpr int kHalfBytes = kChunkTile * 128;        // such a block of a K or V tile, or of a query block
+    static constexpr int kTileBytes = kHalves * kHalfBytes;
+    static constexpr int kStages = D == 128 ? 5 : 8;           // K and V tiles in turn
+    static constexpr int kOffKv = 2 * kTileBytes;              // behind the two query blocks
+    static constexpr int kOffItem = kOffKv + kStages * kTileBytes;
+    static constexpr int kOffBar = kOffItem + 2 * (int)sizeof(Item);
+    static constexpr int kBars = 2 * kStages + 2 * 4 + 4 + 1;
+    static constexpr int kOffMask = kOffBar + 8 * kBars;
+    static constexpr int kOffMisc = kOffMask + 4 * kMaskRing;
+    static constexpr int kBytes = kOffMisc + 16;
+    static constexpr size_t kDynamic = (size_t)kBytes + 1024;  // the tiles start on 1,024 bytes
+    static_assert(kDynamic <= 227 * 1024, "shared memory of a CTA");
+};
+
+struct Bars {
+    uint32_t base;
+    int stages;
+    __device__ uint32_t kv_full(int s) const { return base + 8 * s; }
+    __device__ uint32_t kv_empty(int s) const { return base + 8 * (stages + s); }
+    __device__ uint32_t q_full(int t) const { return base + 8 * (2 * stages + t); }
+    __device__ uint32_t s_full(int t) const { return base + 8 * (2 * stages + 2 + t); }
+    __device__ uint32_t p_full(int t) const { return base + 8 * (2 * stages + 4 + t); }
+    __device__ uint32_t o_done(int t) const { return base + 8 * (2 * stages + 6 + t); }
+    __device__ uint32_t item_full(int i) const { return base + 8 * (2 * stages + 8 + i); }
+    __device__ uint32_t item_empty(int i) const { return base + 8 * (2 * stages + 10 + i); }
+    __device__ uint32_t last() const { return base + 8 * (2 * stages + 12); }
+};
+
+// What the CTA's roles share to give up together.
+struct Guard {
+    volatile int* fail;
+    volatile int* beat;            // moves while a warp forms rows token by token: the others' waits start anew
+    DebugWord* dbg;
+
+    __device__ void give_up(int where) const {
+        *fail = 1;
+        record_error(&dbg->kind, &dbg->index, 4, where);
+    }
+    // False once the wait has run out or another role has given up; the same for all lanes of the warp.
+    __device__ bool wait(uint32_t bar, uint32_t phase, int where) const {
+        bool ok = mbar_test(bar, phase);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        long long t0 = clock64();
+        int seen = *beat;
+        while (!ok && !*fail) {
+            ok = mbar_test(bar, phase);
+            if (*beat != seen) {
+                seen = *beat;
+                t0 = clock64();
+            }
+            if (!ok && clock64() - t0 > kWaitCycles) {
+                give_up(where);
+                break;
+            }
+        }
+        return __all_sync(0xffffffffu, ok);
+    }
+    // For what is in flight when a role stops: nobody is told.
+    __device__ void drain(uint32_t bar, uint32_t phase) const {
+        const long long t0 = clock64();
+        while (!mbar_test(bar, phase))
+            if (clock64() - t0 > kWaitCycles) return;
+    }
+};
+
+// The tiles of a block: how many of the item's cache tiles its rows see.
+struct Blocks {
+    int rows[2], count[2];
+};
+__device__ __forceinline__ Blocks blocks_of(const Item& it, int g_log2) {
+    Blocks r;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        r.rows[t] = clamp_int(it.rows - kBlock * t, 0, kBlock);
+        const int tiles = r.rows[t] ? (limit_of(it.r0 + kBlock * t + r.rows[t] - 1, it.pos0, g_log2) + kChunkTile - 1) / kChunkTile : 0;
+        r.count[t] = max(min(it.kv1, tiles) - it.kv0, 0);
+    }
+    return r;
+}
+
+__device__ __forceinline__ Item read_item(const Item* slot) {
+    Item it;
+    const int4* s = reinterpret_cast<const int4*>(slot);
+    int4* d = reinterpret_cast<int4*>(&it);
+    d[0] = s[0];
+    d[1] = s[1];
+    d[2] = s[2];
+    return it;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split_f32x2(uint64_t x, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// One row's accumulator token by token, for rows that an infinity or NaN of a token behind their own has reached; the
+// whole warp works on it, lane l on channels l D / 32 and on.
+template <int D>
+__device__ __noinline__ void form_row(const ChunkArgs& a, const Item& it, int r, int g_log2, float m, int lane,
+                                      const Guard& guard, float (&acc)[D / 32]) {
+    constexpr int kChannels = D / 32;
+    const int limit = min(limit_of(r, it.pos0, g_log2), it.kv1 * kChunkTile);
+    const uint16_t* q = a.q + (int64_t)(it.tok0 + (r >> g_log2)) * a.q_stride + ((it.head << g_log2) + (r & (a.g - 1))) * D;
+#pragma unroll
+    for (int c = 0; c < kChannels; ++c) acc[c] = 0.0f;
+    for (int t0 = it.kv0 * kChunkTile; t0 < limit; t0 += 32) {
+        if (lane == 0) *guard.beat = *guard.beat + 1;
+        const int t = t0 + lane;
+        const int id = t < limit ? a.tables[(int64_t)it.b * a.stride + t / kPage] : -1;
+        const bool there = id >= 0 && id < a.pages;
+        const uint16_t* k = a.pool + (((int64_t)(there ? id : 0) * a.h_kv + it.head) * 2 * kPage + t % kPage) * D;
+        float dot = 0.0f;
+        if (there) {
+            for (int c = 0; c < D; c += 8) {
+                const uint4 x = *reinterpret_cast<const uint4*>(q + c), y = *reinterpret_cast<const uint4*>(k + c);
+                dot += bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) +
+                       bf16_hi(x.y) * bf16_hi(y.y) + bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z) +
+                       bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
+            }
+        }
+        const float p = there ? bf16_lo(bf16_pair(exp2_approx(fmaf(dot, a.scale_log2, -m)), 0.0f)) : 0.0f;
+        const int64_t v_row = (((int64_t)(there ? id : 0) * a.h_kv + it.head) * 2 + 1) * kPage + t % kPage;
+        for (int i = 0; i < 32; ++i) {
+            const float pi = __shfl_sync(0xffffffffu, p, i);
+            const int64_t row = __shfl_sync(0xffffffffu, v_row, i);
+            if (pi == 0.0f) continue;
+            const uint16_t* v = a.pool + row * D + lane * kChannels;
+#pragma unroll
+            for (int c = 0; c < kChannels; ++c) acc[c] += pi * __uint_as_float((uint32_t)v[c] << 16);
+        }
+    }
+}
+
+// Stores a row's channels first .. first + N: normalised and rounded to the output, or as they are to the part.
+template <int D, int N>
+__device__ __forceinline__ void store_row(const ChunkArgs& a, const Work& w, const Item& it, int r, int g_log2, int first,
+                                          const float (&x)[N], float inv) {
+    if (it.part >= 0) {
+        float* to = w.part_acc + (int64_t)(it.part + r - it.r0) * D + first;
+        if constexpr (N % 4 == 0) {
+#pragma unroll
+            for (int c = 0; c < N; c += 4) *reinterpret_cast<float4*>(to + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < N; c += 2) *reinterpret_cast<float2*>(to + c) = make_float2(x[c], x[c + 1]);
+        }
+        return;
+    }
+    const int64_t row = (int64_t)(it.tok0 + (r >> g_log2)) * (a.h_kv << g_log2) + (it.head << g_log2) + (r & (a.g - 1));
+    uint16_t* to = a.out + row * D + first;
+    uint32_t u[N / 2];
+#pragma unroll
+    for (int c = 0; c < N / 2; ++c) u[c] = bf16_pair(x[2 * c] * inv, x[2 * c + 1] * inv);
+    if constexpr (N % 8 == 0) {
+#pragma unroll
+        for (int c = 0; c < N / 2; c += 4) *reinterpret_cast<uint4*>(to + 2 * c) = make_uint4(u[c], u[c + 1], u[c + 2], u[c + 3]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < N / 2; ++c) *reinterpret_cast<uint32_t*>(to + 2 * c) = u[c];
+    }
+}
+
+// Loader: work items to the other roles, K and V pages to the ring.
+template <int D>
+__device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, const CUtensorMap* map, uint32_t kv,
+                                          const Bars& bars, const Guard& guard, volatile int* masks, Item* slots, int lane) {
+    using L = Layout<D>;
+    constexpr int kBoxes = kTilePages * L::kHalves;          // TMA boxes of a K or V tile: 16 tokens x 64 channels
+    const int g_log2 = 31 - __clz(a.g);
+    const int blocks = (int)(a.pages * a.h_kv * 2);          // a block id behind the pool reads as zeros
+    const int n_items = w.head->items;
+    int slot = 0, tile = 0;                                  // ring positions, counted through
+    int item = blockIdx.x;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+        const int next = lane == 0 ? atomicAdd(&w.head->next, 1) + (int)gridDim.x : 0;    // asked for ahead of its use
+        const bool stop = item >= n_items;
+        Item it{};
+        it.rows = -1;
+        if (!stop) it = read_item(w.items + item);
+        ok = guard.wait(bars.item_empty(i & 1), ((i >> 1) & 1) ^ 1, i);
+        if (!ok) break;
+        if (lane == 0) {
+            slots[i & 1] = it;
+            mbar_arrive(bars.item_full(i & 1));
+        }
+        __syncwarp();
+        if (stop) break;
+        const Blocks bl = blocks_of(it, g_log2);
+        const int count = max(bl.count[0], bl.count[1]);
+        const int pages = (it.total + kPage - 1) / kPage;
+        const int32_t* table = a.tables + (int64_t)it.b * a.stride;
+        // page ids of four tiles a load, asked for four tiles ahead; -1 where there is no page to read
+        const int last_page = min(pages, (it.kv0 + count) * kTilePages);
+        auto look_up = [&](int j) {
+            const int page = (it.kv0 + j) * kTilePages + lane;
+            return page < last_page ? table[page] : -1;
+        };
+        int ids = -1, ahead = count ? look_up(0) : -1;
+        for (int j = 0; j < count && ok; ++j) {
+            if (j % 4 == 0) {
+                ids = ahead;
+                ahead = look_up(j + 4);
+                if (ids < 0 || ids >= a.pages) {
+                    if (a.debug && (it.kv0 + j) * kTilePages + lane < last_page) record_error(&a.dbg->kind, &a.dbg->index, 2, ids);
+                    ids = -1;
+                }
+            }
+            const uint32_t there = __ballot_sync(0xffffffffu, ids >= 0);
+            const int box = lane % kBoxes;                   // lanes beyond the boxes only follow
+            const int page = box / L::kHalves, half = box % L::kHalves;
+            const int id = __shfl_sync(0xffffffffu, ids, j % 4 * kTilePages + page);
+            const int z = id >= 0 ? (id * a.h_kv + it.head) * 2 : blocks;
+            if (lane == 0) masks[tile % kMaskRing] = (there >> (j % 4 * kTilePages)) & 0xff;
+            __syncwarp();
+#pragma unroll
+            for (int kind = 0; kind < 2; ++kind) {           // K, then V
+                const int s = slot % L::kStages;
+                ok = guard.wait(bars.kv_empty(s), ((slot / L::kStages) & 1) ^ 1, 1000 + i);
+                if (!ok) break;
+                if (lane == 0) mbar_expect_tx(bars.kv_full(s), L::kTileBytes);
+                __syncwarp();
+                if (lane < kBoxes)
+                    tma_load_3d(kv + s * L::kTileBytes + half * L::kHalfBytes + page * (kPage * 128), map, 64 * half, 0,
+                                id >= 0 ? z + kind : blocks, bars.kv_full(s));
+                ++slot;
+            }
+            ++tile;
+        }
+        item = __shfl_sync(0xffffffffu, next, 0);
+    }
+    // what was asked for lands before the CTA may leave
+    for (int s = max(slot - L::kStages, 0); s < slot; ++s) guard.drain(bars.kv_full(s % L::kStages), (s / L::kStages) & 1);
+}
+
+// Issuer of the matrix products.
+template <int D>
+__device__ __forceinline__ void issue_role(const ChunkArgs& a, uint8_t* smem_kv, uint32_t q, uint32_t kv, uint32_t tmem,
+                                           const Bars& bars, const Guard& guard, const Item* slots, int lane) {
+    using L = Layout<D>;
+    constexpr uint32_t kScores = idesc_bf16(kBlock, kChunkTile, false), kValues = idesc_bf16(kBlock, D, true);
+    const int g_log2 = 31 - __clz(a.g);
+    int slot = 0;
+    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+    bool ok = true, issued = false;
+    auto scores = [&](int t, uint32_t k_tile) {              // S of block t, from lane 0
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (ks / 4) * L::kHalfBytes + (ks % 4) * 32;
+            umma_ss(tmem + t * kChunkTile, sw128_desc(q + t * L::kTileBytes + off, 0), sw128_desc(k_tile + off, 0), kScores, ks > 0);
+        }
+        umma_commit(bars.s_full(t));
+    };
+    for (int i = 0; ok; ++i) {
+        ok = guard.wait(bars.item_full(i & 1), (i >> 1) & 1, 2000 + i);
+        if (!ok) break;
+        const Item it = read_item(slots + (i & 1));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.item_empty(i & 1));
+        if (it.rows < 0) break;
+        const Blocks bl = blocks_of(it, g_log2);
+        const int count = max(bl.count[0], bl.count[1]);
+        if (count == 0) continue;
+        // S of the first tile
+        int ks = slot++;
+        ok = guard.wait(bars.kv_full(ks % L::kStages), (ks / L::kStages) & 1, 3000 + i);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (!ok || bl.count[t] == 0) continue;
+            ok = guard.wait(bars.q_full(t), q_phase[t], 4000 + i);
+            q_phase[t] ^= 1;
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) scores(t, kv + (ks % L::kStages) * L::kTileBytes);
+            issued = true;
+        }
+        if (!ok) break;
+        if (lane == 0) umma_commit(bars.kv_empty(ks % L::kStages));
+        for (int j = 0; j < count && ok; ++j) {
+            const int vs = slot++;
+            const uint32_t v_tile = kv + (vs % L::kStages) * L::kTileBytes;
+            ok = guard.wait(bars.kv_full(vs % L::kStages), (vs / L::kStages) & 1, 5000 + i);
+            if (!ok) break;
+            const int tail = it.total % kPage;
+            if (tail && it.kv0 + j == it.total / kChunkTile) {
+                // rows of the last page behind the sequence may hold anything: zeros for the product
+                const int first = it.total % kChunkTile, left = kPage - tail;
+                uint8_t* tile = smem_kv + (vs % L::kStages) * L::kTileBytes;
+                for (int c = lane; c < left * 8 * L::kHalves; c += 32) {
+                    const int half = c / (left * 8), rest = c % (left * 8);
+                    *reinterpret_cast<uint4*>(tile + half * L::kHalfBytes + first * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async();
+                __syncwarp();
+            }
+            const bool more = j + 1 < count;
+            const int kn = more ? slot++ : 0;
+            bool here = false;                               // K of the next tile
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (j < bl.count[t]) {
+                    ok = guard.wait(bars.p_full(t), p_phase[t], 7000 + i);
+                    p_phase[t] ^= 1;
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int k16 = 0; k16 < kChunkTile / 16; ++k16)
+                            umma_ts(tmem + 2 * kChunkTile + t * D, tmem + t * kChunkTile + k16 * 8,
+                                    sw128_desc(v_tile + k16 * 2048, L::kHalfBytes), kValues, j > 0 || k16 > 0);
+                        umma_commit(bars.o_done(t));
+                    }
+                }
+                if (t == 1 && lane == 0) umma_commit(bars.kv_empty(vs % L::kStages));
+                if (j + 1 < bl.count[t]) {
+                    if (!here) ok = guard.wait(bars.kv_full(kn % L::kStages), (kn / L::kStages) & 1, 6000 + i);
+                    here = true;
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) scores(t, kv + (kn % L::kStages) * L::kTileBytes);
+                }
+            }
+            if (ok && more && lane == 0) umma_commit(bars.kv_empty(kn % L::kStages));
+        }
+    }
+    // the last matrix products are done before tensor memory is freed
+    if (issued) {
+        if (lane == 0) umma_commit(bars.last());
+        __syncwarp();
+        guard.drain(bars.last(), 0);
+    }
+}
+
+// Softmax of block t: one thread a row.
+template <int D>
+__device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, uint8_t* smem_q, uint32_t tmem,
+                                             const Bars& bars, const Guard& guard, const volatile int* masks,
+                                             const Item* slots, int t, int warp, int lane) {
+    using L = Layout<D>;
+    const int g_log2 = 31 - __clz(a.g), in_group = warp * 32 + lane;
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    const uint32_t s_col = tmem + lanes + t * kChunkTile, o_col = tmem + lanes + 2 * kChunkTile + t * D;
+    const uint64_t scale = f32x2(a.scale_log2, a.scale_log2);
+    uint8_t* q_tile = smem_q + t * L::kTileBytes;
+    int tile = 0, step = 0;                      // tiles of the CTA, steps of this block, counted through
+    for (int i = 0;; ++i) {
+        if (!guard.wait(bars.item_full(i & 1), (i >> 1) & 1, 8000 + i)) return;
+        const Item it = read_item(slots + (i & 1));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.item_empty(i & 1));
+        if (it.rows < 0) return;
+        const Blocks bl = blocks_of(it, g_log2);
+        const int rows = t ? bl.rows[1] : bl.rows[0], count = t ? bl.count[1] : bl.count[0], tile0 = tile;
+        tile += max(bl.count[0], bl.count[1]);
+        if (rows == 0) continue;
+        const int local = kBlock * t + in_group, r = it.r0 + local;      // row of the item, of the request
+        const bool mine = in_group < rows, working = 32 * warp < rows;
+        if (count > 0) {
+            // the block's queries, 16 bytes at a time, into the swizzled layout; zeros behind the last row
+#pragma unroll
+            for (int c0 = 0; c0 < D / 8; ++c0) {
+                const int at = c0 * kBlock + in_group, row = at / (D / 8), c = at % (D / 8);
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (row < rows) {
+                    const int rr = it.r0 + kBlock * t + row;
+                    x = *reinterpret_cast<const uint4*>(a.q + (int64_t)(it.tok0 + (rr >> g_log2)) * a.q_stride +
+                                                        ((it.head << g_log2) + (rr & (a.g - 1))) * D + c * 8);
+                }
+                *reinterpret_cast<uint4*>(q_tile + c / 8 * L::kHalfBytes + row * 128 + (((c % 8) ^ (row % 8)) * 16)) = x;
+            }
+            fence_async();
+            mbar_arrive(bars.q_full(t));
+        }
+        // rows behind the last one see everything: their zeros need no mask
+        const int limit = mine ? limit_of(r, it.pos0, g_log2) : 0x7fffffff;
+        float m = kNoReference, sum = 0.0f;
+        for (int j = 0; j < count; ++j, ++step) {
+            if (!guard.wait(bars.s_full(t), step & 1, 9000 + i)) return;
+            if (!working) {                      // no row of this warp is any: what its lanes hold as weights reaches nothing
+                mbar_arrive(bars.p_full(t));
+                continue;
+            }
+            tc_fence_after();
+            uint32_t u[kChunkTile];
+#pragma unroll
+            for (int c = 0; c < kChunkTile; c += 32) tmem_ld32(s_col + c, u + c);
+            const int seen = limit - (it.kv0 + j) * kChunkTile;
+            const int mask = masks[(tile0 + j) % kMaskRing];
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < kChunkTile; c += 32) loaded32(u + c);
+            if (__any_sync(0xffffffffu, seen < kChunkTile || mask != 0xff)) {
+#pragma unroll
+                for (int c = 0; c < kChunkTile; ++c)
+                    if (c >= seen || !(mask >> (c / kPage) & 1)) u[c] = 0xff800000u;         // -infinity
+            }
+            float top[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) top[c] = __uint_as_float(u[c]);
+#pragma unroll
+            for (int c = 4; c + 8 <= kChunkTile; c += 8) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    top[k] = fmax3(top[k], __uint_as_float(u[c + 2 * k]), __uint_as_float(u[c + 2 * k + 1]));
+            }
+            top[0] = fmax3(top[0], __uint_as_float(u[124]), __uint_as_float(u[125]));
+            top[1] = fmax3(top[1], __uint_as_float(u[126]), __uint_as_float(u[127]));
+            const float high = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * a.scale_log2;
+            const bool rise = high > m + kHeadroom;
+            if (__any_sync(0xffffffffu, rise)) {
+                const float to = rise ? high : m, f = exp2_approx(m - to);
+                m = to;
+                sum *= f;
+                if (j > 0) {                     // behind the scores, the block's products before them are done too
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_col + c, o);
+                        tmem_wait_ld();
+                        loaded32(o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st32(o_col + c, o);
+                    }
+                }
+            }
+            const uint64_t less = f32x2(-m, -m);
+            uint64_t part[2] = {0, 0};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    float x, y;
+                    split_f32x2(fma_f32x2(f32x2(__uint_as_float(u[64 * h + 2 * c]), __uint_as_float(u[64 * h + 2 * c + 1])), scale, less), x, y);
+                    pk[c] = bf16_pair(exp2_approx(x), exp2_approx(y));
+                    part[c % 2] = add_f32x2(part[c % 2], f32x2(bf16_lo(pk[c]), bf16_hi(pk[c])));
+                }
+                tmem_st32(s_col + 32 * h, pk);
+            }
+            float x, y;
+            split_f32x2(add_f32x2(part[0], part[1]), x, y);
+            sum += x + y;
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bars.p_full(t));
+        }
+        if (count > 0 && !guard.wait(bars.o_done(t), (step - 1) & 1, 10000 + i)) return;
+        if (!working) continue;
+        tc_fence_after();
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (it.part >= 0 && mine) w.part_ml[it.part + local] = make_float2(m, sum);
+        bool odd = false;
+        if (count > 0) {                         // first look at the whole row: form_row reads its query, which out may lie over
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_col + c, o);
+                tmem_wait_ld();
+                loaded32(o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) odd |= !(fabsf(__uint_as_float(o[k])) <= 3.402823466e38f);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            float x[32];
+            if (count > 0) {
+                tmem_ld32(o_col + c, o);
+                tmem_wait_ld();
+                loaded32(o);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = count > 0 ? __uint_as_float(o[k]) : 0.0f;
+            if (mine && !odd) store_row<D, 32>(a, w, it, r, g_log2, c, x, inv);
+        }
+        tc_fence_before();
+        for (uint32_t todo = __ballot_sync(0xffffffffu, odd && mine); todo; todo &= todo - 1) {
+            const int src = __ffs(todo) - 1, row = r - lane + src;
+            float acc[D / 32];
+            form_row<D>(a, it, row, g_log2, __shfl_sync(0xffffffffu, m, src), lane, guard, acc);
+            store_row<D, D / 32>(a, w, it, row, g_log2, lane * (D / 32), acc, __shfl_sync(0xffffffffu, inv, src));
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) chunk_attend_kernel(const __grid_constant__ ChunkArgs a,
+                                                                   const __grid_constant__ Work w,
+                                                                   const __grid_constant__ CUtensorMap map) {
+    using L = Layout<D>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = raw + (1024 - smem_u32(raw) % 1024) % 1024;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t sb = smem_u32(smem);
+    const Bars bars{sb + L::kOffBar, L::kStages};
+    volatile int* masks = reinterpret_cast<volatile int*>(smem + L::kOffMask);
+    Item* slots = reinterpret_cast<Item*>(smem + L::kOffItem);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+    const Guard guard{reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4),
+                      reinterpret_cast<volatile int*>(smem + L::kOffMisc + 8), a.dbg};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(bars.kv_full(s), 1);
+            mbar_init(bars.kv_empty(s), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(bars.q_full(t), kBlock);
+            mbar_init(bars.s_full(t), 1);
+            mbar_init(bars.p_full(t), kBlock);
+            mbar_init(bars.o_done(t), 1);
+            mbar_init(bars.item_full(t), 1);
+            mbar_init(bars.item_empty(t), kSoftmaxWarps + 1);
+        }
+        mbar_init(bars.last(), 1);
+        *guard.fail = 0;
+        *guard.beat = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async();
+    }
+    if (warp == 9) {                             // all of tensor memory: S of two blocks, O of two blocks
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(tmem_slot)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_wait();
+    grid_release();
+
+    // registers: 384 x 168 at launch; 256 x 208 + 128 x 80 = 63,488 of those 64,512
+    if (warp < kSoftmaxWarps) {
+        more_registers<208>();
+        softmax_role<D>(a, w, smem, tmem, bars, guard, masks, slots, warp / 4, warp % 4, lane);
+    } else {
+        fewer_registers<80>();
+        if (warp == kSoftmaxWarps) load_role<D>(a, w, &map, sb + L::kOffKv, bars, guard, masks, slots, lane);
+        if (warp == kSoftmaxWarps + 1)
+            issue_role<D>(a, smem + L::kOffKv, sb, sb + L::kOffKv, tmem, bars, guard, slots, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512) : "memory");
+    }
+}
+
+// ---- join ---------------------------------------------------------------------------------------------------
+
+// Adds the parts of cut items, in their order: a piece's CTA takes its share of the rows, a warp a row.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkArgs a, const Work w) {
+    constexpr int kChannels = D / 32;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g_log2 = 31 - __clz(a.g);
+    grid_release();
+    grid_wait();
+    const int n_items = w.head->items;
+    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+        Item it = read_item(w.items + item);
+        if (it.part < 0) continue;
+        const int base = it.part - it.piece * it.rows;
+        const int end = (int)((long long)it.rows * (it.piece + 1) / it.pieces);
+        for (int local = (int)((long long)it.rows * it.piece / it.pieces) + warp; local < end; local += kJoinThreads / 32) {
+            float m = kNoReference;
+            for (int p = lane; p < it.pieces; p += 32) {
+                const float2 ml = w.part_ml[base + p * it.rows + local];
+                if (ml.y != 0.0f) m = fmaxf(m, ml.x);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float acc[kChannels] = {}, sum = 0.0f;
+            for (int p0 = 0; p0 < it.pieces; p0 += 32) {
+                float2 ml = make_float2(0.0f, 0.0f);
+                if (p0 + lane < it.pieces) ml = w.part_ml[base + (p0 + lane) * it.rows + local];
+                const float f = ml.y == 0.0f ? 0.0f : exp2_approx(ml.x - m);
+                const int count = min(32, it.pieces - p0);
+                for (int p = 0; p < count; ++p) {
+                    const float fp = __shfl_sync(0xffffffffu, f, p), lp = __shfl_sync(0xffffffffu, ml.y, p);
+                    if (fp == 0.0f) continue;    // no weight: what the part holds does not count, and may not be there
+                    sum += fp * lp;
+                    const float* from = w.part_acc + (int64_t)(base + (p0 + p) * it.rows + local) * D + lane * kChannels;
+#pragma unroll
+                    for (int c = 0; c < kChannels; ++c) acc[c] += fp * from[c];
+                }
+            }
+            const int part = it.part;
+            it.part = -1;
+            store_row<D, kChannels>(a, w, it, it.r0 + local, g_log2, lane * kChannels, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
+            it.part = part;
+        }
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------------------------------
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// The pool as [pages H_kv 2][16 tokens][d], boxes of one page's 16 tokens x 64 channels, 128-byte swizzle.
+bool make_pool_map(CUtensorMap* map, const ChunkArgs& a, int d) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, kPage, (cuuint64_t)a.pages * a.h_kv * 2};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)kPage * d * 2};
+    const cuuint32_t box[3] = {64, kPage, 1}, step[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.pool), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const ChunkArgs& a, const ChunkPlan& plan, void* workspace, int num_sms, cudaStream_t st) {
+    using L = Layout<D>;
+    CUtensorMap map;
+    if (!make_pool_map(&map, a, D)) return cudaErrorInvalidValue;
+    cudaError_t e = smem_opt_in<chunk_attend_kernel<D>>(L::kDynamic);
+    if (e != cudaSuccess) return e;
+    char* base = static_cast<char*>(workspace);
+    const Work w{reinterpret_cast<Header*>(base), reinterpret_cast<int*>(base + plan.tiles),
+                 reinterpret_cast<int2*>(base + plan.units), reinterpret_cast<Item*>(base + plan.items),
+                 reinterpret_cast<float2*>(base + plan.part_ml), reinterpret_cast<float*>(base + plan.part_acc)};
+    const int grid = num_sms < plan.item_cap ? num_sms : plan.item_cap;
+    e = launch_dependent(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a, w, plan.unit_cap, plan.item_cap,
+                         plan.part_cap, num_sms);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(chunk_attend_kernel<D>, dim3(grid), dim3(kThreads), L::kDynamic, st, 1, a, w, map);
+    if (e != cudaSuccess) return e;
+    const int joins = 4 * num_sms < plan.item_cap ? 4 * num_sms : plan.item_cap;
+    return launch_dependent(chunk_join_kernel<D>, dim3(joins), dim3(kJoinThreads), 0, st, 1, a, w);
+}
+
+}  // namespace
+
+ChunkPlan plan_chunk(const Shape& s, int num_sms, int batch, int n) {
+    const int g = s.h_q / s.h_kv;
+    const int64_t rows = (int64_t)n * g;
+    ChunkPlan p{};
+    p.unit_cap = (int)((rows + kChunkRows - 1) / kChunkRows) + (batch < n ? batch : n);
+    // cutting at L tiles makes all / L more items at most, L half an SM's share or more; the pieces of cut items are
+    // longer than L / 2
+    p.item_cap = p.unit_cap * s.h_kv + 2 * num_sms;
+    p.part_cap = 4 * num_sms * (int)(rows < kChunkRows ? rows : kChunkRows);
+    size_t at = 0;
+    auto place = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    place(sizeof(Header));
+    p.tiles = place(((size_t)batch + 1) * sizeof(int));
+    p.units = place((size_t)p.unit_cap * sizeof(int2));
+    p.items = place((size_t)p.item_cap * sizeof(Item));
+    p.part_ml = place((size_t)p.part_cap * sizeof(float2));
+    p.part_acc = place((size_t)p.part_cap * s.d * sizeof(float));
+    p.total = at;
+    return p;
+}
+
+cudaError_t launch_chunk(const ChunkArgs& a, const ChunkPlan& plan, void* workspace, int d, int num_sms, cudaStream_t st) {
+    return d == 128 ? launch<128>(a, plan, workspace, num_sms, st) : launch<64>(a, plan, workspace, num_sms, st);
+}
+
+}  // namespace oscar

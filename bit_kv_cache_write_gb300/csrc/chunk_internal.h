@@ -25,4 +25,29 @@ struct RopeArgs {
 };
 cudaError_t launch_norm_rope(const RopeArgs& a, int d, int num_sms, cudaStream_t st);
 
+// ---- attention of new tokens over BF16 pages (chunk_attend.cu)
+constexpr int kChunkRows = 256;              // query rows (token, head of the group) of a work item
+constexpr int kChunkTile = 128;              // cached tokens of a step
+
+// Where the parts of a call's workspace lie, in bytes.
+struct ChunkPlan {
+    int unit_cap;                            // row blocks of all requests at most
+    int item_cap;                            // work items at most
+    int part_cap;                            // rows of split items at most
+    size_t tiles, units, items, part_ml, part_acc, total;
+};
+struct ChunkArgs {
+    const uint16_t* q; int64_t q_stride;     // token stride in elements
+    const uint16_t* pool; int64_t pages;
+    const int32_t* tables; int stride;
+    const int32_t* row_start;                // [batch + 1]
+    const int32_t* total_len;                // [batch]
+    uint16_t* out;                           // [n][H_q][d]
+    int batch, n, h_kv, g;
+    float scale_log2;                        // sm_scale * log2(e)
+    int debug; DebugWord* dbg;
+};
+ChunkPlan plan_chunk(const Shape& s, int num_sms, int batch, int n);
+cudaError_t launch_chunk(const ChunkArgs& a, const ChunkPlan& plan, void* workspace, int d, int num_sms, cudaStream_t st);
+
 }  // namespace oscar

@@ -70,13 +70,15 @@ _SIGS = {
                                       _vp, _sz, _i, _vp]),
     "oscar_norm_rope": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, ctypes.c_float, _vp, _i, _i,
                              ctypes.c_float, _vp, _vp, _vp, _i, _i, _vp]),
+    "oscar_extend_bf16_workspace_size": (_sz, [_vp, _i, _i]),
+    "oscar_extend_bf16": (_i, [_vp, _vp, _i64, _vp, _i64, _vp, _i, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp]),
     "oscar_profile_enable": (_i, [_vp, _i]),
     "oscar_profile_read": (_i, [_vp, _i, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_longlong)]),
 }
 
 OSCAR_KERNEL_WRITE, OSCAR_KERNEL_QROT, OSCAR_KERNEL_SPLIT, OSCAR_KERNEL_MERGE = 0, 1, 2, 3
 OSCAR_KERNEL_PLAN, OSCAR_KERNEL_APPEND, OSCAR_KERNEL_SELECT, OSCAR_KERNEL_ATTEND = 4, 5, 6, 7
-OSCAR_KERNEL_ROPE = 8
+OSCAR_KERNEL_ROPE, OSCAR_KERNEL_EXTEND = 8, 9
 OSCAR_OUT_FP32, OSCAR_OUT_BF16 = 0, 1
 OSCAR_ROPE_HALF, OSCAR_ROPE_INTERLEAVED = 0, 1
 
@@ -523,6 +525,28 @@ def oscar_norm_rope(ctx, q, k, q_out, k_out, turns, positions=None, row_start=No
         _check(st, "oscar_norm_rope")
 
 
+def oscar_extend_bf16_workspace_size(ctx, batch, n):
+    return lib().oscar_extend_bf16_workspace_size(ctx, _bound(batch, "batch"), _bound(n, "tokens"))
+
+
+def oscar_extend_bf16(ctx, q, bf16_pool, tables, row_start, total_len, out, workspace, stream=None):
+    """q: bf16 [n][H_q][d], rows at any stride; tables int32 [B][stride]; row_start int32 [B + 1] and total_len int32
+    [B] of the plan; out bf16 [n][H_q][d]; workspace uint8."""
+    import torch
+    h_q, h_kv, d, dev, _ = _config_of(ctx)
+    bf16, i32 = torch.bfloat16, torch.int32
+    qp, qs = _rows(q, bf16, h_q, d, dev, "q")
+    n, batch, size = q.shape[0], total_len.numel(), bf16_pool.numel()
+    tp, ts = _table(tables, batch, i32, dev)
+    wp, ws = _scratch(workspace, dev)
+    st = lib().oscar_extend_bf16(
+        ctx, qp, qs, _ptr(bf16_pool, bf16, size, dev, "bf16_pool"), size // (h_kv * 32 * d), tp, ts,
+        _ptr(row_start, i32, batch + 1, dev, "row_start"), _ptr(total_len, i32, batch, dev, "total_len"), batch,
+        _bound(n, "tokens"), _ptr(out, bf16, n * h_q * d, dev, "out"), wp, ws, _stream_on(stream, dev))
+    if st:
+        _check(st, "oscar_extend_bf16")
+
+
 def oscar_debug_error(ctx):
     """Returns (status, kind, index) and clears the device error word."""
     kind = _i(0)
@@ -620,6 +644,12 @@ class Oscar:
                   k_weight=None, eps=1e-6, layout=OSCAR_ROPE_HALF, scale=1.0, stream=None):
         oscar_norm_rope(self.ctx, q, k, q_out, k_out, turns, positions, row_start, total_len, q_weight, k_weight, eps,
                         layout, scale, stream)
+
+    def extend_bf16_workspace_size(self, batch, n):
+        return oscar_extend_bf16_workspace_size(self.ctx, batch, n)
+
+    def extend_bf16(self, q, bf16_pool, tables, row_start, total_len, out, workspace, stream=None):
+        oscar_extend_bf16(self.ctx, q, bf16_pool, tables, row_start, total_len, out, workspace, stream)
 
     def int2_page_bytes(self):
         return oscar_int2_page_bytes(self.ctx)

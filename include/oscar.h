@@ -450,7 +450,7 @@ OSCAR_API oscar_status oscar_decode_bf16_sparse(oscar_ctx_t* ctx, const void* q,
                                                 int batch, void* stream);
 
 /* ---------------------------------------------------------------------------
- * Chunks of new tokens: norm and rotation
+ * Chunks of new tokens: norm and rotation, attention over the BF16 cache
  * ---------------------------------------------------------------------------
  * What stands between a layer's projections and the caches (no counterpart on
  * the pages, whose caches hold keys as attention reads them). */
@@ -498,6 +498,47 @@ OSCAR_API oscar_status oscar_norm_rope(oscar_ctx_t* ctx, const void* q, int64_t 
                                        const int32_t* positions, const int32_t* row_start, const int32_t* total_len,
                                        int batch, int n, void* stream);
 
+/* Attention of chunks of new tokens over their BF16 cache, which holds them
+ * already (oscar_append_bf16): prompts, whole or in chunks, drafted tokens to
+ * check, single tokens, all in one call. Request b's new tokens are the rows
+ * row_start[b] .. row_start[b + 1] of q and the last ones of its total_len[b]
+ * cached tokens; row i sees those up to and with its own:
+ *   out_i = softmax(sm_scale * q_i . K^T) V over the tokens t <= p_i,
+ *   p_i = total_len[b] - row_start[b + 1] + i.
+ *   q:          DEVICE bf16, row i at q + i * q_stride elements, [H_q][d].
+ *               q_stride is a multiple of 8 up to 2^31, q 16-byte aligned.
+ *   tables:     DEVICE int32 [batch][table_stride].
+ *   row_start:  DEVICE int32 [batch + 1], ascending, within [0, n]; total_len:
+ *               DEVICE int32 [batch], within [0, 16 * table_stride] (a length
+ *               outside counts as the nearer end; recorded with debug_bounds).
+ *               oscar_plan_append's outputs are: but of a request that it
+ *               rejected, whose tokens the cache does not hold, the rows mean
+ *               nothing.
+ *   n:          rows of q and out, at most 2^24. Rows that no request has are not
+ *               read, and left as they were in out. A row whose position is below 0
+ *               sees nothing and gives zeros.
+ *   out:        DEVICE bf16 [n][H_q][d], 16-byte aligned. It may be q itself where
+ *               q_stride is H_q * d; nothing else overlaps it.
+ *   workspace:  DEVICE, >= oscar_extend_bf16_workspace_size(ctx, batch, n) bytes,
+ *               256-byte aligned; scratch, nothing in it is kept. The size serves
+ *               every smaller batch and n too. Calls that overlap on the GPU need a
+ *               workspace each.
+ * The work is cut by the lengths on the device; no bound of them is asked for.
+ * Logits, the softmax and all sums are fp32. The weights are rounded to bf16 for
+ * their product with V (off by 2^-8 of each at most) and normalised by the sum of
+ * the rounded ones; the output is rounded once to bf16.
+ * Tokens that a row does not see do not matter to it, nor does what lies behind a
+ * sequence: NaN and infinity neither. Logits and values that are infinite or NaN
+ * count as in oscar_decode_bf16, as do page ids outside the pool.
+ * The result does not change from run to run.
+ * Asynchronous on `stream`. n == 0 or batch == 0 is a no-op; batch > 65535 returns
+ * OSCAR_ERR_UNSUPPORTED. */
+OSCAR_API size_t oscar_extend_bf16_workspace_size(const oscar_ctx_t* ctx, int batch, int n);
+OSCAR_API oscar_status oscar_extend_bf16(oscar_ctx_t* ctx, const void* q, int64_t q_stride, const void* bf16_pool,
+                                         int64_t bf16_pool_pages, const int32_t* tables, int table_stride,
+                                         const int32_t* row_start, const int32_t* total_len, int batch, int n,
+                                         void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Bytes of one INT2 page (all heads, K and V) and of one BF16 page. */
 OSCAR_API size_t oscar_int2_page_bytes(const oscar_ctx_t* ctx);
 OSCAR_API size_t oscar_bf16_page_bytes(const oscar_ctx_t* ctx);
@@ -513,7 +554,8 @@ typedef enum {
     OSCAR_KERNEL_SELECT = 6,  /* page scores and selection of the sparse decode */
     OSCAR_KERNEL_ATTEND = 7,  /* attention over BF16 pages and the join of its splits */
     OSCAR_KERNEL_ROPE = 8,    /* oscar_norm_rope */
-    OSCAR_KERNEL_COUNT = 9
+    OSCAR_KERNEL_EXTEND = 9,  /* oscar_extend_bf16: plan, attention and join */
+    OSCAR_KERNEL_COUNT = 10
 } oscar_kernel_id;
 
 /* Measurement hook (no counterpart on the pages): while enabled, every launch

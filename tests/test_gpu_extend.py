@@ -1,0 +1,293 @@
+"""oscar_extend_bf16 against its fp64 definition (chunk_oracle.py, which derives the tolerances)."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import chunk_oracle
+import rope_oracle
+from bit_kv_cache_write_gb300 import oscar as O
+from bit_kv_cache_write_gb300 import rope
+
+pytestmark = pytest.mark.gpu
+P = 16
+BF, I32, I64 = torch.bfloat16, torch.int32, torch.int64
+
+
+def context(h_q, h_kv, d, **over):
+    c = dict(n_layers=1, n_q_heads=h_q, n_kv_heads=h_kv, head_dim=d, group=32)
+    c.update(over)
+    return O.Oscar(**c)
+
+
+def bf16(x):
+    """The values rounded to bf16, as float64."""
+    return torch.from_numpy(np.asarray(x, np.float32)).to(BF).double().numpy()
+
+
+class Case:
+    """Requests of (cached, new) tokens over shuffled pages; rows and pages beyond them hold what `fill` says."""
+
+    def __init__(self, lens, h_q, h_kv, d, seed=0, spare=0, spread=1.0, integers=False, more_pages=2):
+        r = np.random.default_rng(seed)
+        self.h_q, self.h_kv, self.d, self.spare = h_q, h_kv, d, spare
+        self.new = np.array([n for _, n in lens])
+        self.total = np.array([c + n for c, n in lens])
+        self.start = np.concatenate([[0], np.cumsum(self.new)])
+        n = int(self.start[-1]) + spare
+        count = -(-self.total // P)
+        ids = r.permutation(int(count.sum()) + more_pages)
+        self.tables = np.zeros((len(lens), max(1, int(count.max(initial=0)))), np.int32)
+        at = 0
+        for b, c in enumerate(count):
+            self.tables[b, :c] = ids[at:at + c]
+            at += c
+        shape = (int(count.sum()) + more_pages, h_kv, 2, P, d)
+        if integers:
+            # q = e_c scaled, k small integers: logits are small whole numbers, weights powers of two
+            self.q = np.zeros((n, h_q, d))
+            self.q[np.arange(n)[:, None], np.arange(h_q)[None], r.integers(0, d, (n, h_q))] = 1.0
+            self.pool = r.integers(-4, 5, shape).astype(np.float64)
+        else:
+            self.q, self.pool = bf16(r.normal(0, spread, (n, h_q, d))), bf16(r.normal(0, 1, shape))
+
+    def run(self, cuda, ctx=None, stream=None, out=None, total=None, start=None, q=None):
+        ctx = ctx or context(self.h_q, self.h_kv, self.d)
+        t = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).to(cuda).to(dt)
+        q = t(self.q, BF) if q is None else q
+        out = torch.full(q.shape, 7.0, dtype=BF, device=cuda) if out is None else out
+        ws = torch.full((ctx.extend_bf16_workspace_size(len(self.total), len(self.q)),), 255, dtype=torch.uint8, device=cuda)
+        ctx.extend_bf16(q, t(self.pool, BF), t(self.tables, I32), t(self.start if start is None else start, I32),
+                        t(self.total if total is None else total, I32), out, ws, stream)
+        torch.cuda.synchronize()
+        assert ctx.debug_error()[0] == 0
+        return out
+
+    def check(self, out, sm_scale=None, exact=False):
+        want, bound = chunk_oracle.extend(self.q, self.pool, self.tables, self.start, self.total,
+                                          sm_scale or 1 / math.sqrt(self.d), exact)
+        got = out.double().cpu().numpy()
+        n = len(got) - self.spare
+        assert (got[n:] == 7).all()
+        err = np.abs(got[:n] - want[:n])
+        assert (err <= bound[:n]).all(), ("off by", err.max(), "rows", np.unique(np.where(~(err <= bound[:n]))[0])[:8])
+
+
+SHAPES = [([(0, 1)], 4, 2, 64), ([(1339, 5)], 4, 2, 64), ([(0, 16)], 1, 1, 128), ([(0, 17)], 8, 1, 128),
+          ([(0, 128)], 2, 2, 64), ([(0, 129)], 2, 1, 128), ([(127, 1)], 8, 8, 128), ([(128, 1)], 16, 2, 128),
+          ([(0, 300)], 4, 4, 128), ([(37, 333)], 8, 2, 64), ([(0, 0), (5, 0), (0, 3), (40, 1), (513, 70), (0, 0), (2, 1)], 8, 2, 128),
+          ([(5000, 3)], 8, 1, 128), ([(9000, 1), (20, 200), (3000, 2)], 4, 1, 64), ([(i * 13 % 300, i % 4) for i in range(90)], 4, 2, 64),
+          ([(1000, 700), (0, 900)], 4, 2, 128)]
+
+
+@pytest.mark.parametrize("lens,h_q,h_kv,d", SHAPES)
+def test_matches_the_definition(cuda, lens, h_q, h_kv, d):
+    c = Case(lens, h_q, h_kv, d, seed=len(lens) + d, spare=3)
+    c.check(c.run(cuda))
+
+
+@pytest.mark.parametrize("lens,h_q,h_kv,d", SHAPES)
+def test_exact_weights(cuda, lens, h_q, h_kv, d):
+    """Logits that are whole in log2 units: weights and sums are exact, so that every token counts to the last bit."""
+    c = Case(lens, h_q, h_kv, d, seed=d, integers=True)
+    scale = math.log(2)
+    c.check(c.run(cuda, context(h_q, h_kv, d, sm_scale=scale)), scale, exact=True)
+
+
+def test_runs_are_alike_and_streams_apart(cuda):
+    c = Case([(3000, 5), (0, 200), (700, 1)], 8, 2, 128, seed=4)
+    ctx, a = context(8, 2, 128), None
+    side = torch.cuda.Stream()
+    for stream in (None, None, side):
+        b = c.run(cuda, ctx, stream=stream)
+        assert a is None or torch.equal(a, b)
+        a = b
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_nothing_unseen_matters(cuda, d):
+    """NaN and infinity behind the sequences, in unused pages and in tokens that come after a row's own."""
+    lens = [(0, 150), (130, 5), (1000, 40), (5, 1), (2000, 2)]
+    c = Case(lens, 4, 2, d, seed=d, more_pages=3)
+    want = c.run(cuda).double().cpu().numpy()
+    used = np.zeros(len(c.pool), bool)
+    for b, total in enumerate(c.total):
+        pages = c.tables[b, :-(-total // P)]
+        used[pages] = True
+        if total % P:
+            c.pool[pages[-1], :, :, total % P:] = np.nan
+    c.pool[~used] = np.inf
+    got = c.run(cuda).double().cpu().numpy()
+    assert np.array_equal(got, want)
+    # the last token of the first and third request: rows in front of it do not see it, its own row does
+    for b, bad in ((0, np.nan), (2, np.inf)):
+        t = c.total[b] - 1
+        c.pool[c.tables[b, t // P], :, 1, t % P, 3] = bad
+    n = c.run(cuda).double().cpu().numpy()
+    last = [c.start[1] - 1, c.start[3] - 1]
+    rows = np.setdiff1d(np.arange(len(n)), last)
+    oracle, bound = chunk_oracle.extend(c.q, np.where(np.isfinite(c.pool), c.pool, 0.0), c.tables, c.start, c.total, 1 / math.sqrt(d))
+    assert (np.abs(n[rows] - oracle[rows]) <= bound[rows]).all()
+    assert np.isnan(n[last[0], :, 3]).all() and np.isposinf(n[last[1], :, 3]).all()
+    rest = np.setdiff1d(np.arange(d), [3])
+    assert (np.abs(n[last][:, :, rest] - oracle[last][:, :, rest]) <= bound[last][:, :, rest]).all()
+
+
+def test_unseen_keys_of_nan(cuda):
+    """A NaN key gives its rows NaN and the rows in front of it nothing."""
+    c = Case([(20, 300)], 4, 2, 64, seed=8)
+    want = c.run(cuda)
+    t = 20 + 250
+    c.pool[c.tables[0, t // P], 1, 0, t % P, 5] = np.nan
+    got = c.run(cuda)
+    assert torch.equal(got[:250], want[:250]) and torch.equal(got[:, :2], want[:, :2])
+    assert torch.isnan(got[250:, 2:]).all()
+
+
+def test_pages_outside_the_pool_are_masked(cuda):
+    c = Case([(700, 30), (50, 9), (10, 3)], 8, 2, 128, seed=5)
+    c.tables[0, 3], c.tables[0, 40], c.tables[1, 0], c.tables[2, 0] = -1, len(c.pool), 2 ** 31 - 1, -2 ** 31
+    c.check(c.run(cuda))                                 # the third request sees nothing at all: zeros
+    ctx = context(8, 2, 128, debug_bounds=1)
+    t = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).to(cuda).to(dt)
+    out = torch.empty(c.q.shape, dtype=BF, device=cuda)
+    ws = torch.empty(ctx.extend_bf16_workspace_size(3, len(c.q)), dtype=torch.uint8, device=cuda)
+    ctx.extend_bf16(t(c.q, BF), t(c.pool, BF), t(c.tables, I32), t(c.start, I32), t(c.total, I32), out, ws)
+    st, kind, index = ctx.debug_error()
+    assert (st, kind) == (-5, 2) and index in (-1, len(c.pool), 2 ** 31 - 1, -2 ** 31)
+
+
+def test_rows_without_room_and_bad_lengths(cuda):
+    """Positions below 0 see nothing; lengths outside the table count as the nearer end; starts that do not ascend or
+    pass the rows touch nothing else."""
+    c = Case([(0, 40), (0, 30), (4, 20)], 4, 2, 64, seed=6, spare=2)
+    total = c.total.copy()
+    total[0] = 7
+    got = c.run(cuda, total=total).double().cpu().numpy()
+    c.total[0] = 7
+    want, bound = chunk_oracle.extend(c.q, c.pool, c.tables, c.start, c.total, 1 / 8)
+    assert (got[:33] == 0).all() and (np.abs(got - want)[:90] <= bound[:90]).all() and (got[90:] == 7).all()
+    total[:] = [-5, 30, 2 ** 31 - 1]
+    got = c.run(cuda, total=total).double().cpu().numpy()
+    assert (got[:40] == 0).all() and (np.abs(got - want)[40:70] <= bound[40:70]).all() and (got[90:] == 7).all()
+    for start in ([0, 70, 40, 2 ** 31 - 1], [-9, 40, 30, 92], [92, 0, 92, 0], [0, 0, 0, 0]):
+        c.run(cuda, start=np.array(start))
+    assert (c.run(cuda, start=np.zeros(4, int)) == 7).all()
+
+
+def test_output_over_the_queries(cuda):
+    """out may be q itself, also for rows that are formed a second time."""
+    c = Case([(300, 200), (4000, 3)], 8, 2, 128, seed=7)
+    c.pool[c.tables[0, 31], :, 1, 3, 9] = np.inf         # token 499 of 500
+    c.pool[c.tables[1, 250], :, 1, 2, 8] = -np.inf       # token 4,002 of 4,003
+    want = c.run(cuda)
+    q = torch.from_numpy(c.q).to(BF).to(cuda)
+    c.run(cuda, q=q, out=q)
+    assert torch.equal(q, want)
+
+
+def test_large_logits(cuda):
+    """Logits far apart: references that rise again and again, weights that vanish."""
+    for spread in (30.0, 1000.0):
+        c = Case([(900, 300), (0, 70)], 4, 1, 128, seed=int(spread), spread=spread)
+        c.check(c.run(cuda))
+
+
+def test_infinite_logits(cuda):
+    """A token of logit -inf has no weight; a row without any other gives zeros, and +inf gives NaN."""
+    c = Case([(0, 33)], 2, 1, 64, seed=3)
+    c.q[:], c.pool[:, :, 0] = 1.0, 0.0
+    c.pool[c.tables[0, 0], 0, 0, 0, 0] = -np.inf
+    want, bound = chunk_oracle.extend(c.q, c.pool, c.tables, c.start, c.total, 1 / 8)
+    got = c.run(cuda).double().cpu().numpy()
+    assert (got[0] == 0).all() and (np.abs(got - want)[1:] <= bound[1:]).all()
+    c.pool[c.tables[0, 0], 0, 0, 5, 0] = np.inf
+    got = c.run(cuda).double().cpu().numpy()
+    assert (np.abs(got - want)[1:5] <= bound[1:5]).all() and np.isnan(got[5:]).all()
+
+
+def test_query_rows_at_a_stride(cuda):
+    c = Case([(40, 90), (800, 2)], 4, 2, 64, seed=2)
+    wide = torch.full((92, 4 * 64 + 24), float("nan"), dtype=BF, device=cuda)
+    q = wide[:, 8:264].unflatten(1, (4, 64))
+    q.copy_(torch.from_numpy(c.q).to(BF))
+    c.check(c.run(cuda, q=q, out=torch.empty(92, 4, 64, dtype=BF, device=cuda)))
+
+
+def test_agrees_with_the_decode(cuda):
+    """Single tokens: the decode's fp32 outputs are the definition to 2^-20."""
+    lens = [(0, 1), (15, 1), (4000, 1), (16, 1), (77, 1)]
+    c = Case(lens, 8, 2, 128, seed=1)
+    got = c.run(cuda)
+    ctx = context(8, 2, 128)
+    t = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).to(cuda).to(dt)
+    out = torch.empty(5, 8, 128, device=cuda)
+    ws = torch.empty(max(1, ctx.decode_bf16_workspace_size(5, 4001)), dtype=torch.uint8, device=cuda)
+    ctx.decode_bf16(t(c.q, BF), t(c.pool, BF), t(c.tables, I32), t(c.total, I32), 4001, out, ws)
+    _, bound = chunk_oracle.extend(c.q, c.pool, c.tables, c.start, c.total, 1 / math.sqrt(128))
+    assert (np.abs(got.double().cpu().numpy() - out.double().cpu().numpy()) <= bound + 2.0 ** -20 * out.abs().max().item()).all()
+
+
+@pytest.mark.parametrize("h_q,h_kv,d,layout", [(4, 2, 64, 0), (8, 1, 128, 1)])
+def test_prompt_and_tokens_in_one_captured_loop(cuda, h_q, h_kv, d, layout):
+    """plan, norm and rotation, append, attention: two prompts in chunks, then single tokens, from one captured graph a
+    chunk size, against the whole definition in 64 bits."""
+    r = np.random.default_rng(d)
+    steps = [(70, 33), (1, 40), (1, 1), (1, 1), (0, 1)]
+    n_max = max(sum(s) for s in steps)
+    stride, pages, batch = 8, 20, 2
+    ctx = context(h_q, h_kv, d)
+    turns, scale = rope.rope_turns(d, 1e4, dict(kind="yarn", factor=2, trained=64))
+    t = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).to(cuda).to(dt)
+    z = lambda *s, dt=I32: torch.zeros(s, dtype=dt, device=cuda)
+    free, pool, tables = t(r.permutation(pages), I32), torch.full((pages, h_kv, 2, P, d), float("nan"), dtype=BF, device=cuda), z(batch, stride)
+    seq, new, state, start, total = z(batch), z(batch), z(4), z(batch + 1), z(batch)
+    slots = z(n_max, dt=I64)
+    qkv = torch.zeros(n_max, h_q + 2 * h_kv, d, dtype=BF, device=cuda)
+    qw, kw = (t(r.normal(1, 0.2, d), torch.float32) for _ in range(2))
+    qr, kr, out = z(n_max, h_q, d, dt=BF), z(n_max, h_kv, d, dt=BF), z(n_max, h_q, d, dt=BF)
+    ws = torch.empty(ctx.extend_bf16_workspace_size(batch, n_max), dtype=torch.uint8, device=cuda)
+    tt = torch.from_numpy(turns).to(cuda)
+
+    def step():
+        ctx.plan_append(seq, new, free, state[:1], tables, slots, start, total, state)
+        ctx.norm_rope(qkv[:, :h_q], qkv[:, h_q:h_q + h_kv], qr, kr, tt, row_start=start, total_len=total, q_weight=qw,
+                      k_weight=kw, layout=layout, scale=scale)
+        ctx.append_bf16(kr, qkv[:, h_q + h_kv:], slots, pool)
+        ctx.extend_bf16(qr, pool, tables, start, total, out, ws)
+        seq.copy_(total)
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for x in (seq, state, tables):
+        x.zero_()
+    have = [np.zeros((0, 2, h_kv, d)) for _ in range(batch)]
+    for counts in steps:
+        new.copy_(t(np.array(counts), I32))
+        x = bf16(r.normal(0, 1, (n_max, h_q + 2 * h_kv, d)))
+        qkv.copy_(t(x, BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert state[2].item() == 0 and ctx.debug_error()[0] == 0
+        got_q, got_k, got = (a.double().cpu().numpy() for a in (qr, kr, out))
+        row = 0
+        for b, m in enumerate(counts):
+            rows = slice(row, row + m)
+            pos = len(have[b]) + np.arange(m)
+            for y, g, w in ((x[rows, :h_q], got_q[rows], qw), (x[rows, h_q:h_q + h_kv], got_k[rows], kw)):
+                want, bound = rope_oracle.norm_rope(y, w.cpu().numpy(), 1e-6, turns.view(np.uint64).tolist(), layout == 1, scale, pos)
+                assert (np.abs(g - want) <= bound).all()
+            have[b] = np.concatenate([have[b], np.stack([got_k[rows], x[rows, h_q + h_kv:]], 1)])
+            row += m
+        for b, m in enumerate(counts):
+            k = len(have[b])
+            one = np.zeros((-(-k // P), h_kv, 2, P, d))
+            for i in range(k):
+                one[i // P, :, :, i % P] = have[b][i].transpose(1, 0, 2)
+            lo = sum(counts[:b])
+            want, bound = chunk_oracle.extend(got_q[lo:lo + m], one, np.arange(len(one))[None], [0, m], [k], 1 / math.sqrt(d))
+            assert (np.abs(got[lo:lo + m] - want) <= bound).all()
