@@ -375,50 +375,22 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return r;
 }
 
-// One row's accumulator token by token, for rows that an infinity or NaN of a token behind their own has reached; the
-// whole warp works on it, lane l on channels l D / 32 and on.
+// Where a row's result goes: its part of a cut item, or the output.
+struct Place {
+    float* part;
+    uint16_t* out;
+};
 template <int D>
-__device__ __noinline__ void form_row(const ChunkArgs& a, const Item& it, int r, int g_log2, float m, int lane,
-                                      const Guard& guard, float (&acc)[D / 32]) {
-    constexpr int kChannels = D / 32;
-    const int limit = min(limit_of(r, it.pos0, g_log2), it.kv1 * kChunkTile);
-    const uint16_t* q = a.q + (int64_t)(it.tok0 + (r >> g_log2)) * a.q_stride + ((it.head << g_log2) + (r & (a.g - 1))) * D;
-#pragma unroll
-    for (int c = 0; c < kChannels; ++c) acc[c] = 0.0f;
-    for (int t0 = it.kv0 * kChunkTile; t0 < limit; t0 += 32) {
-        if (lane == 0) *guard.beat = *guard.beat + 1;
-        const int t = t0 + lane;
-        const int id = t < limit ? a.tables[(int64_t)it.b * a.stride + t / kPage] : -1;
-        const bool there = id >= 0 && id < a.pages;
-        const uint16_t* k = a.pool + (((int64_t)(there ? id : 0) * a.h_kv + it.head) * 2 * kPage + t % kPage) * D;
-        float dot = 0.0f;
-        if (there) {
-            for (int c = 0; c < D; c += 8) {
-                const uint4 x = *reinterpret_cast<const uint4*>(q + c), y = *reinterpret_cast<const uint4*>(k + c);
-                dot += bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) +
-                       bf16_hi(x.y) * bf16_hi(y.y) + bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z) +
-                       bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
-            }
-        }
-        const float p = there ? bf16_lo(bf16_pair(exp2_approx(fmaf(dot, a.scale_log2, -m)), 0.0f)) : 0.0f;
-        const int64_t v_row = (((int64_t)(there ? id : 0) * a.h_kv + it.head) * 2 + 1) * kPage + t % kPage;
-        for (int i = 0; i < 32; ++i) {
-            const float pi = __shfl_sync(0xffffffffu, p, i);
-            const int64_t row = __shfl_sync(0xffffffffu, v_row, i);
-            if (pi == 0.0f) continue;
-            const uint16_t* v = a.pool + row * D + lane * kChannels;
-#pragma unroll
-            for (int c = 0; c < kChannels; ++c) acc[c] += pi * __uint_as_float((uint32_t)v[c] << 16);
-        }
-    }
+__device__ __forceinline__ Place place_of(const ChunkArgs& a, const Work& w, const Item& it, int r, int g_log2) {
+    const int64_t row = (int64_t)(it.tok0 + (r >> g_log2)) * (a.h_kv << g_log2) + (it.head << g_log2) + (r & (a.g - 1));
+    return {it.part >= 0 ? w.part_acc + (int64_t)(it.part + r - it.r0) * D : nullptr, a.out + row * D};
 }
 
 // Stores a row's channels first .. first + N: normalised and rounded to the output, or as they are to the part.
 template <int D, int N>
-__device__ __forceinline__ void store_row(const ChunkArgs& a, const Work& w, const Item& it, int r, int g_log2, int first,
-                                          const float (&x)[N], float inv) {
-    if (it.part >= 0) {
-        float* to = w.part_acc + (int64_t)(it.part + r - it.r0) * D + first;
+__device__ __forceinline__ void store_row(const Place& to_row, int first, const float (&x)[N], float inv) {
+    if (to_row.part) {
+        float* to = to_row.part + first;
         if constexpr (N % 4 == 0) {
 #pragma unroll
             for (int c = 0; c < N; c += 4) *reinterpret_cast<float4*>(to + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
@@ -428,8 +400,7 @@ __device__ __forceinline__ void store_row(const ChunkArgs& a, const Work& w, con
         }
         return;
     }
-    const int64_t row = (int64_t)(it.tok0 + (r >> g_log2)) * (a.h_kv << g_log2) + (it.head << g_log2) + (r & (a.g - 1));
-    uint16_t* to = a.out + row * D + first;
+    uint16_t* to = to_row.out + first;
     uint32_t u[N / 2];
 #pragma unroll
     for (int c = 0; c < N / 2; ++c) u[c] = bf16_pair(x[2 * c] * inv, x[2 * c + 1] * inv);
@@ -440,6 +411,43 @@ __device__ __forceinline__ void store_row(const ChunkArgs& a, const Work& w, con
 #pragma unroll
         for (int c = 0; c < N / 2; ++c) *reinterpret_cast<uint32_t*>(to + 2 * c) = u[c];
     }
+}
+
+// One row token by token, for rows that an infinity or NaN of a token behind their own has reached; the
+// whole warp works on it, lane l on channels l D / 32 and on: query q, tokens [first, limit), reference m.
+template <int D>
+__device__ __noinline__ void form_row(const ChunkArgs& a, const uint16_t* q, const int32_t* table, int head, int first,
+                                      int limit, float m, float inv, Place place, volatile int* beat) {
+    constexpr int kChannels = D / 32;
+    const int lane = threadIdx.x % 32;
+    float acc[kChannels] = {};
+    for (int t0 = first; t0 < limit; t0 += 32) {
+        if (lane == 0) *beat = *beat + 1;
+        const int t = t0 + lane;
+        const int id = t < limit ? table[t / kPage] : -1;
+        const bool there = id >= 0 && id < a.pages;
+        const uint16_t* k = a.pool + (((int64_t)(there ? id : 0) * a.h_kv + head) * 2 * kPage + t % kPage) * D;
+        float dot = 0.0f;
+        if (there) {
+            for (int c = 0; c < D; c += 8) {
+                const uint4 x = *reinterpret_cast<const uint4*>(q + c), y = *reinterpret_cast<const uint4*>(k + c);
+                dot += bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) +
+                       bf16_hi(x.y) * bf16_hi(y.y) + bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z) +
+                       bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
+            }
+        }
+        const float p = there ? bf16_lo(bf16_pair(exp2_approx(fmaf(dot, a.scale_log2, -m)), 0.0f)) : 0.0f;
+        const int64_t v_row = (((int64_t)(there ? id : 0) * a.h_kv + head) * 2 + 1) * kPage + t % kPage;
+        for (int i = 0; i < 32; ++i) {
+            const float pi = __shfl_sync(0xffffffffu, p, i);
+            const int64_t row = __shfl_sync(0xffffffffu, v_row, i);
+            if (pi == 0.0f) continue;
+            const uint16_t* v = a.pool + row * D + lane * kChannels;
+#pragma unroll
+            for (int c = 0; c < kChannels; ++c) acc[c] += pi * __uint_as_float((uint32_t)v[c] << 16);
+        }
+    }
+    store_row<D, kChannels>(place, lane * kChannels, acc, inv);
 }
 
 // Loader: work items to the other roles, K and V pages to the ring.
@@ -526,10 +534,11 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, uint8_t* smem_kv,
     uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
     bool ok = true, issued = false;
     auto scores = [&](int t, uint32_t k_tile) {              // S of block t, from lane 0
+        const uint32_t qd = sw128_desc(q + t * L::kTileBytes, 0), kd = sw128_desc(k_tile, 0);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks / 4) * L::kHalfBytes + (ks % 4) * 32;
-            umma_ss(tmem + t * kChunkTile, sw128_desc(q + t * L::kTileBytes + off, 0), sw128_desc(k_tile + off, 0), kScores, ks > 0);
+            const uint32_t off = ((ks / 4) * L::kHalfBytes + (ks % 4) * 32) >> 4;
+            umma_ss(tmem + t * kChunkTile, qd + off, kd + off, kScores, ks > 0);
         }
         umma_commit(bars.s_full(t));
     };
@@ -586,10 +595,11 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, uint8_t* smem_kv,
                     if (!ok) break;
                     tc_fence_after();
                     if (lane == 0) {
+                        const uint32_t vd = sw128_desc(v_tile, L::kHalfBytes);
 #pragma unroll
                         for (int k16 = 0; k16 < kChunkTile / 16; ++k16)
-                            umma_ts(tmem + 2 * kChunkTile + t * D, tmem + t * kChunkTile + k16 * 8,
-                                    sw128_desc(v_tile + k16 * 2048, L::kHalfBytes), kValues, j > 0 || k16 > 0);
+                            umma_ts(tmem + 2 * kChunkTile + t * D, tmem + t * kChunkTile + k16 * 8, vd + k16 * (2048 >> 4),
+                                    kValues, j > 0 || k16 > 0);
                         umma_commit(bars.o_done(t));
                     }
                 }
@@ -664,13 +674,9 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
             }
             tc_fence_after();
             uint32_t u[kChunkTile];
-#pragma unroll
-            for (int c = 0; c < kChunkTile; c += 32) tmem_ld32(s_col + c, u + c);
+            tmem_read128(s_col, u);
             const int seen = limit - (it.kv0 + j) * kChunkTile;
             const int mask = masks[(tile0 + j) % kMaskRing];
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < kChunkTile; c += 32) loaded32(u + c);
             if (__any_sync(0xffffffffu, seen < kChunkTile || mask != 0xff)) {
 #pragma unroll
                 for (int c = 0; c < kChunkTile; ++c)
@@ -697,9 +703,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
 #pragma unroll
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
-                        tmem_ld32(o_col + c, o);
-                        tmem_wait_ld();
-                        loaded32(o);
+                        tmem_read32(o_col + c, o);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                         tmem_st32(o_col + c, o);
@@ -732,14 +736,13 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
         tc_fence_after();
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         if (it.part >= 0 && mine) w.part_ml[it.part + local] = make_float2(m, sum);
+        const Place place = place_of<D>(a, w, it, r, g_log2);
         bool odd = false;
         if (count > 0) {                         // first look at the whole row: form_row reads its query, which out may lie over
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
-                tmem_ld32(o_col + c, o);
-                tmem_wait_ld();
-                loaded32(o);
+                tmem_read32(o_col + c, o);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) odd |= !(fabsf(__uint_as_float(o[k])) <= 3.402823466e38f);
             }
@@ -748,21 +751,18 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
         for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
             float x[32];
-            if (count > 0) {
-                tmem_ld32(o_col + c, o);
-                tmem_wait_ld();
-                loaded32(o);
-            }
+            if (count > 0) tmem_read32(o_col + c, o);
 #pragma unroll
             for (int k = 0; k < 32; ++k) x[k] = count > 0 ? __uint_as_float(o[k]) : 0.0f;
-            if (mine && !odd) store_row<D, 32>(a, w, it, r, g_log2, c, x, inv);
+            if (mine && !odd) store_row<D, 32>(place, c, x, inv);
         }
         tc_fence_before();
         for (uint32_t todo = __ballot_sync(0xffffffffu, odd && mine); todo; todo &= todo - 1) {
             const int src = __ffs(todo) - 1, row = r - lane + src;
-            float acc[D / 32];
-            form_row<D>(a, it, row, g_log2, __shfl_sync(0xffffffffu, m, src), lane, guard, acc);
-            store_row<D, D / 32>(a, w, it, row, g_log2, lane * (D / 32), acc, __shfl_sync(0xffffffffu, inv, src));
+            form_row<D>(a, a.q + (int64_t)(it.tok0 + (row >> g_log2)) * a.q_stride + ((it.head << g_log2) + (row & (a.g - 1))) * D,
+                        a.tables + (int64_t)it.b * a.stride, it.head, it.kv0 * kChunkTile,
+                        min(limit_of(row, it.pos0, g_log2), it.kv1 * kChunkTile), __shfl_sync(0xffffffffu, m, src),
+                        __shfl_sync(0xffffffffu, inv, src), place_of<D>(a, w, it, row, g_log2), guard.beat);
         }
     }
 }
@@ -813,12 +813,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attend_kernel(const __grid_
     grid_wait();
     grid_release();
 
-    // registers: 384 x 168 at launch; 256 x 208 + 128 x 80 = 63,488 of those 64,512
+    // registers: 384 x 168 at launch; 256 x 200 + 128 x 96 = 63,488 of those 64,512
     if (warp < kSoftmaxWarps) {
-        more_registers<208>();
+        more_registers<200>();
         softmax_role<D>(a, w, smem, tmem, bars, guard, masks, slots, warp / 4, warp % 4, lane);
     } else {
-        fewer_registers<80>();
+        fewer_registers<96>();
         if (warp == kSoftmaxWarps) load_role<D>(a, w, &map, sb + L::kOffKv, bars, guard, masks, slots, lane);
         if (warp == kSoftmaxWarps + 1)
             issue_role<D>(a, smem + L::kOffKv, sb, sb + L::kOffKv, tmem, bars, guard, slots, lane);
@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkArg
     grid_wait();
     const int n_items = w.head->items;
     for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-        Item it = read_item(w.items + item);
+        const Item it = read_item(w.items + item);
         if (it.part < 0) continue;
         const int base = it.part - it.piece * it.rows;
         const int end = (int)((long long)it.rows * (it.piece + 1) / it.pieces);
@@ -869,10 +869,8 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkArg
                     for (int c = 0; c < kChannels; ++c) acc[c] += fp * from[c];
                 }
             }
-            const int part = it.part;
-            it.part = -1;
-            store_row<D, kChannels>(a, w, it, it.r0 + local, g_log2, lane * kChannels, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
-            it.part = part;
+            store_row<D, kChannels>({nullptr, place_of<D>(a, w, it, it.r0 + local, g_log2).out}, lane * kChannels, acc,
+                                    sum == 0.0f ? 0.0f : 1.0f / sum);
         }
     }
 }
