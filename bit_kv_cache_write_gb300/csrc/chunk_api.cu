@@ -130,12 +130,12 @@ oscar_status oscar_extend_bf16(oscar_ctx_t* ctx, const void* q, int64_t q_stride
                               0x7ffffff0LL / (2 * s.h_kv));
     const int width = s.h_q * s.d;
     if (q_stride < 0 || q_stride % 8 || q_stride > (int64_t)1 << 31 || !aligned(q, 16) || !aligned(bf16_pool, 32) ||
-        !aligned(out, 16))
+        !aligned(out, 32))
         return record_failure(OSCAR_ERR_INVALID_ARG,
-                              "q and out must be 16-byte aligned, the pool 32-byte, q_stride a multiple of 8 up to 2^31 (is %lld)",
+                              "q must be 16-byte aligned, the pool and out 32-byte, q_stride a multiple of 8 up to 2^31 (is %lld)",
                               (long long)q_stride);
-    if (!(q == out && (n == 1 || q_stride == width)) && share({q, q_stride, width}, {out, width, width}, n))
-        return record_failure(OSCAR_ERR_INVALID_ARG, "out overlaps q without being it");
+    if (share({q, q_stride, width}, {out, width, width}, n))
+        return record_failure(OSCAR_ERR_INVALID_ARG, "out overlaps q");
     const oscar::ChunkPlan plan = oscar::plan_chunk(s, ctx->num_sms, batch, n);
     if (!workspace || workspace_bytes < plan.total)
         return record_failure(OSCAR_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace_bytes, plan.total);

@@ -13,14 +13,13 @@
 //   warps 0..7  one warp group a block, a thread a row: the row's 128 logits in registers, weights rounded to bf16
 //               over the logits' own columns, O scaled only where the reference rises.
 // The weights' rounding to bf16 is the operand type of the product (a second piece would cost half again of the
-// tensor time that bounds long prompts). Their sum takes the rounded weights, in fp32, so each output is an exactly
-// normalised mean with weights off by 2^-8 at most; it is then rounded once to bf16.
+// tensor time that bounds long prompts); their sum is of the unrounded ones, in fp32.
 //
 // Items of requests with long caches and few rows are cut along the cache: chunk_plan_kernel chooses the cut from the
 // lengths on the device, so that the items fill the SMs evenly; chunk_join_kernel adds the parts of cut items.
 //
 // A weight of 0 does not undo an infinity or NaN in the value of a token that a row must not see (0 x inf): rows whose
-// accumulator is not finite are formed again token by token, with the tokens that they see alone.
+// accumulator is not finite are marked, and chunk_join_kernel forms them again with the tokens that they see alone.
 //
 // Every wait is bounded: a role that gives up records kind 4 and sets a flag, the others stop, copies and matrix
 // products in flight are waited for (bounded too), tensor memory is freed.
@@ -37,20 +36,22 @@ constexpr int kBlock = 128;                      // query rows of a block
 constexpr int kTilePages = kChunkTile / kPage;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = 384;                    // two softmax warp groups, one of loader and issuer
+constexpr int kItemRing = 4;                     // items that the loader may be ahead with the others
 constexpr int kMaskRing = 16;                    // tiles whose page masks are kept: more than the loader is ahead
 constexpr int kPlanThreads = 1024;
 constexpr int kJoinThreads = 256;
 constexpr float kNoReference = -3.402823466e38f; // reference before any token: no finite logit is below it
 constexpr float kHeadroom = 8.0f;                // the reference rises when a logit passes it by this much (log2)
-constexpr long long kWaitCycles = 2000000000LL;
+constexpr uint32_t kWaitTicks = 1000000000u;      // nanoseconds of a wait at most
 
 // A work item: rows r0 .. r0 + rows of request b's row space against cache tiles [kv0, kv1).
 struct alignas(16) Item {
     int b, head, tok0, r0;        // tok0: the request's first row of q
     int rows, pos0, kv0, kv1;     // pos0: position of the request's first new token (below 0 where it has no room)
     int total, part, piece, pieces;   // part: first row of its partial results, or -1
+    int self, pad[3];             // its number
 };
-static_assert(sizeof(Item) == 48, "copied as twelve words");
+static_assert(sizeof(Item) == 64, "copied as four words of 16 bytes");
 
 struct Header {
     int items, next;              // next: item after the CTAs' first ones
@@ -61,6 +62,7 @@ struct Work {
     int* tiles;                   // [batch + 1] first row block of each request
     int2* units;                  // per row block: request, cache tiles
     Item* items;
+    uint32_t* odd;                // [items][8] rows to form again, a word for each softmax warp
     float2* part_ml;              // per row of a cut item: reference and sum
     float* part_acc;              // [rows][d]
 };
@@ -232,6 +234,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
             it.total = r.total;
             const int part = part_base + first_part[at] + (it.head * p + it.piece) * it.rows;
             it.part = p > 1 ? min(part, part_cap - it.rows) : -1;
+            it.self = item_base + i;
             w.items[item_base + i] = it;
         }
         item_base += items;
@@ -246,6 +249,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
 
 // ---- attention ----------------------------------------------------------------------------------------------
 
+// Shared memory of a CTA, by addresses: `base` and constants, so that a role keeps one register for all of it.
 template <int D>
 struct Layout {
     static constexpr int kHalves = D / 64;                     // blocks of 64 channels, 128 bytes a row
@@ -254,63 +258,69 @@ struct Layout {
     static constexpr int kStages = D == 128 ? 5 : 8;           // K and V tiles in turn
     static constexpr int kOffKv = 2 * kTileBytes;              // behind the two query blocks
     static constexpr int kOffItem = kOffKv + kStages * kTileBytes;
-    static constexpr int kOffBar = kOffItem + 2 * (int)sizeof(Item);
-    static constexpr int kBars = 2 * kStages + 2 * 4 + 4 + 1;
+    static constexpr int kOffBar = kOffItem + kItemRing * (int)sizeof(Item);
+    static constexpr int kBars = 2 * kStages + 2 * 4 + 1 + 2 * kItemRing;
     static constexpr int kOffMask = kOffBar + 8 * kBars;
-    static constexpr int kOffMisc = kOffMask + 4 * kMaskRing;
-    static constexpr int kBytes = kOffMisc + 16;
-    static constexpr size_t kDynamic = (size_t)kBytes + 1024;  // the tiles start on 1,024 bytes
-    static_assert(kDynamic <= 227 * 1024, "shared memory of a CTA");
-};
+    static constexpr int kOffTmem = kOffMask + 4 * kMaskRing;
+    static constexpr int kOffFail = kOffTmem + 4;
+    static constexpr int kBytes = kOffFail + 12;
+    static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
 
-struct Bars {
     uint32_t base;
-    int stages;
-    __device__ uint32_t kv_full(int s) const { return base + 8 * s; }
-    __device__ uint32_t kv_empty(int s) const { return base + 8 * (stages + s); }
-    __device__ uint32_t q_full(int t) const { return base + 8 * (2 * stages + t); }
-    __device__ uint32_t s_full(int t) const { return base + 8 * (2 * stages + 2 + t); }
-    __device__ uint32_t p_full(int t) const { return base + 8 * (2 * stages + 4 + t); }
-    __device__ uint32_t o_done(int t) const { return base + 8 * (2 * stages + 6 + t); }
-    __device__ uint32_t item_full(int i) const { return base + 8 * (2 * stages + 8 + i); }
-    __device__ uint32_t item_empty(int i) const { return base + 8 * (2 * stages + 10 + i); }
-    __device__ uint32_t last() const { return base + 8 * (2 * stages + 12); }
-};
+    __device__ uint32_t q(int t) const { return base + t * kTileBytes; }
+    __device__ uint32_t kv(int slot) const { return base + kOffKv + slot % kStages * kTileBytes; }
+    __device__ uint32_t item(int i) const { return base + kOffItem + i % kItemRing * (int)sizeof(Item); }
+    __device__ uint32_t mask(int tile) const { return base + kOffMask + 4 * (tile % kMaskRing); }
+    __device__ uint32_t tmem() const { return base + kOffTmem; }
+    __device__ uint32_t fail() const { return base + kOffFail; }
+    // mbarriers; those of a ring come with the phase of its i-th turn
+    __device__ uint32_t bar(int i) const { return base + kOffBar + 8 * i; }
+    __device__ uint32_t kv_full(int slot) const { return bar(slot % kStages); }
+    __device__ uint32_t kv_empty(int slot) const { return bar(kStages + slot % kStages); }
+    __device__ static uint32_t kv_phase(int slot) { return slot / kStages & 1; }
+    __device__ uint32_t q_full(int t) const { return bar(2 * kStages + t); }
+    __device__ uint32_t s_full(int t) const { return bar(2 * kStages + 2 + t); }
+    __device__ uint32_t p_full(int t) const { return bar(2 * kStages + 4 + t); }
+    __device__ uint32_t o_done(int t) const { return bar(2 * kStages + 6 + t); }
+    __device__ uint32_t last() const { return bar(2 * kStages + 8); }
+    __device__ uint32_t item_full(int i) const { return bar(2 * kStages + 9 + i % kItemRing); }
+    __device__ uint32_t item_empty(int i) const { return bar(2 * kStages + 9 + kItemRing + i % kItemRing); }
+    __device__ static uint32_t item_phase(int i) { return i / kItemRing & 1; }
 
-// What the CTA's roles share to give up together.
-struct Guard {
-    volatile int* fail;
-    volatile int* beat;            // moves while a warp forms rows token by token: the others' waits start anew
-    DebugWord* dbg;
-
-    __device__ void give_up(int where) const {
-        *fail = 1;
+    // A role that gives up: the others stop at their next wait.
+    __device__ void give_up(DebugWord* dbg, int where) const {
+        sts32(fail(), 1);
         record_error(&dbg->kind, &dbg->index, 4, where);
     }
     // False once the wait has run out or another role has given up; the same for all lanes of the warp.
-    __device__ bool wait(uint32_t bar, uint32_t phase, int where) const {
-        bool ok = mbar_test(bar, phase);
-        if (__all_sync(0xffffffffu, ok)) return true;
-        long long t0 = clock64();
-        int seen = *beat;
-        while (!ok && !*fail) {
-            ok = mbar_test(bar, phase);
-            if (*beat != seen) {
-                seen = *beat;
-                t0 = clock64();
-            }
-            if (!ok && clock64() - t0 > kWaitCycles) {
-                give_up(where);
+    __device__ __forceinline__ bool wait(uint32_t at, uint32_t phase, DebugWord* dbg, int where) const {
+        if (__all_sync(0xffffffffu, mbar_test(at, phase))) return true;
+        return wait_longer(at, phase, dbg, where);
+    }
+    __device__ __forceinline__ bool wait_longer(uint32_t at, uint32_t phase, DebugWord* dbg, int where) const {
+        const uint32_t t0 = time_ns();
+        bool ok;
+        while (!(ok = mbar_test(at, phase)) && !lds32(fail())) {
+            if (time_ns() - t0 > kWaitTicks) {
+                give_up(dbg, where);
                 break;
             }
         }
         return __all_sync(0xffffffffu, ok);
     }
     // For what is in flight when a role stops: nobody is told.
-    __device__ void drain(uint32_t bar, uint32_t phase) const {
-        const long long t0 = clock64();
-        while (!mbar_test(bar, phase))
-            if (clock64() - t0 > kWaitCycles) return;
+    __device__ void drain(uint32_t at, uint32_t phase) const {
+        const uint32_t t0 = time_ns();
+        while (!mbar_test(at, phase))
+            if (time_ns() - t0 > kWaitTicks) return;
+    }
+    __device__ Item read_item(int i) const {
+        Item it;
+        lds128(item(i), reinterpret_cast<uint32_t*>(&it));
+        lds128(item(i) + 16, reinterpret_cast<uint32_t*>(&it) + 4);
+        lds128(item(i) + 32, reinterpret_cast<uint32_t*>(&it) + 8);
+        lds128(item(i) + 48, reinterpret_cast<uint32_t*>(&it) + 12);
+        return it;
     }
 };
 
@@ -327,16 +337,6 @@ __device__ __forceinline__ Blocks blocks_of(const Item& it, int g_log2) {
         r.count[t] = max(min(it.kv1, tiles) - it.kv0, 0);
     }
     return r;
-}
-
-__device__ __forceinline__ Item read_item(const Item* slot) {
-    Item it;
-    const int4* s = reinterpret_cast<const int4*>(slot);
-    int4* d = reinterpret_cast<int4*>(&it);
-    d[0] = s[0];
-    d[1] = s[1];
-    d[2] = s[2];
-    return it;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -364,6 +364,11 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ uint64_t sub_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -374,86 +379,15 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-
-// Where a row's result goes: its part of a cut item, or the output.
-struct Place {
-    float* part;
-    uint16_t* out;
-};
-template <int D>
-__device__ __forceinline__ Place place_of(const ChunkArgs& a, const Work& w, const Item& it, int r, int g_log2) {
-    const int64_t row = (int64_t)(it.tok0 + (r >> g_log2)) * (a.h_kv << g_log2) + (it.head << g_log2) + (r & (a.g - 1));
-    return {it.part >= 0 ? w.part_acc + (int64_t)(it.part + r - it.r0) * D : nullptr, a.out + row * D};
-}
-
-// Stores a row's channels first .. first + N: normalised and rounded to the output, or as they are to the part.
-template <int D, int N>
-__device__ __forceinline__ void store_row(const Place& to_row, int first, const float (&x)[N], float inv) {
-    if (to_row.part) {
-        float* to = to_row.part + first;
-        if constexpr (N % 4 == 0) {
-#pragma unroll
-            for (int c = 0; c < N; c += 4) *reinterpret_cast<float4*>(to + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
-        } else {
-#pragma unroll
-            for (int c = 0; c < N; c += 2) *reinterpret_cast<float2*>(to + c) = make_float2(x[c], x[c + 1]);
-        }
-        return;
-    }
-    uint16_t* to = to_row.out + first;
-    uint32_t u[N / 2];
-#pragma unroll
-    for (int c = 0; c < N / 2; ++c) u[c] = bf16_pair(x[2 * c] * inv, x[2 * c + 1] * inv);
-    if constexpr (N % 8 == 0) {
-#pragma unroll
-        for (int c = 0; c < N / 2; c += 4) *reinterpret_cast<uint4*>(to + 2 * c) = make_uint4(u[c], u[c + 1], u[c + 2], u[c + 3]);
-    } else {
-#pragma unroll
-        for (int c = 0; c < N / 2; ++c) *reinterpret_cast<uint32_t*>(to + 2 * c) = u[c];
-    }
-}
-
-// One row token by token, for rows that an infinity or NaN of a token behind their own has reached; the
-// whole warp works on it, lane l on channels l D / 32 and on: query q, tokens [first, limit), reference m.
-template <int D>
-__device__ __noinline__ void form_row(const ChunkArgs& a, const uint16_t* q, const int32_t* table, int head, int first,
-                                      int limit, float m, float inv, Place place, volatile int* beat) {
-    constexpr int kChannels = D / 32;
-    const int lane = threadIdx.x % 32;
-    float acc[kChannels] = {};
-    for (int t0 = first; t0 < limit; t0 += 32) {
-        if (lane == 0) *beat = *beat + 1;
-        const int t = t0 + lane;
-        const int id = t < limit ? table[t / kPage] : -1;
-        const bool there = id >= 0 && id < a.pages;
-        const uint16_t* k = a.pool + (((int64_t)(there ? id : 0) * a.h_kv + head) * 2 * kPage + t % kPage) * D;
-        float dot = 0.0f;
-        if (there) {
-            for (int c = 0; c < D; c += 8) {
-                const uint4 x = *reinterpret_cast<const uint4*>(q + c), y = *reinterpret_cast<const uint4*>(k + c);
-                dot += bf16_lo(x.x) * bf16_lo(y.x) + bf16_hi(x.x) * bf16_hi(y.x) + bf16_lo(x.y) * bf16_lo(y.y) +
-                       bf16_hi(x.y) * bf16_hi(y.y) + bf16_lo(x.z) * bf16_lo(y.z) + bf16_hi(x.z) * bf16_hi(y.z) +
-                       bf16_lo(x.w) * bf16_lo(y.w) + bf16_hi(x.w) * bf16_hi(y.w);
-            }
-        }
-        const float p = there ? bf16_lo(bf16_pair(exp2_approx(fmaf(dot, a.scale_log2, -m)), 0.0f)) : 0.0f;
-        const int64_t v_row = (((int64_t)(there ? id : 0) * a.h_kv + head) * 2 + 1) * kPage + t % kPage;
-        for (int i = 0; i < 32; ++i) {
-            const float pi = __shfl_sync(0xffffffffu, p, i);
-            const int64_t row = __shfl_sync(0xffffffffu, v_row, i);
-            if (pi == 0.0f) continue;
-            const uint16_t* v = a.pool + row * D + lane * kChannels;
-#pragma unroll
-            for (int c = 0; c < kChannels; ++c) acc[c] += pi * __uint_as_float((uint32_t)v[c] << 16);
-        }
-    }
-    store_row<D, kChannels>(place, lane * kChannels, acc, inv);
+// 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void store32(void* p, const uint32_t* u) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
 }
 
 // Loader: work items to the other roles, K and V pages to the ring.
 template <int D>
-__device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, const CUtensorMap* map, uint32_t kv,
-                                          const Bars& bars, const Guard& guard, volatile int* masks, Item* slots, int lane) {
+__device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, const CUtensorMap* map, const Layout<D> sm, int lane) {
     using L = Layout<D>;
     constexpr int kBoxes = kTilePages * L::kHalves;          // TMA boxes of a K or V tile: 16 tokens x 64 channels
     const int g_log2 = 31 - __clz(a.g);
@@ -467,21 +401,23 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
         const bool stop = item >= n_items;
         Item it{};
         it.rows = -1;
-        if (!stop) it = read_item(w.items + item);
-        ok = guard.wait(bars.item_empty(i & 1), ((i >> 1) & 1) ^ 1, i);
+        if (!stop) it = w.items[item];
+        ok = sm.wait(sm.item_empty(i), sm.item_phase(i) ^ 1, a.dbg, i);
         if (!ok) break;
         if (lane == 0) {
-            slots[i & 1] = it;
-            mbar_arrive(bars.item_full(i & 1));
+            const int4* from = reinterpret_cast<const int4*>(&it);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                sts128(sm.item(i) + 16 * c, make_uint4(from[c].x, from[c].y, from[c].z, from[c].w));
+            mbar_arrive(sm.item_full(i));
         }
         __syncwarp();
         if (stop) break;
         const Blocks bl = blocks_of(it, g_log2);
         const int count = max(bl.count[0], bl.count[1]);
-        const int pages = (it.total + kPage - 1) / kPage;
         const int32_t* table = a.tables + (int64_t)it.b * a.stride;
         // page ids of four tiles a load, asked for four tiles ahead; -1 where there is no page to read
-        const int last_page = min(pages, (it.kv0 + count) * kTilePages);
+        const int last_page = min((it.total + kPage - 1) / kPage, (it.kv0 + count) * kTilePages);
         auto look_up = [&](int j) {
             const int page = (it.kv0 + j) * kTilePages + lane;
             return page < last_page ? table[page] : -1;
@@ -501,18 +437,17 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
             const int page = box / L::kHalves, half = box % L::kHalves;
             const int id = __shfl_sync(0xffffffffu, ids, j % 4 * kTilePages + page);
             const int z = id >= 0 ? (id * a.h_kv + it.head) * 2 : blocks;
-            if (lane == 0) masks[tile % kMaskRing] = (there >> (j % 4 * kTilePages)) & 0xff;
+            if (lane == 0) sts32(sm.mask(tile), (there >> (j % 4 * kTilePages)) & 0xff);
             __syncwarp();
 #pragma unroll
             for (int kind = 0; kind < 2; ++kind) {           // K, then V
-                const int s = slot % L::kStages;
-                ok = guard.wait(bars.kv_empty(s), ((slot / L::kStages) & 1) ^ 1, 1000 + i);
+                ok = sm.wait(sm.kv_empty(slot), sm.kv_phase(slot) ^ 1, a.dbg, 1000 + i);
                 if (!ok) break;
-                if (lane == 0) mbar_expect_tx(bars.kv_full(s), L::kTileBytes);
+                if (lane == 0) mbar_expect_tx(sm.kv_full(slot), L::kTileBytes);
                 __syncwarp();
                 if (lane < kBoxes)
-                    tma_load_3d(kv + s * L::kTileBytes + half * L::kHalfBytes + page * (kPage * 128), map, 64 * half, 0,
-                                id >= 0 ? z + kind : blocks, bars.kv_full(s));
+                    tma_load_3d(sm.kv(slot) + half * L::kHalfBytes + page * (kPage * 128), map, 64 * half, 0,
+                                id >= 0 ? z + kind : blocks, sm.kv_full(slot));
                 ++slot;
             }
             ++tile;
@@ -520,67 +455,63 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
         item = __shfl_sync(0xffffffffu, next, 0);
     }
     // what was asked for lands before the CTA may leave
-    for (int s = max(slot - L::kStages, 0); s < slot; ++s) guard.drain(bars.kv_full(s % L::kStages), (s / L::kStages) & 1);
+    for (int s = max(slot - L::kStages, 0); s < slot; ++s) sm.drain(sm.kv_full(s), sm.kv_phase(s));
 }
 
 // Issuer of the matrix products.
 template <int D>
-__device__ __forceinline__ void issue_role(const ChunkArgs& a, uint8_t* smem_kv, uint32_t q, uint32_t kv, uint32_t tmem,
-                                           const Bars& bars, const Guard& guard, const Item* slots, int lane) {
+__device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> sm, uint32_t tmem, int lane) {
     using L = Layout<D>;
     constexpr uint32_t kScores = idesc_bf16(kBlock, kChunkTile, false), kValues = idesc_bf16(kBlock, D, true);
     const int g_log2 = 31 - __clz(a.g);
     int slot = 0;
     uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
     bool ok = true, issued = false;
-    auto scores = [&](int t, uint32_t k_tile) {              // S of block t, from lane 0
-        const uint32_t qd = sw128_desc(q + t * L::kTileBytes, 0), kd = sw128_desc(k_tile, 0);
+    auto scores = [&](int t, int k_slot) {                   // S of block t, from lane 0
+        const uint32_t qd = sw128_desc(sm.q(t), 0), kd = sw128_desc(sm.kv(k_slot), 0);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = ((ks / 4) * L::kHalfBytes + (ks % 4) * 32) >> 4;
             umma_ss(tmem + t * kChunkTile, qd + off, kd + off, kScores, ks > 0);
         }
-        umma_commit(bars.s_full(t));
+        umma_commit(sm.s_full(t));
     };
     for (int i = 0; ok; ++i) {
-        ok = guard.wait(bars.item_full(i & 1), (i >> 1) & 1, 2000 + i);
+        ok = sm.wait(sm.item_full(i), sm.item_phase(i), a.dbg, 2000 + i);
         if (!ok) break;
-        const Item it = read_item(slots + (i & 1));
+        const Item it = sm.read_item(i);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars.item_empty(i & 1));
+        if (lane == 0) mbar_arrive(sm.item_empty(i));
         if (it.rows < 0) break;
         const Blocks bl = blocks_of(it, g_log2);
         const int count = max(bl.count[0], bl.count[1]);
         if (count == 0) continue;
         // S of the first tile
-        int ks = slot++;
-        ok = guard.wait(bars.kv_full(ks % L::kStages), (ks / L::kStages) & 1, 3000 + i);
+        const int k0 = slot++;
+        ok = sm.wait(sm.kv_full(k0), sm.kv_phase(k0), a.dbg, 3000 + i);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             if (!ok || bl.count[t] == 0) continue;
-            ok = guard.wait(bars.q_full(t), q_phase[t], 4000 + i);
+            ok = sm.wait(sm.q_full(t), q_phase[t], a.dbg, 4000 + i);
             q_phase[t] ^= 1;
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) scores(t, kv + (ks % L::kStages) * L::kTileBytes);
+            if (lane == 0) scores(t, k0);
             issued = true;
         }
         if (!ok) break;
-        if (lane == 0) umma_commit(bars.kv_empty(ks % L::kStages));
+        if (lane == 0) umma_commit(sm.kv_empty(k0));
         for (int j = 0; j < count && ok; ++j) {
             const int vs = slot++;
-            const uint32_t v_tile = kv + (vs % L::kStages) * L::kTileBytes;
-            ok = guard.wait(bars.kv_full(vs % L::kStages), (vs / L::kStages) & 1, 5000 + i);
+            ok = sm.wait(sm.kv_full(vs), sm.kv_phase(vs), a.dbg, 5000 + i);
             if (!ok) break;
             const int tail = it.total % kPage;
             if (tail && it.kv0 + j == it.total / kChunkTile) {
                 // rows of the last page behind the sequence may hold anything: zeros for the product
-                const int first = it.total % kChunkTile, left = kPage - tail;
-                uint8_t* tile = smem_kv + (vs % L::kStages) * L::kTileBytes;
-                for (int c = lane; c < left * 8 * L::kHalves; c += 32) {
-                    const int half = c / (left * 8), rest = c % (left * 8);
-                    *reinterpret_cast<uint4*>(tile + half * L::kHalfBytes + first * 128 + rest * 16) = make_uint4(0, 0, 0, 0);
-                }
+                const int left = kPage - tail;
+                const uint32_t to = sm.kv(vs) + it.total % kChunkTile * 128;
+                for (int c = lane; c < left * 8 * L::kHalves; c += 32)
+                    sts128(to + c / (left * 8) * L::kHalfBytes + c % (left * 8) * 16, make_uint4(0, 0, 0, 0));
                 fence_async();
                 __syncwarp();
             }
@@ -590,180 +521,235 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, uint8_t* smem_kv,
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (j < bl.count[t]) {
-                    ok = guard.wait(bars.p_full(t), p_phase[t], 7000 + i);
+                    ok = sm.wait(sm.p_full(t), p_phase[t], a.dbg, 7000 + i);
                     p_phase[t] ^= 1;
                     if (!ok) break;
                     tc_fence_after();
                     if (lane == 0) {
-                        const uint32_t vd = sw128_desc(v_tile, L::kHalfBytes);
+                        const uint32_t vd = sw128_desc(sm.kv(vs), L::kHalfBytes), o = tmem + 2 * kChunkTile + t * D;
+                        const uint32_t p = tmem + t * kChunkTile;
 #pragma unroll
-                        for (int k16 = 0; k16 < kChunkTile / 16; ++k16)
-                            umma_ts(tmem + 2 * kChunkTile + t * D, tmem + t * kChunkTile + k16 * 8, vd + k16 * (2048 >> 4),
-                                    kValues, j > 0 || k16 > 0);
-                        umma_commit(bars.o_done(t));
+                        for (int k16 = 0; k16 < kTilePages; ++k16)
+                            umma_ts(o, p + k16 * 8, vd + k16 * (2048 >> 4), kValues, j > 0 || k16 > 0);
+                        umma_commit(sm.o_done(t));
                     }
                 }
-                if (t == 1 && lane == 0) umma_commit(bars.kv_empty(vs % L::kStages));
+                if (t == 1 && lane == 0) umma_commit(sm.kv_empty(vs));
                 if (j + 1 < bl.count[t]) {
-                    if (!here) ok = guard.wait(bars.kv_full(kn % L::kStages), (kn / L::kStages) & 1, 6000 + i);
+                    if (!here) ok = sm.wait(sm.kv_full(kn), sm.kv_phase(kn), a.dbg, 6000 + i);
                     here = true;
                     if (!ok) break;
                     tc_fence_after();
-                    if (lane == 0) scores(t, kv + (kn % L::kStages) * L::kTileBytes);
+                    if (lane == 0) scores(t, kn);
                 }
             }
-            if (ok && more && lane == 0) umma_commit(bars.kv_empty(kn % L::kStages));
+            if (ok && more && lane == 0) umma_commit(sm.kv_empty(kn));
         }
     }
     // the last matrix products are done before tensor memory is freed
     if (issued) {
-        if (lane == 0) umma_commit(bars.last());
+        if (lane == 0) umma_commit(sm.last());
         __syncwarp();
-        guard.drain(bars.last(), 0);
+        sm.drain(sm.last(), 0);
     }
+}
+
+// A block's queries, 16 bytes at a time, into the swizzled layout; zeros behind the last row.
+template <int D>
+__device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item& it, const Layout<D> sm, int t, int rows,
+                                             int thread, int g_log2) {
+    using L = Layout<D>;
+    const int c = thread % (D / 8);
+    const uint16_t* from = a.q + (int64_t)it.tok0 * a.q_stride + (it.head << g_log2) * D + c * 8;
+    const int r0 = it.r0 + kBlock * t;
+#pragma unroll 8
+    for (int row = thread / (D / 8); row < kBlock; row += kBlock * 8 / D) {
+        const int r = r0 + row;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row < rows) x = *reinterpret_cast<const uint4*>(from + (int64_t)(r >> g_log2) * a.q_stride + (r & (a.g - 1)) * D);
+        sts128(sm.q(t) + c / 8 * L::kHalfBytes + row * 128 + (((c % 8) ^ (row % 8)) * 16), x);
+    }
+    fence_async();
+}
+
+// Logits of 32 tokens that the row does not see count as -infinity: from `seen` on, and those of absent pages.
+__device__ __forceinline__ void hide(uint32_t (&u)[32], int seen, int mask) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+        if (c >= seen || !(mask >> (c / kPage) & 1)) u[c] = 0xff800000u;
+}
+
+// The largest of 32 logits and `top`.
+__device__ __forceinline__ float max32(const uint32_t (&u)[32], float top) {
+    float m[4] = {top, __uint_as_float(u[0]), __uint_as_float(u[1]), __uint_as_float(u[2])};
+#pragma unroll
+    for (int c = 3; c < 31; c += 2) m[c / 2 % 4] = fmax3(m[c / 2 % 4], __uint_as_float(u[c]), __uint_as_float(u[c + 1]));
+    m[0] = fmax3(m[0], m[1], __uint_as_float(u[31]));
+    return fmax3(m[0], m[2], m[3]);
+}
+
+// Weights 2^(scale u - m) of a row's 128 tokens, in bf16 to pk, and the sum of the unrounded ones. In stages of 32 that
+// overlap by hand (a warp issues in order, and ex2 has its result long after its issue): all in the logits' registers.
+// 128 ex2 of 4 cycles each bound it, 512 cycles a warp.
+__device__ __forceinline__ float weigh128(uint32_t (&u)[4][32], uint64_t scale, uint64_t less, uint32_t (&pk)[2][32]) {
+    uint64_t sum[2] = {0, 0};
+    auto scaled = [&](int c) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            float x, y;
+            split_f32x2(fma_f32x2(f32x2(__uint_as_float(u[c][k]), __uint_as_float(u[c][k + 1])), scale, less), x, y);
+            u[c][k] = __float_as_uint(x);
+            u[c][k + 1] = __float_as_uint(y);
+        }
+    };
+    auto power = [&](int c, int k) { u[c][k] = __float_as_uint(exp2_approx(__uint_as_float(u[c][k]))); };
+    auto packed = [&](int c, int k) {
+        const float x = __uint_as_float(u[c][k]), y = __uint_as_float(u[c][k + 1]);
+        pk[c / 2][c % 2 * 16 + k / 2] = bf16_pair(x, y);
+        sum[k / 2 % 2] = add_f32x2(sum[k / 2 % 2], f32x2(x, y));
+    };
+    scaled(0);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) power(0, k);
+#pragma unroll
+    for (int c = 1; c < 4; ++c) {
+        scaled(c);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            power(c, k);
+            power(c, k + 1);
+            packed(c - 1, k);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) packed(3, k);
+    float x, y;
+    split_f32x2(add_f32x2(sum[0], sum[1]), x, y);
+    return x + y;
 }
 
 // Softmax of block t: one thread a row.
 template <int D>
-__device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, uint8_t* smem_q, uint32_t tmem,
-                                             const Bars& bars, const Guard& guard, const volatile int* masks,
-                                             const Item* slots, int t, int warp, int lane) {
-    using L = Layout<D>;
-    const int g_log2 = 31 - __clz(a.g), in_group = warp * 32 + lane;
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    const uint32_t s_col = tmem + lanes + t * kChunkTile, o_col = tmem + lanes + 2 * kChunkTile + t * D;
-    const uint64_t scale = f32x2(a.scale_log2, a.scale_log2);
-    uint8_t* q_tile = smem_q + t * L::kTileBytes;
+__device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, const Layout<D> sm, uint32_t tmem, int t,
+                                             int warp, int lane) {
+    const int g_log2 = 31 - __clz(a.g), in_block = warp * 32 + lane;
+    const uint32_t s_col = tmem + ((uint32_t)(32 * warp) << 16) + t * kChunkTile;
+    const uint32_t o_col = tmem + ((uint32_t)(32 * warp) << 16) + 2 * kChunkTile + t * D;
     int tile = 0, step = 0;                      // tiles of the CTA, steps of this block, counted through
-    for (int i = 0;; ++i) {
-        if (!guard.wait(bars.item_full(i & 1), (i >> 1) & 1, 8000 + i)) return;
-        const Item it = read_item(slots + (i & 1));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.item_empty(i & 1));
-        if (it.rows < 0) return;
+    // Waits for the next item and puts its queries in place; the block's products with the last ones are done then.
+    auto next_item = [&](int i) {
+        if (!sm.wait(sm.item_full(i), sm.item_phase(i), a.dbg, 8000 + i)) return false;
+        const Item it = sm.read_item(i);
+        if (it.rows < 0) return true;
         const Blocks bl = blocks_of(it, g_log2);
-        const int rows = t ? bl.rows[1] : bl.rows[0], count = t ? bl.count[1] : bl.count[0], tile0 = tile;
-        tile += max(bl.count[0], bl.count[1]);
-        if (rows == 0) continue;
-        const int local = kBlock * t + in_group, r = it.r0 + local;      // row of the item, of the request
-        const bool mine = in_group < rows, working = 32 * warp < rows;
-        if (count > 0) {
-            // the block's queries, 16 bytes at a time, into the swizzled layout; zeros behind the last row
-#pragma unroll
-            for (int c0 = 0; c0 < D / 8; ++c0) {
-                const int at = c0 * kBlock + in_group, row = at / (D / 8), c = at % (D / 8);
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (row < rows) {
-                    const int rr = it.r0 + kBlock * t + row;
-                    x = *reinterpret_cast<const uint4*>(a.q + (int64_t)(it.tok0 + (rr >> g_log2)) * a.q_stride +
-                                                        ((it.head << g_log2) + (rr & (a.g - 1))) * D + c * 8);
-                }
-                *reinterpret_cast<uint4*>(q_tile + c / 8 * L::kHalfBytes + row * 128 + (((c % 8) ^ (row % 8)) * 16)) = x;
-            }
-            fence_async();
-            mbar_arrive(bars.q_full(t));
+        if (t ? bl.count[1] : bl.count[0]) {
+            load_queries<D>(a, it, sm, t, t ? bl.rows[1] : bl.rows[0], in_block, g_log2);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sm.q_full(t));
         }
-        // rows behind the last one see everything: their zeros need no mask
-        const int limit = mine ? limit_of(r, it.pos0, g_log2) : 0x7fffffff;
+        return true;
+    };
+    if (!next_item(0)) return;
+    for (int i = 0;; ++i) {
+        int count, seen;
+        bool working;
+        const int tile0 = tile;
+        {
+            const Item it = sm.read_item(i);
+            if (it.rows < 0) return;
+            const Blocks bl = blocks_of(it, g_log2);
+            const int rows = t ? bl.rows[1] : bl.rows[0];
+            count = t ? bl.count[1] : bl.count[0];
+            tile += max(bl.count[0], bl.count[1]);
+            working = 32 * warp < rows;
+            // rows behind the last one see everything: their zeros need no mask
+            seen = in_block < rows ? limit_of(it.r0 + kBlock * t + in_block, it.pos0, g_log2) - it.kv0 * kChunkTile : 0x7fffffff;
+        }
         float m = kNoReference, sum = 0.0f;
-        for (int j = 0; j < count; ++j, ++step) {
-            if (!guard.wait(bars.s_full(t), step & 1, 9000 + i)) return;
+        for (int j = 0; j < count; ++j, ++step, seen -= kChunkTile) {
+            if (!sm.wait(sm.s_full(t), step & 1, a.dbg, 9000 + i)) return;
             if (!working) {                      // no row of this warp is any: what its lanes hold as weights reaches nothing
-                mbar_arrive(bars.p_full(t));
+                if (lane == 0) mbar_arrive(sm.p_full(t));
                 continue;
             }
             tc_fence_after();
-            uint32_t u[kChunkTile];
-            tmem_read128(s_col, u);
-            const int seen = limit - (it.kv0 + j) * kChunkTile;
-            const int mask = masks[(tile0 + j) % kMaskRing];
-            if (__any_sync(0xffffffffu, seen < kChunkTile || mask != 0xff)) {
+            uint32_t u[4][32];
 #pragma unroll
-                for (int c = 0; c < kChunkTile; ++c)
-                    if (c >= seen || !(mask >> (c / kPage) & 1)) u[c] = 0xff800000u;         // -infinity
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, u[c]);
+            const int mask = lds32(sm.mask(tile0 + j));
+            const bool hidden = __any_sync(0xffffffffu, seen < kChunkTile || mask != 0xff);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_wait(u[c]);
+            if (hidden) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) hide(u[c], seen - 32 * c, mask >> 2 * c);
             }
-            float top[4];
+            float high = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) top[c] = __uint_as_float(u[c]);
-#pragma unroll
-            for (int c = 4; c + 8 <= kChunkTile; c += 8) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    top[k] = fmax3(top[k], __uint_as_float(u[c + 2 * k]), __uint_as_float(u[c + 2 * k + 1]));
-            }
-            top[0] = fmax3(top[0], __uint_as_float(u[124]), __uint_as_float(u[125]));
-            top[1] = fmax3(top[1], __uint_as_float(u[126]), __uint_as_float(u[127]));
-            const float high = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * a.scale_log2;
+            for (int c = 0; c < 4; ++c) high = max32(u[c], high);
+            high *= a.scale_log2;
             const bool rise = high > m + kHeadroom;
             if (__any_sync(0xffffffffu, rise)) {
                 const float to = rise ? high : m, f = exp2_approx(m - to);
                 m = to;
                 sum *= f;
                 if (j > 0) {                     // behind the scores, the block's products before them are done too
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_read32(o_col + c, o);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        tmem_st32(o_col + c, o);
-                    }
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 8) tmem_scale8(o_col + c, f);
                 }
             }
-            const uint64_t less = f32x2(-m, -m);
-            uint64_t part[2] = {0, 0};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    float x, y;
-                    split_f32x2(fma_f32x2(f32x2(__uint_as_float(u[64 * h + 2 * c]), __uint_as_float(u[64 * h + 2 * c + 1])), scale, less), x, y);
-                    pk[c] = bf16_pair(exp2_approx(x), exp2_approx(y));
-                    part[c % 2] = add_f32x2(part[c % 2], f32x2(bf16_lo(pk[c]), bf16_hi(pk[c])));
-                }
-                tmem_st32(s_col + 32 * h, pk);
-            }
-            float x, y;
-            split_f32x2(add_f32x2(part[0], part[1]), x, y);
-            sum += x + y;
+            uint32_t pk[2][32];
+            sum += weigh128(u, f32x2(a.scale_log2, a.scale_log2), f32x2(-m, -m), pk);
+            tmem_st32(s_col, pk[0]);             // over logits that the thread has read
+            tmem_st32(s_col + 32, pk[1]);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(bars.p_full(t));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sm.p_full(t));
         }
-        if (count > 0 && !guard.wait(bars.o_done(t), (step - 1) & 1, 10000 + i)) return;
-        if (!working) continue;
-        tc_fence_after();
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (it.part >= 0 && mine) w.part_ml[it.part + local] = make_float2(m, sum);
-        const Place place = place_of<D>(a, w, it, r, g_log2);
-        bool odd = false;
-        if (count > 0) {                         // first look at the whole row: form_row reads its query, which out may lie over
-#pragma unroll
+        if (!next_item(i + 1)) return;           // its queries travel while this one's products end
+        if (count > 0 && !sm.wait(sm.o_done(t), (step - 1) & 1, a.dbg, 10000 + i)) return;
+        if (working) {
+            tc_fence_after();
+            const Item it = sm.read_item(i);
+            const bool mine = kBlock * t + in_block < it.rows;
+            const int r = it.r0 + kBlock * t + in_block;                 // row of the request
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int64_t row = (int64_t)(it.tok0 + (r >> g_log2)) * (a.h_kv << g_log2) + (it.head << g_log2) + (r & (a.g - 1));
+            const int part = it.part + r - it.r0;
+            if (it.part >= 0 && mine) w.part_ml[part] = make_float2(m, sum);
+            bool odd = false;
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
-                tmem_read32(o_col + c, o);
+                if (count > 0) {
+                    tmem_read32(o_col + c, o);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = 0;
+                }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) odd |= !(fabsf(__uint_as_float(o[k])) <= 3.402823466e38f);
+                if (!mine) continue;
+                if (it.part >= 0) {              // a part of a cut item, as it is
+                    float* to = w.part_acc + (int64_t)part * D + c;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) store32(to + k, o + k);
+                } else {
+                    uint32_t y[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) y[k] = bf16_pair(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+                    uint16_t* to = a.out + row * D + c;
+                    store32(to, y);
+                    store32(to + 16, y + 8);
+                }
             }
+            tc_fence_before();
+            const uint32_t again = __ballot_sync(0xffffffffu, odd && mine);
+            if (lane == 0) w.odd[(int64_t)it.self * 8 + 4 * t + warp] = again;
         }
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            float x[32];
-            if (count > 0) tmem_read32(o_col + c, o);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = count > 0 ? __uint_as_float(o[k]) : 0.0f;
-            if (mine && !odd) store_row<D, 32>(place, c, x, inv);
-        }
-        tc_fence_before();
-        for (uint32_t todo = __ballot_sync(0xffffffffu, odd && mine); todo; todo &= todo - 1) {
-            const int src = __ffs(todo) - 1, row = r - lane + src;
-            form_row<D>(a, a.q + (int64_t)(it.tok0 + (row >> g_log2)) * a.q_stride + ((it.head << g_log2) + (row & (a.g - 1))) * D,
-                        a.tables + (int64_t)it.b * a.stride, it.head, it.kv0 * kChunkTile,
-                        min(limit_of(row, it.pos0, g_log2), it.kv1 * kChunkTile), __shfl_sync(0xffffffffu, m, src),
-                        __shfl_sync(0xffffffffu, inv, src), place_of<D>(a, w, it, row, g_log2), guard.beat);
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.item_empty(i));
     }
 }
 
@@ -772,60 +758,52 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attend_kernel(const __grid_
                                                                    const __grid_constant__ Work w,
                                                                    const __grid_constant__ CUtensorMap map) {
     using L = Layout<D>;
-    extern __shared__ uint8_t raw[];
-    uint8_t* smem = raw + (1024 - smem_u32(raw) % 1024) % 1024;
+    extern __shared__ __align__(1024) uint8_t smem[];        // the tiles' swizzle wants them on 1,024 bytes
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t sb = smem_u32(smem);
-    const Bars bars{sb + L::kOffBar, L::kStages};
-    volatile int* masks = reinterpret_cast<volatile int*>(smem + L::kOffMask);
-    Item* slots = reinterpret_cast<Item*>(smem + L::kOffItem);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
-    const Guard guard{reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4),
-                      reinterpret_cast<volatile int*>(smem + L::kOffMisc + 8), a.dbg};
-
+    const L sm{smem_u32(smem)};
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::kStages; ++s) {
-            mbar_init(bars.kv_full(s), 1);
-            mbar_init(bars.kv_empty(s), 1);
+            mbar_init(sm.kv_full(s), 1);
+            mbar_init(sm.kv_empty(s), 1);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(bars.q_full(t), kBlock);
-            mbar_init(bars.s_full(t), 1);
-            mbar_init(bars.p_full(t), kBlock);
-            mbar_init(bars.o_done(t), 1);
-            mbar_init(bars.item_full(t), 1);
-            mbar_init(bars.item_empty(t), kSoftmaxWarps + 1);
+            mbar_init(sm.q_full(t), kSoftmaxWarps / 2);
+            mbar_init(sm.s_full(t), 1);
+            mbar_init(sm.p_full(t), kSoftmaxWarps / 2);
+            mbar_init(sm.o_done(t), 1);
         }
-        mbar_init(bars.last(), 1);
-        *guard.fail = 0;
-        *guard.beat = 0;
+        for (int i = 0; i < kItemRing; ++i) {
+            mbar_init(sm.item_full(i), 1);
+            mbar_init(sm.item_empty(i), kSoftmaxWarps + 1);
+        }
+        mbar_init(sm.last(), 1);
+        sts32(sm.fail(), 0);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
     }
-    if (warp == 9) {                             // all of tensor memory: S of two blocks, O of two blocks
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(tmem_slot)), "r"(512) : "memory");
+    if (warp == kSoftmaxWarps + 1) {             // all of tensor memory: S of two blocks, O of two blocks
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(sm.tmem()), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = lds32(sm.tmem());
     grid_wait();
     grid_release();
 
     // registers: 384 x 168 at launch; 256 x 200 + 128 x 96 = 63,488 of those 64,512
     if (warp < kSoftmaxWarps) {
         more_registers<200>();
-        softmax_role<D>(a, w, smem, tmem, bars, guard, masks, slots, warp / 4, warp % 4, lane);
+        softmax_role<D>(a, w, sm, tmem, warp / 4, warp % 4, lane);
     } else {
         fewer_registers<96>();
-        if (warp == kSoftmaxWarps) load_role<D>(a, w, &map, sb + L::kOffKv, bars, guard, masks, slots, lane);
-        if (warp == kSoftmaxWarps + 1)
-            issue_role<D>(a, smem + L::kOffKv, sb, sb + L::kOffKv, tmem, bars, guard, slots, lane);
+        if (warp == kSoftmaxWarps) load_role<D>(a, w, &map, sm, lane);
+        if (warp == kSoftmaxWarps + 1) issue_role<D>(a, sm, tmem, lane);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kSoftmaxWarps + 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512) : "memory");
     }
@@ -833,44 +811,129 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attend_kernel(const __grid_
 
 // ---- join ---------------------------------------------------------------------------------------------------
 
-// Adds the parts of cut items, in their order: a piece's CTA takes its share of the rows, a warp a row.
+template <int N>
+__device__ __forceinline__ void store_bf16(uint16_t* to, const float (&x)[N], float f) {
+#pragma unroll
+    for (int c = 0; c < N; c += 2) *reinterpret_cast<uint32_t*>(to + c) = bf16_pair(x[c] * f, x[c + 1] * f);
+}
+
+// Row r of an item's request from the beginning, 32 tokens at a time by the whole warp, with the tokens alone that it
+// sees: for rows that an infinity or NaN has reached, its own or one behind it.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkArgs a, const Work w) {
+__device__ __noinline__ void form_row(const ChunkArgs& a, const Item& it, int r, int lane) {
     constexpr int kChannels = D / 32;
+    const int g_log2 = 31 - __clz(a.g), limit = min(limit_of(r, it.pos0, g_log2), it.total);
+    const int64_t token = it.tok0 + (r >> g_log2);
+    const int q_head = (it.head << g_log2) + (r & (a.g - 1));
+    const uint16_t* q = a.q + token * a.q_stride + q_head * D;
+    const int32_t* table = a.tables + (int64_t)it.b * a.stride;
+    float m = kNoReference, sum = 0.0f, acc[kChannels] = {};
+    for (int t0 = 0; t0 < limit; t0 += 32) {
+        const int t = t0 + lane;
+        const int id = t < limit ? table[t / kPage] : -1;
+        const bool there = id >= 0 && id < a.pages;
+        const int64_t k_row = ((int64_t)(there ? id : 0) * a.h_kv + it.head) * 2 * kPage + t % kPage;
+        float x = -INFINITY;
+        if (there) {
+            float dot = 0.0f;
+            const uint16_t* k = a.pool + k_row * D;
+            for (int c = 0; c < D; c += 8) {
+                const uint4 u = *reinterpret_cast<const uint4*>(q + c), v = *reinterpret_cast<const uint4*>(k + c);
+                dot += bf16_lo(u.x) * bf16_lo(v.x) + bf16_hi(u.x) * bf16_hi(v.x) + bf16_lo(u.y) * bf16_lo(v.y) +
+                       bf16_hi(u.y) * bf16_hi(v.y) + bf16_lo(u.z) * bf16_lo(v.z) + bf16_hi(u.z) * bf16_hi(v.z) +
+                       bf16_lo(u.w) * bf16_lo(v.w) + bf16_hi(u.w) * bf16_hi(v.w);
+            }
+            x = dot * a.scale_log2;
+        }
+        float top = x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (top > m) {
+            const float f = exp2_approx(m - top);
+            m = top;
+            sum *= f;
+#pragma unroll
+            for (int c = 0; c < kChannels; ++c) acc[c] = f == 0.0f ? 0.0f : acc[c] * f;
+        }
+        const float p = there ? bf16_lo(bf16_pair(exp2_approx(x - m), 0.0f)) : 0.0f;
+        for (int i = 0; i < 32; ++i) {
+            const float pi = __shfl_sync(0xffffffffu, p, i);
+            const int64_t row = __shfl_sync(0xffffffffu, k_row, i) + kPage;
+            if (pi == 0.0f) continue;
+            sum += pi;
+            const uint16_t* v = a.pool + row * D + lane * kChannels;
+#pragma unroll
+            for (int c = 0; c < kChannels; ++c) acc[c] += pi * __uint_as_float((uint32_t)v[c] << 16);
+        }
+    }
+    store_bf16(a.out + (token * (a.h_kv << g_log2) + q_head) * D + lane * kChannels, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
+}
+
+// Adds the parts of cut items, in their order: a piece's CTA takes its share of the rows, a warp a row. Rows that are
+// marked in any of the pieces are formed again.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ ChunkArgs a,
+                                                                  const __grid_constant__ Work w) {
+    constexpr int kChannels = D / 32, kDepth = 8;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g_log2 = 31 - __clz(a.g);
     grid_release();
     grid_wait();
     const int n_items = w.head->items;
     for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-        const Item it = read_item(w.items + item);
-        if (it.part < 0) continue;
+        const Item it = w.items[item];
+        if (it.part < 0) {                       // each warp looks after 32 rows, as one of the softmax did
+            if (32 * warp >= it.rows) continue;
+            for (uint32_t todo = w.odd[(int64_t)item * 8 + warp]; todo; todo &= todo - 1) form_row<D>(a, it, it.r0 + 32 * warp + __ffs(todo) - 1, lane);
+            continue;
+        }
         const int base = it.part - it.piece * it.rows;
         const int end = (int)((long long)it.rows * (it.piece + 1) / it.pieces);
         for (int local = (int)((long long)it.rows * it.piece / it.pieces) + warp; local < end; local += kJoinThreads / 32) {
-            float m = kNoReference;
-            for (int p = lane; p < it.pieces; p += 32) {
-                const float2 ml = w.part_ml[base + p * it.rows + local];
-                if (ml.y != 0.0f) m = fmaxf(m, ml.x);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            float acc[kChannels] = {}, sum = 0.0f;
+            float m = kNoReference, sum = 0.0f, acc[kChannels] = {};
+            bool again = false;
             for (int p0 = 0; p0 < it.pieces; p0 += 32) {
-                float2 ml = make_float2(0.0f, 0.0f);
-                if (p0 + lane < it.pieces) ml = w.part_ml[base + (p0 + lane) * it.rows + local];
+                const int p = p0 + lane;
+                float2 ml = make_float2(kNoReference, 0.0f);
+                if (p < it.pieces) {
+                    ml = w.part_ml[base + p * it.rows + local];
+                    again |= w.odd[(int64_t)(item + (p - it.piece) * a.h_kv) * 8 + local / 32] >> (local % 32) & 1;
+                }
+                float top = ml.y != 0.0f ? fmaxf(m, ml.x) : m;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float back = exp2_approx(m - top);
+                m = top;
+                sum *= back;
+#pragma unroll
+                for (int c = 0; c < kChannels; ++c) acc[c] *= back;
                 const float f = ml.y == 0.0f ? 0.0f : exp2_approx(ml.x - m);
                 const int count = min(32, it.pieces - p0);
-                for (int p = 0; p < count; ++p) {
-                    const float fp = __shfl_sync(0xffffffffu, f, p), lp = __shfl_sync(0xffffffffu, ml.y, p);
-                    if (fp == 0.0f) continue;    // no weight: what the part holds does not count, and may not be there
-                    sum += fp * lp;
-                    const float* from = w.part_acc + (int64_t)(base + (p0 + p) * it.rows + local) * D + lane * kChannels;
+                for (int q0 = 0; q0 < count; q0 += kDepth) {
+                    float x[kDepth][kChannels];
 #pragma unroll
-                    for (int c = 0; c < kChannels; ++c) acc[c] += fp * from[c];
+                    for (int k = 0; k < kDepth; ++k) {
+                        const float* from = w.part_acc + (int64_t)(base + (p0 + min(q0 + k, count - 1)) * it.rows + local) * D + lane * kChannels;
+#pragma unroll
+                        for (int c = 0; c < kChannels; c += 2) *reinterpret_cast<float2*>(&x[k][c]) = *reinterpret_cast<const float2*>(from + c);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kDepth; ++k) {
+                        // no weight: what the part holds does not count
+                        const float fp = __shfl_sync(0xffffffffu, f, q0 + k), lp = __shfl_sync(0xffffffffu, ml.y, q0 + k);
+                        if (q0 + k >= count || fp == 0.0f) continue;
+                        sum += fp * lp;
+#pragma unroll
+                        for (int c = 0; c < kChannels; ++c) acc[c] += fp * x[k][c];
+                    }
                 }
             }
-            store_row<D, kChannels>({nullptr, place_of<D>(a, w, it, it.r0 + local, g_log2).out}, lane * kChannels, acc,
-                                    sum == 0.0f ? 0.0f : 1.0f / sum);
+            const int r = it.r0 + local;
+            if (__any_sync(0xffffffffu, again)) {
+                form_row<D>(a, it, r, lane);
+                continue;
+            }
+            const int64_t row = (int64_t)(it.tok0 + (r >> g_log2)) * (a.h_kv << g_log2) + (it.head << g_log2) + (r & (a.g - 1));
+            store_bf16(a.out + row * D + lane * kChannels, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
         }
     }
 }
@@ -906,17 +969,17 @@ cudaError_t launch(const ChunkArgs& a, const ChunkPlan& plan, void* workspace, i
     using L = Layout<D>;
     CUtensorMap map;
     if (!make_pool_map(&map, a, D)) return cudaErrorInvalidValue;
-    cudaError_t e = smem_opt_in<chunk_attend_kernel<D>>(L::kDynamic);
+    cudaError_t e = smem_opt_in<chunk_attend_kernel<D>>(L::kBytes);
     if (e != cudaSuccess) return e;
     char* base = static_cast<char*>(workspace);
     const Work w{reinterpret_cast<Header*>(base), reinterpret_cast<int*>(base + plan.tiles),
                  reinterpret_cast<int2*>(base + plan.units), reinterpret_cast<Item*>(base + plan.items),
-                 reinterpret_cast<float2*>(base + plan.part_ml), reinterpret_cast<float*>(base + plan.part_acc)};
+                 reinterpret_cast<uint32_t*>(base + plan.odd), reinterpret_cast<float2*>(base + plan.part_ml), reinterpret_cast<float*>(base + plan.part_acc)};
     const int grid = num_sms < plan.item_cap ? num_sms : plan.item_cap;
     e = launch_dependent(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a, w, plan.unit_cap, plan.item_cap,
                          plan.part_cap, num_sms);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(chunk_attend_kernel<D>, dim3(grid), dim3(kThreads), L::kDynamic, st, 1, a, w, map);
+    e = launch_dependent(chunk_attend_kernel<D>, dim3(grid), dim3(kThreads), L::kBytes, st, 1, a, w, map);
     if (e != cudaSuccess) return e;
     const int joins = 4 * num_sms < plan.item_cap ? 4 * num_sms : plan.item_cap;
     return launch_dependent(chunk_join_kernel<D>, dim3(joins), dim3(kJoinThreads), 0, st, 1, a, w);
@@ -943,6 +1006,7 @@ ChunkPlan plan_chunk(const Shape& s, int num_sms, int batch, int n) {
     p.tiles = place(((size_t)batch + 1) * sizeof(int));
     p.units = place((size_t)p.unit_cap * sizeof(int2));
     p.items = place((size_t)p.item_cap * sizeof(Item));
+    p.odd = place((size_t)p.item_cap * 8 * sizeof(uint32_t));
     p.part_ml = place((size_t)p.part_cap * sizeof(float2));
     p.part_acc = place((size_t)p.part_cap * s.d * sizeof(float));
     p.total = at;

@@ -34,7 +34,7 @@ struct ChunkPlan {
     int unit_cap;                            // row blocks of all requests at most
     int item_cap;                            // work items at most
     int part_cap;                            // rows of split items at most
-    size_t tiles, units, items, part_ml, part_acc, total;
+    size_t tiles, units, items, odd, part_ml, part_acc, total;
 };
 struct ChunkArgs {
     const uint16_t* q; int64_t q_stride;     // token stride in elements

@@ -517,8 +517,8 @@ OSCAR_API oscar_status oscar_norm_rope(oscar_ctx_t* ctx, const void* q, int64_t 
  *   n:          rows of q and out, at most 2^24. Rows that no request has are not
  *               read, and left as they were in out. A row whose position is below 0
  *               sees nothing and gives zeros.
- *   out:        DEVICE bf16 [n][H_q][d], 16-byte aligned. It may be q itself where
- *               q_stride is H_q * d; nothing else overlaps it.
+ *   out:        DEVICE bf16 [n][H_q][d], 32-byte aligned; no other buffer overlaps it
+ *               (one that spans q's rows is refused).
  *   workspace:  DEVICE, >= oscar_extend_bf16_workspace_size(ctx, batch, n) bytes,
  *               256-byte aligned; scratch, nothing in it is kept. The size serves
  *               every smaller batch and n too. Calls that overlap on the GPU need a

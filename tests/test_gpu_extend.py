@@ -177,15 +177,16 @@ def test_rows_without_room_and_bad_lengths(cuda):
     assert (c.run(cuda, start=np.zeros(4, int)) == 7).all()
 
 
-def test_output_over_the_queries(cuda):
-    """out may be q itself, also for rows that are formed a second time."""
+def test_infinite_values(cuda):
+    """Infinite values of tokens with weight, in whole and in cut items: their channels are infinite, the others are not."""
     c = Case([(300, 200), (4000, 3)], 8, 2, 128, seed=7)
     c.pool[c.tables[0, 31], :, 1, 3, 9] = np.inf         # token 499 of 500
-    c.pool[c.tables[1, 250], :, 1, 2, 8] = -np.inf       # token 4,002 of 4,003
-    want = c.run(cuda)
-    q = torch.from_numpy(c.q).to(BF).to(cuda)
-    c.run(cuda, q=q, out=q)
-    assert torch.equal(q, want)
+    c.pool[c.tables[1, 250], :, 1, 2, 100] = -np.inf     # token 4,002 of 4,003
+    got = c.run(cuda).double().cpu().numpy()
+    want, bound = chunk_oracle.extend(c.q, np.where(np.isfinite(c.pool), c.pool, 0.0), c.tables, c.start, c.total, 1 / math.sqrt(128))
+    assert np.isposinf(got[199, :, 9]).all() and np.isneginf(got[202, :, 100]).all()
+    got[199, :, 9], got[202, :, 100] = want[199, :, 9], want[202, :, 100]
+    assert (np.abs(got - want) <= bound).all()
 
 
 def test_large_logits(cuda):
