@@ -39,6 +39,7 @@ constexpr int kThreads = 384;                    // two softmax warp groups, one
 constexpr int kItemRing = 4;                     // items that the loader may be ahead with the others
 constexpr int kMaskRing = 16;                    // tiles whose page masks are kept: more than the loader is ahead
 constexpr int kPlanThreads = 1024;
+constexpr int kSelfUnits = 128;                  // row blocks and requests up to which each loader plans for itself
 constexpr int kJoinThreads = 256;
 constexpr float kNoReference = -3.402823466e38f; // reference before any token: no finite logit is below it
 constexpr float kHeadroom = 8.0f;                // the reference rises when a logit passes it by this much (log2)
@@ -58,6 +59,8 @@ struct Header {
 };
 
 struct Work {
+    int self, sms;                // each CTA's loader plans for itself, for this many
+    int item_cap, part_cap;
     Header* head;
     int* tiles;                   // [batch + 1] first row block of each request
     int2* units;                  // per row block: request, cache tiles
@@ -128,11 +131,49 @@ __device__ __forceinline__ int last_at_most(const int* at, int n, int x) {
     return lo;
 }
 
-// Work items from the lengths, by one CTA. Cutting every row block's tiles into pieces of at most L gives items whose
-// time on `sms` SMs is at most min(waves * (L + s), all / sms + L + s), s the cost of starting an item; each warp
-// tries one L. A cut item costs its share of the join, hence no L below half an SM's share.
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArgs a, const Work w, int unit_cap,
-                                                                  int item_cap, int part_cap, int sms) {
+// Cutting every row block's tiles into pieces of at most L gives items whose time on `sms` SMs is at most
+// min(waves * (L + s), all / sms + L + s), s the cost of starting an item. The i-th L that a plan looks at: an SM's share
+// of all tiles times 2^(1 - i / 15), the last one without a cut. A cut item costs its share of the join, hence no L below
+// half an SM's share.
+constexpr int kStart = 3;                        // tiles' worth of starting an item
+__device__ __forceinline__ int piece_length(int i, int share, int longest) {
+    return i == 31 ? max(longest, 1) : max(1, (int)ceilf((float)share * exp2f(1.0f - (float)i / 15.0f)));
+}
+__device__ __forceinline__ int pieces_of(int tiles, int len) { return max(1, (tiles + len - 1) / len); }
+__device__ __forceinline__ float cost_of(long long pieces, int len, long long all, int sms) {
+    const float one = (float)(len + kStart);
+    return fminf((float)((pieces + sms - 1) / sms) * one, ((float)all + (float)(kStart * pieces)) / (float)sms + one);
+}
+
+// The tiles that row block `block` of a request sees.
+__device__ __forceinline__ int tiles_of(const Request& r, int block, int g, int g_log2) {
+    const int last = min((block + 1) * kChunkRows, r.count * g) - 1;
+    return (limit_of(last, r.pos0, g_log2) + kChunkTile - 1) / kChunkTile;
+}
+
+// Piece rest / H_kv of head rest % H_kv of a row block of `tiles` tiles in p pieces; part: first row of its parts.
+__device__ __forceinline__ Item item_of(const ChunkArgs& a, int b, const Request& r, int block, int tiles, int p, int rest,
+                                        int part, int part_cap, int self) {
+    Item it{};
+    it.b = b;
+    it.head = rest % a.h_kv;
+    it.tok0 = r.tok0;
+    it.r0 = block * kChunkRows;
+    it.rows = min(kChunkRows, r.count * a.g - it.r0);
+    it.pos0 = r.pos0;
+    it.piece = rest / a.h_kv;
+    it.pieces = p;
+    it.kv0 = (int)((long long)tiles * it.piece / p);
+    it.kv1 = (int)((long long)tiles * (it.piece + 1) / p);
+    it.total = r.total;
+    it.part = p > 1 ? min(part + (it.head * p + it.piece) * it.rows, part_cap - it.rows) : -1;
+    it.self = self;
+    return it;
+}
+
+// Work items from the lengths, by one CTA; each warp tries one L.
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArgs a, const Work w, int unit_cap) {
+    const int sms = w.sms, item_cap = w.item_cap, part_cap = w.part_cap;
     __shared__ int shared[32];
     __shared__ long long sum;
     __shared__ int longest;
@@ -140,7 +181,6 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     __shared__ int first_item[kPlanThreads], unit_pieces[kPlanThreads], first_part[kPlanThreads];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int g_log2 = 31 - __clz(a.g);
-    constexpr int kStart = 3;                    // tiles' worth of starting an item
     grid_release();
     if (tid == 0) { sum = 0; longest = 0; }
     grid_wait();
@@ -167,8 +207,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     for (int u = tid; u < units; u += kPlanThreads) {
         const int b = last_at_most(w.tiles, a.batch, u);
         const Request r = request(a, b);
-        const int last = min((w.tiles[b + 1] - u) * kChunkRows, r.count * a.g) - 1;
-        const int tiles = (limit_of(last, r.pos0, g_log2) + kChunkTile - 1) / kChunkTile;
+        const int tiles = tiles_of(r, w.tiles[b + 1] - 1 - u, a.g, g_log2);
         w.units[u] = make_int2(b, tiles);
         my_longest = max(my_longest, tiles);
         my_sum += tiles;
@@ -177,28 +216,21 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     atomicAdd(reinterpret_cast<unsigned long long*>(&sum), (unsigned long long)my_sum);
     __syncthreads();
     const long long all = sum * a.h_kv;
-    // L of this warp: an SM's share times 2^(1 - warp / 15), the last warp without a cut
     const int share = (int)((all + sms - 1) / sms);
-    auto length_of = [&](int i) {
-        return i == 31 ? max(longest, 1) : max(1, (int)ceilf((float)share * exp2f(1.0f - (float)i / 15.0f)));
-    };
     {
-        const int len = min(length_of(warp), max(longest, 1));
+        const int len = min(piece_length(warp, share, longest), max(longest, 1));
         long long pieces = 0;
-        for (int u = lane; u < units; u += 32) pieces += max(1, (w.units[u].y + len - 1) / len);
+        for (int u = lane; u < units; u += 32) pieces += pieces_of(w.units[u].y, len);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
         pieces *= a.h_kv;
-        const float one = (float)(len + kStart);
-        const float waves = (float)((pieces + sms - 1) / sms) * one;
-        const float packed = ((float)all + (float)(kStart * pieces)) / (float)sms + one;
-        if (lane == 0) cost[warp] = fminf(waves, packed);
+        if (lane == 0) cost[warp] = cost_of(pieces, len, all, sms);
     }
     __syncthreads();
     int best = 31;
     for (int i = 30; i >= 0; --i)
         if (cost[i] < cost[best]) best = i;
-    const int len = length_of(best);
+    const int len = piece_length(best, share, longest);
 
     int item_base = 0, part_base = 0;
     for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
@@ -206,7 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         int pieces = 0, rows = 0;
         if (u < units) {
             const int2 unit = w.units[u];
-            pieces = max(1, (unit.y + len - 1) / len);
+            pieces = pieces_of(unit.y, len);
             rows = pieces > 1 ? pieces * a.h_kv * min(kChunkRows, request(a, unit.x).count * a.g - (w.tiles[unit.x + 1] - 1 - u) * kChunkRows) : 0;
         }
         int items, parts;
@@ -219,23 +251,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
             const int at = last_at_most(first_item, min(kPlanThreads, units - u0), i);
             const int2 unit = w.units[u0 + at];
             const Request r = request(a, unit.x);
-            const int p = unit_pieces[at], rest = i - first_item[at];
-            Item it;
-            it.b = unit.x;
-            it.head = rest % a.h_kv;
-            it.tok0 = r.tok0;
-            it.r0 = (w.tiles[unit.x + 1] - 1 - (u0 + at)) * kChunkRows;
-            it.rows = min(kChunkRows, r.count * a.g - it.r0);
-            it.pos0 = r.pos0;
-            it.piece = rest / a.h_kv;
-            it.pieces = p;
-            it.kv0 = (int)((long long)unit.y * it.piece / p);
-            it.kv1 = (int)((long long)unit.y * (it.piece + 1) / p);
-            it.total = r.total;
-            const int part = part_base + first_part[at] + (it.head * p + it.piece) * it.rows;
-            it.part = p > 1 ? min(part, part_cap - it.rows) : -1;
-            it.self = item_base + i;
-            w.items[item_base + i] = it;
+            w.items[item_base + i] = item_of(a, unit.x, r, w.tiles[unit.x + 1] - 1 - (u0 + at), unit.y, unit_pieces[at],
+                                             i - first_item[at], part_base + first_part[at], part_cap, item_base + i);
         }
         item_base += items;
         part_base += parts;
@@ -263,7 +280,8 @@ struct Layout {
     static constexpr int kOffMask = kOffBar + 8 * kBars;
     static constexpr int kOffTmem = kOffMask + 4 * kMaskRing;
     static constexpr int kOffFail = kOffTmem + 4;
-    static constexpr int kBytes = kOffFail + 12;
+    static constexpr int kOffPlan = kOffFail + 12;
+    static constexpr int kBytes = kOffPlan + 16 * kSelfUnits;
     static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
 
     uint32_t base;
@@ -364,11 +382,6 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint64_t sub_f32x2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -385,23 +398,129 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* u) {
                  :: "l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
 }
 
+// A loader's own plan: the row blocks of few requests, in shared memory.
+struct SelfPlan {
+    int2 unit[kSelfUnits];                       // request, tiles
+    int first_item[kSelfUnits], block[kSelfUnits];
+};
+
+// The plan kernel's work by one warp: (units, items), and the L that cuts them.
+template <int D>
+__device__ __forceinline__ int2 plan_here(const ChunkArgs& a, const Layout<D> sm, SelfPlan* plan, int sms, int& len, int lane) {
+    const int g_log2 = 31 - __clz(a.g);
+    int units = 0, longest = 0;
+    long long sum = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const int b = b0 + lane;
+        Request r{};
+        if (b < a.batch) r = request(a, b);
+        const int blocks = (r.count * a.g + kChunkRows - 1) / kChunkRows;
+        int at = blocks;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += y;
+        }
+        const int all = __shfl_sync(0xffffffffu, at, 31);
+        at += units - blocks;
+        for (int k = 0; k < blocks && at + k < kSelfUnits; ++k) {        // the last block, which sees the most, first
+            const int tiles = tiles_of(r, blocks - 1 - k, a.g, g_log2);
+            plan->unit[at + k] = make_int2(b, tiles);
+            plan->block[at + k] = blocks - 1 - k;
+            longest = max(longest, tiles);
+            sum += tiles;
+        }
+        units += all;
+    }
+    units = min(units, kSelfUnits);              // more only where the starts do not ascend
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    __syncwarp();
+    const long long all = sum * a.h_kv;
+    const int share = (int)((all + sms - 1) / sms);
+    len = min(piece_length(lane, share, longest), max(longest, 1));
+    int pieces = 0;
+    for (int u = 0; u < units; ++u) pieces += pieces_of(plan->unit[u].y, len);
+    float best = cost_of((long long)pieces * a.h_kv, len, all, sms);
+    int at = 31 - lane;                          // of equal costs the longest pieces' with the least to join
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, best, o);
+        const int where = __shfl_xor_sync(0xffffffffu, at, o);
+        if (other < best || (other == best && where < at)) {
+            best = other;
+            at = where;
+        }
+    }
+    len = __shfl_sync(0xffffffffu, len, 31 - at);
+    int items = 0;
+    for (int u0 = 0; u0 < units; u0 += 32) {
+        const int u = u0 + lane;
+        const int mine = u < units ? pieces_of(plan->unit[u].y, len) * a.h_kv : 0;
+        int s = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        if (u < units) plan->first_item[u] = items + s - mine;
+        items += __shfl_sync(0xffffffffu, s, 31);
+    }
+    __syncwarp();
+    return make_int2(units, items);
+}
+
+// Item `item` of that plan.
+__device__ __forceinline__ Item item_here(const ChunkArgs& a, const SelfPlan* plan, int units, int len, int item, int part_cap,
+                                          int lane) {
+    const int at = last_at_most(plan->first_item, units, item);
+    const Request r = request(a, plan->unit[at].x);
+    int parts = 0;                               // rows of the cut units before it
+    for (int u = lane; u < at; u += 32) {
+        const int p = pieces_of(plan->unit[u].y, len);
+        if (p > 1) parts += p * a.h_kv * min(kChunkRows, request(a, plan->unit[u].x).count * a.g - plan->block[u] * kChunkRows);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) parts += __shfl_xor_sync(0xffffffffu, parts, o);
+    return item_of(a, plan->unit[at].x, r, plan->block[at], plan->unit[at].y, pieces_of(plan->unit[at].y, len),
+                   item - plan->first_item[at], parts, part_cap, item);
+}
+
 // Loader: work items to the other roles, K and V pages to the ring.
 template <int D>
-__device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, const CUtensorMap* map, const Layout<D> sm, int lane) {
+__device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, const CUtensorMap* map, const Layout<D> sm,
+                                          SelfPlan* plan, int lane) {
     using L = Layout<D>;
     constexpr int kBoxes = kTilePages * L::kHalves;          // TMA boxes of a K or V tile: 16 tokens x 64 channels
     const int g_log2 = 31 - __clz(a.g);
     const int blocks = (int)(a.pages * a.h_kv * 2);          // a block id behind the pool reads as zeros
-    const int n_items = w.head->items;
+    int n_items, units = 0, len = 0;
+    if (w.self) {
+        const int2 found = plan_here(a, sm, plan, w.sms, len, lane);
+        units = found.x;
+        n_items = min(found.y, w.item_cap);
+        if (blockIdx.x == 0 && lane == 0) w.head->items = n_items;
+    } else {
+        n_items = w.head->items;
+    }
     int slot = 0, tile = 0;                                  // ring positions, counted through
     int item = blockIdx.x;
     bool ok = true;
     for (int i = 0; ok; ++i) {
-        const int next = lane == 0 ? atomicAdd(&w.head->next, 1) + (int)gridDim.x : 0;    // asked for ahead of its use
+        // asked for ahead of its use; the few items of an own plan go round in turn
+        const int next = w.self ? item + (int)gridDim.x : lane == 0 ? atomicAdd(&w.head->next, 1) + (int)gridDim.x : 0;
         const bool stop = item >= n_items;
         Item it{};
         it.rows = -1;
-        if (!stop) it = w.items[item];
+        if (!stop && w.self) {
+            it = item_here(a, plan, units, len, item, w.part_cap, lane);
+            if (lane == 0) w.items[item] = it;               // for the join
+        } else if (!stop) {
+            it = w.items[item];
+        }
         ok = sm.wait(sm.item_empty(i), sm.item_phase(i) ^ 1, a.dbg, i);
         if (!ok) break;
         if (lane == 0) {
@@ -798,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attend_kernel(const __grid_
         softmax_role<D>(a, w, sm, tmem, warp / 4, warp % 4, lane);
     } else {
         fewer_registers<96>();
-        if (warp == kSoftmaxWarps) load_role<D>(a, w, &map, sm, lane);
+        if (warp == kSoftmaxWarps) load_role<D>(a, w, &map, sm, reinterpret_cast<SelfPlan*>(smem + L::kOffPlan), lane);
         if (warp == kSoftmaxWarps + 1) issue_role<D>(a, sm, tmem, lane);
     }
     tc_fence_before();
@@ -972,13 +1091,16 @@ cudaError_t launch(const ChunkArgs& a, const ChunkPlan& plan, void* workspace, i
     cudaError_t e = smem_opt_in<chunk_attend_kernel<D>>(L::kBytes);
     if (e != cudaSuccess) return e;
     char* base = static_cast<char*>(workspace);
-    const Work w{reinterpret_cast<Header*>(base), reinterpret_cast<int*>(base + plan.tiles),
+    // Few row blocks: every loader plans by itself, which takes one warp less time than a kernel in front. {}
+    const Work w{plan.unit_cap <= kSelfUnits && a.batch <= kSelfUnits, num_sms, plan.item_cap, plan.part_cap,
+                 reinterpret_cast<Header*>(base), reinterpret_cast<int*>(base + plan.tiles),
                  reinterpret_cast<int2*>(base + plan.units), reinterpret_cast<Item*>(base + plan.items),
                  reinterpret_cast<uint32_t*>(base + plan.odd), reinterpret_cast<float2*>(base + plan.part_ml), reinterpret_cast<float*>(base + plan.part_acc)};
     const int grid = num_sms < plan.item_cap ? num_sms : plan.item_cap;
-    e = launch_dependent(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a, w, plan.unit_cap, plan.item_cap,
-                         plan.part_cap, num_sms);
-    if (e != cudaSuccess) return e;
+    if (!w.self) {
+        e = launch_dependent(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a, w, plan.unit_cap);
+        if (e != cudaSuccess) return e;
+    }
     e = launch_dependent(chunk_attend_kernel<D>, dim3(grid), dim3(kThreads), L::kBytes, st, 1, a, w, map);
     if (e != cudaSuccess) return e;
     const int joins = 4 * num_sms < plan.item_cap ? 4 * num_sms : plan.item_cap;
