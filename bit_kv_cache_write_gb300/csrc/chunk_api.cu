@@ -148,7 +148,7 @@ oscar_status oscar_extend_bf16(oscar_ctx_t* ctx, const void* q, int64_t q_stride
     a.tables = tables; a.stride = table_stride;
     a.row_start = row_start; a.total_len = total_len;
     a.out = static_cast<uint16_t*>(out);
-    a.batch = batch; a.n = n; a.h_kv = s.h_kv; a.g = s.h_q / s.h_kv;
+    a.batch = batch; a.n = n; a.h_kv = s.h_kv; a.g = s.h_q / s.h_kv; a.d = s.d;
     a.scale_log2 = (float)(s.sm_scale * 1.4426950408889634073599);
     a.debug = s.debug; a.dbg = ctx->dbg;
     oscar::ProfScope ps(&ctx->prof, OSCAR_KERNEL_EXTEND, static_cast<cudaStream_t>(stream));

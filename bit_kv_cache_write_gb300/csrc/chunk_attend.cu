@@ -56,6 +56,7 @@ static_assert(sizeof(Item) == 64, "copied as four words of 16 bytes");
 
 struct Header {
     int items, next;              // next: item after the CTAs' first ones
+    int cut;                      // whether any item is
 };
 
 struct Work {
@@ -63,7 +64,7 @@ struct Work {
     int item_cap, part_cap;
     Header* head;
     int* tiles;                   // [batch + 1] first row block of each request
-    int2* units;                  // per row block: request, cache tiles
+    int2* units;                  // per row block: request, cache tiles and rows (unit_word)
     Item* items;
     uint32_t* odd;                // [items][8] rows to form again, a word for each softmax warp
     float2* part_ml;              // per row of a cut item: reference and sum
@@ -132,24 +133,29 @@ __device__ __forceinline__ int last_at_most(const int* at, int n, int x) {
 }
 
 // Cutting every row block's tiles into pieces of at most L gives items whose time on `sms` SMs is at most
-// min(waves * (L + s), all / sms + L + s), s the cost of starting an item. The i-th L that a plan looks at: an SM's share
-// of all tiles times 2^(1 - i / 15), the last one without a cut. A cut item costs its share of the join, hence no L below
-// half an SM's share.
+// min(waves * (L + s), all / sms + L + s), s the cost of starting an item, and parts whose rows are written and read
+// again. The i-th L that a plan looks at: an SM's share of all tiles times 2^(1 - i / 15), the last one without a cut. A
+// cut item costs its share of the join, hence no L below half an SM's share.
 constexpr int kStart = 3;                        // tiles' worth of starting an item
+constexpr float kJoined = 1.0f / 65536;          // tiles' worth of a part's element
 __device__ __forceinline__ int piece_length(int i, int share, int longest) {
     return i == 31 ? max(longest, 1) : max(1, (int)ceilf((float)share * exp2f(1.0f - (float)i / 15.0f)));
 }
 __device__ __forceinline__ int pieces_of(int tiles, int len) { return max(1, (tiles + len - 1) / len); }
-__device__ __forceinline__ float cost_of(long long pieces, int len, long long all, int sms) {
+__device__ __forceinline__ float cost_of(long long pieces, long long parts, int len, long long all, const ChunkArgs& a, int sms) {
     const float one = (float)(len + kStart);
-    return fminf((float)((pieces + sms - 1) / sms) * one, ((float)all + (float)(kStart * pieces)) / (float)sms + one);
+    return fminf((float)((pieces + sms - 1) / sms) * one, ((float)all + (float)(kStart * pieces)) / (float)sms + one) +
+           (float)parts * (float)a.d * kJoined;
 }
 
-// The tiles that row block `block` of a request sees.
-__device__ __forceinline__ int tiles_of(const Request& r, int block, int g, int g_log2) {
-    const int last = min((block + 1) * kChunkRows, r.count * g) - 1;
-    return (limit_of(last, r.pos0, g_log2) + kChunkTile - 1) / kChunkTile;
+// A row block's tiles (at most 2^23: 24 bits) and rows less one (8 bits) in a word.
+__device__ __forceinline__ int unit_word(const Request& r, int block, int g, int g_log2) {
+    const int rows = min(kChunkRows, r.count * g - block * kChunkRows);
+    const int tiles = (limit_of(block * kChunkRows + rows - 1, r.pos0, g_log2) + kChunkTile - 1) / kChunkTile;
+    return (int)((unsigned)(rows - 1) << 24) | tiles;
 }
+__device__ __forceinline__ int tiles_of(int word) { return word & 0xffffff; }
+__device__ __forceinline__ int rows_of(int word) { return (int)((unsigned)word >> 24) + 1; }
 
 // Piece rest / H_kv of head rest % H_kv of a row block of `tiles` tiles in p pieces; part: first row of its parts.
 __device__ __forceinline__ Item item_of(const ChunkArgs& a, int b, const Request& r, int block, int tiles, int p, int rest,
@@ -171,18 +177,24 @@ __device__ __forceinline__ Item item_of(const ChunkArgs& a, int b, const Request
     return it;
 }
 
-// Work items from the lengths, by one CTA; each warp tries one L.
+// Work items from the lengths, by one CTA; each warp tries one L. Requests and row blocks are held in shared memory where
+// they fit, else read again.
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArgs a, const Work w, int unit_cap) {
-    const int sms = w.sms, item_cap = w.item_cap, part_cap = w.part_cap;
     __shared__ int shared[32];
     __shared__ long long sum;
     __shared__ int longest;
     __shared__ float cost[32];
-    __shared__ int first_item[kPlanThreads], unit_pieces[kPlanThreads], first_part[kPlanThreads];
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    __shared__ int first_item[kPlanThreads], first_part[kPlanThreads];
+    __shared__ Request s_request[kPlanThreads];
+    __shared__ int s_tiles[kPlanThreads + 1];
+    __shared__ int2 s_units[kPlanThreads];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, sms = w.sms;
     const int g_log2 = 31 - __clz(a.g);
     grid_release();
     if (tid == 0) { sum = 0; longest = 0; }
+    const bool held = a.batch <= kPlanThreads;
+    int* const first_block = held ? s_tiles : w.tiles;
+    auto request_at = [&](int b) { return held ? s_request[b] : request(a, b); };
     grid_wait();
 
     // row blocks of each request, numbered through; a request's last block, which sees the most, comes first
@@ -193,38 +205,52 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         if (b < a.batch) {
             const Request r = request(a, b);
             blocks = (int)(((long long)r.count * a.g + kChunkRows - 1) / kChunkRows);
+            if (held) s_request[b] = r;
         }
         int total;
         const int at = block_scan(blocks, shared, total);
-        if (b < a.batch) w.tiles[b] = base + at;
+        if (b < a.batch) first_block[b] = base + at;
         base += total;
     }
-    if (tid == 0) w.tiles[a.batch] = base;
+    if (tid == 0) first_block[a.batch] = base;
     const int units = min(base, unit_cap);       // more only where the starts do not ascend
+    int2* const unit = units <= kPlanThreads ? s_units : w.units;
     __syncthreads();
     int my_longest = 0;
     long long my_sum = 0;
     for (int u = tid; u < units; u += kPlanThreads) {
-        const int b = last_at_most(w.tiles, a.batch, u);
-        const Request r = request(a, b);
-        const int tiles = tiles_of(r, w.tiles[b + 1] - 1 - u, a.g, g_log2);
-        w.units[u] = make_int2(b, tiles);
-        my_longest = max(my_longest, tiles);
-        my_sum += tiles;
+        const int b = last_at_most(first_block, a.batch, u);
+        const int word = unit_word(request_at(b), first_block[b + 1] - 1 - u, a.g, g_log2);
+        unit[u] = make_int2(b, word);
+        my_longest = max(my_longest, tiles_of(word));
+        my_sum += tiles_of(word);
     }
-    atomicMax(&longest, my_longest);
-    atomicAdd(reinterpret_cast<unsigned long long*>(&sum), (unsigned long long)my_sum);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        my_longest = max(my_longest, __shfl_xor_sync(0xffffffffu, my_longest, o));
+        my_sum += __shfl_xor_sync(0xffffffffu, my_sum, o);
+    }
+    if (lane == 0) {
+        atomicMax(&longest, my_longest);
+        atomicAdd(reinterpret_cast<unsigned long long*>(&sum), (unsigned long long)my_sum);
+    }
     __syncthreads();
     const long long all = sum * a.h_kv;
     const int share = (int)((all + sms - 1) / sms);
     {
         const int len = min(piece_length(warp, share, longest), max(longest, 1));
-        long long pieces = 0;
-        for (int u = lane; u < units; u += 32) pieces += pieces_of(w.units[u].y, len);
+        long long pieces = 0, parts = 0;
+        for (int u = lane; u < units; u += 32) {
+            const int p = pieces_of(tiles_of(unit[u].y), len);
+            pieces += p;
+            if (p > 1) parts += p * rows_of(unit[u].y);
+        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
-        pieces *= a.h_kv;
-        if (lane == 0) cost[warp] = cost_of(pieces, len, all, sms);
+        for (int o = 16; o > 0; o >>= 1) {
+            pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
+            parts += __shfl_xor_sync(0xffffffffu, parts, o);
+        }
+        if (lane == 0) cost[warp] = cost_of(pieces * a.h_kv, parts * a.h_kv, len, all, a, sms);
     }
     __syncthreads();
     int best = 31;
@@ -237,31 +263,27 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         const int u = u0 + tid;
         int pieces = 0, rows = 0;
         if (u < units) {
-            const int2 unit = w.units[u];
-            pieces = pieces_of(unit.y, len);
-            rows = pieces > 1 ? pieces * a.h_kv * min(kChunkRows, request(a, unit.x).count * a.g - (w.tiles[unit.x + 1] - 1 - u) * kChunkRows) : 0;
+            const int word = unit[u].y;
+            pieces = pieces_of(tiles_of(word), len);
+            rows = pieces > 1 ? pieces * a.h_kv * rows_of(word) : 0;
         }
         int items, parts;
         first_item[tid] = block_scan(pieces * a.h_kv, shared, items);
         first_part[tid] = block_scan(rows, shared, parts);
-        unit_pieces[tid] = pieces;
         __syncthreads();
-        items = min(items, item_cap - item_base);
+        items = min(items, w.item_cap - item_base);
         for (int i = tid; i < items; i += kPlanThreads) {
             const int at = last_at_most(first_item, min(kPlanThreads, units - u0), i);
-            const int2 unit = w.units[u0 + at];
-            const Request r = request(a, unit.x);
-            w.items[item_base + i] = item_of(a, unit.x, r, w.tiles[unit.x + 1] - 1 - (u0 + at), unit.y, unit_pieces[at],
-                                             i - first_item[at], part_base + first_part[at], part_cap, item_base + i);
+            const int2 here = unit[u0 + at];
+            w.items[item_base + i] = item_of(a, here.x, request_at(here.x), first_block[here.x + 1] - 1 - (u0 + at),
+                                             tiles_of(here.y), pieces_of(tiles_of(here.y), len), i - first_item[at],
+                                             part_base + first_part[at], w.part_cap, item_base + i);
         }
         item_base += items;
         part_base += parts;
         __syncthreads();
     }
-    if (tid == 0) {
-        w.head->items = item_base;
-        w.head->next = 0;
-    }
+    if (tid == 0) *w.head = Header{item_base, 0, part_base > 0};
 }
 
 // ---- attention ----------------------------------------------------------------------------------------------
@@ -400,13 +422,15 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* u) {
 
 // A loader's own plan: the row blocks of few requests, in shared memory.
 struct SelfPlan {
-    int2 unit[kSelfUnits];                       // request, tiles
+    int2 unit[kSelfUnits];                       // request, unit_word
     int first_item[kSelfUnits], block[kSelfUnits];
 };
+struct SelfResult {
+    int units, items, len, cut;
+};
 
-// The plan kernel's work by one warp: (units, items), and the L that cuts them.
-template <int D>
-__device__ __forceinline__ int2 plan_here(const ChunkArgs& a, const Layout<D> sm, SelfPlan* plan, int sms, int& len, int lane) {
+// The plan kernel's work by one warp.
+__device__ __forceinline__ SelfResult plan_here(const ChunkArgs& a, SelfPlan* plan, int sms, int lane) {
     const int g_log2 = 31 - __clz(a.g);
     int units = 0, longest = 0;
     long long sum = 0;
@@ -424,11 +448,11 @@ __device__ __forceinline__ int2 plan_here(const ChunkArgs& a, const Layout<D> sm
         const int all = __shfl_sync(0xffffffffu, at, 31);
         at += units - blocks;
         for (int k = 0; k < blocks && at + k < kSelfUnits; ++k) {        // the last block, which sees the most, first
-            const int tiles = tiles_of(r, blocks - 1 - k, a.g, g_log2);
-            plan->unit[at + k] = make_int2(b, tiles);
+            const int word = unit_word(r, blocks - 1 - k, a.g, g_log2);
+            plan->unit[at + k] = make_int2(b, word);
             plan->block[at + k] = blocks - 1 - k;
-            longest = max(longest, tiles);
-            sum += tiles;
+            longest = max(longest, tiles_of(word));
+            sum += tiles_of(word);
         }
         units += all;
     }
@@ -441,11 +465,15 @@ __device__ __forceinline__ int2 plan_here(const ChunkArgs& a, const Layout<D> sm
     __syncwarp();
     const long long all = sum * a.h_kv;
     const int share = (int)((all + sms - 1) / sms);
-    len = min(piece_length(lane, share, longest), max(longest, 1));
-    int pieces = 0;
-    for (int u = 0; u < units; ++u) pieces += pieces_of(plan->unit[u].y, len);
-    float best = cost_of((long long)pieces * a.h_kv, len, all, sms);
-    int at = 31 - lane;                          // of equal costs the longest pieces' with the least to join
+    int len = min(piece_length(lane, share, longest), max(longest, 1));
+    int pieces = 0, parts = 0;
+    for (int u = 0; u < units; ++u) {
+        const int p = pieces_of(tiles_of(plan->unit[u].y), len);
+        pieces += p;
+        if (p > 1) parts += p * rows_of(plan->unit[u].y);
+    }
+    float best = cost_of((long long)pieces * a.h_kv, (long long)parts * a.h_kv, len, all, a, sms);
+    int at = 31 - lane;                          // of equal costs the one with the longest pieces
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float other = __shfl_xor_sync(0xffffffffu, best, o);
@@ -456,10 +484,11 @@ __device__ __forceinline__ int2 plan_here(const ChunkArgs& a, const Layout<D> sm
         }
     }
     len = __shfl_sync(0xffffffffu, len, 31 - at);
+    parts = __shfl_sync(0xffffffffu, parts, 31 - at);
     int items = 0;
     for (int u0 = 0; u0 < units; u0 += 32) {
         const int u = u0 + lane;
-        const int mine = u < units ? pieces_of(plan->unit[u].y, len) * a.h_kv : 0;
+        const int mine = u < units ? pieces_of(tiles_of(plan->unit[u].y), len) * a.h_kv : 0;
         int s = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -470,22 +499,22 @@ __device__ __forceinline__ int2 plan_here(const ChunkArgs& a, const Layout<D> sm
         items += __shfl_sync(0xffffffffu, s, 31);
     }
     __syncwarp();
-    return make_int2(units, items);
+    return {units, items, len, parts > 0};
 }
 
 // Item `item` of that plan.
-__device__ __forceinline__ Item item_here(const ChunkArgs& a, const SelfPlan* plan, int units, int len, int item, int part_cap,
-                                          int lane) {
-    const int at = last_at_most(plan->first_item, units, item);
-    const Request r = request(a, plan->unit[at].x);
+__device__ __forceinline__ Item item_here(const ChunkArgs& a, const SelfPlan* plan, const SelfResult& found, int item,
+                                          int part_cap, int lane) {
+    const int at = last_at_most(plan->first_item, found.units, item);
     int parts = 0;                               // rows of the cut units before it
     for (int u = lane; u < at; u += 32) {
-        const int p = pieces_of(plan->unit[u].y, len);
-        if (p > 1) parts += p * a.h_kv * min(kChunkRows, request(a, plan->unit[u].x).count * a.g - plan->block[u] * kChunkRows);
+        const int p = pieces_of(tiles_of(plan->unit[u].y), found.len);
+        if (p > 1) parts += p * a.h_kv * rows_of(plan->unit[u].y);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) parts += __shfl_xor_sync(0xffffffffu, parts, o);
-    return item_of(a, plan->unit[at].x, r, plan->block[at], plan->unit[at].y, pieces_of(plan->unit[at].y, len),
+    const int tiles = tiles_of(plan->unit[at].y);
+    return item_of(a, plan->unit[at].x, request(a, plan->unit[at].x), plan->block[at], tiles, pieces_of(tiles, found.len),
                    item - plan->first_item[at], parts, part_cap, item);
 }
 
@@ -497,12 +526,12 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
     constexpr int kBoxes = kTilePages * L::kHalves;          // TMA boxes of a K or V tile: 16 tokens x 64 channels
     const int g_log2 = 31 - __clz(a.g);
     const int blocks = (int)(a.pages * a.h_kv * 2);          // a block id behind the pool reads as zeros
-    int n_items, units = 0, len = 0;
+    SelfResult found{};
+    int n_items;
     if (w.self) {
-        const int2 found = plan_here(a, sm, plan, w.sms, len, lane);
-        units = found.x;
-        n_items = min(found.y, w.item_cap);
-        if (blockIdx.x == 0 && lane == 0) w.head->items = n_items;
+        found = plan_here(a, plan, w.sms, lane);
+        n_items = min(found.items, w.item_cap);
+        if (blockIdx.x == 0 && lane == 0) *w.head = Header{n_items, 0, found.cut};
     } else {
         n_items = w.head->items;
     }
@@ -516,7 +545,7 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
         Item it{};
         it.rows = -1;
         if (!stop && w.self) {
-            it = item_here(a, plan, units, len, item, w.part_cap, lane);
+            it = item_here(a, plan, found, item, w.part_cap, lane);
             if (lane == 0) w.items[item] = it;               // for the join
         } else if (!stop) {
             it = w.items[item];
@@ -828,6 +857,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
         }
         if (!next_item(i + 1)) return;           // its queries travel while this one's products end
         if (count > 0 && !sm.wait(sm.o_done(t), (step - 1) & 1, a.dbg, 10000 + i)) return;
+        uint32_t again = 0;
         if (working) {
             tc_fence_after();
             const Item it = sm.read_item(i);
@@ -864,9 +894,9 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
                 }
             }
             tc_fence_before();
-            const uint32_t again = __ballot_sync(0xffffffffu, odd && mine);
-            if (lane == 0) w.odd[(int64_t)it.self * 8 + 4 * t + warp] = again;
+            again = __ballot_sync(0xffffffffu, odd && mine);
         }
+        if (lane == 0) w.odd[(int64_t)sm.read_item(i).self * 8 + 4 * t + warp] = again;
         __syncwarp();
         if (lane == 0) mbar_arrive(sm.item_empty(i));
     }
@@ -997,17 +1027,30 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g_log2 = 31 - __clz(a.g);
     grid_release();
     grid_wait();
-    const int n_items = w.head->items;
-    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-        const Item it = w.items[item];
-        if (it.part < 0) {                       // each warp looks after 32 rows, as one of the softmax did
-            if (32 * warp >= it.rows) continue;
-            for (uint32_t todo = w.odd[(int64_t)item * 8 + warp]; todo; todo &= todo - 1) form_row<D>(a, it, it.r0 + 32 * warp + __ffs(todo) - 1, lane);
-            continue;
+    const Header head = *w.head;
+    // rows to form again of whole items: a word of 32 rows each, almost always 0
+    for (int64_t word = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; word - lane < (int64_t)head.items * 8; word += (int64_t)gridDim.x * kJoinThreads) {
+        const uint32_t mine = word < (int64_t)head.items * 8 ? w.odd[word] : 0;
+        for (uint32_t who = __ballot_sync(0xffffffffu, mine != 0); who; who &= who - 1) {
+            const int src = __ffs(who) - 1;
+            const int64_t at = word - lane + src;
+            const Item it = w.items[at / 8];
+            if (it.part >= 0) continue;
+            for (uint32_t todo = __shfl_sync(0xffffffffu, mine, src); todo; todo &= todo - 1)
+                form_row<D>(a, it, it.r0 + 32 * (int)(at % 8) + __ffs(todo) - 1, lane);
         }
+    }
+    if (!head.cut) return;
+    // with more CTAs than items, `per` of them share an item's rows
+    const int per = max((int)gridDim.x / max(head.items, 1), 1), sub = (int)blockIdx.x / max(head.items, 1);
+    if (sub >= per) return;
+    for (int item = per > 1 ? (int)blockIdx.x % head.items : (int)blockIdx.x; item < head.items; item += gridDim.x) {
+        const Item it = w.items[item];
+        if (it.part < 0) continue;
         const int base = it.part - it.piece * it.rows;
         const int end = (int)((long long)it.rows * (it.piece + 1) / it.pieces);
-        for (int local = (int)((long long)it.rows * it.piece / it.pieces) + warp; local < end; local += kJoinThreads / 32) {
+        for (int local = (int)((long long)it.rows * it.piece / it.pieces) + sub * (kJoinThreads / 32) + warp; local < end;
+             local += per * (kJoinThreads / 32)) {
             float m = kNoReference, sum = 0.0f, acc[kChannels] = {};
             bool again = false;
             for (int p0 = 0; p0 < it.pieces; p0 += 32) {
@@ -1103,7 +1146,9 @@ cudaError_t launch(const ChunkArgs& a, const ChunkPlan& plan, void* workspace, i
     }
     e = launch_dependent(chunk_attend_kernel<D>, dim3(grid), dim3(kThreads), L::kBytes, st, 1, a, w, map);
     if (e != cudaSuccess) return e;
-    const int joins = 4 * num_sms < plan.item_cap ? 4 * num_sms : plan.item_cap;
+    // rows that may be cut, a warp each; at least a CTA an SM, at most eight
+    const int64_t rows = (int64_t)a.n * a.g * a.h_kv, per = kJoinThreads / 32;
+    const int joins = rows > 8 * per * num_sms ? 8 * num_sms : rows > per * num_sms ? (int)((rows + per - 1) / per) : num_sms;
     return launch_dependent(chunk_join_kernel<D>, dim3(joins), dim3(kJoinThreads), 0, st, 1, a, w);
 }
 

@@ -43,7 +43,7 @@ struct ChunkArgs {
     const int32_t* row_start;                // [batch + 1]
     const int32_t* total_len;                // [batch]
     uint16_t* out;                           // [n][H_q][d]
-    int batch, n, h_kv, g;
+    int batch, n, h_kv, g, d;
     float scale_log2;                        // sm_scale * log2(e)
     int debug; DebugWord* dbg;
 };
