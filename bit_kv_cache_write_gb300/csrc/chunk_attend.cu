@@ -50,7 +50,9 @@ struct alignas(16) Item {
     int b, head, tok0, r0;        // tok0: the request's first row of q
     int rows, pos0, kv0, kv1;     // pos0: position of the request's first new token (below 0 where it has no room)
     int total, part, piece, pieces;   // part: first row of its partial results, or -1
-    int self, pad[3];             // its number
+    // its number, and how far the next piece's is; piece p's parts begin p * step rows behind piece 0's, which lie `lead`
+    // rows further
+    int self, stride, step, lead;
 };
 static_assert(sizeof(Item) == 64, "copied as four words of 16 bytes");
 
@@ -174,6 +176,8 @@ __device__ __forceinline__ Item item_of(const ChunkArgs& a, int b, const Request
     it.total = r.total;
     it.part = p > 1 ? min(part + (it.head * p + it.piece) * it.rows, part_cap - it.rows) : -1;
     it.self = self;
+    it.stride = a.h_kv;
+    it.step = it.rows;
     return it;
 }
 
@@ -427,18 +431,21 @@ struct SelfPlan {
 };
 struct SelfResult {
     int units, items, len, cut;
+    int stream, all;                             // CTAs that share all tiles evenly, or 0
 };
 
 // The plan kernel's work by one warp.
 __device__ __forceinline__ SelfResult plan_here(const ChunkArgs& a, SelfPlan* plan, int sms, int lane) {
     const int g_log2 = 31 - __clz(a.g);
-    int units = 0, longest = 0;
+    int units = 0, longest = 0, most = 0;        // most: rows of a block at most
     long long sum = 0;
+    bool even = true;                            // no two row blocks share tiles, none is without
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
         const int b = b0 + lane;
         Request r{};
         if (b < a.batch) r = request(a, b);
         const int blocks = (r.count * a.g + kChunkRows - 1) / kChunkRows;
+        even = even && blocks <= 1;
         int at = blocks;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -453,6 +460,8 @@ __device__ __forceinline__ SelfResult plan_here(const ChunkArgs& a, SelfPlan* pl
             plan->block[at + k] = blocks - 1 - k;
             longest = max(longest, tiles_of(word));
             sum += tiles_of(word);
+            even = even && tiles_of(word) > 0;
+            most = max(most, rows_of(word));
         }
         units += all;
     }
@@ -460,6 +469,7 @@ __device__ __forceinline__ SelfResult plan_here(const ChunkArgs& a, SelfPlan* pl
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
     __syncwarp();
@@ -485,6 +495,25 @@ __device__ __forceinline__ SelfResult plan_here(const ChunkArgs& a, SelfPlan* pl
     }
     len = __shfl_sync(0xffffffffu, len, 31 - at);
     parts = __shfl_sync(0xffffffffu, parts, 31 - at);
+    // or equal stretches of all tiles in a line, which may begin and end within an item each
+    const int ctas = (int)min((long long)gridDim.x, all);
+    if (__all_sync(0xffffffffu, even) && all > 0 && (all + 1) * sms < 0x7fffffff &&       // products of both in 32 bits
+        (float)(share + 2 * kStart) + 2.0f * (float)(ctas * most) * (float)a.d * kJoined < best) {
+        int pos = 0;
+        for (int u0 = 0; u0 < units; u0 += 32) {
+            const int u = u0 + lane, mine = u < units ? tiles_of(plan->unit[u].y) * a.h_kv : 0;
+            int s = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += y;
+            }
+            if (u < units) plan->first_item[u] = pos + s - mine;     // here: its first tile of all
+            pos += __shfl_sync(0xffffffffu, s, 31);
+        }
+        __syncwarp();
+        return {units, units * a.h_kv + ctas - 1, 0, ctas > 1, ctas, (int)all};
+    }
     int items = 0;
     for (int u0 = 0; u0 < units; u0 += 32) {
         const int u = u0 + lane;
@@ -499,7 +528,7 @@ __device__ __forceinline__ SelfResult plan_here(const ChunkArgs& a, SelfPlan* pl
         items += __shfl_sync(0xffffffffu, s, 31);
     }
     __syncwarp();
-    return {units, items, len, parts > 0};
+    return {units, items, len, parts > 0, 0, 0};
 }
 
 // Item `item` of that plan.
@@ -516,6 +545,34 @@ __device__ __forceinline__ Item item_here(const ChunkArgs& a, const SelfPlan* pl
     const int tiles = tiles_of(plan->unit[at].y);
     return item_of(a, plan->unit[at].x, request(a, plan->unit[at].x), plan->block[at], tiles, pieces_of(tiles, found.len),
                    item - plan->first_item[at], parts, part_cap, item);
+}
+
+// Where row blocks share no tiles, all tiles stand in one line (row block by row block, head by head) and each CTA takes
+// an equal stretch of it. The item at tile `at` of the line, up to the end of its (row block, head) or of the CTA's
+// stretch. Its number is that of its (row block, head) plus the CTA's; a stretch that begins with a (row block, head)
+// leaves a number out, which `gap` is then (else -1).
+__device__ __forceinline__ int stretch(int cta, const SelfResult& found) {
+    return (int)((unsigned)found.all * min(cta, found.stream) / (unsigned)found.stream);
+}
+__device__ __forceinline__ Item item_in_line(const ChunkArgs& a, const SelfPlan* plan, const SelfResult& found, int at, int end,
+                                             int cta, int slot_rows, int& gap) {
+    const int u = last_at_most(plan->first_item, found.units, at);
+    const int tiles = tiles_of(plan->unit[u].y), head = (at - plan->first_item[u]) / tiles;
+    const int begin = plan->first_item[u] + head * tiles, number = u * a.h_kv + head;
+    auto cta_of = [&](int x) { return (int)(((unsigned)(x + 1) * found.stream - 1) / (unsigned)found.all); };
+    const int c0 = cta_of(begin), pieces = cta_of(begin + tiles - 1) - c0 + 1;
+    Item it = item_of(a, plan->unit[u].x, request(a, plan->unit[u].x), plan->block[u], tiles, 1, head, 0, 0, number + cta);
+    it.kv0 = at - begin;
+    it.kv1 = min(tiles, end - begin);
+    it.piece = cta - c0;
+    it.pieces = pieces;
+    // a CTA has at most two pieces of cut items: the rest of one, and the beginning of one
+    it.stride = 1;
+    it.step = 2 * slot_rows;
+    it.lead = slot_rows;
+    it.part = pieces > 1 ? 2 * slot_rows * cta + (it.piece == 0 ? slot_rows : 0) : -1;
+    gap = it.piece == 0 && cta > 0 && at == stretch(cta, found) ? number + cta - 1 : -1;
+    return it;
 }
 
 // Loader: work items to the other roles, K and V pages to the ring.
@@ -536,15 +593,30 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
         n_items = w.head->items;
     }
     int slot = 0, tile = 0;                                  // ring positions, counted through
-    int item = blockIdx.x;
+    int item = blockIdx.x, line = 0, line_end = 0;
+    if (found.stream) {
+        line = stretch(item, found);
+        line_end = stretch(item + 1, found);
+    }
     bool ok = true;
     for (int i = 0; ok; ++i) {
         // asked for ahead of its use; the few items of an own plan go round in turn
         const int next = w.self ? item + (int)gridDim.x : lane == 0 ? atomicAdd(&w.head->next, 1) + (int)gridDim.x : 0;
-        const bool stop = item >= n_items;
+        const bool stop = found.stream ? line >= line_end : item >= n_items;
         Item it{};
         it.rows = -1;
-        if (!stop && w.self) {
+        if (!stop && found.stream) {
+            int gap;
+            it = item_in_line(a, plan, found, line, line_end, blockIdx.x, w.part_cap / (4 * w.sms), gap);
+            if (lane == 0) w.items[it.self] = it;            // for the join
+            if (gap >= 0) {
+                Item none{};
+                none.part = -1;
+                if (lane == 0) w.items[gap] = none;
+                if (lane < 8) w.odd[(int64_t)gap * 8 + lane] = 0;
+            }
+            line += it.kv1 - it.kv0;
+        } else if (!stop && w.self) {
             it = item_here(a, plan, found, item, w.part_cap, lane);
             if (lane == 0) w.items[item] = it;               // for the join
         } else if (!stop) {
@@ -941,12 +1013,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attend_kernel(const __grid_
     grid_wait();
     grid_release();
 
-    // registers: 384 x 168 at launch; 256 x 200 + 128 x 96 = 63,488 of those 64,512
+    // registers: 384 x 168 at launch; 256 x 192 + 128 x 112 = 63,488 of those 64,512
     if (warp < kSoftmaxWarps) {
-        more_registers<200>();
+        more_registers<192>();
         softmax_role<D>(a, w, sm, tmem, warp / 4, warp % 4, lane);
     } else {
-        fewer_registers<96>();
+        fewer_registers<112>();
         if (warp == kSoftmaxWarps) load_role<D>(a, w, &map, sm, reinterpret_cast<SelfPlan*>(smem + L::kOffPlan), lane);
         if (warp == kSoftmaxWarps + 1) issue_role<D>(a, sm, tmem, lane);
     }
@@ -1047,7 +1119,8 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
     for (int item = per > 1 ? (int)blockIdx.x % head.items : (int)blockIdx.x; item < head.items; item += gridDim.x) {
         const Item it = w.items[item];
         if (it.part < 0) continue;
-        const int base = it.part - it.piece * it.rows;
+        const int base = it.part - it.piece * it.step - (it.piece ? 0 : it.lead);
+        auto part_of = [&](int p, int local) { return base + p * it.step + (p ? 0 : it.lead) + local; };
         const int end = (int)((long long)it.rows * (it.piece + 1) / it.pieces);
         for (int local = (int)((long long)it.rows * it.piece / it.pieces) + sub * (kJoinThreads / 32) + warp; local < end;
              local += per * (kJoinThreads / 32)) {
@@ -1057,8 +1130,8 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
                 const int p = p0 + lane;
                 float2 ml = make_float2(kNoReference, 0.0f);
                 if (p < it.pieces) {
-                    ml = w.part_ml[base + p * it.rows + local];
-                    again |= w.odd[(int64_t)(item + (p - it.piece) * a.h_kv) * 8 + local / 32] >> (local % 32) & 1;
+                    ml = w.part_ml[part_of(p, local)];
+                    again |= w.odd[(int64_t)(item + (p - it.piece) * it.stride) * 8 + local / 32] >> (local % 32) & 1;
                 }
                 float top = ml.y != 0.0f ? fmaxf(m, ml.x) : m;
 #pragma unroll
@@ -1074,7 +1147,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
                     float x[kDepth][kChannels];
 #pragma unroll
                     for (int k = 0; k < kDepth; ++k) {
-                        const float* from = w.part_acc + (int64_t)(base + (p0 + min(q0 + k, count - 1)) * it.rows + local) * D + lane * kChannels;
+                        const float* from = w.part_acc + (int64_t)part_of(p0 + min(q0 + k, count - 1), local) * D + lane * kChannels;
 #pragma unroll
                         for (int c = 0; c < kChannels; c += 2) *reinterpret_cast<float2*>(&x[k][c]) = *reinterpret_cast<const float2*>(from + c);
                     }

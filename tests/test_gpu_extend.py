@@ -292,3 +292,47 @@ def test_prompt_and_tokens_in_one_captured_loop(cuda, h_q, h_kv, d, layout):
             lo = sum(counts[:b])
             want, bound = chunk_oracle.extend(got_q[lo:lo + m], one, np.arange(len(one))[None], [0, m], [k], 1 / math.sqrt(d))
             assert (np.abs(got[lo:lo + m] - want) <= bound).all()
+
+
+@pytest.mark.parametrize("lens,h_q,h_kv,d", [
+    ([(300 * i + 17, 1 + i % 3) for i in range(12)], 8, 2, 128), ([(128 * i, 1) for i in range(1, 40)], 4, 1, 64),
+    ([(1279, 1)] * 19, 8, 8, 64), ([(127, 1), (20000, 2), (255, 1), (9, 3)], 2, 2, 128), ([(128 * 8 - 1, 1)] * 38, 4, 4, 64),
+    ([(3, 1)] * 100, 2, 1, 64), ([(5000, 4), (6000, 0), (128, 128)], 2, 1, 128)])
+def test_tiles_in_a_line(cuda, lens, h_q, h_kv, d):
+    """Requests of one row block each: the tiles of all of them go to the CTAs in equal stretches, which begin and end
+    anywhere, also with an item."""
+    c = Case(lens, h_q, h_kv, d, seed=len(lens), spare=1)
+    c.check(c.run(cuda))
+    c = Case(lens, h_q, h_kv, d, seed=len(lens), integers=True)
+    c.check(c.run(cuda, context(h_q, h_kv, d, sm_scale=math.log(2))), math.log(2), exact=True)
+
+
+def test_infinities_in_a_line(cuda):
+    """Rows that are formed again, in items that stretches cut and in whole ones."""
+    lens = [(40 * i + 5, 2) for i in range(60)]
+    c = Case(lens, 4, 2, 64, seed=9)
+    for b in range(0, 60, 7):
+        t = c.total[b] - 1                                   # seen by the second row alone
+        c.pool[c.tables[b, t // P], :, 1, t % P, 7] = np.inf
+    want, bound = chunk_oracle.extend(c.q, np.where(np.isfinite(c.pool), c.pool, 0.0), c.tables, c.start, c.total, 1 / 8)
+    got = c.run(cuda).double().cpu().numpy()
+    rows = [int(c.start[b + 1]) - 1 for b in range(0, 60, 7)]
+    assert np.isposinf(got[rows, :, 7]).all()
+    got[rows, :, 7] = want[rows, :, 7]
+    assert (np.abs(got - want) <= bound).all()
+
+
+@pytest.mark.parametrize("batch,new_hi,h_q,h_kv,d", [(200, 2, 4, 2, 64), (1100, 3, 2, 1, 64), (150, 40, 8, 2, 128), (3, 9000, 4, 1, 64)])
+def test_many_requests_and_rows(cuda, batch, new_hi, h_q, h_kv, d):
+    """More requests or row blocks than a loader plans for: the plan kernel, its lists in shared memory and outside."""
+    r = np.random.default_rng(batch)
+    lens = [(int(r.integers(0, 90)), int(r.integers(0, new_hi + 1))) for _ in range(batch)]
+    c = Case(lens, h_q, h_kv, d, seed=batch, spare=2)
+    out = c.run(cuda)
+    got = out.double().cpu().numpy()
+    assert (got[-2:] == 7).all()
+    rows = np.unique(np.concatenate([r.integers(0, len(got) - 2, 60), c.start[1:][c.new > 0][:40] - 1]))
+    for row in rows:                                         # single rows of the definition
+        b = int(np.searchsorted(c.start, row, side="right")) - 1
+        one = chunk_oracle.extend(c.q[row:row + 1], c.pool, c.tables[b:b + 1], [0, 1], [c.total[b] - (c.start[b + 1] - 1 - row)], 1 / math.sqrt(d))
+        assert (np.abs(got[row] - one[0][0]) <= one[1][0]).all(), row
