@@ -39,7 +39,7 @@ constexpr int kThreads = 384;                    // two softmax warp groups, one
 constexpr int kItemRing = 4;                     // items that the loader may be ahead with the others
 constexpr int kMaskRing = 16;                    // tiles whose page masks are kept: more than the loader is ahead
 constexpr int kPlanThreads = 1024;
-constexpr int kSelfUnits = 128;                  // row blocks and requests up to which each loader plans for itself
+constexpr int kSelfUnits = 80;                   // row blocks and requests up to which each loader plans for itself
 constexpr int kJoinThreads = 256;
 constexpr float kNoReference = -3.402823466e38f; // reference before any token: no finite logit is below it
 constexpr float kHeadroom = 8.0f;                // the reference rises when a logit passes it by this much (log2)
@@ -144,11 +144,13 @@ __device__ __forceinline__ int piece_length(int i, int share, int longest) {
     return i == 31 ? max(longest, 1) : max(1, (int)ceilf((float)share * exp2f(1.0f - (float)i / 15.0f)));
 }
 __device__ __forceinline__ int pieces_of(int tiles, int len) { return max(1, (tiles + len - 1) / len); }
-__device__ __forceinline__ float cost_of(long long pieces, long long parts, int len, long long all, const ChunkArgs& a, int sms) {
+__device__ __forceinline__ float cost_of(int pieces, int parts, int len, float all, const ChunkArgs& a, int sms) {
     const float one = (float)(len + kStart);
-    return fminf((float)((pieces + sms - 1) / sms) * one, ((float)all + (float)(kStart * pieces)) / (float)sms + one) +
+    return fminf((float)((pieces + sms - 1) / sms) * one, (all + (float)kStart * (float)pieces) / (float)sms + one) +
            (float)parts * (float)a.d * kJoined;
 }
+// An SM's share of all tiles, a tile more at most.
+__device__ __forceinline__ int share_of(float all, int sms) { return (int)(all / (float)sms) + 1; }
 
 // A row block's tiles (at most 2^23: 24 bits) and rows less one (8 bits) in a word.
 __device__ __forceinline__ int unit_word(const Request& r, int block, int g, int g_log2) {
@@ -159,21 +161,25 @@ __device__ __forceinline__ int unit_word(const Request& r, int block, int g, int
 __device__ __forceinline__ int tiles_of(int word) { return word & 0xffffff; }
 __device__ __forceinline__ int rows_of(int word) { return (int)((unsigned)word >> 24) + 1; }
 
-// Piece rest / H_kv of head rest % H_kv of a row block of `tiles` tiles in p pieces; part: first row of its parts.
-__device__ __forceinline__ Item item_of(const ChunkArgs& a, int b, const Request& r, int block, int tiles, int p, int rest,
-                                        int part, int part_cap, int self) {
+// A row block: `block` of request b.
+struct Unit {
+    int b, block, word, tok0, pos0, total;
+};
+// Piece rest / H_kv of head rest % H_kv of a row block in p pieces; part: first row of its parts.
+__device__ __forceinline__ Item item_of(const ChunkArgs& a, const Unit& u, int p, int rest, int part, int part_cap, int self) {
     Item it{};
-    it.b = b;
+    const int tiles = tiles_of(u.word);
+    it.b = u.b;
     it.head = rest % a.h_kv;
-    it.tok0 = r.tok0;
-    it.r0 = block * kChunkRows;
-    it.rows = min(kChunkRows, r.count * a.g - it.r0);
-    it.pos0 = r.pos0;
+    it.tok0 = u.tok0;
+    it.r0 = u.block * kChunkRows;
+    it.rows = rows_of(u.word);
+    it.pos0 = u.pos0;
     it.piece = rest / a.h_kv;
     it.pieces = p;
     it.kv0 = (int)((long long)tiles * it.piece / p);
     it.kv1 = (int)((long long)tiles * (it.piece + 1) / p);
-    it.total = r.total;
+    it.total = u.total;
     it.part = p > 1 ? min(part + (it.head * p + it.piece) * it.rows, part_cap - it.rows) : -1;
     it.self = self;
     it.stride = a.h_kv;
@@ -239,11 +245,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         atomicAdd(reinterpret_cast<unsigned long long*>(&sum), (unsigned long long)my_sum);
     }
     __syncthreads();
-    const long long all = sum * a.h_kv;
-    const int share = (int)((all + sms - 1) / sms);
+    const float all = (float)(sum * a.h_kv);
+    const int share = share_of(all, sms);
     {
         const int len = min(piece_length(warp, share, longest), max(longest, 1));
-        long long pieces = 0, parts = 0;
+        int pieces = 0, parts = 0;
         for (int u = lane; u < units; u += 32) {
             const int p = pieces_of(tiles_of(unit[u].y), len);
             pieces += p;
@@ -279,8 +285,9 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         for (int i = tid; i < items; i += kPlanThreads) {
             const int at = last_at_most(first_item, min(kPlanThreads, units - u0), i);
             const int2 here = unit[u0 + at];
-            w.items[item_base + i] = item_of(a, here.x, request_at(here.x), first_block[here.x + 1] - 1 - (u0 + at),
-                                             tiles_of(here.y), pieces_of(tiles_of(here.y), len), i - first_item[at],
+            const Request r = request_at(here.x);
+            w.items[item_base + i] = item_of(a, Unit{here.x, first_block[here.x + 1] - 1 - (u0 + at), here.y, r.tok0, r.pos0, r.total},
+                                             pieces_of(tiles_of(here.y), len), i - first_item[at],
                                              part_base + first_part[at], w.part_cap, item_base + i);
         }
         item_base += items;
@@ -307,7 +314,7 @@ struct Layout {
     static constexpr int kOffTmem = kOffMask + 4 * kMaskRing;
     static constexpr int kOffFail = kOffTmem + 4;
     static constexpr int kOffPlan = kOffFail + 12;
-    static constexpr int kBytes = kOffPlan + 16 * kSelfUnits;
+    static constexpr int kBytes = kOffPlan + 28 * kSelfUnits + 24;
     static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
 
     uint32_t base;
@@ -424,18 +431,23 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* u) {
                  :: "l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
 }
 
-// A loader's own plan: the row blocks of few requests, in shared memory.
+// A loader's own plan, in shared memory: the row blocks of few requests, and how they are cut.
 struct SelfPlan {
-    int2 unit[kSelfUnits];                       // request, unit_word
-    int first_item[kSelfUnits], block[kSelfUnits];
-};
-struct SelfResult {
+    Unit unit[kSelfUnits];
+    int first_item[kSelfUnits];
     int units, items, len, cut;
-    int stream, all;                             // CTAs that share all tiles evenly, or 0
+    int stream, all;                             // CTAs that share all tiles evenly, or 0; all tiles
 };
+static_assert(sizeof(SelfPlan) == 28 * kSelfUnits + 24, "as much as Layout reserves");
 
 // The plan kernel's work by one warp.
-__device__ __forceinline__ SelfResult plan_here(const ChunkArgs& a, SelfPlan* plan, int sms, int lane) {
+__device__ __forceinline__ void plan_here(const ChunkArgs& a, SelfPlan* plan, int sms, int lane) {
+    auto found = [&](int units, int items, int len, int cut, int stream, int all) {
+        if (lane == 0) {
+            plan->units = units; plan->items = items; plan->len = len; plan->cut = cut; plan->stream = stream; plan->all = all;
+        }
+        __syncwarp();
+    };
     const int g_log2 = 31 - __clz(a.g);
     int units = 0, longest = 0, most = 0;        // most: rows of a block at most
     long long sum = 0;
@@ -456,8 +468,7 @@ __device__ __forceinline__ SelfResult plan_here(const ChunkArgs& a, SelfPlan* pl
         at += units - blocks;
         for (int k = 0; k < blocks && at + k < kSelfUnits; ++k) {        // the last block, which sees the most, first
             const int word = unit_word(r, blocks - 1 - k, a.g, g_log2);
-            plan->unit[at + k] = make_int2(b, word);
-            plan->block[at + k] = blocks - 1 - k;
+            plan->unit[at + k] = Unit{b, blocks - 1 - k, word, r.tok0, r.pos0, r.total};
             longest = max(longest, tiles_of(word));
             sum += tiles_of(word);
             even = even && tiles_of(word) > 0;
@@ -474,15 +485,15 @@ __device__ __forceinline__ SelfResult plan_here(const ChunkArgs& a, SelfPlan* pl
     }
     __syncwarp();
     const long long all = sum * a.h_kv;
-    const int share = (int)((all + sms - 1) / sms);
+    const int share = share_of((float)all, sms);
     int len = min(piece_length(lane, share, longest), max(longest, 1));
     int pieces = 0, parts = 0;
     for (int u = 0; u < units; ++u) {
-        const int p = pieces_of(tiles_of(plan->unit[u].y), len);
+        const int p = pieces_of(tiles_of(plan->unit[u].word), len);
         pieces += p;
-        if (p > 1) parts += p * rows_of(plan->unit[u].y);
+        if (p > 1) parts += p * rows_of(plan->unit[u].word);
     }
-    float best = cost_of((long long)pieces * a.h_kv, (long long)parts * a.h_kv, len, all, a, sms);
+    float best = cost_of(pieces * a.h_kv, parts * a.h_kv, len, (float)all, a, sms);
     int at = 31 - lane;                          // of equal costs the one with the longest pieces
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -501,7 +512,7 @@ __device__ __forceinline__ SelfResult plan_here(const ChunkArgs& a, SelfPlan* pl
         (float)(share + 2 * kStart) + 2.0f * (float)(ctas * most) * (float)a.d * kJoined < best) {
         int pos = 0;
         for (int u0 = 0; u0 < units; u0 += 32) {
-            const int u = u0 + lane, mine = u < units ? tiles_of(plan->unit[u].y) * a.h_kv : 0;
+            const int u = u0 + lane, mine = u < units ? tiles_of(plan->unit[u].word) * a.h_kv : 0;
             int s = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -511,13 +522,12 @@ __device__ __forceinline__ SelfResult plan_here(const ChunkArgs& a, SelfPlan* pl
             if (u < units) plan->first_item[u] = pos + s - mine;     // here: its first tile of all
             pos += __shfl_sync(0xffffffffu, s, 31);
         }
-        __syncwarp();
-        return {units, units * a.h_kv + ctas - 1, 0, ctas > 1, ctas, (int)all};
+        return found(units, units * a.h_kv + ctas - 1, 0, ctas > 1, ctas, (int)all);
     }
     int items = 0;
     for (int u0 = 0; u0 < units; u0 += 32) {
         const int u = u0 + lane;
-        const int mine = u < units ? pieces_of(tiles_of(plan->unit[u].y), len) * a.h_kv : 0;
+        const int mine = u < units ? pieces_of(tiles_of(plan->unit[u].word), len) * a.h_kv : 0;
         int s = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -527,41 +537,38 @@ __device__ __forceinline__ SelfResult plan_here(const ChunkArgs& a, SelfPlan* pl
         if (u < units) plan->first_item[u] = items + s - mine;
         items += __shfl_sync(0xffffffffu, s, 31);
     }
-    __syncwarp();
-    return {units, items, len, parts > 0, 0, 0};
+    found(units, items, len, parts > 0, 0, 0);
 }
 
 // Item `item` of that plan.
-__device__ __forceinline__ Item item_here(const ChunkArgs& a, const SelfPlan* plan, const SelfResult& found, int item,
-                                          int part_cap, int lane) {
-    const int at = last_at_most(plan->first_item, found.units, item);
+__device__ __forceinline__ Item item_here(const ChunkArgs& a, const SelfPlan* plan, int item, int part_cap, int lane) {
+    const int at = last_at_most(plan->first_item, plan->units, item);
     int parts = 0;                               // rows of the cut units before it
     for (int u = lane; u < at; u += 32) {
-        const int p = pieces_of(tiles_of(plan->unit[u].y), found.len);
-        if (p > 1) parts += p * a.h_kv * rows_of(plan->unit[u].y);
+        const int p = pieces_of(tiles_of(plan->unit[u].word), plan->len);
+        if (p > 1) parts += p * a.h_kv * rows_of(plan->unit[u].word);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) parts += __shfl_xor_sync(0xffffffffu, parts, o);
-    const int tiles = tiles_of(plan->unit[at].y);
-    return item_of(a, plan->unit[at].x, request(a, plan->unit[at].x), plan->block[at], tiles, pieces_of(tiles, found.len),
-                   item - plan->first_item[at], parts, part_cap, item);
+    return item_of(a, plan->unit[at], pieces_of(tiles_of(plan->unit[at].word), plan->len), item - plan->first_item[at], parts,
+                   part_cap, item);
 }
 
 // Where row blocks share no tiles, all tiles stand in one line (row block by row block, head by head) and each CTA takes
 // an equal stretch of it. The item at tile `at` of the line, up to the end of its (row block, head) or of the CTA's
 // stretch. Its number is that of its (row block, head) plus the CTA's; a stretch that begins with a (row block, head)
 // leaves a number out, which `gap` is then (else -1).
-__device__ __forceinline__ int stretch(int cta, const SelfResult& found) {
-    return (int)((unsigned)found.all * min(cta, found.stream) / (unsigned)found.stream);
+__device__ __forceinline__ int stretch(int cta, const SelfPlan* plan) {
+    return (int)((unsigned)plan->all * min(cta, plan->stream) / (unsigned)plan->stream);
 }
-__device__ __forceinline__ Item item_in_line(const ChunkArgs& a, const SelfPlan* plan, const SelfResult& found, int at, int end,
-                                             int cta, int slot_rows, int& gap) {
-    const int u = last_at_most(plan->first_item, found.units, at);
-    const int tiles = tiles_of(plan->unit[u].y), head = (at - plan->first_item[u]) / tiles;
+__device__ __forceinline__ Item item_in_line(const ChunkArgs& a, const SelfPlan* plan, int at, int end, int cta,
+                                             int slot_rows, int& gap) {
+    const int u = last_at_most(plan->first_item, plan->units, at);
+    const int tiles = tiles_of(plan->unit[u].word), head = (at - plan->first_item[u]) / tiles;
     const int begin = plan->first_item[u] + head * tiles, number = u * a.h_kv + head;
-    auto cta_of = [&](int x) { return (int)(((unsigned)(x + 1) * found.stream - 1) / (unsigned)found.all); };
+    auto cta_of = [&](int x) { return (int)(((unsigned)(x + 1) * plan->stream - 1) / (unsigned)plan->all); };
     const int c0 = cta_of(begin), pieces = cta_of(begin + tiles - 1) - c0 + 1;
-    Item it = item_of(a, plan->unit[u].x, request(a, plan->unit[u].x), plan->block[u], tiles, 1, head, 0, 0, number + cta);
+    Item it = item_of(a, plan->unit[u], 1, head, 0, 0, number + cta);
     it.kv0 = at - begin;
     it.kv1 = min(tiles, end - begin);
     it.piece = cta - c0;
@@ -571,8 +578,29 @@ __device__ __forceinline__ Item item_in_line(const ChunkArgs& a, const SelfPlan*
     it.step = 2 * slot_rows;
     it.lead = slot_rows;
     it.part = pieces > 1 ? 2 * slot_rows * cta + (it.piece == 0 ? slot_rows : 0) : -1;
-    gap = it.piece == 0 && cta > 0 && at == stretch(cta, found) ? number + cta - 1 : -1;
+    gap = it.piece == 0 && cta > 0 && at == stretch(cta, plan) ? number + cta - 1 : -1;
     return it;
+}
+
+// Item `item` of the loader's own plan (or the one at tile `item` of the line, whose stretch ends at `end`) to the CTA's
+// ring and to the list that the join reads. Out of line: the loader's registers are short.
+__device__ __noinline__ void put_own_item(const ChunkArgs& a, const Work& w, const SelfPlan* plan, uint32_t to, int item, int end) {
+    const int lane = threadIdx.x % 32;
+    int gap = -1;
+    const Item it = plan->stream ? item_in_line(a, plan, item, end, blockIdx.x, w.part_cap / (4 * w.sms), gap)
+                                 : item_here(a, plan, item, w.part_cap, lane);
+    if (lane == 0) {
+        const uint4* from = reinterpret_cast<const uint4*>(&it);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sts128(to + 16 * c, from[c]);
+        w.items[it.self] = it;
+    }
+    if (gap >= 0) {
+        Item none{};
+        none.part = -1;
+        if (lane == 0) w.items[gap] = none;
+        if (lane < 8) w.odd[(int64_t)gap * 8 + lane] = 0;
+    }
 }
 
 // Loader: work items to the other roles, K and V pages to the ring.
@@ -583,56 +611,38 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
     constexpr int kBoxes = kTilePages * L::kHalves;          // TMA boxes of a K or V tile: 16 tokens x 64 channels
     const int g_log2 = 31 - __clz(a.g);
     const int blocks = (int)(a.pages * a.h_kv * 2);          // a block id behind the pool reads as zeros
-    SelfResult found{};
     int n_items;
     if (w.self) {
-        found = plan_here(a, plan, w.sms, lane);
-        n_items = min(found.items, w.item_cap);
-        if (blockIdx.x == 0 && lane == 0) *w.head = Header{n_items, 0, found.cut};
+        plan_here(a, plan, w.sms, lane);
+        n_items = min(plan->items, w.item_cap);
+        if (blockIdx.x == 0 && lane == 0) *w.head = Header{n_items, 0, plan->cut};
     } else {
         n_items = w.head->items;
     }
     int slot = 0, tile = 0;                                  // ring positions, counted through
-    int item = blockIdx.x, line = 0, line_end = 0;
-    if (found.stream) {
-        line = stretch(item, found);
-        line_end = stretch(item + 1, found);
-    }
+    // item: its number, or the tile of the line where it begins
+    const bool in_line = w.self && plan->stream;
+    int item = in_line ? stretch(blockIdx.x, plan) : blockIdx.x;
+    if (in_line) n_items = stretch(blockIdx.x + 1, plan);
     bool ok = true;
     for (int i = 0; ok; ++i) {
         // asked for ahead of its use; the few items of an own plan go round in turn
-        const int next = w.self ? item + (int)gridDim.x : lane == 0 ? atomicAdd(&w.head->next, 1) + (int)gridDim.x : 0;
-        const bool stop = found.stream ? line >= line_end : item >= n_items;
-        Item it{};
-        it.rows = -1;
-        if (!stop && found.stream) {
-            int gap;
-            it = item_in_line(a, plan, found, line, line_end, blockIdx.x, w.part_cap / (4 * w.sms), gap);
-            if (lane == 0) w.items[it.self] = it;            // for the join
-            if (gap >= 0) {
-                Item none{};
-                none.part = -1;
-                if (lane == 0) w.items[gap] = none;
-                if (lane < 8) w.odd[(int64_t)gap * 8 + lane] = 0;
-            }
-            line += it.kv1 - it.kv0;
-        } else if (!stop && w.self) {
-            it = item_here(a, plan, found, item, w.part_cap, lane);
-            if (lane == 0) w.items[item] = it;               // for the join
-        } else if (!stop) {
-            it = w.items[item];
-        }
+        int next = w.self ? item + (int)gridDim.x : lane == 0 ? atomicAdd(&w.head->next, 1) + (int)gridDim.x : 0;
+        const bool stop = item >= n_items;
         ok = sm.wait(sm.item_empty(i), sm.item_phase(i) ^ 1, a.dbg, i);
         if (!ok) break;
-        if (lane == 0) {
-            const int4* from = reinterpret_cast<const int4*>(&it);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                sts128(sm.item(i) + 16 * c, make_uint4(from[c].x, from[c].y, from[c].z, from[c].w));
-            mbar_arrive(sm.item_full(i));
+        if (!stop && w.self) {
+            put_own_item(a, w, plan, sm.item(i), item, n_items);
+        } else if (lane < 4) {                   // 16 bytes a lane; no rows: the end
+            uint4 x = make_uint4(lane == 1 ? 0xffffffffu : 0, 0, 0, 0);
+            if (!stop) x = reinterpret_cast<const uint4*>(w.items + item)[lane];
+            sts128(sm.item(i) + 16 * lane, x);
         }
         __syncwarp();
+        if (lane == 0) mbar_arrive(sm.item_full(i));
         if (stop) break;
+        const Item it = sm.read_item(i);
+        if (in_line) next = item + it.kv1 - it.kv0;
         const Blocks bl = blocks_of(it, g_log2);
         const int count = max(bl.count[0], bl.count[1]);
         const int32_t* table = a.tables + (int64_t)it.b * a.stride;
