@@ -10,14 +10,16 @@
 // HBM bounds it: each channel is read and written once. d / 8 lanes take a head, 8 channels a lane: the four pairs
 // 4 l .. 4 l + 3 (channels 4 l .. and rot / 2 + 4 l .., or 8 l ..), and the lanes behind rot / 8 pass 8 channels on. All
 // heads of a token turn by the same angles, so a lane forms its four sines and cosines once a token and uses them
-// for every head that its warp takes.
+// for every head that its warp takes. Four heads of a lane group in flight and CTAs of four warps: 131,072 tokens x 40
+// heads of 128 in 433 us, 92 % of the measured copy rate (449 us with eight warps a CTA, 660 with eight heads in flight),
+// 5,003 tokens x 72 heads of 64 in 14.8 us, 95 %; single tokens 3 us.
 #include "chunk_internal.h"
 #include "paged_device.cuh"
 
 namespace oscar {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeDepth = 4;                // heads that a lane group has in flight
 
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
@@ -174,7 +176,8 @@ template <int D>
 cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t st) {
     using B = RopeBatch<D, false>;
     const int batches = (a.q.heads + a.k.heads + B::kHeads - 1) / B::kHeads;
-    // A warp takes a batch of heads while that gives no more warps than run at once, else a whole token's heads.
+    // A warp takes a batch of heads while that gives no more warps than run at once (256 tokens x 40 heads: 4.4 us, 9.6
+    // with a token a warp), else a whole token's heads (131,072: 449 us, 658 with a batch a warp).
     const bool spread = (int64_t)a.n * batches <= (int64_t)num_sms * 32;
     const int parts = spread ? batches : 1, span = spread ? 1 : batches;
     const int64_t warps = (int64_t)a.n * parts, per = kRopeThreads / 32;

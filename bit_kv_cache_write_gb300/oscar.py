@@ -485,16 +485,20 @@ def oscar_decode_bf16_sparse(ctx, q, bf16_pool, key_steps, key_bounds, tables, s
         _check(st, "oscar_decode_bf16_sparse")
 
 
-def _pair(x, out, weight, bf16, heads, d, n, device, torch, name):
+def _pair(x, out, weight, fp32, bf16, heads, d, n, device, name):
     """Pointers and strides of rows, their output's rows and their weights; nothing of either for None."""
     if x is None and out is None:
         return None, 0, None, 0, None
     xp, xs = _rows(x, bf16, heads, d, device, name)
-    op, os_ = _rows(out, bf16, heads, d, device, name + "_out")
-    if x.shape[0] != n or out.shape[0] != n:
-        raise ValueError("%s and %s_out must have %d rows, have %d and %d" % (name, name, n, x.shape[0], out.shape[0]))
-    wp = _ptr(weight, torch.float32, d, device, name + "_weight") if weight is not None else None
-    return xp, xs, op, os_, wp
+    if x.shape[0] != n:
+        raise ValueError("%s must have %d rows, has %d" % (name, n, x.shape[0]))
+    if out is not None and out.is_contiguous():
+        op, os_ = _ptr(out, bf16, n * heads * d, device, name + "_out"), heads * d
+    else:
+        op, os_ = _rows(out, bf16, heads, d, device, name + "_out")
+        if out.shape[0] != n:
+            raise ValueError("%s_out must have %d rows, has %d" % (name, n, out.shape[0]))
+    return xp, xs, op, os_, None if weight is None else _ptr(weight, fp32, d, device, name + "_weight")
 
 
 def oscar_norm_rope(ctx, q, k, q_out, k_out, turns, positions=None, row_start=None, total_len=None, q_weight=None,
@@ -504,10 +508,10 @@ def oscar_norm_rope(ctx, q, k, q_out, k_out, turns, positions=None, row_start=No
     of the plan; weights fp32 [d] or None."""
     import torch
     h_q, h_kv, d, dev, _ = _config_of(ctx)
-    bf16, i32 = torch.bfloat16, torch.int32
+    bf16, fp32, i32 = torch.bfloat16, torch.float32, torch.int32
     n = q.shape[0] if q is not None else k.shape[0] if k is not None else 0
-    qp, qs, qop, qos, qw = _pair(q, q_out, q_weight, bf16, h_q, d, n, dev, torch, "q")
-    kp, ks, kop, kos, kw = _pair(k, k_out, k_weight, bf16, h_kv, d, n, dev, torch, "k")
+    qp, qs, qop, qos, qw = _pair(q, q_out, q_weight, fp32, bf16, h_q, d, n, dev, "q")
+    kp, ks, kop, kos, kw = _pair(k, k_out, k_weight, fp32, bf16, h_kv, d, n, dev, "k")
     half = turns.numel() if turns is not None else 0
     pp = _ptr(positions, i32, n, dev, "positions") if positions is not None else None
     batch, rp, tp = 0, None, None
