@@ -43,7 +43,7 @@ constexpr int kSelfUnits = 80;                   // row blocks and requests up t
 constexpr int kJoinThreads = 256;
 constexpr float kNoReference = -3.402823466e38f; // reference before any token: no finite logit is below it
 constexpr float kHeadroom = 8.0f;                // the reference rises when a logit passes it by this much (log2)
-constexpr uint32_t kWaitTicks = 1000000000u;      // nanoseconds of a wait at most
+constexpr uint32_t kWaitTicks = 2000000000u;      // cycles of a wait at most, about a second
 
 // A work item: rows r0 .. r0 + rows of request b's row space against cache tiles [kv0, kv1).
 struct alignas(16) Item {
@@ -63,7 +63,7 @@ struct Header {
 
 struct Work {
     int self, sms;                // each CTA's loader plans for itself, for this many
-    int item_cap, part_cap;
+    int unit_cap, item_cap, part_cap;     // as in ChunkPlan
     Header* head;
     int* tiles;                   // [batch + 1] first row block of each request
     int2* units;                  // per row block: request, cache tiles and rows (unit_word)
@@ -189,7 +189,7 @@ __device__ __forceinline__ Item item_of(const ChunkArgs& a, const Unit& u, int p
 
 // Work items from the lengths, by one CTA; each warp tries one L. Requests and row blocks are held in shared memory where
 // they fit, else read again.
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArgs a, const Work w, int unit_cap) {
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArgs a, const Work w) {
     __shared__ int shared[32];
     __shared__ long long sum;
     __shared__ int longest;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     __shared__ int s_tiles[kPlanThreads + 1];
     __shared__ int2 s_units[kPlanThreads];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, sms = w.sms;
-    const int g_log2 = 31 - __clz(a.g);
+    const int g_log2 = 31 - __clz(a.g), unit_cap = w.unit_cap;
     grid_release();
     if (tid == 0) { sum = 0; longest = 0; }
     const bool held = a.batch <= kPlanThreads;
@@ -219,11 +219,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         }
         int total;
         const int at = block_scan(blocks, shared, total);
-        if (b < a.batch) first_block[b] = base + at;
-        base += total;
+        if (b < a.batch) first_block[b] = min(base + at, unit_cap);
+        base = min(base + total, unit_cap);      // more only where the starts do not ascend
     }
     if (tid == 0) first_block[a.batch] = base;
-    const int units = min(base, unit_cap);       // more only where the starts do not ascend
+    const int units = base;
     int2* const unit = units <= kPlanThreads ? s_units : w.units;
     __syncthreads();
     int my_longest = 0;
@@ -349,10 +349,10 @@ struct Layout {
         return wait_longer(at, phase, dbg, where);
     }
     __device__ __forceinline__ bool wait_longer(uint32_t at, uint32_t phase, DebugWord* dbg, int where) const {
-        const uint32_t t0 = time_ns();
+        const uint32_t t0 = cycles();
         bool ok;
         while (!(ok = mbar_test(at, phase)) && !lds32(fail())) {
-            if (time_ns() - t0 > kWaitTicks) {
+            if (cycles() - t0 > kWaitTicks) {
                 give_up(dbg, where);
                 break;
             }
@@ -361,9 +361,9 @@ struct Layout {
     }
     // For what is in flight when a role stops: nobody is told.
     __device__ void drain(uint32_t at, uint32_t phase) const {
-        const uint32_t t0 = time_ns();
+        const uint32_t t0 = cycles();
         while (!mbar_test(at, phase))
-            if (time_ns() - t0 > kWaitTicks) return;
+            if (cycles() - t0 > kWaitTicks) return;
     }
     __device__ Item read_item(int i) const {
         Item it;
@@ -441,7 +441,7 @@ struct SelfPlan {
 static_assert(sizeof(SelfPlan) == 28 * kSelfUnits + 24, "as much as Layout reserves");
 
 // The plan kernel's work by one warp.
-__device__ __forceinline__ void plan_here(const ChunkArgs& a, SelfPlan* plan, int sms, int lane) {
+__device__ __forceinline__ void plan_here(const ChunkArgs& a, SelfPlan* plan, int unit_cap, int sms, int lane) {
     auto found = [&](int units, int items, int len, int cut, int stream, int all) {
         if (lane == 0) {
             plan->units = units; plan->items = items; plan->len = len; plan->cut = cut; plan->stream = stream; plan->all = all;
@@ -466,7 +466,7 @@ __device__ __forceinline__ void plan_here(const ChunkArgs& a, SelfPlan* plan, in
         }
         const int all = __shfl_sync(0xffffffffu, at, 31);
         at += units - blocks;
-        for (int k = 0; k < blocks && at + k < kSelfUnits; ++k) {        // the last block, which sees the most, first
+        for (int k = 0; k < blocks && at + k < unit_cap; ++k) {          // the last block, which sees the most, first
             const int word = unit_word(r, blocks - 1 - k, a.g, g_log2);
             plan->unit[at + k] = Unit{b, blocks - 1 - k, word, r.tok0, r.pos0, r.total};
             longest = max(longest, tiles_of(word));
@@ -476,7 +476,7 @@ __device__ __forceinline__ void plan_here(const ChunkArgs& a, SelfPlan* plan, in
         }
         units += all;
     }
-    units = min(units, kSelfUnits);              // more only where the starts do not ascend
+    units = min(units, unit_cap);                // more only where the starts do not ascend
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
@@ -613,7 +613,7 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
     const int blocks = (int)(a.pages * a.h_kv * 2);          // a block id behind the pool reads as zeros
     int n_items;
     if (w.self) {
-        plan_here(a, plan, w.sms, lane);
+        plan_here(a, plan, w.unit_cap, w.sms, lane);
         n_items = min(plan->items, w.item_cap);
         if (blockIdx.x == 0 && lane == 0) *w.head = Header{n_items, 0, plan->cut};
     } else {
@@ -1100,6 +1100,22 @@ __device__ __noinline__ void form_row(const ChunkArgs& a, const Item& it, int r,
     store_bf16(a.out + (token * (a.h_kv << g_log2) + q_head) * D + lane * kChannels, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
 }
 
+// Whether an item's indexes lie within the call's buffers: a CTA that gave up leaves entries of the list unwritten.
+__device__ __forceinline__ bool sane(const ChunkArgs& a, const Work& w, const Item& it, int item, int g_log2) {
+    if (it.b < 0 || it.b >= a.batch || it.head < 0 || it.head >= a.h_kv || it.tok0 < 0 || it.tok0 >= a.n || it.r0 < 0 ||
+        it.rows < 1 || it.rows > kChunkRows || it.r0 > (a.n << g_log2) || it.tok0 + ((it.r0 + it.rows - 1) >> g_log2) >= a.n ||
+        it.total < 0 || it.total > a.stride * kPage)
+        return false;
+    if (it.part < 0) return true;
+    if (it.pieces < 2 || it.pieces > w.item_cap || it.piece < 0 || it.piece >= it.pieces || it.step < 1 || it.lead < 0 ||
+        it.step > w.part_cap || it.lead > w.part_cap || it.stride < 1 || it.stride > a.h_kv)
+        return false;
+    const long long base = it.part - (long long)it.piece * it.step - (it.piece ? 0 : it.lead);
+    const long long first = item - (long long)it.piece * it.stride, last = first + (long long)(it.pieces - 1) * it.stride;
+    return base >= 0 && base + (long long)(it.pieces - 1) * it.step + it.rows <= w.part_cap && base + it.lead + it.rows <= w.part_cap &&
+           first >= 0 && last < w.item_cap;
+}
+
 // Adds the parts of cut items, in their order: a piece's CTA takes its share of the rows, a warp a row. Rows that are
 // marked in any of the pieces are formed again.
 template <int D>
@@ -1109,7 +1125,8 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g_log2 = 31 - __clz(a.g);
     grid_release();
     grid_wait();
-    const Header head = *w.head;
+    Header head = *w.head;
+    head.items = clamp_int(head.items, 0, w.item_cap);
     // rows to form again of whole items: a word of 32 rows each, almost always 0
     for (int64_t word = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; word - lane < (int64_t)head.items * 8; word += (int64_t)gridDim.x * kJoinThreads) {
         const uint32_t mine = word < (int64_t)head.items * 8 ? w.odd[word] : 0;
@@ -1117,9 +1134,12 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
             const int src = __ffs(who) - 1;
             const int64_t at = word - lane + src;
             const Item it = w.items[at / 8];
-            if (it.part >= 0) continue;
-            for (uint32_t todo = __shfl_sync(0xffffffffu, mine, src); todo; todo &= todo - 1)
-                form_row<D>(a, it, it.r0 + 32 * (int)(at % 8) + __ffs(todo) - 1, lane);
+            const uint32_t marked = __shfl_sync(0xffffffffu, mine, src);
+            if (it.part >= 0 || !sane(a, w, it, (int)(at / 8), g_log2)) continue;
+            for (uint32_t todo = marked; todo; todo &= todo - 1) {
+                const int local = 32 * (int)(at % 8) + __ffs(todo) - 1;
+                if (local < it.rows) form_row<D>(a, it, it.r0 + local, lane);
+            }
         }
     }
     if (!head.cut) return;
@@ -1128,7 +1148,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
     if (sub >= per) return;
     for (int item = per > 1 ? (int)blockIdx.x % head.items : (int)blockIdx.x; item < head.items; item += gridDim.x) {
         const Item it = w.items[item];
-        if (it.part < 0) continue;
+        if (it.part < 0 || !sane(a, w, it, item, g_log2)) continue;
         const int base = it.part - it.piece * it.step - (it.piece ? 0 : it.lead);
         auto part_of = [&](int p, int local) { return base + p * it.step + (p ? 0 : it.lead) + local; };
         const int end = (int)((long long)it.rows * (it.piece + 1) / it.pieces);
@@ -1218,13 +1238,13 @@ cudaError_t launch(const ChunkArgs& a, const ChunkPlan& plan, void* workspace, i
     if (e != cudaSuccess) return e;
     char* base = static_cast<char*>(workspace);
     // Few row blocks: every loader plans by itself, which takes one warp less time than a kernel in front. {}
-    const Work w{plan.unit_cap <= kSelfUnits && a.batch <= kSelfUnits, num_sms, plan.item_cap, plan.part_cap,
+    const Work w{plan.unit_cap <= kSelfUnits && a.batch <= kSelfUnits, num_sms, plan.unit_cap, plan.item_cap, plan.part_cap,
                  reinterpret_cast<Header*>(base), reinterpret_cast<int*>(base + plan.tiles),
                  reinterpret_cast<int2*>(base + plan.units), reinterpret_cast<Item*>(base + plan.items),
                  reinterpret_cast<uint32_t*>(base + plan.odd), reinterpret_cast<float2*>(base + plan.part_ml), reinterpret_cast<float*>(base + plan.part_acc)};
     const int grid = num_sms < plan.item_cap ? num_sms : plan.item_cap;
     if (!w.self) {
-        e = launch_dependent(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a, w, plan.unit_cap);
+        e = launch_dependent(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a, w);
         if (e != cudaSuccess) return e;
     }
     e = launch_dependent(chunk_attend_kernel<D>, dim3(grid), dim3(kThreads), L::kBytes, st, 1, a, w, map);

@@ -24,10 +24,10 @@ __device__ __forceinline__ void lds128(uint32_t at, uint32_t* x) {
 __device__ __forceinline__ void sts128(uint32_t at, uint4 x) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
-// Nanoseconds, modulo 2^32.
-__device__ __forceinline__ uint32_t time_ns() {
+// Cycles of the SM, modulo 2^32.
+__device__ __forceinline__ uint32_t cycles() {
     uint32_t t;
-    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    asm volatile("mov.u32 %0, %%clock;" : "=r"(t));
     return t;
 }
 

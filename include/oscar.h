@@ -525,8 +525,8 @@ OSCAR_API oscar_status oscar_norm_rope(oscar_ctx_t* ctx, const void* q, int64_t 
  *               workspace each.
  * The work is cut by the lengths on the device; no bound of them is asked for.
  * Logits, the softmax and all sums are fp32. The weights are rounded to bf16 for
- * their product with V (off by 2^-8 of each at most) and normalised by the sum of
- * the rounded ones; the output is rounded once to bf16.
+ * their product with V (off by 2^-8 of each at most); the output is rounded once
+ * to bf16.
  * Tokens that a row does not see do not matter to it, nor does what lies behind a
  * sequence: NaN and infinity neither. Logits and values that are infinite or NaN
  * count as in oscar_decode_bf16, as do page ids outside the pool.

@@ -336,3 +336,14 @@ def test_many_requests_and_rows(cuda, batch, new_hi, h_q, h_kv, d):
         b = int(np.searchsorted(c.start, row, side="right")) - 1
         one = chunk_oracle.extend(c.q[row:row + 1], c.pool, c.tables[b:b + 1], [0, 1], [c.total[b] - (c.start[b + 1] - 1 - row)], 1 / math.sqrt(d))
         assert (np.abs(got[row] - one[0][0]) <= one[1][0]).all(), row
+
+
+@pytest.mark.parametrize("batch", [30, 1500])
+def test_starts_that_do_not_ascend(cuda, batch):
+    """Requests that claim the same rows again and again touch nothing but those."""
+    c = Case([(20, 300)] + [(5, 0)] * (batch - 1), 8, 1, 64, seed=batch, spare=4)
+    start = np.where(np.arange(batch + 1) % 2, 300, 0)
+    got = c.run(cuda, start=start)
+    assert (got[300:] == 7).all()
+    ordered = c.run(cuda)
+    c.check(ordered)
