@@ -152,6 +152,20 @@ __device__ __forceinline__ float cost_of(int pieces, int parts, int len, float a
 // An SM's share of all tiles, a tile more at most.
 __device__ __forceinline__ int share_of(float all, int sms) { return (int)(all / (float)sms) + 1; }
 
+// The lane with the least cost, of equal ones the last: the one with the longest pieces, or without a cut.
+__device__ __forceinline__ int cheapest(float cost, int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, cost, o);
+        const int where = __shfl_xor_sync(0xffffffffu, lane, o);
+        if (other < cost || (other == cost && where > lane)) {
+            cost = other;
+            lane = where;
+        }
+    }
+    return lane;
+}
+
 // A row block's tiles (at most 2^23: 24 bits) and rows less one (8 bits) in a word.
 __device__ __forceinline__ int unit_word(const Request& r, int block, int g, int g_log2) {
     const int rows = min(kChunkRows, r.count * g - block * kChunkRows);
@@ -177,8 +191,8 @@ __device__ __forceinline__ Item item_of(const ChunkArgs& a, const Unit& u, int p
     it.pos0 = u.pos0;
     it.piece = rest / a.h_kv;
     it.pieces = p;
-    it.kv0 = (int)((long long)tiles * it.piece / p);
-    it.kv1 = (int)((long long)tiles * (it.piece + 1) / p);
+    it.kv0 = p > 1 ? (int)((long long)tiles * it.piece / p) : 0;
+    it.kv1 = p > 1 ? (int)((long long)tiles * (it.piece + 1) / p) : tiles;
     it.total = u.total;
     it.part = p > 1 ? min(part + (it.head * p + it.piece) * it.rows, part_cap - it.rows) : -1;
     it.self = self;
@@ -263,10 +277,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         if (lane == 0) cost[warp] = cost_of(pieces * a.h_kv, parts * a.h_kv, len, all, a, sms);
     }
     __syncthreads();
-    int best = 31;
-    for (int i = 30; i >= 0; --i)
-        if (cost[i] < cost[best]) best = i;
-    const int len = piece_length(best, share, longest);
+    const int len = piece_length(cheapest(cost[lane], lane), share, longest);
 
     int item_base = 0, part_base = 0;
     for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
@@ -493,19 +504,11 @@ __device__ __forceinline__ void plan_here(const ChunkArgs& a, SelfPlan* plan, in
         pieces += p;
         if (p > 1) parts += p * rows_of(plan->unit[u].word);
     }
-    float best = cost_of(pieces * a.h_kv, parts * a.h_kv, len, (float)all, a, sms);
-    int at = 31 - lane;                          // of equal costs the one with the longest pieces
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float other = __shfl_xor_sync(0xffffffffu, best, o);
-        const int where = __shfl_xor_sync(0xffffffffu, at, o);
-        if (other < best || (other == best && where < at)) {
-            best = other;
-            at = where;
-        }
-    }
-    len = __shfl_sync(0xffffffffu, len, 31 - at);
-    parts = __shfl_sync(0xffffffffu, parts, 31 - at);
+    const float cost = cost_of(pieces * a.h_kv, parts * a.h_kv, len, (float)all, a, sms);
+    const int at = cheapest(cost, lane);
+    const float best = __shfl_sync(0xffffffffu, cost, at);
+    len = __shfl_sync(0xffffffffu, len, at);
+    parts = __shfl_sync(0xffffffffu, parts, at);
     // or equal stretches of all tiles in a line, which may begin and end within an item each
     const int ctas = (int)min((long long)gridDim.x, all);
     if (__all_sync(0xffffffffu, even) && all > 0 && (all + 1) * sms < 0x7fffffff &&       // products of both in 32 bits
@@ -523,6 +526,36 @@ __device__ __forceinline__ void plan_here(const ChunkArgs& a, SelfPlan* plan, in
             pos += __shfl_sync(0xffffffffu, s, 31);
         }
         return found(units, units * a.h_kv + ctas - 1, 0, ctas > 1, ctas, (int)all);
+    }
+    // more items than CTAs: the longest pieces first, so that what follows them evens the CTAs out
+    if (__shfl_sync(0xffffffffu, pieces, at) * a.h_kv > (int)gridDim.x) {
+        auto length = [&](int u) {
+            const int tiles = tiles_of(plan->unit[u].word);
+            return tiles / pieces_of(tiles, len);
+        };
+        constexpr int kMine = (kSelfUnits + 31) / 32;
+        Unit mine[kMine];
+        int rank[kMine] = {};
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+            const int u = 32 * k + lane;
+            if (u < units) mine[k] = plan->unit[u];
+            if (u < units) plan->first_item[u] = length(u);
+        }
+        __syncwarp();
+        for (int v = 0; v < units; ++v) {
+            const int other = plan->first_item[v];
+#pragma unroll
+            for (int k = 0; k < kMine; ++k) {
+                const int u = 32 * k + lane;
+                if (u < units) rank[k] += other > plan->first_item[u] || (other == plan->first_item[u] && v < u);
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kMine; ++k)
+            if (32 * k + lane < units) plan->unit[rank[k]] = mine[k];
+        __syncwarp();
     }
     int items = 0;
     for (int u0 = 0; u0 < units; u0 += 32) {
@@ -626,8 +659,9 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
     if (in_line) n_items = stretch(blockIdx.x + 1, plan);
     bool ok = true;
     for (int i = 0; ok; ++i) {
-        // asked for ahead of its use; the few items of an own plan go round in turn
-        int next = w.self ? item + (int)gridDim.x : lane == 0 ? atomicAdd(&w.head->next, 1) + (int)gridDim.x : 0;
+        // asked for ahead of its use; the few items of an own plan go round to and fro
+        int next = !w.self && lane == 0 ? atomicAdd(&w.head->next, 1) + (int)gridDim.x : 0;
+        if (w.self) next = (i + 1) * (int)gridDim.x + (i % 2 ? (int)blockIdx.x : (int)(gridDim.x - 1 - blockIdx.x));
         const bool stop = item >= n_items;
         ok = sm.wait(sm.item_empty(i), sm.item_phase(i) ^ 1, a.dbg, i);
         if (!ok) break;
