@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     __shared__ Request s_request[kPlanThreads];
     __shared__ int s_tiles[kPlanThreads + 1];
     __shared__ int2 s_units[kPlanThreads];
+    __shared__ int s_block[kPlanThreads];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, sms = w.sms;
     const int g_log2 = 31 - __clz(a.g), unit_cap = w.unit_cap;
     grid_release();
@@ -279,6 +280,25 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     __syncthreads();
     const int len = piece_length(cheapest(cost[lane], lane), share, longest);
 
+    // the longest pieces first, where the row blocks are held: what comes last is short
+    const bool sorted = units <= kPlanThreads;
+    if (sorted) {
+        int2 mine = make_int2(0, 0);
+        int length = 0, rank = 0;
+        if (tid < units) {
+            mine = s_units[tid];
+            length = tiles_of(mine.y) / pieces_of(tiles_of(mine.y), len);
+            first_item[tid] = length;
+        }
+        __syncthreads();
+        if (tid < units) {
+            for (int v = 0; v < units; ++v) rank += first_item[v] > length || (first_item[v] == length && v < tid);
+            s_units[rank] = mine;
+            s_block[rank] = first_block[mine.x + 1] - 1 - tid;
+        }
+        __syncthreads();
+    }
+
     int item_base = 0, part_base = 0;
     for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
         const int u = u0 + tid;
@@ -297,7 +317,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
             const int at = last_at_most(first_item, min(kPlanThreads, units - u0), i);
             const int2 here = unit[u0 + at];
             const Request r = request_at(here.x);
-            w.items[item_base + i] = item_of(a, Unit{here.x, first_block[here.x + 1] - 1 - (u0 + at), here.y, r.tok0, r.pos0, r.total},
+            w.items[item_base + i] = item_of(a, Unit{here.x, sorted ? s_block[at] : first_block[here.x + 1] - 1 - (u0 + at), here.y,
+                                                  r.tok0, r.pos0, r.total},
                                              pieces_of(tiles_of(here.y), len), i - first_item[at],
                                              part_base + first_part[at], w.part_cap, item_base + i);
         }
