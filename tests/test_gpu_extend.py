@@ -347,3 +347,73 @@ def test_starts_that_do_not_ascend(cuda, batch):
     assert (got[300:] == 7).all()
     ordered = c.run(cuda)
     c.check(ordered)
+
+
+def test_far_into_the_pool(cuda):
+    """Pages whose bytes and elements lie past 32 bits, and query rows as far apart; also rows that are formed again."""
+    c = Case([(70, 60), (300, 2)], 8, 8, 128, seed=11)
+    pages = 140000                                           # 9.2 GB
+    far = torch.empty(pages, 8, 2, P, 128, dtype=BF, device=cuda)
+    used = len(c.pool)
+    far[pages - used:] = torch.from_numpy(c.pool).to(BF).to(cuda)
+    t = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).to(cuda).to(dt)
+    wide = torch.empty(len(c.q), 36 << 20, dtype=BF, device=cuda)        # 62 rows of 75 MB
+    q = wide[:, -1024:].unflatten(1, (8, 128))
+    q.copy_(torch.from_numpy(c.q).to(BF))
+    ctx = context(8, 8, 128)
+    ws = torch.empty(ctx.extend_bf16_workspace_size(2, len(c.q)), dtype=torch.uint8, device=cuda)
+    for bad in (False, True):
+        if bad:                                              # the last token of the first request
+            c.pool[c.tables[0, 129 // P], :, 1, 129 % P, 3] = np.inf
+            far[pages - used:] = torch.from_numpy(c.pool).to(BF).to(cuda)
+        out = torch.full(q.shape, 7.0, dtype=BF, device=cuda)
+        ctx.extend_bf16(q, far, t(c.tables + (pages - used), I32), t(c.start, I32), t(c.total, I32), out, ws)
+        torch.cuda.synchronize()
+        got = out.double().cpu().numpy()
+        want, bound = chunk_oracle.extend(c.q, np.where(np.isfinite(c.pool), c.pool, 0.0), c.tables, c.start, c.total, 1 / math.sqrt(128))
+        if bad:
+            assert np.isposinf(got[59, :, 3]).all()
+            got[59, :, 3] = want[59, :, 3]
+        assert (np.abs(got - want) <= bound).all()
+
+
+def test_two_graphs_of_one_workspace(cuda):
+    """Captured calls that share a workspace and run one after the other; a workspace that serves a larger call too."""
+    a, b = Case([(3000, 2), (100, 1)], 8, 2, 128, seed=12), Case([(0, 300), (50, 7)], 8, 2, 128, seed=13)
+    ctx = context(8, 2, 128)
+    t = lambda x, dt: torch.from_numpy(np.ascontiguousarray(x)).to(cuda).to(dt)
+    ws = torch.full((ctx.extend_bf16_workspace_size(5, 400),), 255, dtype=torch.uint8, device=cuda)
+    calls = []
+    for c in (a, b):
+        args = [t(c.q, BF), t(c.pool, BF), t(c.tables, I32), t(c.start, I32), t(c.total, I32), torch.zeros(c.q.shape, dtype=BF, device=cuda), ws]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            ctx.extend_bf16(*args)
+        calls.append((graph, args, c))
+    for graph, args, c in calls * 3:
+        args[5].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        want, bound = chunk_oracle.extend(c.q, c.pool, c.tables, c.start, c.total, 1 / math.sqrt(128))
+        assert (np.abs(args[5].double().cpu().numpy() - want) <= bound).all()
+
+
+def test_calls_at_once(cuda):
+    """Two calls with a workspace each on two streams."""
+    cases = [Case([(2000, 3), (40, 90)], 4, 2, 64, seed=14), Case([(0, 260)], 4, 2, 64, seed=15)]
+    ctx = context(4, 2, 64)
+    t = lambda x, dt: torch.from_numpy(np.ascontiguousarray(x)).to(cuda).to(dt)
+    ready = []
+    for c in cases:
+        ws = torch.empty(ctx.extend_bf16_workspace_size(len(c.total), len(c.q)), dtype=torch.uint8, device=cuda)
+        ready.append([t(c.q, BF), t(c.pool, BF), t(c.tables, I32), t(c.start, I32), t(c.total, I32), torch.zeros(c.q.shape, dtype=BF, device=cuda), ws])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for args, stream in zip(ready, streams):
+            ctx.extend_bf16(*args, stream=stream)
+    torch.cuda.synchronize()
+    for args, c in zip(ready, cases):
+        want, bound = chunk_oracle.extend(c.q, c.pool, c.tables, c.start, c.total, 1 / 8)
+        assert (np.abs(args[5].double().cpu().numpy() - want) <= bound).all()

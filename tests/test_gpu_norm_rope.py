@@ -155,3 +155,18 @@ def test_captured_on_another_stream(cuda):
         pos = np.array([0, 49, 3000]) + step
         check(qo, q, None, 0, turns, 0, 1.0, pos)
         check(ko, k, None, 0, turns, 0, 1.0, pos)
+
+
+def test_rows_far_apart(cuda):
+    """Row offsets past 32 bits, in and out."""
+    n, h, d = 70, 4, 64
+    wide = torch.empty(n, 36 << 20, dtype=BF, device=cuda)               # 70 rows of 75 MB
+    q, out = (wide[:, at:at + h * d].unflatten(1, (h, d)) for at in (0, 1 << 20))
+    x = torch.randn(n, h, d, device=cuda).to(BF)
+    q.copy_(x)
+    turns, _ = rope.rope_turns(d)
+    w = torch.linspace(0.5, 2, d, device=cuda)
+    context(h, h, d).norm_rope(q, None, out, None, torch.from_numpy(turns).to(cuda), q_weight=w,
+                               positions=torch.arange(n, dtype=I32, device=cuda))
+    check(out, x, w, 1e-6, turns, 0, 1.0, range(n))
+    assert torch.equal(q, x)
