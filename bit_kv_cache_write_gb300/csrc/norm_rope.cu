@@ -9,17 +9,19 @@
 //
 // HBM bounds it: each channel is read and written once. d / 8 lanes take a head, 8 channels a lane: the four pairs
 // 4 l .. 4 l + 3 (channels 4 l .. and rot / 2 + 4 l .., or 8 l ..), and the lanes behind rot / 8 pass 8 channels on. All
-// heads of a token turn by the same angles, so a lane forms its four sines and cosines once a token and uses them
-// for every head that its warp takes. Four heads of a lane group in flight and CTAs of four warps: 131,072 tokens x 40
-// heads of 128 in 433 us, 92 % of the measured copy rate (449 us with eight warps a CTA, 660 with eight heads in flight),
-// 5,003 tokens x 72 heads of 64 in 14.8 us, 95 %; single tokens 3 us.
+// heads of a token turn by the same angles, so a lane forms its four sines and cosines once a token, multiplies the
+// norm's weights into them, and uses both for every head that its warp takes; two pairs go through one instruction
+// (with the weights read and multiplied head by head the kernel was bound by its instructions: 433 us where it now takes
+// 398). Four heads of a lane group in flight, CTAs of two warps, so that a token's warp leaves its place to another at
+// once: 131,072 tokens x 40 heads of 128 in 398 us, 100 % of the measured copy rate (464 us with eight warps a CTA, 435
+// with two heads in flight); 5,003 tokens x 72 heads of 64 in 12.7 us; single tokens 2.4 us.
 #include "chunk_internal.h"
 #include "paged_device.cuh"
 
 namespace oscar {
 namespace {
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeThreads = 64;
 constexpr int kRopeDepth = 4;                // heads that a lane group has in flight
 
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
@@ -47,7 +49,52 @@ __device__ __forceinline__ int request_of(const int32_t* row_start, int batch, i
     return lo;
 }
 
-// One batch of kRopeDepth heads a lane group: heads h0 + group, + kGroups, ... of the token's q heads, then k heads.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split_f32x2(uint64_t x, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// A lane's four pairs (a, b), two at a time: a' = f (a aa - b ab), b' = f (b bb + a ba), with the norm's weights in the
+// coefficients and f the head's reciprocal root; b' and a' alone where the lane's channels do not turn.
+struct Turn {
+    uint64_t aa[2], ab[2], ba[2], bb[2];
+
+    __device__ __forceinline__ void set(const float* w, bool interleaved, int ca, int cb, bool turn, const float (&cs)[4],
+                                        const float (&sn)[4]) {
+        float wa[4] = {1, 1, 1, 1}, wb[4] = {1, 1, 1, 1};
+        if (w) {
+            const float4 x = *reinterpret_cast<const float4*>(w + ca), y = *reinterpret_cast<const float4*>(w + cb);
+            wa[0] = x.x; wb[3] = y.w;
+            wa[1] = interleaved ? x.z : x.y; wb[0] = interleaved ? x.y : y.x;
+            wa[2] = interleaved ? y.x : x.z; wb[1] = interleaved ? x.w : y.y;
+            wa[3] = interleaved ? y.z : x.w; wb[2] = interleaved ? y.y : y.z;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int k = 2 * j, l = 2 * j + 1;
+            aa[j] = turn ? f32x2(wa[k] * cs[k], wa[l] * cs[l]) : f32x2(wa[k], wa[l]);
+            bb[j] = turn ? f32x2(wb[k] * cs[k], wb[l] * cs[l]) : f32x2(wb[k], wb[l]);
+            ab[j] = f32x2(-wb[k] * sn[k], -wb[l] * sn[l]);
+            ba[j] = f32x2(wa[k] * sn[k], wa[l] * sn[l]);
+        }
+    }
+};
+
+// One batch of kRopeDepth heads a lane group: heads h0 + group, + kGroups, ... of a token's q or k heads.
 template <int D, bool Interleaved>
 struct RopeBatch {
     static constexpr int kLanes = D / 8;             // lanes of a head
@@ -55,81 +102,104 @@ struct RopeBatch {
     static constexpr int kHeads = kGroups * kRopeDepth;
     uint2 a[kRopeDepth], b[kRopeDepth];
 
-    __device__ __forceinline__ static const uint16_t* source(const RopeArgs& r, int64_t t, int h) {
-        return h < r.q.heads ? r.q.in + t * r.q.in_stride + h * D : r.k.in + t * r.k.in_stride + (h - r.q.heads) * D;
-    }
-    __device__ __forceinline__ void load(const RopeArgs& r, int64_t t, int h0, int group, int ca, int cb) {
+    __device__ __forceinline__ void load(const RopeRows& r, int64_t t, int h0, int group, int ca, int cb) {
+        const uint16_t* p = r.in + t * r.in_stride + (h0 + group) * D;
 #pragma unroll
         for (int i = 0; i < kRopeDepth; ++i) {
-            const int h = h0 + i * kGroups + group;
-            if (h < r.q.heads + r.k.heads) {
-                const uint16_t* p = source(r, t, h);
-                a[i] = *reinterpret_cast<const uint2*>(p + ca);
-                b[i] = *reinterpret_cast<const uint2*>(p + cb);
-            } else {
-                a[i] = b[i] = make_uint2(0, 0);
+            a[i] = b[i] = make_uint2(0, 0);
+            if (h0 + i * kGroups + group < r.heads) {
+                a[i] = *reinterpret_cast<const uint2*>(p + i * kGroups * D + ca);
+                b[i] = *reinterpret_cast<const uint2*>(p + i * kGroups * D + cb);
             }
         }
     }
-    __device__ __forceinline__ void finish(const RopeArgs& r, int64_t t, int h0, int group, int ca, int cb, bool turn,
-                                           const float (&cs)[4], const float (&sn)[4]) const {
+    __device__ __forceinline__ void finish(const RopeRows& r, float eps, int64_t t, int h0, int group, int ca, int cb, bool turn,
+                                           const Turn& c) const {
+        uint16_t* p = r.out + t * r.out_stride + (h0 + group) * D;
 #pragma unroll
         for (int i = 0; i < kRopeDepth; ++i) {
-            const int h = h0 + i * kGroups + group;
-            const bool mine = h < r.q.heads + r.k.heads, is_q = h < r.q.heads;
-            float x[8] = {bf16_lo(a[i].x), bf16_hi(a[i].x), bf16_lo(a[i].y), bf16_hi(a[i].y),
-                          bf16_lo(b[i].x), bf16_hi(b[i].x), bf16_lo(b[i].y), bf16_hi(b[i].y)};
-            const float* w = is_q ? r.q.weight : r.k.weight;
-            if (r.q.weight || r.k.weight) {          // the same branch for all lanes: they sum together
-                float ss = 0.0f;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) ss += x[c] * x[c];
+            if (h0 + i * kGroups >= r.heads) break;          // none of the warp's
+            // a's and b's of the pairs, two at a time
+            uint64_t x[2], y[2];
+            if (Interleaved) {
+                x[0] = f32x2(bf16_lo(a[i].x), bf16_lo(a[i].y)); y[0] = f32x2(bf16_hi(a[i].x), bf16_hi(a[i].y));
+                x[1] = f32x2(bf16_lo(b[i].x), bf16_lo(b[i].y)); y[1] = f32x2(bf16_hi(b[i].x), bf16_hi(b[i].y));
+            } else {
+                x[0] = f32x2(bf16_lo(a[i].x), bf16_hi(a[i].x)); x[1] = f32x2(bf16_lo(a[i].y), bf16_hi(a[i].y));
+                y[0] = f32x2(bf16_lo(b[i].x), bf16_hi(b[i].x)); y[1] = f32x2(bf16_lo(b[i].y), bf16_hi(b[i].y));
+            }
+            float f = 1.0f;
+            if (r.weight) {
+                float lo, hi;
+                split_f32x2(fma_f32x2(y[1], y[1], fma_f32x2(y[0], y[0], fma_f32x2(x[1], x[1], mul_f32x2(x[0], x[0])))), lo, hi);
+                float ss = lo + hi;
 #pragma unroll
                 for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                float f = rsqrtf(ss * (1.0f / D) + r.eps);
+                f = rsqrtf(ss * (1.0f / D) + eps);
                 if (__any_sync(0xffffffffu, !(ss <= 3.0e38f))) {     // the sum may have passed fp32: in units of 2^64
-                    float s2 = 0.0f;
+                    const uint64_t down = f32x2(0x1p-64f, 0x1p-64f);
+                    uint64_t s = f32x2(0.0f, 0.0f);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) s2 += (x[c] * 0x1p-64f) * (x[c] * 0x1p-64f);
+                    for (int k = 0; k < 2; ++k) {
+                        const uint64_t u = mul_f32x2(x[k], down), v = mul_f32x2(y[k], down);
+                        s = fma_f32x2(v, v, fma_f32x2(u, u, s));
+                    }
+                    split_f32x2(s, lo, hi);
+                    float s2 = lo + hi;
 #pragma unroll
                     for (int o = kLanes / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-                    if (!(ss <= 3.0e38f)) f = rsqrtf(s2 * (1.0f / D) + r.eps * 0x1p-128f) * 0x1p-64f;
-                }
-                if (w) {
-                    const float4 wa = *reinterpret_cast<const float4*>(w + ca), wb = *reinterpret_cast<const float4*>(w + cb);
-                    x[0] *= f * wa.x; x[1] *= f * wa.y; x[2] *= f * wa.z; x[3] *= f * wa.w;
-                    x[4] *= f * wb.x; x[5] *= f * wb.y; x[6] *= f * wb.z; x[7] *= f * wb.w;
-                }
-            }
-            if (turn) {
+                    if (!(ss <= 3.0e38f)) {
+                        // 2^64 of the root goes to the values: the coefficients times it might not be a float
+                        f = rsqrtf(s2 * (1.0f / D) + eps * 0x1p-128f);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int ia = Interleaved ? 2 * j : j, ib = Interleaved ? 2 * j + 1 : 4 + j;
-                    const float u = x[ia], v = x[ib];
-                    x[ia] = u * cs[j] - v * sn[j];
-                    x[ib] = v * cs[j] + u * sn[j];
+                        for (int k = 0; k < 2; ++k) {
+                            x[k] = mul_f32x2(x[k], down);
+                            y[k] = mul_f32x2(y[k], down);
+                        }
+                    }
                 }
             }
-            if (mine) {
-                uint16_t* p = is_q ? r.q.out + t * r.q.out_stride + h * D
-                                   : r.k.out + t * r.k.out_stride + (h - r.q.heads) * D;
-                *reinterpret_cast<uint2*>(p + ca) = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
-                *reinterpret_cast<uint2*>(p + cb) = make_uint2(bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7]));
+            uint64_t u[2], v[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                u[k] = mul_f32x2(x[k], c.aa[k]);
+                v[k] = mul_f32x2(y[k], c.bb[k]);
+                if (turn) {
+                    u[k] = fma_f32x2(y[k], c.ab[k], u[k]);
+                    v[k] = fma_f32x2(x[k], c.ba[k], v[k]);
+                }
+                if (r.weight) {
+                    u[k] = mul_f32x2(u[k], f32x2(f, f));
+                    v[k] = mul_f32x2(v[k], f32x2(f, f));
+                }
+            }
+            float m[4], n[4];
+            split_f32x2(u[0], m[0], m[1]); split_f32x2(u[1], m[2], m[3]);
+            split_f32x2(v[0], n[0], n[1]); split_f32x2(v[1], n[2], n[3]);
+            if (h0 + i * kGroups + group < r.heads) {
+                uint16_t* to = p + i * kGroups * D;
+                if (Interleaved) {
+                    *reinterpret_cast<uint2*>(to + ca) = make_uint2(bf16_pair(m[0], n[0]), bf16_pair(m[1], n[1]));
+                    *reinterpret_cast<uint2*>(to + cb) = make_uint2(bf16_pair(m[2], n[2]), bf16_pair(m[3], n[3]));
+                } else {
+                    *reinterpret_cast<uint2*>(to + ca) = make_uint2(bf16_pair(m[0], m[1]), bf16_pair(m[2], m[3]));
+                    *reinterpret_cast<uint2*>(to + cb) = make_uint2(bf16_pair(n[0], n[1]), bf16_pair(n[2], n[3]));
+                }
             }
         }
     }
 };
 
-// A warp takes `span` batches of heads of one token; `parts` warps take a token.
+// A warp takes `span` batches of heads of one token; `parts` warps take a token. Batches of q heads come first.
 template <int D, bool Interleaved>
 __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeArgs r, int parts, int span) {
     using B = RopeBatch<D, Interleaved>;
     const int lane = threadIdx.x % 32, group = lane / B::kLanes, l = lane % B::kLanes;
     const int64_t item = (int64_t)blockIdx.x * (kRopeThreads / 32) + threadIdx.x / 32;
     const int64_t t = item / parts;
-    const int heads = r.q.heads + r.k.heads;
-    int h0 = (int)(item % parts) * span * B::kHeads;
-    const int end = min(heads, h0 + span * B::kHeads);
+    const int q_batches = (r.q.heads + B::kHeads - 1) / B::kHeads, all = q_batches + (r.k.heads + B::kHeads - 1) / B::kHeads;
+    int at = (int)(item % parts) * span;
+    const int end = min(all, at + span);
     const bool turn = 8 * l < r.rot;
     const int ca = Interleaved ? 8 * l : (turn ? 4 * l : 8 * l);
     const int cb = Interleaved ? ca + 4 : (turn ? r.rot / 2 + 4 * l : ca + 4);
@@ -140,8 +210,14 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeArgs 
     }
     grid_wait();
     if (t >= r.n) return;
+    auto load = [&](B& b, int i) {
+        if (i < q_batches)
+            b.load(r.q, t, i * B::kHeads, group, ca, cb);
+        else
+            b.load(r.k, t, (i - q_batches) * B::kHeads, group, ca, cb);
+    };
     B now;
-    now.load(r, t, h0, group, ca, cb);
+    load(now, at);
     int64_t pos = 0;
     if (r.positions) {
         pos = r.positions[t];
@@ -161,23 +237,28 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeArgs 
         cs[j] *= r.scale;
         sn[j] *= r.scale;
     }
+    Turn c;
+    c.set(at < q_batches ? r.q.weight : r.k.weight, Interleaved, ca, cb, turn, cs, sn);
     for (;;) {
-        const int next = h0 + B::kHeads;
         B ahead;
-        if (next < end) ahead.load(r, t, next, group, ca, cb);
-        now.finish(r, t, h0, group, ca, cb, turn, cs, sn);
-        if (next >= end) break;
+        if (at + 1 < end) load(ahead, at + 1);
+        if (at < q_batches)
+            now.finish(r.q, r.eps, t, at * B::kHeads, group, ca, cb, turn, c);
+        else
+            now.finish(r.k, r.eps, t, (at - q_batches) * B::kHeads, group, ca, cb, turn, c);
+        if (++at >= end) break;
         now = ahead;
-        h0 = next;
+        if (at == q_batches) c.set(r.k.weight, Interleaved, ca, cb, turn, cs, sn);
     }
 }
 
 template <int D>
 cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t st) {
     using B = RopeBatch<D, false>;
-    const int batches = (a.q.heads + a.k.heads + B::kHeads - 1) / B::kHeads;
-    // A warp takes a batch of heads while that gives no more warps than run at once (256 tokens x 40 heads: 4.4 us, 9.6
-    // with a token a warp), else a whole token's heads (131,072: 449 us, 658 with a batch a warp).
+    const int batches = (a.q.heads + B::kHeads - 1) / B::kHeads + (a.k.heads + B::kHeads - 1) / B::kHeads;
+    // A warp takes a batch of heads while that gives no more warps than run at once (256 tokens x 40 heads: 3.5 us, more
+    // than twice that with a token a warp), else a whole token's heads (131,072: 398 us, half as much again with a batch
+    // a warp).
     const bool spread = (int64_t)a.n * batches <= (int64_t)num_sms * 32;
     const int parts = spread ? batches : 1, span = spread ? 1 : batches;
     const int64_t warps = (int64_t)a.n * parts, per = kRopeThreads / 32;
