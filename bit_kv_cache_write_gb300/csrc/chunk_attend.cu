@@ -447,6 +447,11 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -839,22 +844,21 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> s
     }
 }
 
-// A block's queries, 16 bytes at a time, into the swizzled layout; zeros behind the last row.
+// Asks for a block's queries, 16 bytes at a time, into the swizzled layout; zeros behind the last row. There after
+// async_copies_done.
 template <int D>
-__device__ __forceinline__ void load_queries(const ChunkArgs& a, const Item& it, const Layout<D> sm, int t, int rows,
-                                             int thread, int g_log2) {
+__device__ __forceinline__ void ask_queries(const ChunkArgs& a, const Item& it, const Layout<D> sm, int t, int rows,
+                                            int thread, int g_log2) {
     using L = Layout<D>;
     const int c = thread % (D / 8);
     const uint16_t* from = a.q + (int64_t)it.tok0 * a.q_stride + (it.head << g_log2) * D + c * 8;
     const int r0 = it.r0 + kBlock * t;
-#pragma unroll 8
+#pragma unroll 4
     for (int row = thread / (D / 8); row < kBlock; row += kBlock * 8 / D) {
         const int r = r0 + row;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (row < rows) x = *reinterpret_cast<const uint4*>(from + (int64_t)(r >> g_log2) * a.q_stride + (r & (a.g - 1)) * D);
-        sts128(sm.q(t) + c / 8 * L::kHalfBytes + row * 128 + (((c % 8) ^ (row % 8)) * 16), x);
+        const uint16_t* at = from + (row < rows ? (int64_t)(r >> g_log2) * a.q_stride + (r & (a.g - 1)) * D : 0);
+        async_copy16(sm.q(t) + c / 8 * L::kHalfBytes + row * 128 + (((c % 8) ^ (row % 8)) * 16), at, row < rows);
     }
-    fence_async();
 }
 
 // Logits of 32 tokens that the row does not see count as -infinity: from `seen` on, and those of absent pages.
@@ -921,20 +925,27 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
     const uint32_t s_col = tmem + ((uint32_t)(32 * warp) << 16) + t * kChunkTile;
     const uint32_t o_col = tmem + ((uint32_t)(32 * warp) << 16) + 2 * kChunkTile + t * D;
     int tile = 0, step = 0;                      // tiles of the CTA, steps of this block, counted through
-    // Waits for the next item and puts its queries in place; the block's products with the last ones are done then.
-    auto next_item = [&](int i) {
+    // Waits for item i and asks for its queries, once the products with the last ones are done; says that they are there.
+    bool asked = false;
+    auto ask = [&](int i) {
         if (!sm.wait(sm.item_full(i), sm.item_phase(i), a.dbg, 8000 + i)) return false;
         const Item it = sm.read_item(i);
         if (it.rows < 0) return true;
         const Blocks bl = blocks_of(it, g_log2);
-        if (t ? bl.count[1] : bl.count[0]) {
-            load_queries<D>(a, it, sm, t, t ? bl.rows[1] : bl.rows[0], in_block, g_log2);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sm.q_full(t));
-        }
+        asked = (t ? bl.count[1] : bl.count[0]) > 0;
+        if (asked) ask_queries<D>(a, it, sm, t, t ? bl.rows[1] : bl.rows[0], in_block, g_log2);
         return true;
     };
-    if (!next_item(0)) return;
+    auto there = [&] {
+        if (!asked) return;
+        async_copies_done();
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.q_full(t));
+        asked = false;
+    };
+    if (!ask(0)) return;
+    there();
     for (int i = 0;; ++i) {
         int count, seen;
         bool working;
@@ -951,8 +962,15 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
             seen = in_block < rows ? limit_of(it.r0 + kBlock * t + in_block, it.pos0, g_log2) - it.kv0 * kChunkTile : 0x7fffffff;
         }
         float m = kNoReference, sum = 0.0f;
+        bool early = false;
         for (int j = 0; j < count; ++j, ++step, seen -= kChunkTile) {
             if (!sm.wait(sm.s_full(t), step & 1, a.dbg, 9000 + i)) return;
+            // the last logits: the next item's queries travel while their weights are formed and the products end. Not
+            // waited for here: the loader may need these weights to get that far.
+            if (j + 1 == count && __all_sync(0xffffffffu, mbar_over(sm.item_full(i + 1), sm.item_phase(i + 1)))) {
+                if (!ask(i + 1)) return;
+                early = true;
+            }
             if (!working) {                      // no row of this warp is any: what its lanes hold as weights reaches nothing
                 if (lane == 0) mbar_arrive(sm.p_full(t));
                 continue;
@@ -992,7 +1010,8 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
             __syncwarp();
             if (lane == 0) mbar_arrive(sm.p_full(t));
         }
-        if (!next_item(i + 1)) return;           // its queries travel while this one's products end
+        if (!early && !ask(i + 1)) return;
+        there();
         if (count > 0 && !sm.wait(sm.o_done(t), (step - 1) & 1, a.dbg, 10000 + i)) return;
         uint32_t again = 0;
         if (working) {
@@ -1004,7 +1023,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
             const int64_t row = (int64_t)(it.tok0 + (r >> g_log2)) * (a.h_kv << g_log2) + (it.head << g_log2) + (r & (a.g - 1));
             const int part = it.part + r - it.r0;
             if (it.part >= 0 && mine) w.part_ml[part] = make_float2(m, sum);
-            bool odd = false;
+            uint64_t probe = 0;                  // 0 * x of all channels: NaN where one is infinite or NaN
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -1015,7 +1034,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
                     for (int k = 0; k < 32; ++k) o[k] = 0;
                 }
 #pragma unroll
-                for (int k = 0; k < 32; ++k) odd |= !(fabsf(__uint_as_float(o[k])) <= 3.402823466e38f);
+                for (int k = 0; k < 32; k += 2) probe = fma_f32x2(f32x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), 0ull, probe);
                 if (!mine) continue;
                 if (it.part >= 0) {              // a part of a cut item, as it is
                     float* to = w.part_acc + (int64_t)part * D + c;
@@ -1024,14 +1043,20 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
                 } else {
                     uint32_t y[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) y[k] = bf16_pair(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+                    for (int k = 0; k < 16; ++k) {
+                        float lo, hi;
+                        split_f32x2(mul_f32x2(f32x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), f32x2(inv, inv)), lo, hi);
+                        y[k] = bf16_pair(lo, hi);
+                    }
                     uint16_t* to = a.out + row * D + c;
                     store32(to, y);
                     store32(to + 16, y + 8);
                 }
             }
             tc_fence_before();
-            again = __ballot_sync(0xffffffffu, odd && mine);
+            float lo, hi;
+            split_f32x2(probe, lo, hi);
+            again = __ballot_sync(0xffffffffu, lo + hi != 0.0f && mine);
         }
         if (lane == 0) w.odd[(int64_t)sm.read_item(i).self * 8 + 4 * t + warp] = again;
         __syncwarp();
@@ -1087,6 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attend_kernel(const __grid_
         if (warp == kSoftmaxWarps) load_role<D>(a, w, &map, sm, reinterpret_cast<SelfPlan*>(smem + L::kOffPlan), lane);
         if (warp == kSoftmaxWarps + 1) issue_role<D>(a, sm, tmem, lane);
     }
+    async_copies_done();                         // of a role that stopped
     tc_fence_before();
     __syncthreads();
     if (warp == kSoftmaxWarps + 1) {

@@ -24,6 +24,12 @@ __device__ __forceinline__ void lds128(uint32_t at, uint32_t* x) {
 __device__ __forceinline__ void sts128(uint32_t at, uint4 x) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
 }
+// 16 bytes from global to shared memory without registers, zeros instead where `there` is false; done by
+// async_copies_done, for the thread's own.
+__device__ __forceinline__ void async_copy16(uint32_t to, const void* from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void async_copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Cycles of the SM, modulo 2^32.
 __device__ __forceinline__ uint32_t cycles() {
     uint32_t t;
@@ -44,6 +50,14 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t phase) {
     uint32_t ok;
     asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(bar), "r"(phase) : "memory");
+    return ok != 0;
+}
+
+// The same without sleeping.
+__device__ __forceinline__ bool mbar_over(uint32_t bar, uint32_t phase) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
                  : "=r"(ok) : "r"(bar), "r"(phase) : "memory");
     return ok != 0;
 }
