@@ -754,17 +754,18 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> s
     using L = Layout<D>;
     constexpr uint32_t kScores = idesc_bf16(kBlock, kChunkTile, false), kValues = idesc_bf16(kBlock, D, true);
     const int g_log2 = 31 - __clz(a.g);
+    const uint32_t leader = elected();
     int slot = 0;
     uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
     bool ok = true, issued = false;
-    auto scores = [&](int t, int k_slot) {                   // S of block t, from lane 0
+    auto scores = [&](int t, int k_slot) {                   // S of block t
         const uint32_t qd = sw128_desc(sm.q(t), 0), kd = sw128_desc(sm.kv(k_slot), 0);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = ((ks / 4) * L::kHalfBytes + (ks % 4) * 32) >> 4;
-            umma_ss(tmem + t * kChunkTile, qd + off, kd + off, kScores, ks > 0);
+            umma_ss(leader, tmem + t * kChunkTile, qd + off, kd + off, kScores, ks > 0);
         }
-        umma_commit(sm.s_full(t));
+        umma_commit(leader, sm.s_full(t));
     };
     for (int i = 0; ok; ++i) {
         ok = sm.wait(sm.item_full(i), sm.item_phase(i), a.dbg, 2000 + i);
@@ -786,11 +787,11 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> s
             q_phase[t] ^= 1;
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) scores(t, k0);
+            scores(t, k0);
             issued = true;
         }
         if (!ok) break;
-        if (lane == 0) umma_commit(sm.kv_empty(k0));
+        umma_commit(leader, sm.kv_empty(k0));
         for (int j = 0; j < count && ok; ++j) {
             const int vs = slot++;
             ok = sm.wait(sm.kv_full(vs), sm.kv_phase(vs), a.dbg, 5000 + i);
@@ -815,30 +816,28 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> s
                     p_phase[t] ^= 1;
                     if (!ok) break;
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t vd = sw128_desc(sm.kv(vs), L::kHalfBytes), o = tmem + 2 * kChunkTile + t * D;
-                        const uint32_t p = tmem + t * kChunkTile;
+                    const uint32_t vd = sw128_desc(sm.kv(vs), L::kHalfBytes), o = tmem + 2 * kChunkTile + t * D;
+                    const uint32_t p = tmem + t * kChunkTile;
 #pragma unroll
-                        for (int k16 = 0; k16 < kTilePages; ++k16)
-                            umma_ts(o, p + k16 * 8, vd + k16 * (2048 >> 4), kValues, j > 0 || k16 > 0);
-                        umma_commit(sm.o_done(t));
-                    }
+                    for (int k16 = 0; k16 < kTilePages; ++k16)
+                        umma_ts(leader, o, p + k16 * 8, vd + k16 * (2048 >> 4), kValues, j > 0 || k16 > 0);
+                    umma_commit(leader, sm.o_done(t));
                 }
-                if (t == 1 && lane == 0) umma_commit(sm.kv_empty(vs));
+                if (t == 1) umma_commit(leader, sm.kv_empty(vs));
                 if (j + 1 < bl.count[t]) {
                     if (!here) ok = sm.wait(sm.kv_full(kn), sm.kv_phase(kn), a.dbg, 6000 + i);
                     here = true;
                     if (!ok) break;
                     tc_fence_after();
-                    if (lane == 0) scores(t, kn);
+                    scores(t, kn);
                 }
             }
-            if (ok && more && lane == 0) umma_commit(sm.kv_empty(kn));
+            if (ok && more) umma_commit(leader, sm.kv_empty(kn));
         }
     }
     // the last matrix products are done before tensor memory is freed
     if (issued) {
-        if (lane == 0) umma_commit(sm.last());
+        umma_commit(leader, sm.last());
         __syncwarp();
         sm.drain(sm.last(), 0);
     }
@@ -1070,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attend_kernel(const __grid_
                                                                    const __grid_constant__ CUtensorMap map) {
     using L = Layout<D>;
     extern __shared__ __align__(1024) uint8_t smem[];        // the tiles' swizzle wants them on 1,024 bytes
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;    // uniform for the compiler too
     const L sm{smem_u32(smem)};
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::kStages; ++s) {
@@ -1099,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attend_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = lds32(sm.tmem());
+    const uint32_t tmem = __shfl_sync(0xffffffffu, lds32(sm.tmem()), 0);
     grid_wait();
     grid_release();
 

@@ -87,21 +87,31 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool b_across) {
            ((uint32_t)(m >> 4) << 24);
 }
 
+// 1 in one lane of the converged warp.
+__device__ __forceinline__ uint32_t elected() {
+    uint32_t x;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(x));
+    return x;
+}
+
+// The matrix instructions are executed by the whole warp with the elected lane's predicate: their operands are the same
+// in all lanes and stay in uniform registers, which a branch of one lane would not let them.
 // D (tensor memory) = A (shared memory) B (shared memory) [+ D].
-__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
-    asm volatile("{ .reg .pred p; .reg .b64 da, db; setp.ne.b32 p, %4, 0; mov.b64 da, {%1, %5}; mov.b64 db, {%2, %5};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p; }"
-                 :: "r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHigh) : "memory");
+__device__ __forceinline__ void umma_ss(uint32_t leader, uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
+    asm volatile("{ .reg .pred p, q; .reg .b64 da, db; setp.ne.b32 q, %6, 0; setp.ne.b32 p, %4, 0; mov.b64 da, {%1, %5}; mov.b64 db, {%2, %5};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p; }"
+                 :: "r"(d_tmem), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHigh), "r"(leader) : "memory");
 }
 // D (tensor memory) = A (tensor memory) B (shared memory) [+ D].
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, bool acc) {
-    asm volatile("{ .reg .pred p; .reg .b64 db; setp.ne.b32 p, %4, 0; mov.b64 db, {%2, %5};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p; }"
-                 :: "r"(d_tmem), "r"(a_tmem), "r"(b), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHigh) : "memory");
+__device__ __forceinline__ void umma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc, bool acc) {
+    asm volatile("{ .reg .pred p, q; .reg .b64 db; setp.ne.b32 q, %6, 0; setp.ne.b32 p, %4, 0; mov.b64 db, {%2, %5};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p; }"
+                 :: "r"(d_tmem), "r"(a_tmem), "r"(b), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHigh), "r"(leader) : "memory");
 }
-// An arrival at the mbarrier once every matrix instruction that this thread issued is done.
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+// An arrival at the mbarrier once every matrix instruction that the elected lane issued is done.
+__device__ __forceinline__ void umma_commit(uint32_t leader, uint32_t bar) {
+    asm volatile("{ .reg .pred q; setp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" :: "r"(bar), "r"(leader) : "memory");
 }
 
 // 32 consecutive 32-bit columns of this thread's lane of tensor memory, on their way until tmem_wait.
