@@ -203,13 +203,13 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeArgs 
     const bool turn = 8 * l < r.rot;
     const int ca = Interleaved ? 8 * l : (turn ? 4 * l : 8 * l);
     const int cb = Interleaved ? ca + 4 : (turn ? r.rot / 2 + 4 * l : ca + 4);
+    grid_wait();                             // the turns may be of the launch before too
+    if (t >= r.n) return;
     uint64_t step[4] = {0, 0, 0, 0};
     if (turn) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) step[j] = r.turns[4 * l + j];
     }
-    grid_wait();
-    if (t >= r.n) return;
     auto load = [&](B& b, int i) {
         if (i < q_batches)
             b.load(r.q, t, i * B::kHeads, group, ca, cb);

@@ -170,3 +170,27 @@ def test_rows_far_apart(cuda):
                                positions=torch.arange(n, dtype=I32, device=cuda))
     check(out, x, w, 1e-6, turns, 0, 1.0, range(n))
     assert torch.equal(q, x)
+
+
+def test_turns_formed_on_the_stream(cuda):
+    """Turns that a kernel in front of the call writes, as when the context's scaling follows the length."""
+    n, h, d = 3, 4, 64
+    q, _ = rows(cuda, n, h, h, d, 5)
+    tables = [torch.from_numpy(rope.rope_turns(d, base)[0]).to(cuda) for base in (1e4, 1e5, 1e6)]
+    t, pos = torch.zeros_like(tables[0]), torch.tensor([3, 1000, 100000], dtype=I32, device=cuda)
+    outs = [torch.empty(n, h, d, dtype=BF, device=cuda) for _ in tables]
+    ctx, side = context(h, h, d), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for table, out in zip(tables, outs):
+            torch.add(table, 0, out=t)
+            ctx.norm_rope(q, None, out, None, t, positions=pos)
+    for _ in range(3):
+        for out in outs:
+            out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for table, out in zip(tables, outs):
+            check(out, q, None, 0, table.cpu().numpy(), 0, 1.0, pos.tolist())
