@@ -13,7 +13,7 @@
 // norm's weights into them, and uses both for every head that its warp takes; two pairs go through one instruction
 // (with the weights read and multiplied head by head the kernel was bound by its instructions: 433 us where it now takes
 // 398). Four heads of a lane group in flight, CTAs of two warps, so that a token's warp leaves its place to another at
-// once: 131,072 tokens x 40 heads of 128 in 398 us, 100 % of the measured copy rate (464 us with eight warps a CTA, 435
+// once: 131,072 tokens x 40 heads of 128 in 399 us, 99 % of the measured copy rate (464 us with eight warps a CTA, 435
 // with two heads in flight); 5,003 tokens x 72 heads of 64 in 12.7 us; single tokens 2.4 us.
 #include "chunk_internal.h"
 #include "paged_device.cuh"
@@ -130,31 +130,37 @@ struct RopeBatch {
             }
             float f = 1.0f;
             if (r.weight) {
+                // sums from here on are right whatever their squares lost (or eps is above that)
+                const float least = eps < 0x1p-60f ? D * 0x1p-60f : 0.0f;
+                const uint32_t from = __float_as_uint(least), span = __float_as_uint(3.0e38f) - from;
                 float lo, hi;
                 split_f32x2(fma_f32x2(y[1], y[1], fma_f32x2(y[0], y[0], fma_f32x2(x[1], x[1], mul_f32x2(x[0], x[0])))), lo, hi);
                 float ss = lo + hi;
 #pragma unroll
                 for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                 f = rsqrtf(ss * (1.0f / D) + eps);
-                if (__any_sync(0xffffffffu, !(ss <= 3.0e38f))) {     // the sum may have passed fp32: in units of 2^64
-                    const uint64_t down = f32x2(0x1p-64f, 0x1p-64f);
+                if (__any_sync(0xffffffffu, __float_as_uint(ss) - from > span)) {       // not within [least, 3e38]
+                    // The sum may have passed fp32, or its squares may be below it with an eps that does not hide that:
+                    // the values in units of 2^72 or 2^-88, where neither is so. The root's unit goes to the values: the
+                    // coefficients times it might not be a float.
+                    const float unit = ss < least ? 0x1p88f : ss <= 3.0e38f ? 1.0f : 0x1p-72f;
+                    const uint64_t by = f32x2(unit, unit);
                     uint64_t s = f32x2(0.0f, 0.0f);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const uint64_t u = mul_f32x2(x[k], down), v = mul_f32x2(y[k], down);
+                        const uint64_t u = mul_f32x2(x[k], by), v = mul_f32x2(y[k], by);
                         s = fma_f32x2(v, v, fma_f32x2(u, u, s));
                     }
                     split_f32x2(s, lo, hi);
                     float s2 = lo + hi;
 #pragma unroll
                     for (int o = kLanes / 2; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-                    if (!(ss <= 3.0e38f)) {
-                        // 2^64 of the root goes to the values: the coefficients times it might not be a float
-                        f = rsqrtf(s2 * (1.0f / D) + eps * 0x1p-128f);
+                    if (unit != 1.0f) {
+                        f = rsqrtf(s2 * (1.0f / D) + eps * unit * unit);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            x[k] = mul_f32x2(x[k], down);
-                            y[k] = mul_f32x2(y[k], down);
+                            x[k] = mul_f32x2(x[k], by);
+                            y[k] = mul_f32x2(y[k], by);
                         }
                     }
                 }

@@ -172,6 +172,35 @@ def test_rows_far_apart(cuda):
     assert torch.equal(q, x)
 
 
+@pytest.mark.parametrize("layout", [0, 1])
+def test_norm_of_the_smallest_and_largest(cuda, layout):
+    """Squares above and below fp32: rows of the largest numbers, one of them, and with no eps (or hardly any) rows of the
+    smallest. Rows of both kinds in one warp."""
+    d, top = 64, torch.finfo(BF).max
+    x = torch.randn(4, 4, d, device=cuda).double()
+    sign = torch.sign(x)
+    x[0] = sign[0] * top
+    x[1] *= 2.0 ** 100
+    x[1, :, 5] = top
+    x[2, 0], x[2, 1], x[2, 2] = x[2, 0] * 2.0 ** -40, x[2, 1] * 2.0 ** -70, x[2, 2] * 2.0 ** -110
+    x[3, :] = sign[3] * 2.0 ** -133                                      # bf16's smallest
+    x[3, 1] = sign[3, 1] * top
+    x = x.to(BF)
+    turns, _ = rope.rope_turns(d)
+    w, pos = torch.linspace(0.5, 2, d, device=cuda), [0, 1, 77, 1 << 20]
+    for eps, rows_of in ((0.0, 4), (1e-30, 2), (1e-6, 3)):
+        out = torch.empty_like(x)
+        context(4, 4, d).norm_rope(x, None, out, None, torch.from_numpy(turns).to(cuda), q_weight=w, eps=eps, layout=layout,
+                                   positions=torch.tensor(pos, dtype=I32, device=cuda))
+        check(out[:rows_of], x[:rows_of], w, float(np.float32(eps)), turns, layout, 1.0, pos[:rows_of])
+    # an eps between the squares of two heads: no root of either's alone
+    x = (torch.randn(1, 4, d, device=cuda).double() * torch.tensor([2.0 ** -52, 2.0 ** -49, 2.0 ** -36, 1.0], device=cuda)[:, None]).to(BF)
+    out = torch.empty_like(x)
+    context(4, 4, d).norm_rope(x, None, out, None, torch.from_numpy(turns).to(cuda), q_weight=w, eps=2.0 ** -100, layout=layout,
+                               positions=torch.zeros(1, dtype=I32, device=cuda))
+    check(out, x, w, 2.0 ** -100, turns, layout, 1.0, [0])
+
+
 def test_turns_formed_on_the_stream(cuda):
     """Turns that a kernel in front of the call writes, as when the context's scaling follows the length."""
     n, h, d = 3, 4, 64
