@@ -51,7 +51,8 @@ constexpr int kSelfUnits = 80;                   // row blocks and requests up t
 constexpr int kJoinThreads = 256;
 constexpr float kNoReference = -3.402823466e38f; // reference before any token: no finite logit is below it
 constexpr float kHeadroom = 8.0f;                // the reference rises when a logit passes it by this much (log2)
-constexpr uint32_t kWaitTicks = 2000000000u;      // cycles of a wait at most, about a second
+constexpr uint32_t kWaitTicks = 2000000000u;     // cycles of a wait at most, about a second
+constexpr int kFold = 512;                       // tiles whose products the tensor core adds up (see Fold)
 
 // A work item: rows r0 .. r0 + rows of request b's row space against cache tiles [kv0, kv1).
 struct alignas(16) Item {
@@ -79,6 +80,9 @@ struct Work {
     uint32_t* odd;                // [items][8] rows to form again, a word for each softmax warp
     float2* part_ml;              // per row of a cut item: reference and sum
     float* part_acc;              // [rows][d]
+    int fold_rows;                // of a CTA
+    float2* fold_ml;              // [SMs][fold_rows] the same of what the tensor core no longer holds (see Fold)
+    float* fold_acc;              // [SMs][fold_rows][d]
 };
 
 __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
@@ -828,7 +832,7 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> s
                     const uint32_t p = tmem + t * kChunkTile;
 #pragma unroll
                     for (int k16 = 0; k16 < kTilePages; ++k16)
-                        umma_ts(leader, o, p + k16 * 8, vd + k16 * (2048 >> 4), kValues, j > 0 || k16 > 0);
+                        umma_ts(leader, o, p + k16 * 8, vd + k16 * (2048 >> 4), kValues, j % kFold > 0 || k16 > 0);
                     umma_commit(leader, sm.o_done(t));
                 }
                 if (t == 1) umma_commit(leader, sm.kv_empty(vs));
@@ -924,6 +928,58 @@ __device__ __forceinline__ float weigh128(uint32_t (&u)[4][32], uint64_t scale, 
     return x + y;
 }
 
+// The tensor core cuts off what its fp32 accumulator does not hold, so a sum of one sign falls short by 2^-25 of itself an
+// addition, eight additions a tile: 0.6 % after 8,192 tiles, 2.6 % after 32,768 (measured). Every kFold tiles the outputs
+// are therefore added, rounded to nearest, to a row in the workspace, and begin anew; at the end they come back. An
+// accumulator is short by 0.04 % then, and 512 tiles take some 600 us, the addition some 5.
+//
+// Adds a thread's row of outputs (reference m, sum) to its folded ones, the first time over them. `there`: whether the
+// thread has a row; tensor memory is read by the whole warp.
+template <int D>
+__device__ __noinline__ void fold_row(float2* ml, float* acc, uint32_t o_col, float m, float sum, bool first, bool there) {
+    const float2 old = first || !there ? make_float2(m, 0.0f) : *ml;
+    const float f = exp2_approx(old.x - m);
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_read32(o_col + c, o);
+        if (!there) continue;
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            float4* at = reinterpret_cast<float4*>(acc + c + k);
+            float4 x = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *at;
+            x.x = fmaf(x.x, f, __uint_as_float(o[k])); x.y = fmaf(x.y, f, __uint_as_float(o[k + 1]));
+            x.z = fmaf(x.z, f, __uint_as_float(o[k + 2])); x.w = fmaf(x.w, f, __uint_as_float(o[k + 3]));
+            *at = x;
+        }
+    }
+    if (there) *ml = make_float2(m, fmaf(old.y, f, sum));
+}
+// Adds a thread's folded row to its outputs in tensor memory, whose reference is m; returns the folded sum.
+template <int D>
+__device__ __noinline__ float unfold_row(const float2* ml, const float* acc, uint32_t o_col, float m, bool there) {
+    const float2 old = there ? *ml : make_float2(m, 0.0f);
+    const float f = exp2_approx(old.x - m);
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_read32(o_col + c, o);
+        if (there) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(acc + c + k);
+                o[k] = __float_as_uint(fmaf(x.x, f, __uint_as_float(o[k])));
+                o[k + 1] = __float_as_uint(fmaf(x.y, f, __uint_as_float(o[k + 1])));
+                o[k + 2] = __float_as_uint(fmaf(x.z, f, __uint_as_float(o[k + 2])));
+                o[k + 3] = __float_as_uint(fmaf(x.w, f, __uint_as_float(o[k + 3])));
+            }
+        }
+        tmem_st32(o_col + c, o);
+    }
+    tmem_wait_st();
+    return old.y * f;
+}
+
 // Softmax of block t: one thread a row.
 template <int D>
 __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, const Layout<D> sm, uint32_t tmem, int t,
@@ -932,6 +988,8 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
     const uint32_t s_col = tmem + ((uint32_t)(32 * warp) << 16) + t * kChunkTile;
     const uint32_t o_col = tmem + ((uint32_t)(32 * warp) << 16) + 2 * kChunkTile + t * D;
     int tile = 0, step = 0;                      // tiles of the CTA, steps of this block, counted through
+    auto mine = [&](const Item& it) { return kBlock * t + in_block < it.rows; };     // the thread has a row
+    auto fold_at = [&] { return (int64_t)blockIdx.x * w.fold_rows + kBlock * t + in_block; };
     // Waits for item i and asks for its queries, once the products with the last ones are done; says that they are there.
     bool asked = false;
     auto ask = [&](int i) {
@@ -983,6 +1041,10 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
                 continue;
             }
             tc_fence_after();
+            if (j % kFold == 0 && j > 0) {       // behind the scores, the block's products before them are done too
+                fold_row<D>(w.fold_ml + fold_at(), w.fold_acc + fold_at() * D, o_col, m, sum, j == kFold, mine(sm.read_item(i)));
+                sum = 0.0f;
+            }
             uint32_t u[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, u[c]);
@@ -1023,13 +1085,13 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
         uint32_t again = 0;
         if (working) {
             tc_fence_after();
+            if (count > kFold) sum += unfold_row<D>(w.fold_ml + fold_at(), w.fold_acc + fold_at() * D, o_col, m, mine(sm.read_item(i)));
             const Item it = sm.read_item(i);
-            const bool mine = kBlock * t + in_block < it.rows;
             const int r = it.r0 + kBlock * t + in_block;                 // row of the request
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             const int64_t row = (int64_t)(it.tok0 + (r >> g_log2)) * (a.h_kv << g_log2) + (it.head << g_log2) + (r & (a.g - 1));
             const int part = it.part + r - it.r0;
-            if (it.part >= 0 && mine) w.part_ml[part] = make_float2(m, sum);
+            if (it.part >= 0 && mine(it)) w.part_ml[part] = make_float2(m, sum);
             uint64_t probe = 0;                  // 0 * x of all channels: NaN where one is infinite or NaN
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -1042,7 +1104,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
                 }
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) probe = fma_f32x2(f32x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), 0ull, probe);
-                if (!mine) continue;
+                if (!mine(it)) continue;
                 if (it.part >= 0) {              // a part of a cut item, as it is
                     float* to = w.part_acc + (int64_t)part * D + c;
 #pragma unroll
@@ -1063,7 +1125,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
             tc_fence_before();
             float lo, hi;
             split_f32x2(probe, lo, hi);
-            again = __ballot_sync(0xffffffffu, lo + hi != 0.0f && mine);
+            again = __ballot_sync(0xffffffffu, lo + hi != 0.0f && mine(it));
         }
         if (lane == 0) w.odd[(int64_t)sm.read_item(i).self * 8 + 4 * t + warp] = again;
         __syncwarp();
@@ -1331,7 +1393,8 @@ cudaError_t launch(const ChunkArgs& a, const ChunkPlan& plan, void* workspace, i
     const Work w{plan.unit_cap <= kSelfUnits && a.batch <= kSelfUnits, num_sms, plan.unit_cap, plan.item_cap, plan.part_cap,
                  reinterpret_cast<Header*>(base), reinterpret_cast<int*>(base + plan.tiles),
                  reinterpret_cast<int2*>(base + plan.units), reinterpret_cast<Item*>(base + plan.items),
-                 reinterpret_cast<uint32_t*>(base + plan.odd), reinterpret_cast<float2*>(base + plan.part_ml), reinterpret_cast<float*>(base + plan.part_acc)};
+                 reinterpret_cast<uint32_t*>(base + plan.odd), reinterpret_cast<float2*>(base + plan.part_ml), reinterpret_cast<float*>(base + plan.part_acc),
+                 plan.fold_rows, reinterpret_cast<float2*>(base + plan.fold_ml), reinterpret_cast<float*>(base + plan.fold_acc)};
     const int grid = num_sms < plan.item_cap ? num_sms : plan.item_cap;
     if (!w.self) {
         e = launch_dependent(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a, w);
@@ -1355,7 +1418,8 @@ ChunkPlan plan_chunk(const Shape& s, int num_sms, int batch, int n) {
     // cutting at L tiles makes all / L more items at most, L half an SM's share or more; the pieces of cut items are
     // longer than L / 2
     p.item_cap = p.unit_cap * s.h_kv + 2 * num_sms;
-    p.part_cap = 4 * num_sms * (int)(rows < kChunkRows ? rows : kChunkRows);
+    p.fold_rows = (int)(rows < kChunkRows ? rows : kChunkRows);
+    p.part_cap = 4 * num_sms * p.fold_rows;
     size_t at = 0;
     auto place = [&](size_t bytes) {
         const size_t here = at;
@@ -1369,6 +1433,8 @@ ChunkPlan plan_chunk(const Shape& s, int num_sms, int batch, int n) {
     p.odd = place((size_t)p.item_cap * 8 * sizeof(uint32_t));
     p.part_ml = place((size_t)p.part_cap * sizeof(float2));
     p.part_acc = place((size_t)p.part_cap * s.d * sizeof(float));
+    p.fold_ml = place((size_t)num_sms * p.fold_rows * sizeof(float2));
+    p.fold_acc = place((size_t)num_sms * p.fold_rows * s.d * sizeof(float));
     p.total = at;
     return p;
 }

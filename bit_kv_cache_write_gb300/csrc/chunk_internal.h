@@ -34,7 +34,8 @@ struct ChunkPlan {
     int unit_cap;                            // row blocks of all requests at most
     int item_cap;                            // work items at most
     int part_cap;                            // rows of split items at most
-    size_t tiles, units, items, odd, part_ml, part_acc, total;
+    int fold_rows;                           // rows of an item at most
+    size_t tiles, units, items, odd, part_ml, part_acc, fold_ml, fold_acc, total;
 };
 struct ChunkArgs {
     const uint16_t* q; int64_t q_stride;     // token stride in elements

@@ -417,3 +417,56 @@ def test_calls_at_once(cuda):
     for args, c in zip(ready, cases):
         want, bound = chunk_oracle.extend(c.q, c.pool, c.tables, c.start, c.total, 1 / 8)
         assert (np.abs(args[5].double().cpu().numpy() - want) <= bound).all()
+
+
+def page_sums(q, pool):
+    """Per query head and page: the sums of 2^(q.k) and of 2^(q.k) v over each number of its first tokens, 0 .. 16."""
+    logits = torch.einsum("rd,ptd->rpt", q, pool[:, 0, 0].double())
+    w = torch.exp2(logits)
+    wv = torch.cumsum(w[..., None] * pool[:, 0, 1].double(), 2)
+    pad = torch.nn.functional.pad
+    return pad(torch.cumsum(w, 2), (1, 0)), pad(wv, (0, 0, 1, 0))
+
+
+@pytest.mark.parametrize("d,new,length", [(64, 70, 4_000_003), (128, 1, 1_500_000), (128, 150, 700_013)])
+def test_sums_of_millions(cuda, d, new, length):
+    """Requests enough that none is cut: an item's sums pass what the tensor core's accumulator holds without loss. The
+    logits are whole and rise by 12 on the way, so that what was added up before is scaled; the values are positive.
+
+    Of 512 tiles an accumulator takes 8 steps each, off by at most 9 * 2^-23 of it at that time, half the last one on
+    average: 512 * 8 * 9 / 2 * 2^-23 of the mean. The stretches' sums, and those of the weights, are rounded to nearest,
+    under 1,100 additions: 2^-13. Weights are powers of two. The output is rounded once: 2^-8."""
+    batch, h_q, pages = torch.cuda.get_device_properties(0).multi_processor_count, 2, 400
+    r = np.random.default_rng(d + new)
+    pool = r.integers(-3, 4, (pages, 1, 2, P, d)).astype(np.float64)
+    pool[pages // 2:, 0, 0] += 12.0
+    pool[:, 0, 1] = r.integers(128, 256, (pages, P, d)) / 128.0
+    pool = torch.from_numpy(pool).to(BF).to(cuda)
+    stride = -(-length // P)
+    gen = torch.Generator(device=cuda).manual_seed(new)
+    tables = torch.randint(0, pages // 2, (batch, stride), dtype=I32, device=cuda, generator=gen)
+    tables[1::2, stride // 3:] += pages // 2                 # the later pages of every other request weigh 2^12 as much
+    tables[0, 2 * stride // 3:] += pages // 2
+    q = torch.zeros(batch * new, h_q, d, dtype=BF, device=cuda)
+    q[:, 0, 5] = q[:, 1, d - 1] = 1.0
+    start = torch.arange(0, batch * new + 1, new, dtype=I32, device=cuda)
+    total = torch.full((batch,), length, dtype=I32, device=cuda)
+    out = torch.empty_like(q)
+    ctx = context(h_q, 1, d, sm_scale=math.log(2))
+    ws = torch.full((ctx.extend_bf16_workspace_size(batch, batch * new),), 255, dtype=torch.uint8, device=cuda)
+    ctx.extend_bf16(q, pool, tables, start, total, out, ws)
+    torch.cuda.synchronize()
+    assert ctx.debug_error()[0] == 0
+    w, wv = page_sums(q[0].double(), pool)
+    relative = 512 * 8 * 9 / 2 * 2.0 ** -23 + 2.0 ** -13
+    for b in range(batch):
+        for i in {0, new // 2, new - 1}:
+            seen = length - new + i + 1
+            count = torch.bincount(tables[b, :seen // P], minlength=pages).double()
+            sums, values = w[:, :, P] @ count, torch.einsum("rpd,p->rd", wv[:, :, P], count)
+            if seen % P:
+                last = int(tables[b, seen // P])
+                sums, values = sums + w[:, last, seen % P], values + wv[:, last, seen % P]
+            want = values / sums[:, None]
+            bound = relative * want + 2.0 ** -8 * want * (1 + relative)
+            assert ((out[b * new + i].double() - want).abs() <= bound).all(), (b, i)
