@@ -1079,6 +1079,9 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
             __syncwarp();
             if (lane == 0) mbar_arrive(sm.p_full(t));
         }
+        // a block without tokens waits for the loader through all of the other block's: a wait's limit for 2^18 of them
+        for (int k = count ? 0 : (tile - tile0) >> 18; k > 0 && !lds32(sm.fail()) && !mbar_over(sm.item_full(i + 1), sm.item_phase(i + 1)); --k)
+            sm.drain(sm.item_full(i + 1), sm.item_phase(i + 1));
         if (!early && !ask(i + 1)) return;
         there();
         if (count > 0 && !sm.wait(sm.o_done(t), (step - 1) & 1, a.dbg, 10000 + i)) return;

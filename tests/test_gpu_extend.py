@@ -470,3 +470,24 @@ def test_sums_of_millions(cuda, d, new, length):
             want = values / sums[:, None]
             bound = relative * want + 2.0 ** -8 * want * (1 + relative)
             assert ((out[b * new + i].double() - want).abs() <= bound).all(), (b, i)
+
+
+def test_items_of_more_than_a_second(cuda):
+    """The longest wait of a CTA's warps without rows is for a whole item of the others: here 1.3 million tiles."""
+    batch, d, pages = torch.cuda.get_device_properties(0).multi_processor_count, 64, 8
+    pool = torch.randint(128, 256, (pages, 1, 2, P, d), device=cuda).to(BF) / 128
+    stride = 10_500_000
+    tables = torch.zeros(batch, stride, dtype=I32, device=cuda)           # 6.4 GB
+    tables[:, ::2] = 3
+    q = torch.zeros(batch, 1, d, dtype=BF, device=cuda)
+    start = torch.arange(batch + 1, dtype=I32, device=cuda)
+    total = torch.full((batch,), stride * P, dtype=I32, device=cuda)
+    out = torch.empty_like(q)
+    ctx = context(1, 1, d)
+    ws = torch.empty(ctx.extend_bf16_workspace_size(batch, batch), dtype=torch.uint8, device=cuda)
+    ctx.extend_bf16(q, pool, tables, start, total, out, ws)
+    torch.cuda.synchronize()
+    assert ctx.debug_error()[0] == 0
+    want = pool[[0, 3], 0, 1].double().mean((0, 1))
+    relative = 512 * 8 * 9 / 2 * 2.0 ** -23 + 2.0 ** -12      # as above, with more stretches
+    assert ((out.double() - want).abs() <= (relative + 2.0 ** -8 * (1 + relative)) * want).all()
