@@ -1240,15 +1240,19 @@ __device__ __noinline__ void form_row(const ChunkArgs& a, const Item& it, int r,
             for (int c = 0; c < kChannels; ++c) acc[c] = f == 0.0f ? 0.0f : acc[c] * f;
         }
         const float p = there ? bf16_lo(bf16_pair(exp2_approx(x - m), 0.0f)) : 0.0f;
+        float sum32 = 0.0f, acc32[kChannels] = {};           // apart: a sum of 2^24 would take no more ones
         for (int i = 0; i < 32; ++i) {
             const float pi = __shfl_sync(0xffffffffu, p, i);
             const int64_t row = __shfl_sync(0xffffffffu, k_row, i) + kPage;
             if (pi == 0.0f) continue;
-            sum += pi;
+            sum32 += pi;
             const uint16_t* v = a.pool + row * D + lane * kChannels;
 #pragma unroll
-            for (int c = 0; c < kChannels; ++c) acc[c] += pi * __uint_as_float((uint32_t)v[c] << 16);
+            for (int c = 0; c < kChannels; ++c) acc32[c] += pi * __uint_as_float((uint32_t)v[c] << 16);
         }
+        sum += sum32;
+#pragma unroll
+        for (int c = 0; c < kChannels; ++c) acc[c] += acc32[c];
     }
     store_bf16(a.out + (token * (a.h_kv << g_log2) + q_head) * D + lane * kChannels, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
 }

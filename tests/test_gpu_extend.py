@@ -491,3 +491,48 @@ def test_items_of_more_than_a_second(cuda):
     want = pool[[0, 3], 0, 1].double().mean((0, 1))
     relative = 512 * 8 * 9 / 2 * 2.0 ** -23 + 2.0 ** -12      # as above, with more stretches
     assert ((out.double() - want).abs() <= (relative + 2.0 ** -8 * (1 + relative)) * want).all()
+
+
+def test_a_long_row_formed_again(cuda):
+    """A row that an infinity has reached, over more tokens than a sum of ones in fp32 counts to: 2^24 values of 1, then
+    as many of 2. Sums of 32 tokens are exact, those of 2^20 such sums off by 2^20 * 2^-24 at most; halved, as the sum of
+    weights is exact."""
+    d, length = 64, 1 << 25
+    pool = torch.zeros(3, 1, 2, P, d, dtype=BF, device=cuda)
+    pool[0, 0, 1], pool[1, 0, 1], pool[2, 0, 1] = 1, 2, 2
+    pool[2, 0, 1, 7, 5] = float("inf")
+    tables = torch.zeros(1, length // P, dtype=I32, device=cuda)
+    tables[0, length // P // 2:] = 1
+    tables[0, -1] = 2
+    q, start = torch.zeros(1, 1, d, dtype=BF, device=cuda), torch.tensor([0, 1], dtype=I32, device=cuda)
+    out, ctx = torch.empty_like(q), context(1, 1, d)
+    ws = torch.empty(ctx.extend_bf16_workspace_size(1, 1), dtype=torch.uint8, device=cuda)
+    ctx.extend_bf16(q, pool, tables, start, torch.tensor([length], dtype=I32, device=cuda), out, ws)
+    torch.cuda.synchronize()
+    assert ctx.debug_error()[0] == 0
+    got = out[0, 0].double()
+    assert torch.isposinf(got[5])
+    got[5] = 1.5
+    assert ((got - 1.5).abs() <= 1.5 * (2.0 ** -4 + 2.0 ** -8)).all()
+
+
+def test_largest_batch(cuda):
+    """65,535 requests, and nearly as many rows as a call takes: as many items for the plan, sampled."""
+    batch, new, d, pages = 65535, 256, 64, 512
+    n = batch * new
+    gen = torch.Generator(device=cuda).manual_seed(3)
+    lens = torch.randint(0, 40, (batch,), generator=gen, device=cuda, dtype=I32)
+    pool = torch.randn(pages, 1, 2, P, d, generator=gen, device=cuda).to(BF)
+    tables = torch.randint(0, pages, (batch, 19), generator=gen, device=cuda, dtype=I32)
+    q = torch.randn(n, 1, d, generator=gen, device=cuda, dtype=BF)
+    start = torch.arange(0, n + 1, new, dtype=I32, device=cuda)
+    out, ctx = torch.full_like(q, 7.0), context(1, 1, d)
+    ws = torch.full((ctx.extend_bf16_workspace_size(batch, n),), 255, dtype=torch.uint8, device=cuda)
+    ctx.extend_bf16(q, pool, tables, start, lens + new, out, ws)
+    torch.cuda.synchronize()
+    assert ctx.debug_error()[0] == 0
+    for b in [0, 1, 777, 32768, 65000, batch - 1]:
+        rows = slice(b * new, (b + 1) * new)
+        want, bound = chunk_oracle.extend(q[rows].double().cpu().numpy(), pool.double().cpu().numpy(), tables[b:b + 1].cpu().numpy(),
+                                          [0, new], [int(lens[b]) + new], 1 / 8)
+        assert (np.abs(out[rows].double().cpu().numpy() - want) <= bound).all(), b
