@@ -8,12 +8,12 @@
 // One CTA an SM takes work items: 256 query rows (two blocks of 128) against a range of 128-token tiles of the cache.
 //   warp 8      loads: K and V pages through TMA (page ids looked up four tiles at a time), 128-byte swizzle;
 //   warp 9      issues tcgen05.mma: S = Q K^T (128 x 128 x d) into tensor memory, O += P V with P read from tensor
-//               memory; a block's next S is issued behind its P V, so the softmax of one block runs under the
-//               matrix products of the other;
+//               memory; at d = 128 a block's next S is issued behind its P V, so the softmax of one block runs under
+//               the matrix products of the other, at d = 64 as soon as the last S is in registers;
 //   warps 0..7  one warp group a block, a thread a row: the row's 128 logits in registers, weights rounded to bf16
-//               over the logits' own columns, O scaled only where the reference rises.
+//               over the logits' own columns or beside them, O scaled only where the reference rises.
 // At d = 128 logits and outputs of two blocks are all of tensor memory (512 columns): P has to lie over S, and a block's
-// next S to wait for its P V. The weights' rounding to bf16 is the operand type of the product (a second piece would
+// next S to wait for its P V; at d = 64 there is room for P beside it. The weights' rounding to bf16 is the operand type of the product (a second piece would
 // cost half again of the tensor time that bounds long prompts); their sum is of the unrounded ones, in fp32.
 //
 // What bounds it (32 query and 8 KV heads of 128 on one GB300): long prompts the tensor cores and the power, 8,192 tokens
@@ -353,13 +353,18 @@ struct Layout {
     static constexpr int kOffKv = 2 * kTileBytes;              // behind the two query blocks
     static constexpr int kOffItem = kOffKv + kStages * kTileBytes;
     static constexpr int kOffBar = kOffItem + kItemRing * (int)sizeof(Item);
-    static constexpr int kBars = 2 * kStages + 2 * 4 + 1 + 2 * kItemRing;
+    static constexpr int kBars = 2 * kStages + 2 * 5 + 1 + 2 * kItemRing;
     static constexpr int kOffMask = kOffBar + 8 * kBars;
     static constexpr int kOffTmem = kOffMask + 4 * kMaskRing;
     static constexpr int kOffFail = kOffTmem + 4;
     static constexpr int kOffPlan = kOffFail + 12;
     static constexpr int kBytes = kOffPlan + 28 * kSelfUnits + 24;
     static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
+    // Columns of tensor memory: logits of the two blocks, outputs, and weights, beside the logits where there is room
+    static constexpr bool kBeside = 2 * kChunkTile + 2 * D + kChunkTile <= 512;
+    __device__ static constexpr int s_col(int t) { return t * kChunkTile; }
+    __device__ static constexpr int o_col(int t) { return 2 * kChunkTile + t * D; }
+    __device__ static constexpr int p_col(int t) { return kBeside ? 2 * kChunkTile + 2 * D + t * (kChunkTile / 2) : s_col(t); }
 
     uint32_t base;
     __device__ uint32_t q(int t) const { return base + t * kTileBytes; }
@@ -377,9 +382,10 @@ struct Layout {
     __device__ uint32_t s_full(int t) const { return bar(2 * kStages + 2 + t); }
     __device__ uint32_t p_full(int t) const { return bar(2 * kStages + 4 + t); }
     __device__ uint32_t o_done(int t) const { return bar(2 * kStages + 6 + t); }
-    __device__ uint32_t last() const { return bar(2 * kStages + 8); }
-    __device__ uint32_t item_full(int i) const { return bar(2 * kStages + 9 + i % kItemRing); }
-    __device__ uint32_t item_empty(int i) const { return bar(2 * kStages + 9 + kItemRing + i % kItemRing); }
+    __device__ uint32_t s_read(int t) const { return bar(2 * kStages + 8 + t); }
+    __device__ uint32_t last() const { return bar(2 * kStages + 10); }
+    __device__ uint32_t item_full(int i) const { return bar(2 * kStages + 11 + i % kItemRing); }
+    __device__ uint32_t item_empty(int i) const { return bar(2 * kStages + 11 + kItemRing + i % kItemRing); }
     __device__ static uint32_t item_phase(int i) { return i / kItemRing & 1; }
 
     // A role that gives up: the others stop at their next wait.
@@ -768,16 +774,36 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> s
     const int g_log2 = 31 - __clz(a.g);
     const uint32_t leader = elected();
     int slot = 0;
-    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+    uint32_t q_phase[2] = {0, 0};
+    int steps[2] = {0, 0};                                   // of each block, before the item
     bool ok = true, issued = false;
     auto scores = [&](int t, int k_slot) {                   // S of block t
         const uint32_t qd = sw128_desc(sm.q(t), 0), kd = sw128_desc(sm.kv(k_slot), 0);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = ((ks / 4) * L::kHalfBytes + (ks % 4) * 32) >> 4;
-            umma_ss(leader, tmem + t * kChunkTile, qd + off, kd + off, kScores, ks > 0);
+            umma_ss(leader, tmem + L::s_col(t), qd + off, kd + off, kScores, ks > 0);
         }
         umma_commit(leader, sm.s_full(t));
+    };
+    auto values = [&](int t, int v_slot, int j) {            // O of block t: tile j of the item
+        const uint32_t vd = sw128_desc(sm.kv(v_slot), L::kHalfBytes), p = tmem + L::p_col(t);
+#pragma unroll
+        for (int k16 = 0; k16 < kTilePages; ++k16)
+            umma_ts(leader, tmem + L::o_col(t), p + k16 * 8, vd + k16 * (2048 >> 4), kValues, j % kFold > 0 || k16 > 0);
+        umma_commit(leader, sm.o_done(t));
+    };
+    // V of tile j, without what may lie behind the sequence on its last page
+    auto clean_values = [&](const Item& it, int v_slot, int j) {
+        const int tail = it.total % kPage;
+        if (tail && it.kv0 + j == it.total / kChunkTile) {
+            const int left = kPage - tail;
+            const uint32_t to = sm.kv(v_slot) + it.total % kChunkTile * 128;
+            for (int c = lane; c < left * 8 * L::kHalves; c += 32)
+                sts128(to + c / (left * 8) * L::kHalfBytes + c % (left * 8) * 16, make_uint4(0, 0, 0, 0));
+            fence_async();
+            __syncwarp();
+        }
     };
     for (int i = 0; ok; ++i) {
         ok = sm.wait(sm.item_full(i), sm.item_phase(i), a.dbg, 2000 + i);
@@ -804,48 +830,78 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> s
         }
         if (!ok) break;
         umma_commit(leader, sm.kv_empty(k0));
-        for (int j = 0; j < count && ok; ++j) {
-            const int vs = slot++;
-            ok = sm.wait(sm.kv_full(vs), sm.kv_phase(vs), a.dbg, 5000 + i);
-            if (!ok) break;
-            const int tail = it.total % kPage;
-            if (tail && it.kv0 + j == it.total / kChunkTile) {
-                // rows of the last page behind the sequence may hold anything: zeros for the product
-                const int left = kPage - tail;
-                const uint32_t to = sm.kv(vs) + it.total % kChunkTile * 128;
-                for (int c = lane; c < left * 8 * L::kHalves; c += 32)
-                    sts128(to + c / (left * 8) * L::kHalfBytes + c % (left * 8) * 16, make_uint4(0, 0, 0, 0));
-                fence_async();
-                __syncwarp();
-            }
-            const bool more = j + 1 < count;
-            const int kn = more ? slot++ : 0;
-            bool here = false;                               // K of the next tile
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (j < bl.count[t]) {
-                    ok = sm.wait(sm.p_full(t), p_phase[t], a.dbg, 7000 + i);
-                    p_phase[t] ^= 1;
+        if constexpr (L::kBeside) {
+            // A block's next logits follow once the last ones are in registers, and its outputs half a step behind the
+            // other block's (8,192 tokens of 32 heads of 64: 254 us, 292 in the order below).
+            int vs = 0, v_last = 0;                          // V of this tile and of the one before
+            for (int j = 0; j <= count && ok; ++j) {
+                v_last = vs;
+                if (j < count) vs = slot++;
+                const bool more = j + 1 < count;
+                const int kn = more ? slot++ : 0;
+                if (more) ok = sm.wait(sm.kv_full(kn), sm.kv_phase(kn), a.dbg, 6000 + i);
+                if (ok && j + 1 < bl.count[0]) {
+                    ok = sm.wait(sm.s_read(0), steps[0] + j & 1, a.dbg, 7000 + i);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t vd = sw128_desc(sm.kv(vs), L::kHalfBytes), o = tmem + 2 * kChunkTile + t * D;
-                    const uint32_t p = tmem + t * kChunkTile;
-#pragma unroll
-                    for (int k16 = 0; k16 < kTilePages; ++k16)
-                        umma_ts(leader, o, p + k16 * 8, vd + k16 * (2048 >> 4), kValues, j % kFold > 0 || k16 > 0);
-                    umma_commit(leader, sm.o_done(t));
+                    scores(0, kn);
                 }
-                if (t == 1) umma_commit(leader, sm.kv_empty(vs));
-                if (j + 1 < bl.count[t]) {
-                    if (!here) ok = sm.wait(sm.kv_full(kn), sm.kv_phase(kn), a.dbg, 6000 + i);
-                    here = true;
+                if (ok && j > 0 && j <= bl.count[1]) {
+                    ok = sm.wait(sm.p_full(1), steps[1] + j + 1 & 1, a.dbg, 7000 + i);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(t, kn);
+                    values(1, v_last, j - 1);
+                }
+                if (ok && j > 0) umma_commit(leader, sm.kv_empty(v_last));
+                if (ok && j + 1 < bl.count[1]) {
+                    ok = sm.wait(sm.s_read(1), steps[1] + j & 1, a.dbg, 7000 + i);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(1, kn);
+                }
+                if (ok && more) umma_commit(leader, sm.kv_empty(kn));
+                if (!ok || j == count) break;
+                ok = sm.wait(sm.kv_full(vs), sm.kv_phase(vs), a.dbg, 5000 + i);
+                if (!ok) break;
+                clean_values(it, vs, j);
+                if (j < bl.count[0]) {
+                    ok = sm.wait(sm.p_full(0), steps[0] + j & 1, a.dbg, 7000 + i);
+                    if (!ok) break;
+                    tc_fence_after();
+                    values(0, vs, j);
                 }
             }
-            if (ok && more) umma_commit(leader, sm.kv_empty(kn));
+        } else {
+            for (int j = 0; j < count && ok; ++j) {
+                const int vs = slot++;
+                ok = sm.wait(sm.kv_full(vs), sm.kv_phase(vs), a.dbg, 5000 + i);
+                if (!ok) break;
+                clean_values(it, vs, j);
+                const bool more = j + 1 < count;
+                const int kn = more ? slot++ : 0;
+                bool here = false;                           // K of the next tile
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (j < bl.count[t]) {
+                        ok = sm.wait(sm.p_full(t), steps[t] + j & 1, a.dbg, 7000 + i);
+                        if (!ok) break;
+                        tc_fence_after();
+                        values(t, vs, j);
+                    }
+                    if (t == 1) umma_commit(leader, sm.kv_empty(vs));
+                    if (j + 1 < bl.count[t]) {
+                        if (!here) ok = sm.wait(sm.kv_full(kn), sm.kv_phase(kn), a.dbg, 6000 + i);
+                        here = true;
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(t, kn);
+                    }
+                }
+                if (ok && more) umma_commit(leader, sm.kv_empty(kn));
+            }
         }
+        steps[0] += bl.count[0];
+        steps[1] += bl.count[1];
     }
     // the last matrix products are done before tensor memory is freed
     if (issued) {
@@ -985,8 +1041,10 @@ template <int D>
 __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, const Layout<D> sm, uint32_t tmem, int t,
                                              int warp, int lane) {
     const int g_log2 = 31 - __clz(a.g), in_block = warp * 32 + lane;
-    const uint32_t s_col = tmem + ((uint32_t)(32 * warp) << 16) + t * kChunkTile;
-    const uint32_t o_col = tmem + ((uint32_t)(32 * warp) << 16) + 2 * kChunkTile + t * D;
+    using L = Layout<D>;
+    const uint32_t s_col = tmem + ((uint32_t)(32 * warp) << 16) + L::s_col(t);
+    const uint32_t o_col = tmem + ((uint32_t)(32 * warp) << 16) + L::o_col(t);
+    const uint32_t p_col = tmem + ((uint32_t)(32 * warp) << 16) + L::p_col(t);
     int tile = 0, step = 0;                      // tiles of the CTA, steps of this block, counted through
     auto mine = [&](const Item& it) { return kBlock * t + in_block < it.rows; };     // the thread has a row
     auto fold_at = [&] { return (int64_t)blockIdx.x * w.fold_rows + kBlock * t + in_block; };
@@ -1036,12 +1094,19 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
                 if (!ask(i + 1)) return;
                 early = true;
             }
+            // The block's products before these logits, which read the weights and add to the outputs: done with the
+            // logits where those were asked for behind them, else waited for.
+            auto done = [&] { return !L::kBeside || j == 0 || sm.wait(sm.o_done(t), (step - 1) & 1, a.dbg, 10000 + i); };
             if (!working) {                      // no row of this warp is any: what its lanes hold as weights reaches nothing
+                if (L::kBeside && lane == 0) mbar_arrive(sm.s_read(t));
+                if (!done()) return;             // nor may it be a step ahead
                 if (lane == 0) mbar_arrive(sm.p_full(t));
                 continue;
             }
             tc_fence_after();
-            if (j % kFold == 0 && j > 0) {       // behind the scores, the block's products before them are done too
+            if (j % kFold == 0 && j > 0) {
+                if (!done()) return;
+                tc_fence_after();
                 fold_row<D>(w.fold_ml + fold_at(), w.fold_acc + fold_at() * D, o_col, m, sum, j == kFold, mine(sm.read_item(i)));
                 sum = 0.0f;
             }
@@ -1052,6 +1117,11 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
             const bool hidden = __any_sync(0xffffffffu, seen < kChunkTile || mask != 0xff);
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_wait(u[c]);
+            if (L::kBeside) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sm.s_read(t));
+            }
             if (hidden) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) hide(u[c], seen - 32 * c, mask >> 2 * c);
@@ -1060,20 +1130,25 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
 #pragma unroll
             for (int c = 0; c < 4; ++c) high = max32(u[c], high);
             high *= a.scale_log2;
+            // Here, not where the weights are stored: that keeps the blocks apart, one finding its largest logits while the
+            // other forms weights (8,192 tokens of 32 heads of 64: 254 us; 284 to 288 with the wait at the store or in
+            // front of the logits, where both blocks fall into step)
+            if (!done()) return;
+            if (L::kBeside) tc_fence_after();
             const bool rise = high > m + kHeadroom;
             if (__any_sync(0xffffffffu, rise)) {
                 const float to = rise ? high : m, f = exp2_approx(m - to);
                 m = to;
                 sum *= f;
-                if (j > 0) {                     // behind the scores, the block's products before them are done too
+                if (j > 0) {
 #pragma unroll 1
                     for (int c = 0; c < D; c += 8) tmem_scale8(o_col + c, f);
                 }
             }
             uint32_t pk[2][32];
             sum += weigh128(u, f32x2(a.scale_log2, a.scale_log2), f32x2(-m, -m), pk);
-            tmem_st32(s_col, pk[0]);             // over logits that the thread has read
-            tmem_st32(s_col + 32, pk[1]);
+            tmem_st32(p_col, pk[0]);             // at most over logits that the thread has read
+            tmem_st32(p_col + 32, pk[1]);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -1154,6 +1229,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attend_kernel(const __grid_
             mbar_init(sm.s_full(t), 1);
             mbar_init(sm.p_full(t), kSoftmaxWarps / 2);
             mbar_init(sm.o_done(t), 1);
+            mbar_init(sm.s_read(t), kSoftmaxWarps / 2);
         }
         for (int i = 0; i < kItemRing; ++i) {
             mbar_init(sm.item_full(i), 1);
