@@ -1277,22 +1277,24 @@ __device__ __forceinline__ void store_bf16(uint16_t* to, const float (&x)[N], fl
     for (int c = 0; c < N; c += 2) *reinterpret_cast<uint32_t*>(to + c) = bf16_pair(x[c] * f, x[c + 1] * f);
 }
 
-// Row r of an item's request from the beginning, 32 tokens at a time by the whole warp, with the tokens alone that it
-// sees: for rows that an infinity or NaN has reached, its own or one behind it.
+// Row r of a request from the beginning, 32 tokens at a time by the whole warp, with the tokens alone that it sees: for
+// rows that an infinity or NaN has reached, its own or one behind it. The item's fields come by value: by reference the item
+// lies in local memory, which costs the shortest calls 1.3 us of 11.
 template <int D>
-__device__ __noinline__ void form_row(const ChunkArgs& a, const Item& it, int r, int lane) {
+__device__ __noinline__ void form_row(const ChunkArgs& a, int b, int head, int tok0, int pos0, int total, int r,
+                                      int lane) {
     constexpr int kChannels = D / 32;
-    const int g_log2 = 31 - __clz(a.g), limit = min(limit_of(r, it.pos0, g_log2), it.total);
-    const int64_t token = it.tok0 + (r >> g_log2);
-    const int q_head = (it.head << g_log2) + (r & (a.g - 1));
+    const int g_log2 = 31 - __clz(a.g), limit = min(limit_of(r, pos0, g_log2), total);
+    const int64_t token = tok0 + (r >> g_log2);
+    const int q_head = (head << g_log2) + (r & (a.g - 1));
     const uint16_t* q = a.q + token * a.q_stride + q_head * D;
-    const int32_t* table = a.tables + (int64_t)it.b * a.stride;
+    const int32_t* table = a.tables + (int64_t)b * a.stride;
     float m = kNoReference, sum = 0.0f, acc[kChannels] = {};
     for (int t0 = 0; t0 < limit; t0 += 32) {
         const int t = t0 + lane;
         const int id = t < limit ? table[t / kPage] : -1;
         const bool there = id >= 0 && id < a.pages;
-        const int64_t k_row = ((int64_t)(there ? id : 0) * a.h_kv + it.head) * 2 * kPage + t % kPage;
+        const int64_t k_row = ((int64_t)(there ? id : 0) * a.h_kv + head) * 2 * kPage + t % kPage;
         float x = -INFINITY;
         if (there) {
             float dot = 0.0f;
@@ -1371,7 +1373,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
             if (it.part >= 0 || !sane(a, w, it, (int)(at / 8), g_log2)) continue;
             for (uint32_t todo = marked; todo; todo &= todo - 1) {
                 const int local = 32 * (int)(at % 8) + __ffs(todo) - 1;
-                if (local < it.rows) form_row<D>(a, it, it.r0 + local, lane);
+                if (local < it.rows) form_row<D>(a, it.b, it.head, it.tok0, it.pos0, it.total, it.r0 + local, lane);
             }
         }
     }
@@ -1427,7 +1429,7 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
             }
             const int r = it.r0 + local;
             if (__any_sync(0xffffffffu, again)) {
-                form_row<D>(a, it, r, lane);
+                form_row<D>(a, it.b, it.head, it.tok0, it.pos0, it.total, r, lane);
                 continue;
             }
             const int64_t row = (int64_t)(it.tok0 + (r >> g_log2)) * (a.h_kv << g_log2) + (it.head << g_log2) + (r & (a.g - 1));
