@@ -13,14 +13,16 @@
 //   warps 0..7  one warp group a block, a thread a row: the row's 128 logits in registers, weights rounded to bf16
 //               over the logits' own columns or beside them, O scaled only where the reference rises.
 // At d = 128 logits and outputs of two blocks are all of tensor memory (512 columns): P has to lie over S, and a block's
-// next S to wait for its P V; at d = 64 there is room for P beside it. The weights' rounding to bf16 is the operand type of the product (a second piece would
-// cost half again of the tensor time that bounds long prompts); their sum is of the unrounded ones, in fp32.
+// next S to wait for its P V; at d = 64 there is room for P beside it. The weights' rounding to bf16 is the operand type
+// of the product (a second piece would cost half again of the tensor time that bounds long prompts); their sum is of the
+// unrounded ones, in fp32.
 //
 // What bounds it (32 query and 8 KV heads of 128 on one GB300): long prompts the tensor cores and the power, 8,192 tokens
-// in 344 us = 1.60 PFLOP/s, 84 % of the measured rate of a large matrix product; the softmax of a block takes 1,250 cycles
-// a tile, its two products 1,024, of two blocks' 2,048. Few rows HBM: 1 to 8 tokens of 32 requests of 4k to 32k in
-// 280 us = 6.5 TB/s, 97 % of the measured copy rate; a lone row block (8 tokens at 100,000, 74.7 us) 81 %, by the parts'
-// writing and join and the items' starts. Short ones the chain of launch, plan, loads, softmax and join: 10.6 us.
+// in 346 us = 1.59 PFLOP/s, 83 % of the measured rate of a large matrix product; the softmax of a block takes 1,250 cycles
+// a tile, its two products 1,024, of two blocks' 2,048. At d = 64 (255 us) the softmax, of which two blocks share the ex2
+// (1,024 cycles) and all else. Few rows HBM: 1 to 8 tokens of 32 requests of 4k to 32k in 280 us = 6.5 TB/s, 97 % of the
+// measured copy rate; a lone row block (8 tokens at 100,000, 74.7 us) 81 %, by the parts' writing and join and the items'
+// starts. Short ones the chain of launch, plan, loads, softmax and join: 11 us.
 //
 // Items of requests with long caches and few rows are cut along the cache, by a plan from the lengths on the device, so
 // that the items fill the SMs evenly: for few row blocks every loader plans for itself, for many chunk_plan_kernel does;
