@@ -1280,7 +1280,8 @@ __device__ __forceinline__ void store_bf16(uint16_t* to, const float (&x)[N], fl
 }
 
 // Row r of a request from the beginning, 32 tokens at a time by the whole warp, with the tokens alone that it sees: for
-// rows that an infinity or NaN has reached, its own or one behind it. The item's fields come by value: by reference the item
+// rows that an infinity or NaN has reached, its own or one behind it, or whose sum of finite values has passed fp32: the
+// values are added in units of 2^31, more than there are tokens. The item's fields come by value: by reference the item
 // lies in local memory, which costs the shortest calls 1.3 us of 11.
 template <int D>
 __device__ __noinline__ void form_row(const ChunkArgs& a, int b, int head, int tok0, int pos0, int total, int r,
@@ -1328,13 +1329,13 @@ __device__ __noinline__ void form_row(const ChunkArgs& a, int b, int head, int t
             sum32 += pi;
             const uint16_t* v = a.pool + row * D + lane * kChannels;
 #pragma unroll
-            for (int c = 0; c < kChannels; ++c) acc32[c] += pi * __uint_as_float((uint32_t)v[c] << 16);
+            for (int c = 0; c < kChannels; ++c) acc32[c] += pi * (__uint_as_float((uint32_t)v[c] << 16) * 0x1p-31f);
         }
         sum += sum32;
 #pragma unroll
         for (int c = 0; c < kChannels; ++c) acc[c] += acc32[c];
     }
-    store_bf16(a.out + (token * (a.h_kv << g_log2) + q_head) * D + lane * kChannels, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
+    store_bf16(a.out + (token * (a.h_kv << g_log2) + q_head) * D + lane * kChannels, acc, sum == 0.0f ? 0.0f : 0x1p31f / sum);
 }
 
 // Whether an item's indexes lie within the call's buffers: a CTA that gave up leaves entries of the list unwritten.
@@ -1430,7 +1431,10 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
                 }
             }
             const int r = it.r0 + local;
-            if (__any_sync(0xffffffffu, again)) {
+            float probe = 0.0f;                  // NaN where the parts' sum is infinite
+#pragma unroll
+            for (int c = 0; c < kChannels; ++c) probe += acc[c] * 0.0f;
+            if (__any_sync(0xffffffffu, again || probe != 0.0f)) {
                 form_row<D>(a, it.b, it.head, it.tok0, it.pos0, it.total, r, lane);
                 continue;
             }

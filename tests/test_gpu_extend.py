@@ -189,6 +189,16 @@ def test_infinite_values(cuda):
     assert (np.abs(got - want) <= bound).all()
 
 
+@pytest.mark.parametrize("lens,h_q,h_kv,d", [([(0, 300), (40, 3)], 4, 2, 64), ([(9000, 2)], 8, 1, 128), ([(5000, 150)], 2, 1, 64)])
+def test_values_whose_sum_passes_fp32(cuda, lens, h_q, h_kv, d):
+    """Their mean does not. Rows of one item and of parts; a channel of the largest numbers and one of ordinary ones."""
+    c = Case(lens, h_q, h_kv, d, seed=21)
+    c.pool[:, :, 1] = bf16(c.pool[:, :, 1] * 2.0 ** 122)
+    c.pool[:, :, 1, :, 3] = float(torch.finfo(BF).max)
+    c.pool[:, :, 1, :, 4] = bf16(np.random.default_rng(1).normal(0, 1, c.pool.shape[:2] + (P,)))
+    c.check(c.run(cuda))
+
+
 def test_large_logits(cuda):
     """Logits far apart: references that rise again and again, weights that vanish."""
     for spread in (30.0, 1000.0):
