@@ -49,6 +49,7 @@ constexpr int kThreads = 384;                    // two softmax warp groups, one
 constexpr int kItemRing = 4;                     // items that the loader may be ahead with the others
 constexpr int kMaskRing = 16;                    // tiles whose page masks are kept: more than the loader is ahead
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanCtas = 8;
 constexpr int kSelfUnits = 80;                   // row blocks and requests up to which each loader plans for itself
 constexpr int kJoinThreads = 256;
 constexpr float kNoReference = -3.402823466e38f; // reference before any token: no finite logit is below it
@@ -158,6 +159,8 @@ __device__ __forceinline__ int piece_length(int i, int share, int longest) {
     return i == 31 ? max(longest, 1) : max(1, (int)ceilf((float)share * exp2f(1.0f - (float)i / 15.0f)));
 }
 __device__ __forceinline__ int pieces_of(int tiles, int len) { return max(1, (tiles + len - 1) / len); }
+// The same for what a plan costs, by 1 / len: exact below 2^21 tiles, one off at most beyond.
+__device__ __forceinline__ int about_pieces(int tiles, int len, float inv) { return max(1, (int)(((float)(tiles + len - 1) + 0.5f) * inv)); }
 __device__ __forceinline__ float cost_of(int pieces, int parts, int len, float all, const ChunkArgs& a, int sms) {
     const float one = (float)(len + kStart);
     return fminf((float)((pieces + sms - 1) / sms) * one, (all + (float)kStart * (float)pieces) / (float)sms + one) +
@@ -205,8 +208,9 @@ __device__ __forceinline__ Item item_of(const ChunkArgs& a, const Unit& u, int p
     it.pos0 = u.pos0;
     it.piece = rest / a.h_kv;
     it.pieces = p;
-    it.kv0 = p > 1 ? (int)((long long)tiles * it.piece / p) : 0;
-    it.kv1 = p > 1 ? (int)((long long)tiles * (it.piece + 1) / p) : tiles;
+    // at most 2^23 tiles in two pieces an SM and one: below 2^32 up to 255 SMs
+    it.kv0 = p > 1 ? (int)((unsigned)tiles * it.piece / (unsigned)p) : 0;
+    it.kv1 = p > 1 ? (int)((unsigned)tiles * (it.piece + 1) / (unsigned)p) : tiles;
     it.total = u.total;
     it.part = p > 1 ? min(part + (it.head * p + it.piece) * it.rows, part_cap - it.rows) : -1;
     it.self = self;
@@ -215,8 +219,9 @@ __device__ __forceinline__ Item item_of(const ChunkArgs& a, const Unit& u, int p
     return it;
 }
 
-// Work items from the lengths, by one CTA; each warp tries one L. Requests and row blocks are held in shared memory where
-// they fit, else read again.
+// Work items from the lengths; each warp tries one L. Requests and row blocks are held in shared memory where they fit, else
+// read again. Every CTA makes the whole plan (and writes the same words of it), but only its share of the items: an SM takes
+// 3 us to write a thousand.
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArgs a, const Work w) {
     __shared__ int shared[32];
     __shared__ long long sum;
@@ -278,9 +283,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     const int share = share_of(all, sms);
     {
         const int len = min(piece_length(warp, share, longest), max(longest, 1));
+        const float inv = 1.0f / (float)len;
         int pieces = 0, parts = 0;
         for (int u = lane; u < units; u += 32) {
-            const int p = pieces_of(tiles_of(unit[u].y), len);
+            const int p = about_pieces(tiles_of(unit[u].y), len, inv);
             pieces += p;
             if (p > 1) parts += p * rows_of(unit[u].y);
         }
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         first_part[tid] = block_scan(rows, shared, parts);
         __syncthreads();
         items = min(items, w.item_cap - item_base);
-        for (int i = tid; i < items; i += kPlanThreads) {
+        for (int i = (warp * gridDim.x + blockIdx.x) * 32 + lane; i < items; i += kPlanThreads * gridDim.x) {
             const int at = last_at_most(first_item, min(kPlanThreads, units - u0), i);
             const int2 here = unit[u0 + at];
             const Request r = request_at(here.x);
@@ -340,7 +346,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         part_base += parts;
         __syncthreads();
     }
-    if (tid == 0) *w.head = Header{item_base, 0, part_base > 0};
+    if (tid == 0 && blockIdx.x == 0) *w.head = Header{item_base, 0, part_base > 0};
 }
 
 // ---- attention ----------------------------------------------------------------------------------------------
@@ -1479,7 +1485,7 @@ cudaError_t launch(const ChunkArgs& a, const ChunkPlan& plan, void* workspace, i
     if (e != cudaSuccess) return e;
     char* base = static_cast<char*>(workspace);
     // Few row blocks: every loader plans by itself, 2 us for a few (five tokens at 1,344: 10.5 us in all, 16.5 with the
-    // kernel in front); its loops grow with them, and it has shared memory for 80. The kernel takes 9 to 12 us for 100
+    // kernel in front); its loops grow with them, and it has shared memory for 80. The kernel takes 7 to 9 us for 100
     // to 200 row blocks, and its items go to whichever CTA is free.
     const Work w{plan.unit_cap <= kSelfUnits && a.batch <= kSelfUnits, num_sms, plan.unit_cap, plan.item_cap, plan.part_cap,
                  reinterpret_cast<Header*>(base), reinterpret_cast<int*>(base + plan.tiles),
@@ -1488,7 +1494,7 @@ cudaError_t launch(const ChunkArgs& a, const ChunkPlan& plan, void* workspace, i
                  plan.fold_rows, reinterpret_cast<float2*>(base + plan.fold_ml), reinterpret_cast<float*>(base + plan.fold_acc)};
     const int grid = num_sms < plan.item_cap ? num_sms : plan.item_cap;
     if (!w.self) {
-        e = launch_dependent(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1, a, w);
+        e = launch_dependent(chunk_plan_kernel, dim3(kPlanCtas), dim3(kPlanThreads), 0, st, 1, a, w);
         if (e != cudaSuccess) return e;
     }
     e = launch_dependent(chunk_attend_kernel<D>, dim3(grid), dim3(kThreads), L::kBytes, st, 1, a, w, map);
