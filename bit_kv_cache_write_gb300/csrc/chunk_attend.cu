@@ -997,6 +997,9 @@ __device__ __forceinline__ float weigh128(uint32_t (&u)[4][32], uint64_t scale, 
 // are therefore added, rounded to nearest, to a row in the workspace, and begin anew; at the end they come back. An
 // accumulator is short by 0.04 % then, and 512 tiles take some 600 us, the addition some 5.
 //
+// Instructions on tensor memory want the warp's lanes together: where some have a row and others none, they meet again
+// in front of each (here and where outputs are stored).
+//
 // Adds a thread's row of outputs (reference m, sum) to its folded ones, the first time over them. `there`: whether the
 // thread has a row; tensor memory is read by the whole warp.
 template <int D>
@@ -1006,15 +1009,17 @@ __device__ __noinline__ void fold_row(float2* ml, float* acc, uint32_t o_col, fl
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
+        __syncwarp();
         tmem_read32(o_col + c, o);
-        if (!there) continue;
+        if (there) {
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-            float4* at = reinterpret_cast<float4*>(acc + c + k);
-            float4 x = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *at;
-            x.x = fmaf(x.x, f, __uint_as_float(o[k])); x.y = fmaf(x.y, f, __uint_as_float(o[k + 1]));
-            x.z = fmaf(x.z, f, __uint_as_float(o[k + 2])); x.w = fmaf(x.w, f, __uint_as_float(o[k + 3]));
-            *at = x;
+            for (int k = 0; k < 32; k += 4) {
+                float4* at = reinterpret_cast<float4*>(acc + c + k);
+                float4 x = first ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *at;
+                x.x = fmaf(x.x, f, __uint_as_float(o[k])); x.y = fmaf(x.y, f, __uint_as_float(o[k + 1]));
+                x.z = fmaf(x.z, f, __uint_as_float(o[k + 2])); x.w = fmaf(x.w, f, __uint_as_float(o[k + 3]));
+                *at = x;
+            }
         }
     }
     if (there) *ml = make_float2(m, fmaf(old.y, f, sum));
@@ -1027,6 +1032,7 @@ __device__ __noinline__ float unfold_row(const float2* ml, const float* acc, uin
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
+        __syncwarp();
         tmem_read32(o_col + c, o);
         if (there) {
 #pragma unroll
@@ -1038,6 +1044,7 @@ __device__ __noinline__ float unfold_row(const float2* ml, const float* acc, uin
                 o[k + 3] = __float_as_uint(fmaf(x.w, f, __uint_as_float(o[k + 3])));
             }
         }
+        __syncwarp();
         tmem_st32(o_col + c, o);
     }
     tmem_wait_st();
@@ -1133,6 +1140,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
             if (hidden) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) hide(u[c], seen - 32 * c, mask >> 2 * c);
+                __syncwarp();
             }
             float high = -INFINITY;
 #pragma unroll
@@ -1182,6 +1190,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
+                __syncwarp();
                 if (count > 0) {
                     tmem_read32(o_col + c, o);
                 } else {
@@ -1190,12 +1199,11 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
                 }
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) probe = fma_f32x2(f32x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), 0ull, probe);
-                if (!mine(it)) continue;
-                if (it.part >= 0) {              // a part of a cut item, as it is
+                if (mine(it) && it.part >= 0) {  // a part of a cut item, as it is
                     float* to = w.part_acc + (int64_t)part * D + c;
 #pragma unroll
                     for (int k = 0; k < 32; k += 8) store32(to + k, o + k);
-                } else {
+                } else if (mine(it)) {
                     uint32_t y[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
@@ -1208,6 +1216,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
                     store32(to + 16, y + 8);
                 }
             }
+            __syncwarp();
             tc_fence_before();
             float lo, hi;
             split_f32x2(probe, lo, hi);
