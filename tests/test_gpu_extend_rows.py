@@ -1,8 +1,13 @@
 """oscar_extend_bf16: blocks that rows fill in part, rows that infinities and NaN reach."""
 
-import pytest
+import math
 
-from test_gpu_extend import Case
+import numpy as np
+import pytest
+import torch
+
+import chunk_oracle
+from test_gpu_extend import BF, I32, P, Case, context
 
 pytestmark = pytest.mark.gpu
 
@@ -16,3 +21,104 @@ def test_partly_filled_warps(cuda, d, cached, h_q):
     new = [1, 2, 31, 32, 33, 63, 97, 127, 128, 129, 161, 255, 257]
     c = Case([(cached if m < 40 else cached % 301, m) for m in new], h_q, 1, d, seed=cached + h_q, spare=2)
     c.check(c.run(cuda))
+
+
+def odd_values(c, scale):
+    """Per output: 0, or what the infinities and NaN among the values that it sees make of it, by the decode's rule: one
+    counts whole however small its token's weight; the logit -infinity has none, and zero times infinity is NaN."""
+    g, out = c.h_q // c.h_kv, np.zeros(c.q.shape)
+    for b, total in enumerate(c.total):
+        lo, hi = c.start[b], c.start[b + 1]
+        for h in range(c.h_kv):
+            k, v, there = chunk_oracle.rows_of(c.pool, c.tables[b], total, h)
+            for t in np.flatnonzero(there & ~np.isfinite(v).all(1)):
+                rows = slice(max(lo, lo + t - (total - (hi - lo))), hi)
+                with np.errstate(invalid="ignore"):
+                    x = (c.q[rows, h * g:(h + 1) * g] @ k[t]) * scale
+                    one = np.where(x > -np.inf, 1.0, 0.0)[..., None]
+                    out[rows, h * g:(h + 1) * g] += np.where(np.isfinite(v[t]), 0.0, one * np.where(np.isfinite(v[t]), 0.0, v[t]))
+    return out
+
+
+def check_odd(c, out, scale):
+    """Infinities and NaN where odd_values has them, the rest within the bound."""
+    odd, got = odd_values(c, scale), out.double().cpu().numpy()
+    some = odd != 0
+    assert some.any() and np.array_equal(got[some], odd[some], equal_nan=True)
+    pool, c.pool = c.pool, np.where(np.isfinite(c.pool), c.pool, 0.0)
+    c.pool[:, :, 0][np.isneginf(pool[:, :, 0])] = -3000.0    # a weight of nothing in 64 bits too
+    want, bound = chunk_oracle.extend(c.q, c.pool, c.tables, c.start, c.total, scale)
+    c.pool = pool
+    n = len(got) - c.spare
+    assert (np.abs(got - want) <= bound)[:n][~some[:n]].all() and (got[n:] == 7).all()
+    return some
+
+
+def spread_infinities(c, seed):
+    """Infinities of both signs and NaN among the values: a few anywhere, the requests' first, last and middle tokens."""
+    r = np.random.default_rng(seed)
+    for x in (np.inf, -np.inf, np.nan):
+        c.pool[r.integers(len(c.pool)), r.integers(c.h_kv), 1, r.integers(P), r.integers(5, c.d)] = x
+    at = lambda b, t: (c.tables[b, t // P], int(r.integers(c.h_kv)), 1, t % P)
+    for b, total in enumerate(c.total):
+        if total == 0 or b > 40:
+            continue
+        c.pool[at(b, 0)][0] = np.inf
+        c.pool[at(b, total - 1)][1] = -np.inf
+        c.pool[at(b, total // 2)][2] = np.nan
+        c.pool[c.tables[b, 0], 0, 1, 0, 3], c.pool[c.tables[b, (total - 1) // P], 0, 1, (total - 1) % P, 3] = np.inf, -np.inf
+
+
+ODD = [([(20, 300)], 4, 2, 64), ([(0, 1)], 2, 1, 128), ([(300, 200), (4000, 3), (0, 40)], 8, 2, 128), ([(9000, 2)], 8, 1, 128),
+       ([(5000, 150)], 2, 1, 64), ([(40 * i + 5, 2) for i in range(60)], 4, 2, 64), ([(i * 7 % 90, i % 3) for i in range(200)], 4, 2, 64),
+       ([(150, 40)] * 45, 8, 2, 128)]
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -5, 4.0])
+@pytest.mark.parametrize("lens,h_q,h_kv,d", ODD, ids=lambda x: str(x) if len(str(x)) < 50 else "many")
+def test_infinite_values_of_any_weight(cuda, lens, h_q, h_kv, d, scale):
+    """At scale 4 most weights are far below what fp32 holds. In whole items and in parts, by either plan."""
+    c = Case(lens, h_q, h_kv, d, seed=len(lens) + d, spare=2)
+    spread_infinities(c, 5)
+    check_odd(c, c.run(cuda, context(h_q, h_kv, d, sm_scale=scale)), scale)
+
+
+@pytest.mark.parametrize("lens", [[(20, 30)], [(3000, 5), (0, 77)]], ids=str)
+def test_infinite_values_without_weight(cuda, lens):
+    """A logit of -infinity weighs zero: with a finite value it adds nothing, zero times infinity is NaN. On pages outside
+    the pool nothing counts, and a row that sees no weight at all is zeros."""
+    c = Case(lens, 4, 2, 64, seed=2)
+    c.q[..., 0] = 1.0
+    c.pool[:, :, 0, :, 0] = 0.0
+    for b, total in enumerate(c.total):
+        page = c.tables[b, total // 2 // P]
+        c.pool[page, :, 0, 4, 0] = -np.inf
+        c.pool[page, 0, 1, 4, 9] = np.inf
+    some = check_odd(c, c.run(cuda), 1 / 8)
+    assert some[..., 9].any() and not some[..., :9].any()
+    c.pool[c.tables[0, :2], :, 0, :, 0] = -np.inf            # the first tokens of all
+    c.pool[c.tables[0, :2], :, 1, :, 3] = -np.inf
+    c.total[0] = c.new[0] + 1                                # row i sees i + 2 tokens
+    got = c.run(cuda).double().cpu().numpy()
+    rows = min(31, c.new[0])
+    assert (got[:rows] == 0).all()
+
+
+def test_infinite_values_as_in_the_decode(cuda):
+    """Single tokens: infinite and NaN at the same places."""
+    lens = [(0, 1), (15, 1), (4000, 1), (16, 1), (77, 1), (9000, 1)]
+    c = Case(lens, 8, 2, 128, seed=1)
+    spread_infinities(c, 6)
+    t = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).to(cuda).to(dt)
+    c.pool[c.tables[4, 1], 1, 0, 3] = -np.inf                # logits of either infinity, and NaN
+    c.pool[c.tables[4, 1], 1, 1, 3, 7] = np.inf
+    for scale in (1 / math.sqrt(128), 4.0):
+        ctx = context(8, 2, 128, sm_scale=scale)
+        got = c.run(cuda, ctx)
+        out = torch.empty(6, 8, 128, device=cuda)
+        ws = torch.empty(max(1, ctx.decode_bf16_workspace_size(6, 9001)), dtype=torch.uint8, device=cuda)
+        ctx.decode_bf16(t(c.q, BF), t(c.pool, BF), t(c.tables, I32), t(c.total, I32), 9001, out, ws)
+        odd = ~torch.isfinite(out)
+        assert odd.any() and torch.equal(torch.isnan(out), torch.isnan(got)) and torch.equal(odd, ~torch.isfinite(got))
+        same = odd & ~torch.isnan(out)
+        assert torch.equal(out[same], got[same].float())
