@@ -29,7 +29,7 @@
 // chunk_join_kernel adds the parts of cut items.
 //
 // A weight of 0 does not undo an infinity or NaN in the value of a token that a row must not see (0 x inf): rows whose
-// accumulator is not finite are marked, and chunk_join_kernel forms them again with the tokens that they see alone.
+// accumulator is not finite are marked, and chunk_join_kernel looks at them again, with the tokens that they see alone.
 //
 // Every wait is bounded: a role that gives up records kind 4 and sets a flag, the others stop, copies and matrix
 // products in flight are waited for (bounded too), tensor memory is freed.
@@ -80,7 +80,8 @@ struct Work {
     int* tiles;                   // [batch + 1] first row block of each request
     int2* units;                  // per row block: request, cache tiles and rows (unit_word)
     Item* items;
-    uint32_t* odd;                // [items][8] rows to form again, a word for each softmax warp
+    uint32_t* odd;                // [items][8] rows to look at again, a word for each softmax warp
+    int* marked;                  // [SMs] whether a CTA has marked any
     float2* part_ml;              // per row of a cut item: reference and sum
     float* part_acc;              // [rows][d]
     int fold_rows;                // of a CTA
@@ -365,6 +366,7 @@ struct Layout {
     static constexpr int kOffMask = kOffBar + 8 * kBars;
     static constexpr int kOffTmem = kOffMask + 4 * kMaskRing;
     static constexpr int kOffFail = kOffTmem + 4;
+    static constexpr int kOffMarked = kOffFail + 4;
     static constexpr int kOffPlan = kOffFail + 12;
     static constexpr int kBytes = kOffPlan + 28 * kSelfUnits + 24;
     static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
@@ -381,6 +383,7 @@ struct Layout {
     __device__ uint32_t mask(int tile) const { return base + kOffMask + 4 * (tile % kMaskRing); }
     __device__ uint32_t tmem() const { return base + kOffTmem; }
     __device__ uint32_t fail() const { return base + kOffFail; }
+    __device__ uint32_t marked() const { return base + kOffMarked; }
     // mbarriers; those of a ring come with the phase of its i-th turn
     __device__ uint32_t bar(int i) const { return base + kOffBar + 8 * i; }
     __device__ uint32_t kv_full(int slot) const { return bar(slot % kStages); }
@@ -515,6 +518,7 @@ __device__ __forceinline__ void plan_here(const ChunkArgs& a, SelfPlan* plan, in
     int units = 0, longest = 0, most = 0;        // most: rows of a block at most
     long long sum = 0;
     bool even = true;                            // no two row blocks share tiles, none is without
+#pragma unroll 1
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
         const int b = b0 + lane;
         Request r{};
@@ -529,6 +533,7 @@ __device__ __forceinline__ void plan_here(const ChunkArgs& a, SelfPlan* plan, in
         }
         const int all = __shfl_sync(0xffffffffu, at, 31);
         at += units - blocks;
+#pragma unroll 1
         for (int k = 0; k < blocks && at + k < unit_cap; ++k) {          // the last block, which sees the most, first
             const int word = unit_word(r, blocks - 1 - k, a.g, g_log2);
             plan->unit[at + k] = Unit{b, blocks - 1 - k, word, r.tok0, r.pos0, r.total};
@@ -566,6 +571,7 @@ __device__ __forceinline__ void plan_here(const ChunkArgs& a, SelfPlan* plan, in
     if (__all_sync(0xffffffffu, even) && all > 0 && (all + 1) * sms < 0x7fffffff &&       // products of both in 32 bits
         (float)(share + 2 * kStart) + 2.0f * (float)(ctas * most) * (float)a.d * kJoined < best) {
         int pos = 0;
+#pragma unroll 1
         for (int u0 = 0; u0 < units; u0 += 32) {
             const int u = u0 + lane, mine = u < units ? tiles_of(plan->unit[u].word) * a.h_kv : 0;
             int s = mine;
@@ -610,6 +616,7 @@ __device__ __forceinline__ void plan_here(const ChunkArgs& a, SelfPlan* plan, in
         __syncwarp();
     }
     int items = 0;
+#pragma unroll 1
     for (int u0 = 0; u0 < units; u0 += 32) {
         const int u = u0 + lane;
         const int mine = u < units ? pieces_of(tiles_of(plan->unit[u].word), len) * a.h_kv : 0;
@@ -1198,6 +1205,8 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
                     for (int k = 0; k < 32; ++k) o[k] = 0;
                 }
 #pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = inv == 0.0f ? 0 : o[k];    // no token with a weight: zeros, whatever values are
+#pragma unroll
                 for (int k = 0; k < 32; k += 2) probe = fma_f32x2(f32x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), 0ull, probe);
                 if (mine(it) && it.part >= 0) {  // a part of a cut item, as it is
                     float* to = w.part_acc + (int64_t)part * D + c;
@@ -1220,9 +1229,10 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
             tc_fence_before();
             float lo, hi;
             split_f32x2(probe, lo, hi);
-            again = __ballot_sync(0xffffffffu, lo + hi != 0.0f && mine(it));
+            again = __ballot_sync(0xffffffffu, lo + hi != 0.0f && mine(it) && inv == inv);       // a sum of NaN: a row of NaN
         }
         if (lane == 0) w.odd[(int64_t)sm.read_item(i).self * 8 + 4 * t + warp] = again;
+        if (lane == 0 && again) sts32(sm.marked(), 1);
         __syncwarp();
         if (lane == 0) mbar_arrive(sm.item_empty(i));
     }
@@ -1254,6 +1264,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attend_kernel(const __grid_
         }
         mbar_init(sm.last(), 1);
         sts32(sm.fail(), 0);
+        sts32(sm.marked(), 0);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
     }
@@ -1280,6 +1291,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attend_kernel(const __grid_
     async_copies_done();                         // of a role that stopped
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) w.marked[blockIdx.x] = lds32(sm.marked());
     if (warp == kSoftmaxWarps + 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(512) : "memory");
@@ -1294,77 +1306,207 @@ __device__ __forceinline__ void store_bf16(uint16_t* to, const float (&x)[N], fl
     for (int c = 0; c < N; c += 2) *reinterpret_cast<uint32_t*>(to + c) = bf16_pair(x[c] * f, x[c + 1] * f);
 }
 
-// Row r of a request from the beginning, 32 tokens at a time by the whole warp, with the tokens alone that it sees: for
-// rows that an infinity or NaN has reached, its own or one behind it, or whose sum of finite values has passed fp32: the
-// values are added in units of 2^31, more than there are tokens. Infinities and NaN are added apart, with weight one for
-// every token that has a weight, however small (0 makes NaN of an infinity, as it should): a channel that has any is
-// that sum, whatever its finite values add. The item's fields come by value: by reference the item
-// lies in local memory, which costs the shortest calls 1.3 us of 11.
+// ---- rows that are not finite
+//
+// An infinity or NaN in V reaches every row of its tile, through a weight of 0 those too that must not see it; and a sum of
+// finite values may pass fp32. A CTA of the join takes up to 32 such rows (of one request and KV head) at a time:
+//   look_again goes over V once for all of them, finds the tokens with an infinity or NaN, and adds those values by
+//   themselves, with weight one for every token that has a weight, however small (0 makes NaN of an infinity, as it
+//   should): a channel that has any is that sum, whatever its finite values add;
+//   form_rows forms what is left, infinite or NaN without such a value among those that the row sees, from the first token.
+// An 8,192-token prompt (32 / 8 heads of 128, 345 us) takes 3.3 ms with an infinite value of token 10 in every head, 1.2 with
+// one in one head, 5.8 with one of token 8,190, whose tile's rows are formed, and 61 where every row's sum passes fp32
+// (3.7 s where a warp formed all rows of four items, a token's values at a time). Loops stay rolled up: a kernel's
+// instructions take the next one's place in the instruction cache even where they do not run. With as many of them again,
+// eight tokens at 100,000 took 80 us instead of 74, all of it at the start of the next call.
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kScanPages = 32 * kJoinWarps;      // pages of a stretch of V, a lane's table entry each
+
 template <int D>
-__device__ __noinline__ void form_row(const ChunkArgs& a, int b, int head, int tok0, int pos0, int total, int r,
-                                      int lane) {
-    constexpr int kChannels = D / 32;
-    const int g_log2 = 31 - __clz(a.g), limit = min(limit_of(r, pos0, g_log2), total);
-    const int64_t token = tok0 + (r >> g_log2);
-    const int q_head = (head << g_log2) + (r & (a.g - 1));
-    const uint16_t* q = a.q + token * a.q_stride + q_head * D;
-    const int32_t* table = a.tables + (int64_t)b * a.stride;
-    float m = kNoReference, sum = 0.0f, acc[kChannels] = {}, odd[kChannels] = {};
-    for (int t0 = 0; t0 < limit; t0 += 32) {
-        const int t = t0 + lane;
-        const int id = t < limit ? table[t / kPage] : -1;
-        const bool there = id >= 0 && id < a.pages;
-        const int64_t k_row = ((int64_t)(there ? id : 0) * a.h_kv + head) * 2 * kPage + t % kPage;
-        float x = -INFINITY;
-        if (there) {
-            float dot = 0.0f;
-            const uint16_t* k = a.pool + k_row * D;
-            for (int c = 0; c < D; c += 8) {
-                const uint4 u = *reinterpret_cast<const uint4*>(q + c), v = *reinterpret_cast<const uint4*>(k + c);
-                dot += bf16_lo(u.x) * bf16_lo(v.x) + bf16_hi(u.x) * bf16_hi(v.x) + bf16_lo(u.y) * bf16_lo(v.y) +
-                       bf16_hi(u.y) * bf16_hi(v.y) + bf16_lo(u.z) * bf16_lo(v.z) + bf16_hi(u.z) * bf16_hi(v.z) +
-                       bf16_lo(u.w) * bf16_lo(v.w) + bf16_hi(u.w) * bf16_hi(v.w);
-            }
-            x = dot * a.scale_log2;
-        }
-        float top = x;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (top > m) {
-            const float f = exp2_approx(m - top);
-            m = top;
-            sum *= f;
-#pragma unroll
-            for (int c = 0; c < kChannels; ++c) acc[c] = f == 0.0f ? 0.0f : acc[c] * f;
-        }
-        const float p = there ? bf16_lo(bf16_pair(exp2_approx(x - m), 0.0f)) : 0.0f;
-        const uint32_t on_pages = __ballot_sync(0xffffffffu, there), weighs = __ballot_sync(0xffffffffu, x > -INFINITY);
-        float sum32 = 0.0f, acc32[kChannels] = {};           // apart: a sum of 2^24 would take no more ones
+struct Again {
+    // tokens of a step of form_rows; the stride lets eight lanes read 16 bytes of a token each without a bank twice
+    alignas(16) uint16_t k[32][D + 8], v[32][D + 8];
+    float acc[32][D];                            // of each row: infinities and NaN; then what form_rows adds
+    const uint16_t* q[32];                       // of each row: its queries, its outputs, the tokens that it sees (0: no row)
+    uint16_t* out[32];
+    int seen[32];
+    float m[32], sum[32];
+    uint32_t words[kJoinThreads];                // marked rows, 32 each: of whole items, or the first eight of a cut one
+    uint32_t bad[kScanPages];                    // per page: tokens with an infinity or NaN
+    uint32_t todo;                               // rows to form
+    uint8_t want[32][32];                        // per row and lane: channels to form
+};
+
+__device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll 1
-        for (int i = 0; i < 32; ++i) {
-            const float pi = __shfl_sync(0xffffffffu, p, i);
-            const int64_t row = __shfl_sync(0xffffffffu, k_row, i) + kPage;
-            if (!(on_pages >> i & 1)) continue;
-            sum32 += pi;
-            const float one = (float)(weighs >> i & 1);
-            const uint16_t* v = a.pool + row * D + lane * kChannels;
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// The channels want[k] of the rows k of s.todo, by the whole CTA: 32 tokens a step, whose K and V go to shared memory. A
+// warp takes every eighth row, a lane a token's logit, then some channels of all tokens. The values are added in units of
+// 2^31, more than there are tokens, so that no sum of them passes fp32.
+template <int D>
+__device__ __forceinline__ void form_rows(const ChunkArgs& a, const int32_t* table, int head, int end, Again<D>& s, int lane, int warp) {
+    constexpr int kChannels = D / 32, kChunks = D / 8;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < 32 * D; i += kJoinThreads) {
+        s.acc[0][i] = 0.0f;
+        s.m[i / D] = kNoReference;
+        s.sum[i / D] = 0.0f;
+    }
+#pragma unroll 1
+    for (int t0 = 0; t0 < end; t0 += 32) {
+        auto page = [&](int t) {
+            const int id = t0 + t < end ? table[(t0 + t) / kPage] : -1;
+            return id < a.pages ? id : -1;
+        };
+#pragma unroll 1
+        for (int i = threadIdx.x; i < 32 * kChunks; i += kJoinThreads) {
+            const int c = i % kChunks * 8, t = i / kChunks, id = page(t);
+            const uint16_t* from = a.pool + (((int64_t)max(id, 0) * a.h_kv + head) * 2 * kPage + t % kPage) * D + c;
+            async_copy16(smem_u32(&s.k[t][c]), from, id >= 0);
+            async_copy16(smem_u32(&s.v[t][c]), from + kPage * D, id >= 0);
+        }
+        const bool there = page(lane) >= 0;
+        async_copies_done();
+        __syncthreads();
+#pragma unroll 1
+        for (int k = warp; k < 32; k += kJoinWarps) {
+            const int seen = s.seen[k] - t0;
+            if (!(s.todo >> k & 1) || seen <= 0) continue;
+            const uint16_t* q = s.q[k];
+            float x = 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 8) {
+                const uint4 u = *reinterpret_cast<const uint4*>(q + c), v = *reinterpret_cast<const uint4*>(&s.k[lane][c]);
+                x += bf16_lo(u.x) * bf16_lo(v.x) + bf16_hi(u.x) * bf16_hi(v.x) + bf16_lo(u.y) * bf16_lo(v.y) +
+                     bf16_hi(u.y) * bf16_hi(v.y) + bf16_lo(u.z) * bf16_lo(v.z) + bf16_hi(u.z) * bf16_hi(v.z) +
+                     bf16_lo(u.w) * bf16_lo(v.w) + bf16_hi(u.w) * bf16_hi(v.w);
+            }
+            x = there && lane < seen ? x * a.scale_log2 : -INFINITY;
+            float m = fmaxf(x, s.m[k]);
+#pragma unroll 1
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float f = exp2_approx(s.m[k] - m), p = bf16_lo(bf16_pair(exp2_approx(x - m), 0.0f));
+            const float sum = s.sum[k] * f + warp_sum(p);
+            float acc[kChannels] = {};               // of the step alone: a sum of 2^24 would take no more ones
+#pragma unroll 1
+            for (int i = 0; i < min(seen, 32); ++i) {
+                const float pi = __shfl_sync(0xffffffffu, p, i) * 0x1p-31f;
+#pragma unroll
+                for (int c = 0; c < kChannels; c += 2) {
+                    const uint32_t v = *reinterpret_cast<const uint32_t*>(&s.v[i][lane * kChannels + c]);
+                    acc[c] += pi * bf16_lo(v);
+                    acc[c + 1] += pi * bf16_hi(v);
+                }
+            }
 #pragma unroll
             for (int c = 0; c < kChannels; ++c) {
-                const float x = __uint_as_float((uint32_t)v[c] << 16);
-                if (fabsf(x) < INFINITY)
-                    acc32[c] += pi * (x * 0x1p-31f);
-                else
-                    odd[c] += one * x;
+                float& to = s.acc[k][lane * kChannels + c];
+                to = (f == 0.0f ? 0.0f : to * f) + acc[c];
+            }
+            __syncwarp();                            // all lanes have read them
+            s.sum[k] = sum;
+            s.m[k] = m;
+            __syncwarp();
+        }
+        __syncthreads();
+    }
+#pragma unroll 1
+    for (int i = threadIdx.x; i < 32 * D; i += kJoinThreads) {
+        const int k = i / D, c = i % D;
+        if (s.todo >> k & 1 && s.want[k][c / kChannels] >> c % kChannels & 1)
+            s.out[k][c] = (uint16_t)bf16_pair(s.sum[k] == 0.0f ? 0.0f : s.acc[k][c] * (0x1p31f / s.sum[k]), 0.0f);
+    }
+}
+
+// The rows `from` + k of an item, for the bits k of `marked`, by the whole CTA; their outputs are there, infinities and NaN
+// among them, and they have a weight.
+template <int D>
+__device__ __noinline__ void look_again(const ChunkArgs& a, const Item* item, int from, uint32_t marked, Again<D>& s) {
+    constexpr int kChannels = D / 32, kLanes = D / 8, kRounds = kPage * kLanes / 32;         // 16 bytes a lane
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, behind = item->rows - from, head = item->head;
+    if (behind < 32) marked &= behind > 0 ? (1u << behind) - 1 : 0;
+    if (!marked) return;
+    const int32_t* table = a.tables + (int64_t)item->b * a.stride;
+    if (threadIdx.x < 32) {
+        const int r = item->r0 + from + lane, g_log2 = 31 - __clz(a.g), channel = (head * a.g + (r & (a.g - 1))) * D;
+        const int64_t token = item->tok0 + (r >> g_log2);
+        s.q[lane] = a.q + token * a.q_stride + channel;
+        s.out[lane] = a.out + token * (a.h_kv * a.g * D) + channel;
+        s.seen[lane] = marked >> lane & 1 ? min(limit_of(r, item->pos0, g_log2), item->total) : 0;
+        if (lane == 0) s.todo = 0;
+    }
+#pragma unroll 1
+    for (int i = threadIdx.x; i < 32 * D; i += kJoinThreads) s.acc[0][i] = 0.0f;
+    __syncthreads();
+    const int end = s.seen[31 - __clz(marked)];
+#pragma unroll 1
+    for (int p0 = 0; p0 * kPage < end; p0 += kScanPages) {
+        const int mine = p0 + (int)threadIdx.x, ids = mine * kPage < end ? table[mine] : -1;
+        bool found = false;
+        s.bad[threadIdx.x] = 0;
+        __syncwarp();
+#pragma unroll 1
+        for (int j = 0; j < 32; ++j) {           // the page of each lane
+            const int id = __shfl_sync(0xffffffffu, ids, j);
+            if (id < 0 || id >= a.pages) continue;
+            const uint4* v = reinterpret_cast<const uint4*>(a.pool + (((int64_t)id * a.h_kv + head) * 2 + 1) * kPage * D) + lane;
+#pragma unroll 4
+            for (int i = 0; i < kRounds; ++i) {
+                const uint4 x = v[32 * i];
+                // an exponent of ones carries into the bit above it
+                const auto carry = [](uint32_t u) { return (u & 0x7f807f80u) + 0x00800080u; };
+                if ((carry(x.x) | carry(x.y) | carry(x.z) | carry(x.w)) & 0x80008000u) {
+                    found = true;
+                    atomicOr(&s.bad[warp * 32 + j], 1u << ((32 * i + lane) / kLanes));
+                }
             }
         }
-        sum += sum32;
-#pragma unroll
-        for (int c = 0; c < kChannels; ++c) acc[c] += acc32[c];
+        if (!__syncthreads_or(found)) continue;
+#pragma unroll 1
+        for (int j = 0; j < kScanPages; ++j) {
+#pragma unroll 1
+            for (uint32_t bad = s.bad[j]; bad; bad &= bad - 1) {
+                const int local = __ffs(bad) - 1;
+                const uint16_t* key = a.pool + (((int64_t)table[p0 + j] * a.h_kv + head) * 2 * kPage + local) * D + lane * kChannels;
+#pragma unroll 1
+                for (int k = warp; k < 32; k += kJoinWarps) {
+                    if ((p0 + j) * kPage + local >= s.seen[k]) continue;
+                    float dot = 0.0f;
+#pragma unroll 1
+                    for (int c = 0; c < kChannels; ++c) dot += bf16_lo(s.q[k][lane * kChannels + c]) * bf16_lo(key[c]);
+                    const float one = warp_sum(dot) * a.scale_log2 > -INFINITY ? 1.0f : 0.0f;
+#pragma unroll 1
+                    for (int c = 0; c < kChannels; ++c) {
+                        const float v = bf16_lo(key[kPage * D + c]);
+                        if (!(fabsf(v) < INFINITY)) s.acc[k][lane * kChannels + c] += one * v;
+                    }
+                }
+            }
+        }
+        __syncthreads();                         // before the next stretch's pages
     }
-#pragma unroll
-    for (int c = 0; c < kChannels; ++c)
-        if (odd[c] != 0.0f && sum != 0.0f) acc[c] = odd[c];
-    store_bf16(a.out + (token * (a.h_kv << g_log2) + q_head) * D + lane * kChannels, acc, sum == 0.0f ? 0.0f : 0x1p31f / sum);
+#pragma unroll 1
+    for (int k = warp; k < 32; k += kJoinWarps) {
+        if (s.seen[k] == 0) continue;
+        uint32_t want = 0;
+#pragma unroll 1
+        for (int c = 0; c < kChannels; ++c) {
+            uint16_t& to = s.out[k][lane * kChannels + c];
+            const float odd = s.acc[k][lane * kChannels + c];
+            if (odd != 0.0f)
+                to = (uint16_t)bf16_pair(odd, 0.0f);
+            else if ((to & 0x7f80) == 0x7f80)
+                want |= 1u << c;
+        }
+        s.want[k][lane] = (uint8_t)want;
+        if (want) atomicOr(&s.todo, 1u << k);
+    }
+    __syncthreads();
+    if (s.todo) form_rows<D>(a, table, head, end, s, lane, warp);
+    __syncthreads();
 }
 
 // Whether an item's indexes lie within the call's buffers: a CTA that gave up leaves entries of the list unwritten.
@@ -1374,7 +1516,7 @@ __device__ __forceinline__ bool sane(const ChunkArgs& a, const Work& w, const It
         it.total < 0 || it.total > a.stride * kPage)
         return false;
     if (it.part < 0) return true;
-    if (it.pieces < 2 || it.pieces > w.item_cap || it.piece < 0 || it.piece >= it.pieces || it.step < 1 || it.lead < 0 ||
+    if (it.pieces < 2 || it.pieces > min(w.item_cap, 1 << 22) || it.piece < 0 || it.piece >= it.pieces || it.step < 1 || it.lead < 0 ||
         it.step > w.part_cap || it.lead > w.part_cap || it.stride < 1 || it.stride > a.h_kv)
         return false;
     const long long base = it.part - (long long)it.piece * it.step - (it.piece ? 0 : it.lead);
@@ -1383,52 +1525,71 @@ __device__ __forceinline__ bool sane(const ChunkArgs& a, const Work& w, const It
            first >= 0 && last < w.item_cap;
 }
 
+// Whole items' marked rows, a word of 32 each. Rows side by side are marked together, hence a CTA's words, one of each
+// thread, lie far apart, and where there are fewer words than CTAs `shares` of them take some rows of each.
+template <int D>
+__device__ __noinline__ void look_at_words(const ChunkArgs& a, const Work& w, int items, Again<D>& s) {
+    const unsigned count = (unsigned)items * 8, shares = clamp_int((int)(gridDim.x / max(count, 1u)), 1, 32);
+#pragma unroll 1
+    for (unsigned u0 = 0; u0 < count * shares; u0 += gridDim.x * kJoinThreads) {
+        const unsigned mine = u0 + threadIdx.x * gridDim.x + blockIdx.x;
+        uint32_t word = mine / shares < count ? w.odd[mine / shares] : 0;
+#pragma unroll 1
+        for (unsigned i = 0; word && i < 32; ++i)
+            if (i % shares != mine % shares) word &= ~(1u << i);
+        s.words[threadIdx.x] = word;
+        if (!__syncthreads_or(word != 0)) continue;
+#pragma unroll 1
+        for (int i = 0; i < kJoinThreads; ++i) {
+            if (!s.words[i]) continue;
+            const unsigned at = (u0 + i * gridDim.x + blockIdx.x) / shares;
+            const Item it = w.items[at / 8];
+            if (it.part < 0 && sane(a, w, it, (int)(at / 8), 31 - __clz(a.g))) look_again<D>(a, w.items + at / 8, 32 * (int)(at % 8), s.words[i], s);
+        }
+        __syncthreads();
+    }
+}
+
 // Adds the parts of cut items, in their order: a piece's CTA takes its share of the rows, a warp a row. Rows that are
-// marked in any of the pieces are formed again.
+// marked, in any of the pieces too, or whose parts' sum is not finite are looked at again.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ ChunkArgs a,
                                                                   const __grid_constant__ Work w) {
     constexpr int kChannels = D / 32, kDepth = 8;
+    __shared__ Again<D> again;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g_log2 = 31 - __clz(a.g);
     grid_release();
+    again.words[threadIdx.x] = 0;
+    __syncthreads();
     grid_wait();
     Header head = *w.head;
+    int marked = 0;
+    for (int i = threadIdx.x; i < w.sms; i += kJoinThreads) marked |= w.marked[i];
     head.items = clamp_int(head.items, 0, w.item_cap);
-    // rows to form again of whole items: a word of 32 rows each, almost always 0
-    for (int64_t word = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; word - lane < (int64_t)head.items * 8; word += (int64_t)gridDim.x * kJoinThreads) {
-        const uint32_t mine = word < (int64_t)head.items * 8 ? w.odd[word] : 0;
-        for (uint32_t who = __ballot_sync(0xffffffffu, mine != 0); who; who &= who - 1) {
-            const int src = __ffs(who) - 1;
-            const int64_t at = word - lane + src;
-            const Item it = w.items[at / 8];
-            const uint32_t marked = __shfl_sync(0xffffffffu, mine, src);
-            if (it.part >= 0 || !sane(a, w, it, (int)(at / 8), g_log2)) continue;
-            for (uint32_t todo = marked; todo; todo &= todo - 1) {
-                const int local = 32 * (int)(at % 8) + __ffs(todo) - 1;
-                if (local < it.rows) form_row<D>(a, it.b, it.head, it.tok0, it.pos0, it.total, it.r0 + local, lane);
-            }
-        }
-    }
-    if (!head.cut) return;
     // with more CTAs than items, `per` of them share an item's rows
     const int per = max((int)gridDim.x / max(head.items, 1), 1), sub = (int)blockIdx.x / max(head.items, 1);
-    if (sub >= per) return;
-    for (int item = per > 1 ? (int)blockIdx.x % head.items : (int)blockIdx.x; item < head.items; item += gridDim.x) {
+    const int first = !head.cut || sub >= per ? head.items : per > 1 ? (int)blockIdx.x % head.items : (int)blockIdx.x;
+#pragma unroll 1
+    for (int item = first; item < head.items; item += gridDim.x) {
         const Item it = w.items[item];
         if (it.part < 0 || !sane(a, w, it, item, g_log2)) continue;
         const int base = it.part - it.piece * it.step - (it.piece ? 0 : it.lead);
         auto part_of = [&](int p, int local) { return base + p * it.step + (p ? 0 : it.lead) + local; };
-        const int end = (int)((long long)it.rows * (it.piece + 1) / it.pieces);
-        for (int local = (int)((long long)it.rows * it.piece / it.pieces) + sub * (kJoinThreads / 32) + warp; local < end;
-             local += per * (kJoinThreads / 32)) {
+        const int end = it.rows * (it.piece + 1) / it.pieces;
+        bool look = false;
+#pragma unroll 1
+        for (int local = it.rows * it.piece / it.pieces + sub * kJoinWarps + warp; local < end;
+             local += per * kJoinWarps) {
             float m = kNoReference, sum = 0.0f, acc[kChannels] = {};
-            bool again = false;
+            bool odd = false, nan = false;
+#pragma unroll 1
             for (int p0 = 0; p0 < it.pieces; p0 += 32) {
                 const int p = p0 + lane;
                 float2 ml = make_float2(kNoReference, 0.0f);
                 if (p < it.pieces) {
                     ml = w.part_ml[part_of(p, local)];
-                    again |= w.odd[(int64_t)(item + (p - it.piece) * it.stride) * 8 + local / 32] >> (local % 32) & 1;
+                    nan |= ml.y != ml.y;
+                    odd |= w.odd[(int64_t)(item + (p - it.piece) * it.stride) * 8 + local / 32] >> (local % 32) & 1;
                 }
                 float top = ml.y != 0.0f ? fmaxf(m, ml.x) : m;
 #pragma unroll
@@ -1440,11 +1601,12 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
                 for (int c = 0; c < kChannels; ++c) acc[c] *= back;
                 const float f = ml.y == 0.0f ? 0.0f : exp2_approx(ml.x - m);
                 const int count = min(32, it.pieces - p0);
+#pragma unroll 1
                 for (int q0 = 0; q0 < count; q0 += kDepth) {
                     float x[kDepth][kChannels];
 #pragma unroll
                     for (int k = 0; k < kDepth; ++k) {
-                        const float* from = w.part_acc + (int64_t)part_of(p0 + min(q0 + k, count - 1), local) * D + lane * kChannels;
+                        const float* from = w.part_acc + (unsigned)(part_of(p0 + min(q0 + k, count - 1), local) * D + lane * kChannels);
 #pragma unroll
                         for (int c = 0; c < kChannels; c += 2) *reinterpret_cast<float2*>(&x[k][c]) = *reinterpret_cast<const float2*>(from + c);
                     }
@@ -1463,14 +1625,21 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_c
             float probe = 0.0f;                  // NaN where the parts' sum is infinite
 #pragma unroll
             for (int c = 0; c < kChannels; ++c) probe += acc[c] * 0.0f;
-            if (__any_sync(0xffffffffu, again || probe != 0.0f)) {
-                form_row<D>(a, it.b, it.head, it.tok0, it.pos0, it.total, r, lane);
-                continue;
+            if (__any_sync(0xffffffffu, nan)) sum = NAN;
+            if (__any_sync(0xffffffffu, odd || probe != 0.0f) && fabsf(sum) > 0.0f) {       // a number other than 0
+                look = true;
+                if (lane == 0) atomicOr(&again.words[local / 32], 1u << (local % 32));
             }
             const int64_t row = (int64_t)(it.tok0 + (r >> g_log2)) * (a.h_kv << g_log2) + (it.head << g_log2) + (r & (a.g - 1));
             store_bf16(a.out + row * D + lane * kChannels, acc, sum == 0.0f ? 0.0f : 1.0f / sum);
         }
+        if (!__syncthreads_or(look)) continue;
+#pragma unroll 1
+        for (int k = 0; k < kChunkRows / 32; ++k) look_again<D>(a, w.items + item, 32 * k, again.words[k], again);
+        if (threadIdx.x < kChunkRows / 32) again.words[threadIdx.x] = 0;
+        __syncthreads();
     }
+    if (__syncthreads_or(marked)) look_at_words<D>(a, w, head.items, again);
 }
 
 // ---- host ---------------------------------------------------------------------------------------------------
@@ -1513,7 +1682,7 @@ cudaError_t launch(const ChunkArgs& a, const ChunkPlan& plan, void* workspace, i
     const Work w{plan.unit_cap <= kSelfUnits && a.batch <= kSelfUnits, num_sms, plan.unit_cap, plan.item_cap, plan.part_cap,
                  reinterpret_cast<Header*>(base), reinterpret_cast<int*>(base + plan.tiles),
                  reinterpret_cast<int2*>(base + plan.units), reinterpret_cast<Item*>(base + plan.items),
-                 reinterpret_cast<uint32_t*>(base + plan.odd), reinterpret_cast<float2*>(base + plan.part_ml), reinterpret_cast<float*>(base + plan.part_acc),
+                 reinterpret_cast<uint32_t*>(base + plan.odd), reinterpret_cast<int*>(base + plan.marked), reinterpret_cast<float2*>(base + plan.part_ml), reinterpret_cast<float*>(base + plan.part_acc),
                  plan.fold_rows, reinterpret_cast<float2*>(base + plan.fold_ml), reinterpret_cast<float*>(base + plan.fold_acc)};
     const int grid = num_sms < plan.item_cap ? num_sms : plan.item_cap;
     if (!w.self) {
@@ -1552,6 +1721,7 @@ ChunkPlan plan_chunk(const Shape& s, int num_sms, int batch, int n) {
     p.units = place((size_t)p.unit_cap * sizeof(int2));
     p.items = place((size_t)p.item_cap * sizeof(Item));
     p.odd = place((size_t)p.item_cap * 8 * sizeof(uint32_t));
+    p.marked = place((size_t)num_sms * sizeof(int));
     p.part_ml = place((size_t)p.part_cap * sizeof(float2));
     p.part_acc = place((size_t)p.part_cap * s.d * sizeof(float));
     p.fold_ml = place((size_t)num_sms * p.fold_rows * sizeof(float2));

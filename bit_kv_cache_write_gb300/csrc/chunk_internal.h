@@ -35,7 +35,7 @@ struct ChunkPlan {
     int item_cap;                            // work items at most
     int part_cap;                            // rows of split items at most
     int fold_rows;                           // rows of an item at most
-    size_t tiles, units, items, odd, part_ml, part_acc, fold_ml, fold_acc, total;
+    size_t tiles, units, items, odd, marked, part_ml, part_acc, fold_ml, fold_acc, total;
 };
 struct ChunkArgs {
     const uint16_t* q; int64_t q_stride;     // token stride in elements

@@ -122,3 +122,64 @@ def test_infinite_values_as_in_the_decode(cuda):
         assert odd.any() and torch.equal(torch.isnan(out), torch.isnan(got)) and torch.equal(odd, ~torch.isfinite(got))
         same = odd & ~torch.isnan(out)
         assert torch.equal(out[same], got[same].float())
+
+
+def spoiled(c, what):
+    """The case's pool with values that reach every row (but the first ones)."""
+    pool = torch.from_numpy(c.pool).to(BF)
+    if what == "past fp32":
+        pool[:, :, 1, :, 3] = 3.0e38
+    else:
+        pool[int(c.tables[0, 0]), :, 1, 10, 3] = float(what)
+    return pool
+
+
+@pytest.mark.parametrize("what,times", [("inf", 100), ("nan", 100), ("past fp32", 1000)])
+def test_a_bad_value_stalls_nothing(cuda, what, times):
+    """A prompt of 4,096 tokens whose rows an infinity, a NaN or a sum past fp32 reaches takes longer, but not as long as
+    if each row were formed by itself (over 10,000 times). Its other channels keep their bits."""
+    c = Case([(0, 4096)], 32, 8, 128, seed=4, more_pages=0)
+    t = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).to(cuda).to(dt)
+    ctx, q, out = context(32, 8, 128), t(c.q, BF), [torch.empty(c.q.shape, dtype=BF, device=cuda) for _ in range(2)]
+    args = t(c.tables, I32), t(c.start, I32), t(c.total, I32)
+    ws = torch.empty(ctx.extend_bf16_workspace_size(1, 4096), dtype=torch.uint8, device=cuda)
+    spent = []
+    for pool, o in zip((torch.from_numpy(c.pool).to(BF).to(cuda), spoiled(c, what).to(cuda)), out):
+        events = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        ctx.extend_bf16(q, pool, *args, o, ws)
+        torch.cuda.synchronize()
+        events[0].record()
+        for _ in range(3):
+            ctx.extend_bf16(q, pool, *args, o, ws)
+        events[1].record()
+        torch.cuda.synchronize()
+        spent.append(events[0].elapsed_time(events[1]))
+    assert spent[1] < times * spent[0], spent
+    rest = [i for i in range(128) if i != 3]
+    assert torch.equal(out[0][..., rest], out[1][..., rest])
+    if what == "past fp32":                                  # the mean of equal values, weights off by 2^-8 at most in all
+        assert (out[1][..., 3].double() / float(torch.tensor(3.0e38).to(BF)) - 1).abs().max() <= 2.0 ** -7
+    else:
+        assert torch.equal(out[1][10:, :, 3], torch.full_like(out[1][10:, :, 3], float(what))) or torch.isnan(out[1][10:, :, 3]).all()
+        assert (out[1][:10, :, 3] - out[0][:10, :, 3]).abs().max() <= 2.0 ** -6 * out[0][:10].abs().max()
+
+
+def test_a_long_sum_past_fp32(cuda):
+    """A row over 2^20 tokens whose values' sum passes fp32, formed in 2^15 steps of 32 tokens: a step's sum is off by at
+    most 32 * 2^-24 of it, each addition of one by 2^-24 of the sum; weights are ones and their sum exact."""
+    d, length, pages = 64, 1 << 20, 40
+    gen = torch.Generator(device=cuda).manual_seed(5)
+    pool = torch.zeros(pages, 1, 2, P, d, dtype=BF, device=cuda)
+    pool[:, 0, 1] = ((1 + torch.rand(pages, P, d, generator=gen, device=cuda, dtype=torch.float64)) * 2.0 ** 125).to(BF)
+    pool[:, 0, 1, :, 7] = 1.0
+    tables = torch.randint(0, pages, (1, length // P), dtype=I32, device=cuda, generator=gen)
+    q, start = torch.zeros(1, 1, d, dtype=BF, device=cuda), torch.tensor([0, 1], dtype=I32, device=cuda)
+    out, ctx = torch.empty_like(q), context(1, 1, d)
+    ws = torch.empty(ctx.extend_bf16_workspace_size(1, 1), dtype=torch.uint8, device=cuda)
+    ctx.extend_bf16(q, pool, tables, start, torch.tensor([length], dtype=I32, device=cuda), out, ws)
+    torch.cuda.synchronize()
+    assert ctx.debug_error()[0] == 0
+    count = torch.bincount(tables[0], minlength=pages).double()
+    want = torch.einsum("p,pd->d", count, pool[:, 0, 1].double().mean(1)) / count.sum()
+    relative = 2.0 ** -9 + 2.0 ** -19 + 2.0 ** -21
+    assert ((out[0, 0].double() / want - 1).abs() <= relative + 2.0 ** -8 * (1 + relative)).all()
