@@ -1315,7 +1315,7 @@ __device__ __forceinline__ void store_bf16(uint16_t* to, const float (&x)[N], fl
 //   should): a channel that has any is that sum, whatever its finite values add;
 //   form_rows forms what is left, infinite or NaN without such a value among those that the row sees, from the first token.
 // An 8,192-token prompt (32 / 8 heads of 128, 345 us) takes 3.3 ms with an infinite value of token 10 in every head, 1.2 with
-// one in one head, 5.8 with one of token 8,190, whose tile's rows are formed, and 61 where every row's sum passes fp32
+// one in one head, 5.8 with one of token 8,190, whose tile's rows are formed, and 121 where every row's sum passes fp32
 // (3.7 s where a warp formed all rows of four items, a token's values at a time). Loops stay rolled up: a kernel's
 // instructions take the next one's place in the instruction cache even where they do not run. With as many of them again,
 // eight tokens at 100,000 took 80 us instead of 74, all of it at the start of the next call.
@@ -1333,7 +1333,7 @@ struct Again {
     float m[32], sum[32];
     uint32_t words[kJoinThreads];                // marked rows, 32 each: of whole items, or the first eight of a cut one
     uint32_t bad[kScanPages];                    // per page: tokens with an infinity or NaN
-    uint32_t todo;                               // rows to form
+    uint32_t todo, left;                         // rows to form, now and in another turn
     uint8_t want[32][32];                        // per row and lane: channels to form
 };
 
@@ -1344,10 +1344,11 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // The channels want[k] of the rows k of s.todo, by the whole CTA: 32 tokens a step, whose K and V go to shared memory. A
-// warp takes every eighth row, a lane a token's logit, then some channels of all tokens. The values are added in units of
-// 2^31, more than there are tokens, so that no sum of them passes fp32.
+// warp takes every eighth row, a lane a token's logit, then some channels of all tokens. The values are added as they are
+// (unit 1), so that the smallest count; the channels whose sum passes fp32 are left for a second turn, where they are added
+// in units of 2^31, more than there are tokens.
 template <int D>
-__device__ __forceinline__ void form_rows(const ChunkArgs& a, const int32_t* table, int head, int end, Again<D>& s, int lane, int warp) {
+__device__ __forceinline__ void form_rows(const ChunkArgs& a, const int32_t* table, int head, int end, float unit, Again<D>& s, int lane, int warp) {
     constexpr int kChannels = D / 32, kChunks = D / 8;
 #pragma unroll 1
     for (int i = threadIdx.x; i < 32 * D; i += kJoinThreads) {
@@ -1393,7 +1394,7 @@ __device__ __forceinline__ void form_rows(const ChunkArgs& a, const int32_t* tab
             float acc[kChannels] = {};               // of the step alone: a sum of 2^24 would take no more ones
 #pragma unroll 1
             for (int i = 0; i < min(seen, 32); ++i) {
-                const float pi = __shfl_sync(0xffffffffu, p, i) * 0x1p-31f;
+                const float pi = __shfl_sync(0xffffffffu, p, i) * unit;
 #pragma unroll
                 for (int c = 0; c < kChannels; c += 2) {
                     const uint32_t v = *reinterpret_cast<const uint32_t*>(&s.v[i][lane * kChannels + c]);
@@ -1413,12 +1414,26 @@ __device__ __forceinline__ void form_rows(const ChunkArgs& a, const int32_t* tab
         }
         __syncthreads();
     }
+    if (threadIdx.x == 0) s.left = 0;
+    __syncthreads();
 #pragma unroll 1
-    for (int i = threadIdx.x; i < 32 * D; i += kJoinThreads) {
-        const int k = i / D, c = i % D;
-        if (s.todo >> k & 1 && s.want[k][c / kChannels] >> c % kChannels & 1)
-            s.out[k][c] = (uint16_t)bf16_pair(s.sum[k] == 0.0f ? 0.0f : s.acc[k][c] * (0x1p31f / s.sum[k]), 0.0f);
+    for (int k = warp; k < 32; k += kJoinWarps) {
+        if (!(s.todo >> k & 1)) continue;
+        const float inv = s.sum[k] == 0.0f ? 0.0f : 1.0f / (s.sum[k] * unit);
+        uint32_t want = s.want[k][lane];
+#pragma unroll 1
+        for (int c = 0; c < kChannels; ++c) {
+            const float y = s.acc[k][lane * kChannels + c] * inv;
+            if (!(want >> c & 1) || (unit == 1.0f && !(fabsf(y) < INFINITY))) continue;
+            s.out[k][lane * kChannels + c] = (uint16_t)bf16_pair(y, 0.0f);
+            want &= ~(1u << c);
+        }
+        s.want[k][lane] = (uint8_t)want;
+        if (want) atomicOr(&s.left, 1u << k);
     }
+    __syncthreads();
+    if (threadIdx.x == 0) s.todo = s.left;
+    __syncthreads();
 }
 
 // The rows `from` + k of an item, for the bits k of `marked`, by the whole CTA; their outputs are there, infinities and NaN
@@ -1505,7 +1520,8 @@ __device__ __noinline__ void look_again(const ChunkArgs& a, const Item* item, in
         if (want) atomicOr(&s.todo, 1u << k);
     }
     __syncthreads();
-    if (s.todo) form_rows<D>(a, table, head, end, s, lane, warp);
+#pragma unroll 1
+    for (float unit = 1.0f; s.todo; unit = 0x1p-31f) form_rows<D>(a, table, head, end, unit, s, lane, warp);
     __syncthreads();
 }
 
@@ -1553,7 +1569,7 @@ __device__ __noinline__ void look_at_words(const ChunkArgs& a, const Work& w, in
 // Adds the parts of cut items, in their order: a piece's CTA takes its share of the rows, a warp a row. Rows that are
 // marked, in any of the pieces too, or whose parts' sum is not finite are looked at again.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const __grid_constant__ ChunkArgs a,
+__global__ void __launch_bounds__(kJoinThreads, D == 64 ? 4 : 2) chunk_join_kernel(const __grid_constant__ ChunkArgs a,
                                                                   const __grid_constant__ Work w) {
     constexpr int kChannels = D / 32, kDepth = 8;
     __shared__ Again<D> again;

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import chunk_oracle
-from test_gpu_extend import BF, I32, P, Case, context
+from test_gpu_extend import BF, I32, P, Case, bf16, context
 
 pytestmark = pytest.mark.gpu
 
@@ -183,3 +183,20 @@ def test_a_long_sum_past_fp32(cuda):
     want = torch.einsum("p,pd->d", count, pool[:, 0, 1].double().mean(1)) / count.sum()
     relative = 2.0 ** -9 + 2.0 ** -19 + 2.0 ** -21
     assert ((out[0, 0].double() / want - 1).abs() <= relative + 2.0 ** -8 * (1 + relative)).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_small_values_beside_a_bad_one(cuda, d):
+    """Rows in front of a token whose values are NaN, over values near the smallest numbers, and others beside them whose
+    sum passes fp32."""
+    c = Case([(0, 100), (60, 50)], 4, 2, d, seed=d)
+    r = np.random.default_rng(d)
+    c.pool[:, :, 1, :, :8] = bf16(r.uniform(1, 2, c.pool.shape[:2] + (P, 8)) * 2.0 ** -120)
+    c.pool[:, :, 1, :, 8:12] = bf16(r.uniform(1, 2, c.pool.shape[:2] + (P, 4)) * 2.0 ** 126)
+    want, bound = chunk_oracle.extend(c.q, c.pool, c.tables, c.start, c.total, 1 / math.sqrt(d))
+    for b, t in ((0, 90), (1, 100)):
+        c.pool[c.tables[b, t // P], :, 1, t % P] = np.nan
+    got = c.run(cuda).double().cpu().numpy()
+    for rows in (slice(0, 90), slice(100, 140)):
+        assert (np.abs(got - want) <= bound)[rows].all()
+    assert np.isnan(got[90:100]).all() and np.isnan(got[140:]).all()
