@@ -1389,8 +1389,9 @@ __device__ __forceinline__ void form_rows(const ChunkArgs& a, const int32_t* tab
             float m = fmaxf(x, s.m[k]);
 #pragma unroll 1
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float f = exp2_approx(s.m[k] - m), p = bf16_lo(bf16_pair(exp2_approx(x - m), 0.0f));
-            const float sum = s.sum[k] * f + warp_sum(p);
+            // rounded for the product and summed unrounded, as in the attention: a row must not change by its being here
+            const float f = exp2_approx(s.m[k] - m), e = exp2_approx(x - m), p = bf16_lo(bf16_pair(e, 0.0f));
+            const float sum = s.sum[k] * f + warp_sum(e);
             float acc[kChannels] = {};               // of the step alone: a sum of 2^24 would take no more ones
 #pragma unroll 1
             for (int i = 0; i < min(seen, 32); ++i) {

@@ -200,3 +200,25 @@ def test_small_values_beside_a_bad_one(cuda, d):
     for rows in (slice(0, 90), slice(100, 140)):
         assert (np.abs(got - want) <= bound)[rows].all()
     assert np.isnan(got[90:100]).all() and np.isnan(got[140:]).all()
+
+
+def test_formed_rows_weigh_alike(cuda):
+    """A row over two tokens, with a token of NaN behind it and without: the same bits. Weights 1 and 2^-0.75, rounded for
+    the product with V and summed unrounded; the first value is 0, so that there is one product, exact in fp32."""
+    d = 64
+    q, pool = torch.zeros(3, 1, d, dtype=BF, device=cuda), torch.zeros(1, 1, 2, P, d, dtype=BF, device=cuda)
+    q[..., 0], pool[0, 0, 0, 1, 0] = 1.0, -0.75
+    v = 1 + torch.arange(d, dtype=torch.float64) / d
+    pool[0, 0, 1, 1] = v.to(BF)
+    w = 2.0 ** -0.75
+    rounded = float(torch.tensor(w).to(BF))
+    want, other = (rounded * v / (1 + w)).to(BF), (rounded * v / (1 + rounded)).to(BF)
+    assert not torch.equal(want, other)
+    t = lambda *x: torch.tensor(x, dtype=I32, device=cuda)
+    ctx = context(1, 1, d, sm_scale=math.log(2))
+    ws = torch.empty(ctx.extend_bf16_workspace_size(1, 3), dtype=torch.uint8, device=cuda)
+    for value in (0.0, float("nan")):
+        pool[0, 0, 1, 2] = value
+        out = torch.empty_like(q)
+        ctx.extend_bf16(q, pool, t(0)[None], t(0, 3), t(3), out, ws)
+        assert torch.equal(out[1, 0].cpu(), want)
