@@ -29,7 +29,9 @@ oscar_status cuda_fail(cudaError_t e, const char* where) {
 }
 
 // Host-side fault injection for tests: OSCAR_FAULT=alloc|upload|launch makes
-// the matching step fail with its error status before touching the device.
+// the matching step fail with its error status before touching the device,
+// OSCAR_FAULT=wait has oscar_extend_bf16 leave out loads, so that its waits run
+// out (after a millisecond) and the call ends as it would then.
 bool fault(const char* what) {
     const char* f = std::getenv("OSCAR_FAULT");
     return f && std::strcmp(f, what) == 0;

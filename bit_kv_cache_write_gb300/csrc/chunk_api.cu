@@ -151,6 +151,8 @@ oscar_status oscar_extend_bf16(oscar_ctx_t* ctx, const void* q, int64_t q_stride
     a.batch = batch; a.n = n; a.h_kv = s.h_kv; a.g = s.h_q / s.h_kv; a.d = s.d;
     a.scale_log2 = (float)(s.sm_scale * 1.4426950408889634073599);
     a.debug = s.debug; a.dbg = ctx->dbg;
+    a.lost_loads = oscar::injected_fault("wait");
+    a.wait_ticks = a.lost_loads ? oscar::kLostWait : oscar::kChunkWait;
     oscar::ProfScope ps(&ctx->prof, OSCAR_KERNEL_EXTEND, static_cast<cudaStream_t>(stream));
     return cuda_status(oscar::launch_chunk(a, plan, workspace, s.d, ctx->num_sms, static_cast<cudaStream_t>(stream)),
                        "chunk attention launch");

@@ -54,7 +54,6 @@ constexpr int kSelfUnits = 80;                   // row blocks and requests up t
 constexpr int kJoinThreads = 256;
 constexpr float kNoReference = -3.402823466e38f; // reference before any token: no finite logit is below it
 constexpr float kHeadroom = 8.0f;                // the reference rises when a logit passes it by this much (log2)
-constexpr uint32_t kWaitTicks = 2000000000u;     // cycles of a wait at most, about a second
 constexpr int kFold = 512;                       // tiles whose products the tensor core adds up (see Fold)
 
 // A work item: rows r0 .. r0 + rows of request b's row space against cache tiles [kv0, kv1).
@@ -400,21 +399,21 @@ struct Layout {
     __device__ static uint32_t item_phase(int i) { return i / kItemRing & 1; }
 
     // A role that gives up: the others stop at their next wait.
-    __device__ void give_up(DebugWord* dbg, int where) const {
+    __device__ void give_up(const ChunkArgs& a, int where) const {
         sts32(fail(), 1);
-        record_error(&dbg->kind, &dbg->index, 4, where);
+        record_error(&a.dbg->kind, &a.dbg->index, 4, where);
     }
     // False once the wait has run out or another role has given up; the same for all lanes of the warp.
-    __device__ __forceinline__ bool wait(uint32_t at, uint32_t phase, DebugWord* dbg, int where) const {
+    __device__ __forceinline__ bool wait(uint32_t at, uint32_t phase, const ChunkArgs& a, int where) const {
         if (__all_sync(0xffffffffu, mbar_test(at, phase))) return true;
-        return wait_longer(at, phase, dbg, where);
+        return wait_longer(at, phase, a, where);
     }
-    __device__ __forceinline__ bool wait_longer(uint32_t at, uint32_t phase, DebugWord* dbg, int where) const {
+    __device__ __forceinline__ bool wait_longer(uint32_t at, uint32_t phase, const ChunkArgs& a, int where) const {
         const uint32_t t0 = cycles();
         bool ok;
         while (!(ok = mbar_test(at, phase)) && !lds32(fail())) {
-            if (cycles() - t0 > kWaitTicks) {
-                give_up(dbg, where);
+            if (cycles() - t0 > a.wait_ticks) {
+                give_up(a, where);
                 break;
             }
         }
@@ -424,7 +423,7 @@ struct Layout {
     __device__ void drain(uint32_t at, uint32_t phase) const {
         const uint32_t t0 = cycles();
         while (!mbar_test(at, phase))
-            if (cycles() - t0 > kWaitTicks) return;
+            if (cycles() - t0 > kChunkWait) return;
     }
     __device__ Item read_item(int i) const {
         Item it;
@@ -722,7 +721,7 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
         int next = !w.self && lane == 0 ? atomicAdd(&w.head->next, 1) + (int)gridDim.x : 0;
         if (w.self) next = (i + 1) * (int)gridDim.x + (i % 2 ? (int)blockIdx.x : (int)(gridDim.x - 1 - blockIdx.x));
         const bool stop = item >= n_items;
-        ok = sm.wait(sm.item_empty(i), sm.item_phase(i) ^ 1, a.dbg, i);
+        ok = sm.wait(sm.item_empty(i), sm.item_phase(i) ^ 1, a, i);
         if (!ok) break;
         if (!stop && w.self) {
             put_own_item(a, w, plan, sm.item(i), item, n_items);
@@ -737,7 +736,8 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
         const Item it = sm.read_item(i);
         if (in_line) next = item + it.kv1 - it.kv0;
         const Blocks bl = blocks_of(it, g_log2);
-        const int count = max(bl.count[0], bl.count[1]);
+        const bool lost = a.lost_loads && blockIdx.x % 2;    // what a test asks for: some tiles of this item, then no more
+        const int count = min(max(bl.count[0], bl.count[1]), lost ? (int)blockIdx.x / 2 % 4 : 0x7fffffff);
         const int32_t* table = a.tables + (int64_t)it.b * a.stride;
         // page ids of four tiles a load, asked for four tiles ahead; -1 where there is no page to read
         const int last_page = min((it.total + kPage - 1) / kPage, (it.kv0 + count) * kTilePages);
@@ -764,7 +764,7 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
             __syncwarp();
 #pragma unroll
             for (int kind = 0; kind < 2; ++kind) {           // K, then V
-                ok = sm.wait(sm.kv_empty(slot), sm.kv_phase(slot) ^ 1, a.dbg, 1000 + i);
+                ok = sm.wait(sm.kv_empty(slot), sm.kv_phase(slot) ^ 1, a, 1000 + i);
                 if (!ok) break;
                 if (lane == 0) mbar_expect_tx(sm.kv_full(slot), L::kTileBytes);
                 __syncwarp();
@@ -775,6 +775,7 @@ __device__ __forceinline__ void load_role(const ChunkArgs& a, const Work& w, con
             }
             ++tile;
         }
+        if (lost) break;
         item = __shfl_sync(0xffffffffu, next, 0);
     }
     // what was asked for lands before the CTA may leave
@@ -821,7 +822,7 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> s
         }
     };
     for (int i = 0; ok; ++i) {
-        ok = sm.wait(sm.item_full(i), sm.item_phase(i), a.dbg, 2000 + i);
+        ok = sm.wait(sm.item_full(i), sm.item_phase(i), a, 2000 + i);
         if (!ok) break;
         const Item it = sm.read_item(i);
         __syncwarp();
@@ -832,11 +833,11 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> s
         if (count == 0) continue;
         // S of the first tile
         const int k0 = slot++;
-        ok = sm.wait(sm.kv_full(k0), sm.kv_phase(k0), a.dbg, 3000 + i);
+        ok = sm.wait(sm.kv_full(k0), sm.kv_phase(k0), a, 3000 + i);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             if (!ok || bl.count[t] == 0) continue;
-            ok = sm.wait(sm.q_full(t), q_phase[t], a.dbg, 4000 + i);
+            ok = sm.wait(sm.q_full(t), q_phase[t], a, 4000 + i);
             q_phase[t] ^= 1;
             if (!ok) break;
             tc_fence_after();
@@ -854,33 +855,33 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> s
                 if (j < count) vs = slot++;
                 const bool more = j + 1 < count;
                 const int kn = more ? slot++ : 0;
-                if (more) ok = sm.wait(sm.kv_full(kn), sm.kv_phase(kn), a.dbg, 6000 + i);
+                if (more) ok = sm.wait(sm.kv_full(kn), sm.kv_phase(kn), a, 6000 + i);
                 if (ok && j + 1 < bl.count[0]) {
-                    ok = sm.wait(sm.s_read(0), steps[0] + j & 1, a.dbg, 7000 + i);
+                    ok = sm.wait(sm.s_read(0), steps[0] + j & 1, a, 7000 + i);
                     if (!ok) break;
                     tc_fence_after();
                     scores(0, kn);
                 }
                 if (ok && j > 0 && j <= bl.count[1]) {
-                    ok = sm.wait(sm.p_full(1), steps[1] + j + 1 & 1, a.dbg, 7000 + i);
+                    ok = sm.wait(sm.p_full(1), steps[1] + j + 1 & 1, a, 7000 + i);
                     if (!ok) break;
                     tc_fence_after();
                     values(1, v_last, j - 1);
                 }
                 if (ok && j > 0) umma_commit(leader, sm.kv_empty(v_last));
                 if (ok && j + 1 < bl.count[1]) {
-                    ok = sm.wait(sm.s_read(1), steps[1] + j & 1, a.dbg, 7000 + i);
+                    ok = sm.wait(sm.s_read(1), steps[1] + j & 1, a, 7000 + i);
                     if (!ok) break;
                     tc_fence_after();
                     scores(1, kn);
                 }
                 if (ok && more) umma_commit(leader, sm.kv_empty(kn));
                 if (!ok || j == count) break;
-                ok = sm.wait(sm.kv_full(vs), sm.kv_phase(vs), a.dbg, 5000 + i);
+                ok = sm.wait(sm.kv_full(vs), sm.kv_phase(vs), a, 5000 + i);
                 if (!ok) break;
                 clean_values(it, vs, j);
                 if (j < bl.count[0]) {
-                    ok = sm.wait(sm.p_full(0), steps[0] + j & 1, a.dbg, 7000 + i);
+                    ok = sm.wait(sm.p_full(0), steps[0] + j & 1, a, 7000 + i);
                     if (!ok) break;
                     tc_fence_after();
                     values(0, vs, j);
@@ -889,7 +890,7 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> s
         } else {
             for (int j = 0; j < count && ok; ++j) {
                 const int vs = slot++;
-                ok = sm.wait(sm.kv_full(vs), sm.kv_phase(vs), a.dbg, 5000 + i);
+                ok = sm.wait(sm.kv_full(vs), sm.kv_phase(vs), a, 5000 + i);
                 if (!ok) break;
                 clean_values(it, vs, j);
                 const bool more = j + 1 < count;
@@ -898,14 +899,14 @@ __device__ __forceinline__ void issue_role(const ChunkArgs& a, const Layout<D> s
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (j < bl.count[t]) {
-                        ok = sm.wait(sm.p_full(t), steps[t] + j & 1, a.dbg, 7000 + i);
+                        ok = sm.wait(sm.p_full(t), steps[t] + j & 1, a, 7000 + i);
                         if (!ok) break;
                         tc_fence_after();
                         values(t, vs, j);
                     }
                     if (t == 1) umma_commit(leader, sm.kv_empty(vs));
                     if (j + 1 < bl.count[t]) {
-                        if (!here) ok = sm.wait(sm.kv_full(kn), sm.kv_phase(kn), a.dbg, 6000 + i);
+                        if (!here) ok = sm.wait(sm.kv_full(kn), sm.kv_phase(kn), a, 6000 + i);
                         here = true;
                         if (!ok) break;
                         tc_fence_after();
@@ -1073,7 +1074,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
     // Waits for item i and asks for its queries, once the products with the last ones are done; says that they are there.
     bool asked = false;
     auto ask = [&](int i) {
-        if (!sm.wait(sm.item_full(i), sm.item_phase(i), a.dbg, 8000 + i)) return false;
+        if (!sm.wait(sm.item_full(i), sm.item_phase(i), a, 8000 + i)) return false;
         const Item it = sm.read_item(i);
         if (it.rows < 0) return true;
         const Blocks bl = blocks_of(it, g_log2);
@@ -1109,7 +1110,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
         float m = kNoReference, sum = 0.0f;
         bool early = false;
         for (int j = 0; j < count; ++j, ++step, seen -= kChunkTile) {
-            if (!sm.wait(sm.s_full(t), step & 1, a.dbg, 9000 + i)) return;
+            if (!sm.wait(sm.s_full(t), step & 1, a, 9000 + i)) return;
             // the last logits: the next item's queries travel while their weights are formed and the products end. Not
             // waited for here: the loader may need these weights to get that far.
             if (j + 1 == count && __all_sync(0xffffffffu, mbar_over(sm.item_full(i + 1), sm.item_phase(i + 1)))) {
@@ -1118,7 +1119,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
             }
             // The block's products before these logits, which read the weights and add to the outputs: done with the
             // logits where those were asked for behind them, else waited for.
-            auto done = [&] { return !L::kBeside || j == 0 || sm.wait(sm.o_done(t), (step - 1) & 1, a.dbg, 10000 + i); };
+            auto done = [&] { return !L::kBeside || j == 0 || sm.wait(sm.o_done(t), (step - 1) & 1, a, 10000 + i); };
             if (!working) {                      // no row of this warp is any: what its lanes hold as weights reaches nothing
                 if (L::kBeside && lane == 0) mbar_arrive(sm.s_read(t));
                 if (!done()) return;             // nor may it be a step ahead
@@ -1182,7 +1183,7 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
             sm.drain(sm.item_full(i + 1), sm.item_phase(i + 1));
         if (!early && !ask(i + 1)) return;
         there();
-        if (count > 0 && !sm.wait(sm.o_done(t), (step - 1) & 1, a.dbg, 10000 + i)) return;
+        if (count > 0 && !sm.wait(sm.o_done(t), (step - 1) & 1, a, 10000 + i)) return;
         uint32_t again = 0;
         if (working) {
             tc_fence_after();

@@ -28,6 +28,8 @@ cudaError_t launch_norm_rope(const RopeArgs& a, int d, int num_sms, cudaStream_t
 // ---- attention of new tokens over BF16 pages (chunk_attend.cu)
 constexpr int kChunkRows = 256;              // query rows (token, head of the group) of a work item
 constexpr int kChunkTile = 128;              // cached tokens of a step
+constexpr uint32_t kChunkWait = 2000000000u; // cycles of a wait at most, about a second
+constexpr uint32_t kLostWait = 2000000u;     // the same where loads are lost on purpose, about a millisecond
 
 // Where the parts of a call's workspace lie, in bytes.
 struct ChunkPlan {
@@ -47,6 +49,8 @@ struct ChunkArgs {
     int batch, n, h_kv, g, d;
     float scale_log2;                        // sm_scale * log2(e)
     int debug; DebugWord* dbg;
+    uint32_t wait_ticks;                     // cycles that a role waits for another at most
+    int lost_loads;                          // every other CTA's loader stops in its first item and tells nobody: waits run out
 };
 ChunkPlan plan_chunk(const Shape& s, int num_sms, int batch, int n);
 cudaError_t launch_chunk(const ChunkArgs& a, const ChunkPlan& plan, void* workspace, int d, int num_sms, cudaStream_t st);

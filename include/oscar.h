@@ -532,7 +532,12 @@ OSCAR_API oscar_status oscar_norm_rope(oscar_ctx_t* ctx, const void* q, int64_t 
  * count as in oscar_decode_bf16, as do page ids outside the pool.
  * The result does not change from run to run.
  * Asynchronous on `stream`. n == 0 or batch == 0 is a no-op; batch > 65535 returns
- * OSCAR_ERR_UNSUPPORTED. */
+ * OSCAR_ERR_UNSUPPORTED.
+ * Its kernels wait for one another's loads and products, a second at most. Should
+ * a wait run out, the call still ends, and writes nothing but rows of requests in
+ * out and the workspace; but these rows are then unwritten or wrong. The
+ * call has returned OSCAR_OK before that: oscar_debug_error tells (kind 4). Later
+ * calls, with the same workspace too, are not touched by it. */
 OSCAR_API size_t oscar_extend_bf16_workspace_size(const oscar_ctx_t* ctx, int batch, int n);
 OSCAR_API oscar_status oscar_extend_bf16(oscar_ctx_t* ctx, const void* q, int64_t q_stride, const void* bf16_pool,
                                          int64_t bf16_pool_pages, const int32_t* tables, int table_stride,
@@ -576,8 +581,9 @@ OSCAR_API const char* oscar_last_error(void);
 /* Read and clear the device error word (debug_bounds mode).
  * Synchronizes the device. Returns OSCAR_OK if nothing was recorded, otherwise
  * OSCAR_ERR_BOUNDS, with *kind set to the check that failed (1 slot, 2 page
- * id, 3 length, 4 a page copy that did not land within its bounded wait) and
- * *index to the offending value (either pointer may be NULL). Kind 4 is
+ * id, 3 length, 4 a wait that ran out: a page copy that did not land or, in
+ * oscar_extend_bf16, a plan, product or softmax that did not come) and *index to
+ * the offending value (kind 4: which wait; either pointer may be NULL). Kind 4 is
  * recorded in every mode; kinds 1-3 only with debug_bounds. */
 OSCAR_API oscar_status oscar_debug_error(oscar_ctx_t* ctx, int* kind, long long* index);
 

@@ -222,3 +222,33 @@ def test_formed_rows_weigh_alike(cuda):
         out = torch.empty_like(q)
         ctx.extend_bf16(q, pool, t(0)[None], t(0, 3), t(3), out, ws)
         assert torch.equal(out[1, 0].cpu(), want)
+
+
+@pytest.mark.parametrize("lens,h_q,h_kv,d", [([(9000, 2)], 8, 1, 128), ([(0, 700), (300, 40)], 8, 2, 64), ([(300, 3)] * 30, 4, 2, 128),
+                                             ([(i * 7 % 90, 1 + i % 3) for i in range(200)], 4, 2, 64)],
+                         ids=["cut", "whole", "line", "many"])
+def test_a_wait_that_runs_out(cuda, monkeypatch, lens, h_q, h_kv, d):
+    """Every other CTA's loader stops in its first item: the call ends, says so afterwards, and writes nothing beyond its rows
+    and workspace, whatever the workspace held; the next call of the same context and workspace is as ever."""
+    c, ctx = Case(lens, h_q, h_kv, d, seed=3, spare=2), context(h_q, h_kv, d)
+    t = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).to(cuda).to(dt)
+    n, size = len(c.q), ctx.extend_bf16_workspace_size(len(c.total), len(c.q))
+    q, pool, tables, start, total = t(c.q, BF), t(c.pool, BF), t(c.tables, I32), t(c.start, I32), t(c.total, I32)
+    outs = torch.full((n + 64, h_q, d), 7.0, dtype=BF, device=cuda)
+    space = torch.full((size + 4096,), 255, dtype=torch.uint8, device=cuda)
+    out, ws = outs[32:32 + n], space[:size]
+
+    def call():
+        ctx.extend_bf16(q, pool, tables, start, total, out, ws)
+        torch.cuda.synchronize()
+        assert (outs[:32] == 7).all() and (outs[32 + n - 2:] == 7).all() and (space[size:] == 255).all()
+        return ctx.debug_error()[:2]
+
+    for again in range(2):                                   # over a workspace of nothing, and one of an earlier call
+        monkeypatch.setenv("OSCAR_FAULT", "wait")
+        assert call() == (-5, 4)
+        monkeypatch.delenv("OSCAR_FAULT")
+        out.fill_(7.0)
+        assert call()[0] == 0
+        c.check(out)
+        out.fill_(7.0)
