@@ -252,3 +252,31 @@ def test_a_wait_that_runs_out(cuda, monkeypatch, lens, h_q, h_kv, d):
         assert call()[0] == 0
         c.check(out)
         out.fill_(7.0)
+
+
+def test_every_row_of_the_largest_batch(cuda):
+    """65,535 requests of 256 rows: all 16.8 million against the definition in 64 bits, with chunk_oracle's bound."""
+    batch, new, d, pages, per = 65535, 256, 64, 512, 19
+    n, scale = batch * new, 1 / 8
+    gen = torch.Generator(device=cuda).manual_seed(8)
+    lens = torch.randint(0, 40, (batch,), generator=gen, device=cuda, dtype=I32)
+    pool = torch.randn(pages, 1, 2, P, d, generator=gen, device=cuda).to(BF)
+    tables = torch.randint(0, pages, (batch, per), generator=gen, device=cuda, dtype=I32)
+    q = torch.randn(n, 1, d, generator=gen, device=cuda, dtype=BF)
+    out, ctx = torch.full_like(q, 7.0), context(1, 1, d)
+    ws = torch.full((ctx.extend_bf16_workspace_size(batch, n),), 255, dtype=torch.uint8, device=cuda)
+    ctx.extend_bf16(q, pool, tables, torch.arange(0, n + 1, new, dtype=I32, device=cuda), lens + new, out, ws)
+    torch.cuda.synchronize()
+    assert ctx.debug_error()[0] == 0
+    token, wide = torch.arange(per * P, device=cuda), pool.double()
+    for b in range(0, batch, 1024):
+        rows, some = slice(b * new, min(b + 1024, batch) * new), slice(b, min(b + 1024, batch))
+        k, v = (wide[tables[some].long(), 0, i].flatten(1, 2) for i in (0, 1))
+        x = q[rows, 0].double().view(-1, new, d)
+        seen = token[None, None] <= (lens[some, None] + torch.arange(new, device=cuda))[..., None]
+        size = torch.where(seen, x.abs() @ k.abs().mT, 0.0).amax(-1, keepdim=True) * scale
+        p = torch.softmax(torch.where(seen, (x @ k.mT) * scale, -math.inf), -1)
+        y, mean = p @ v, p @ v.abs()
+        e = size * (9 * d / 16 + 2) * 2.0 ** -23 + 4 * 2.0 ** -23 + 1.01 * 2.0 ** -8
+        err = e * (mean + y.abs()) * (1 + 2 * e) + (72 * 4 + 64) * 2.0 ** -23 * mean
+        assert ((out[rows, 0].double().view_as(y) - y).abs() <= err + 2.0 ** -8 * (y.abs() + err)).all(), b
