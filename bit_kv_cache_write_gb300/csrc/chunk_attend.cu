@@ -1000,10 +1000,11 @@ __device__ __forceinline__ float weigh128(uint32_t (&u)[4][32], uint64_t scale, 
     return x + y;
 }
 
-// The tensor core cuts off what its fp32 accumulator does not hold, so a sum of one sign falls short by 2^-25 of itself an
-// addition, eight additions a tile: 0.6 % after 8,192 tiles, 2.6 % after 32,768 (measured). Every kFold tiles the outputs
-// are therefore added, rounded to nearest, to a row in the workspace, and begin anew; at the end they come back. An
-// accumulator is short by 0.04 % then, and 512 tiles take some 600 us, the addition some 5.
+// The tensor core cuts off what its fp32 accumulator does not hold, so a sum of one sign falls short, a little more with each
+// of a tile's eight additions: by 0.6 % after 8,192 tiles and 2.6 % after 32,768 (measured: 2^-23.3 of the final sum an
+// addition). Every kFold tiles the outputs are therefore added, rounded to nearest, to a row in the workspace, and begin
+// anew; at the end they come back. An accumulator is short by 0.04 % then (by that rate), and 512 tiles take some 600 us,
+// the addition some 5.
 //
 // Instructions on tensor memory want the warp's lanes together: where some have a row and others none, they meet again
 // in front of each (here and where outputs are stored).
