@@ -18,10 +18,11 @@
 // unrounded ones, in fp32.
 //
 // What bounds it (32 query and 8 KV heads of 128 on one GB300): long prompts the tensor cores and the power, 8,192 tokens
-// in 342 us = 1.61 PFLOP/s, 84 % of the measured rate of a large matrix product; the softmax of a block takes 1,250 cycles
-// a tile, its two products 1,024, of two blocks' 2,048. At d = 64 (255 us) the softmax, of which two blocks share the ex2
+// in 345 us in a graph of a few passes = 1.59 PFLOP/s, 84 % of the measured rate of a large matrix product, and 369 to 375
+// in a loop of calls, where the card is at its power limit (77 %); the softmax of a block takes 1,250 cycles a tile, its
+// two products 1,024, of two blocks' 2,048. At d = 64 (257 us) the softmax, of which two blocks share the ex2
 // (1,024 cycles) and all else. Few rows HBM: 1 to 8 tokens of 32 requests of 4k to 32k in 280 us = 6.5 TB/s, 97 % of the
-// measured copy rate; a lone row block (8 tokens at 100,000, 74.7 us) 81 %, by the parts' writing and join and the items'
+// measured copy rate; a lone row block (8 tokens at 100,000, 74 us) 82 %, by the parts' writing and join and the items'
 // starts. Short ones the chain of launch, plan, loads, softmax and join: 11 us.
 //
 // Items of requests with long caches and few rows are cut along the cache, by a plan from the lengths on the device, so

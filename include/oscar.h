@@ -529,7 +529,12 @@ OSCAR_API oscar_status oscar_norm_rope(oscar_ctx_t* ctx, const void* q, int64_t 
  * to bf16.
  * Tokens that a row does not see do not matter to it, nor does what lies behind a
  * sequence: NaN and infinity neither. Logits and values that are infinite or NaN
- * count as in oscar_decode_bf16, as do page ids outside the pool.
+ * count as in oscar_decode_bf16, as do page ids outside the pool. Rows that an
+ * infinity or NaN among the values reaches, their own or one up to 127 tokens
+ * behind them, are looked at a second time, and so are rows whose finite values'
+ * sum passes fp32: a call with such rows takes some 10 times as long where every
+ * row of a long prompt sees an infinite value, and some 300 times where every
+ * row's sum passes fp32.
  * The result does not change from run to run.
  * Asynchronous on `stream`. n == 0 or batch == 0 is a no-op; batch > 65535 returns
  * OSCAR_ERR_UNSUPPORTED.

@@ -280,3 +280,40 @@ def test_every_row_of_the_largest_batch(cuda):
         e = size * (9 * d / 16 + 2) * 2.0 ** -23 + 4 * 2.0 ** -23 + 1.01 * 2.0 ** -8
         err = e * (mean + y.abs()) * (1 + 2 * e) + (72 * 4 + 64) * 2.0 ** -23 * mean
         assert ((out[rows, 0].double().view_as(y) - y).abs() <= err + 2.0 ** -8 * (y.abs() + err)).all(), b
+
+
+@pytest.mark.parametrize("lens,h_q,h_kv,d", [([(30, 90), (2000, 2), (0, 5)], 8, 2, 64), ([(i * 7 % 90, 1 + i % 3) for i in range(200)], 4, 2, 128)],
+                         ids=["few", "many"])
+def test_bad_values_come_and_go(cuda, lens, h_q, h_kv, d):
+    """One captured call, queries at a stride, values that are finite, spoiled and finite again: nothing of an earlier
+    replay is left."""
+    c = Case(lens, h_q, h_kv, d, seed=17, spare=2)
+    clean = c.pool.copy()
+    t = lambda a, dt: torch.from_numpy(np.ascontiguousarray(a)).to(cuda).to(dt)
+    wide = torch.full((len(c.q), h_q * d + 40), float("nan"), dtype=BF, device=cuda)
+    q = wide[:, 16:16 + h_q * d].unflatten(1, (h_q, d))
+    q.copy_(t(c.q, BF))
+    pool, out = t(c.pool, BF), torch.empty(c.q.shape, dtype=BF, device=cuda)
+    ctx, side = context(h_q, h_kv, d), torch.cuda.Stream()
+    ws = torch.full((ctx.extend_bf16_workspace_size(len(c.total), len(c.q)),), 255, dtype=torch.uint8, device=cuda)
+    args = t(c.tables, I32), t(c.start, I32), t(c.total, I32)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        ctx.extend_bf16(q, pool, *args, out, ws)
+    first = None
+    for step in range(5):
+        c.pool = clean.copy()
+        if step % 2:
+            spread_infinities(c, step)
+        pool.copy_(t(c.pool, BF))
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        if step % 2:
+            check_odd(c, out, 1 / math.sqrt(d))
+        else:
+            c.check(out)
+            first = out.clone() if first is None else first
+            assert torch.equal(out, first)
