@@ -1208,9 +1208,9 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
                     for (int k = 0; k < 32; ++k) o[k] = 0;
                 }
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = inv == 0.0f ? 0 : o[k];    // no token with a weight: zeros, whatever values are
-#pragma unroll
                 for (int k = 0; k < 32; k += 2) probe = fma_f32x2(f32x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), 0ull, probe);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = inv == 0.0f ? 0 : o[k];    // no token with a weight: zeros, whatever values are
                 if (mine(it) && it.part >= 0) {  // a part of a cut item, as it is
                     float* to = w.part_acc + (int64_t)part * D + c;
 #pragma unroll
@@ -1232,7 +1232,8 @@ __device__ __forceinline__ void softmax_role(const ChunkArgs& a, const Work& w, 
             tc_fence_before();
             float lo, hi;
             split_f32x2(probe, lo, hi);
-            again = __ballot_sync(0xffffffffu, lo + hi != 0.0f && mine(it) && inv == inv);       // a sum of NaN: a row of NaN
+            // a sum of NaN is a row of NaN, none a row of zeros; but a part without a weight may hold infinities of its row
+            again = __ballot_sync(0xffffffffu, lo + hi != 0.0f && mine(it) && inv == inv && (inv != 0.0f || it.part >= 0));
         }
         if (lane == 0) w.odd[(int64_t)sm.read_item(i).self * 8 + 4 * t + warp] = again;
         if (lane == 0 && again) sts32(sm.marked(), 1);
@@ -1392,7 +1393,7 @@ __device__ __forceinline__ void form_rows(const ChunkArgs& a, const int32_t* tab
             float m = fmaxf(x, s.m[k]);
 #pragma unroll 1
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            // rounded for the product and summed unrounded, as in the attention: a row must not change by its being here
+            // rounded for the product and summed unrounded, as in the attention
             const float f = exp2_approx(s.m[k] - m), e = exp2_approx(x - m), p = bf16_lo(bf16_pair(e, 0.0f));
             const float sum = s.sum[k] * f + warp_sum(e);
             float acc[kChannels] = {};               // of the step alone: a sum of 2^24 would take no more ones

@@ -104,6 +104,20 @@ def test_infinite_values_without_weight(cuda, lens):
     assert (got[:rows] == 0).all()
 
 
+@pytest.mark.parametrize("lens,h_q,h_kv,d", [([(9000, 2)], 8, 1, 128), ([(3000, 1)] * 12, 4, 2, 64)], ids=["cut", "line"])
+def test_infinite_values_of_a_part_without_weight(cuda, lens, h_q, h_kv, d):
+    """All logits of the first tokens, more than a part's, are -infinity, and one of their values is infinite."""
+    c = Case(lens, h_q, h_kv, d, seed=6)
+    c.q[..., 0] = 1.0
+    c.pool[:, :, 0, :, 0] = 0.0
+    for b, total in enumerate(c.total):
+        c.pool[c.tables[b, :total // 2 // P], :, 0, :, 0] = -np.inf
+        c.pool[c.tables[b, 3], 0, 1, 5, 9] = np.inf
+    some = check_odd(c, c.run(cuda), 1 / math.sqrt(d))
+    g = h_q // h_kv
+    assert some[:, :g, 9].all() and some.sum() == g * len(c.q)
+
+
 def test_infinite_values_as_in_the_decode(cuda):
     """Single tokens: infinite and NaN at the same places."""
     lens = [(0, 1), (15, 1), (4000, 1), (16, 1), (77, 1), (9000, 1)]
