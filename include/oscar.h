@@ -534,7 +534,8 @@ OSCAR_API oscar_status oscar_norm_rope(oscar_ctx_t* ctx, const void* q, int64_t 
  * behind them, are looked at a second time, and so are rows whose finite values'
  * sum passes fp32: a call with such rows takes some 10 times as long where every
  * row of a long prompt sees an infinite value, and some 300 times where every
- * row's sum passes fp32.
+ * row's sum passes fp32. Where it is a token behind a row that holds them, the
+ * row's channels are formed anew, within the same rounding, not to the same bits.
  * The result does not change from run to run.
  * Asynchronous on `stream`. n == 0 or batch == 0 is a no-op; batch > 65535 returns
  * OSCAR_ERR_UNSUPPORTED.
